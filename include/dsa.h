@@ -92,7 +92,10 @@ enum dsa_op {
   DSA_OP_TOPK = 2,
   DSA_OP_FUSED_INDEXER = 3,
   DSA_OP_SPARSE_MLA_ATTN = 4,
-  DSA_OP_FUSED_FORWARD = 5
+  DSA_OP_FUSED_FORWARD = 5,
+  DSA_OP_PREFIX_MLA_ATTN = 6,
+  DSA_OP_ATTN_WEIGHTS = 7,
+  DSA_OP_EVICT = 8
 };
 
 /* Shape, types and sequence layout of one DSA problem. */
@@ -274,6 +277,105 @@ int dsa_fused_indexer_static(const dsa_problem* p, const void* q_idx, const void
 int dsa_indexer_prolog(int32_t total_q, int32_t h_idx, int32_t d_idx, int32_t d_model,
                        const void* q_proj, const void* x, const void* w_h, uint8_t* q_codes,
                        float* q_scale, float* w, void* stream);
+
+/*
+ * The residual's addition and the root-mean-square norm, with the output in the input's type,
+ * in 8 bits with scales, or both ("… New-Architecture LLMs" §4.2: the indexer's preprocessing
+ * normalises the K side; §5.1: the index side is quantised).  For each of `rows` rows of d
+ * elements, in fp32:
+ *   h = x + residual  (h = x without a residual; h_out is h rounded to dtype)
+ *   y = h · rsqrt(Σ h² / d + eps) · weight  (from the unrounded h)
+ *   quant = DSA_FP8_E4M3: scale[r] = max|y| / 448 (f32; 1 where that is below the smallest
+ *     normal number), codes = E4M3(y / scale) (nearest even, saturated to ±448): on rows of
+ *     d_idx elements these are k_idx and k_scale of the FP8 indexer;
+ *   quant = DSA_MXFP8_E4M3: scale[r, g] the E8M0 byte e + 127 of the smallest power of two with
+ *     max|y| <= 448·2^e over the 32 elements of group g (127 for an all-zero group; byte 255
+ *     is never written), codes = E4M3(y / 2^e): k_idx and k_scale of the MXFP8 indexer;
+ *   quant = 0: no codes (codes and scale are ignored).
+ * A row with a NaN or an infinity comes out as NaN where 0 · infinity or a NaN arises, like the formula.
+ * x [rows, d] and residual [rows, d] dtype (F32 or BF16), row strides ld_x, ld_res >= d elements;
+ * weight [d] dtype; h_out [rows, d] dtype, required with residual (NULL without); y [rows, d]
+ * dtype, required without quant (may be NULL with); codes [rows, d] bytes; scale [rows] f32 or
+ * [rows, d/32] bytes.  h_out and y may be x or residual themselves where that one's row stride is
+ * d; other overlaps of an output are refused.  Pointers need the alignment of their element; 16-byte aligned
+ * rows are faster.  Any d in 1 .. 2^24 (MXFP8: a multiple of 32).
+ * One launch, no workspace.  rows = 0 launches nothing and accepts NULL pointers.
+ */
+int dsa_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, int32_t quant, float eps,
+                    const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                    const void* weight, void* h_out, void* y, uint8_t* codes, void* scale,
+                    void* stream);
+
+/*
+ * Dense MLA attention for a batch that shares a prefix.  Every query attends over the prefix's
+ * prefix_len latent rows and, causally, over its own sequence's (the cache rows p describes:
+ * the sequence's tokens after the prefix).  For query row t at position pos of its sequence b
+ * and head h, over the keys x = the prefix rows, then rows 0..pos of sequence b:
+ *   S_x = sm_scale · q[t,h,:] · key_x   (all D columns)
+ *   out[t,h,:] = Σ_x softmax(S)_x · key_x[0:d_c],   lse[t,h] = log Σ_x exp(S_x)
+ * The prefix is attended by all rows together, 128 (token, head) rows at a time, not sequence by
+ * sequence.  prefix_len = 0 gives dense causal attention over each sequence alone (what sparse
+ * attention equals while a history has at most top_k positions).
+ * q, kv, out, lse as in dsa_sparse_mla_attn; h_idx, d_idx, top_k and idx_dtype are not used
+ * (top_k still has to be valid).
+ * prefix_kv [prefix_len, D] kv_dtype, 16-byte aligned: the prefix's rows; or NULL with
+ * prefix_table [ceil(prefix_len / page_size)] device int32 (4-byte aligned): its pages in the
+ * paged cache kv.  Exactly one of the two where prefix_len > 0; prefix_table needs a paged p.
+ * A page outside the cache sets DSA_FLAG_BAD_INDEX; its keys are skipped.  A row without any key
+ * gets out = 0 and lse = -inf.  Rows of a sequence whose cu_q/cu_k are inconsistent are flagged
+ * (DSA_FLAG_BAD_SEQS) and left as they were.
+ * prefix_len + max_k_len < 2^30.
+ */
+int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* prefix_kv,
+                        const int32_t* prefix_table, const void* q, const void* kv, void* out,
+                        float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The attention weight that cached positions received, accumulated (what dsa_evict goes by).
+ * For every query row t of sequence b and every valid entry i of idx[t, :]:
+ *   acc[b, idx[t,i]] += Σ_h exp(sm_scale · q[t,h,:]·kv[row of idx[t,i], :] − lse[t,h])
+ * with idx and lse those of dsa_sparse_mla_attn on the same q and kv.  Entries that attention
+ * skips add nothing (an entry outside [0, pos(t)] or on a page outside the cache sets
+ * DSA_FLAG_BAD_INDEX); neither do heads whose lse is -inf; a repeated entry adds as often
+ * as it appears.  The result does not depend on the order of the additions: the same call gives the
+ * same bytes.
+ * q, kv, idx, lse as in dsa_sparse_mla_attn (lse required); acc [num_seqs, ld_acc] f32, ld_acc >=
+ * max_k_len, added to in place (columns at or past a sequence's length stay as they are).
+ */
+int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void* kv,
+                                const int32_t* idx, const float* lse, float* acc, int64_t ld_acc,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction from the caches by accumulated attention weight.  Sequence b (L_b positions) keeps
+ * n_b = min(L_b, budget): all where L_b <= budget; otherwise its first `sink` positions, its last
+ * `recent` ones, and the budget - sink - recent with the largest acc between them (among equal
+ * ones the smaller positions; NaN counts as largest where its sign is positive).  Kept
+ * positions keep their order and move to the caches' *_out tensors:
+ *   kept[b, 0..n_b-1] = the kept positions, ascending; kept[b, n_b..budget-1] = -1
+ *   cu_k_out[b] = Σ_{b' < b} n_b'                           (num_seqs + 1 entries)
+ *   acc_out[b, i] = acc[b, kept[b, i]] for i < n_b, 0 for n_b <= i < ld_acc_out
+ *   kv_out, k_idx_out, k_scale_out: row of position i of sequence b in the destination =
+ *     the source's row of position kept[b, i].
+ * The destination is packed (sequence b at rows cu_k_out[b] ..; rows_out rows in all), or, with
+ * table_out [num_seqs, max_pages_out] (device int32; p paged), paged with p's page_size over
+ * num_pages_out pages (rows_out is then ignored).  Rows of the destination that
+ * hold no kept position stay as they were.  A page outside either cache, or a packed row at or
+ * past rows_out, sets DSA_FLAG_BAD_SEQS and the row is not moved.  A sequence whose cu_k is inconsistent keeps
+ * nothing (DSA_FLAG_BAD_SEQS).
+ * Each of kv (row: D of kv_dtype), k_idx (d_idx of idx_dtype) and k_scale (4 bytes for FP8, d_idx/32 for
+ * MXFP8) comes with its *_out, or both are NULL (not moved).  Destination rows must not be rows
+ * the call reads: a packed *_out that overlaps its source is refused; with pages, source and
+ * destination may be one pool, in which the destination's pages must not be the sources'.
+ * acc [num_seqs, ld_acc >= max_k_len] f32; acc_out [num_seqs, ld_acc_out >= budget] f32 or NULL,
+ * not overlapping acc; 1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
+ */
+int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t budget, int32_t sink,
+              int32_t recent, int32_t* kept, int32_t* cu_k_out, float* acc_out, int64_t ld_acc_out,
+              const void* kv, void* kv_out, const void* k_idx, void* k_idx_out,
+              const void* k_scale, void* k_scale_out, const int32_t* table_out,
+              int32_t max_pages_out, int32_t num_pages_out, int64_t rows_out, void* ws,
+              size_t ws_bytes, void* stream);
 
 /* Zero the workspace status block (the status word and the kernels' counters; enqueued on
  * `stream`). */

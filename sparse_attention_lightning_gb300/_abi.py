@@ -14,13 +14,15 @@ DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_WORKSPAC
 DSA_F32, DSA_BF16, DSA_FP8_E4M3, DSA_MXFP8_E4M3 = 0, 1, 2, 3
 DSA_FLAG_BAD_INDEX, DSA_FLAG_BAD_SEQS, DSA_FLAG_TIMEOUT, DSA_FLAG_CHECK = 0x1, 0x2, 0x4, 0x8
 OP_INDEXER_SCORES, OP_TOPK, OP_FUSED_INDEXER, OP_SPARSE_MLA_ATTN, OP_FUSED_FORWARD = 1, 2, 3, 4, 5
+OP_PREFIX_MLA_ATTN, OP_ATTN_WEIGHTS, OP_EVICT = 6, 7, 8
 
 # Every symbol include/dsa.h declares.
 EXPORTS = ("dsa_workspace_size", "dsa_indexer_scores", "dsa_topk", "dsa_fused_indexer",
            "dsa_sparse_mla_attn", "dsa_fused_forward", "dsa_clear_status", "dsa_read_status",
            "dsa_status_str", "dsa_last_error", "dsa_abi_version", "dsa_trace_begin",
            "dsa_trace_end", "dsa_trace_count", "dsa_trace_get", "dsa_fused_indexer_static",
-           "dsa_selftest_wait_timeout", "dsa_indexer_prolog")
+           "dsa_selftest_wait_timeout", "dsa_indexer_prolog", "dsa_add_rmsnorm",
+           "dsa_prefix_mla_attn", "dsa_accumulate_attn_weights", "dsa_evict")
 
 
 class DsaProblem(ctypes.Structure):
@@ -85,6 +87,12 @@ def lib() -> ctypes.CDLL:
         "dsa_clear_status": [vp, vp],
         "dsa_selftest_wait_timeout": [vp, ctypes.c_uint64, vp],
         "dsa_indexer_prolog": [ctypes.c_int32] * 4 + [vp] * 7,
+        "dsa_add_rmsnorm": [i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                            vp, i64, vp, i64, vp, vp, vp, vp, vp, vp],
+        "dsa_prefix_mla_attn": [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_accumulate_attn_weights": [P, vp, vp, vp, vp, vp, i64, vp, sz, vp],
+        "dsa_evict": [P, vp, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, i64,
+                      vp, vp, vp, vp, vp, vp, vp, ctypes.c_int32, ctypes.c_int32, i64, vp, sz, vp],
         "dsa_read_status": [vp, vp, ctypes.POINTER(ctypes.c_uint32)],
         "dsa_abi_version": [],
         "dsa_trace_begin": [ctypes.c_int],

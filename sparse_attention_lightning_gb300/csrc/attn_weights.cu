@@ -1,0 +1,124 @@
+// dsa_accumulate_attn_weights: the attention weight each cached position received, added up
+// over heads and queries.
+//
+//   acc[b, idx[t,i]] += Σ_h exp(scale · q[t,h,:]·kv[row_i,:] − lse[t,h])
+//
+// A query's weights are probabilities (the lse is the attention's), so the sum needs no running
+// max.  One CTA = one query × 64 of its selected positions; the CUDA cores compute in fp32.
+//
+// Order.  Where no sequence has more than one query, a position receives additions of one value
+// only (a repeated index adds the same weight again), so plain fp32 atomics give the same bytes
+// in every order.  Otherwise the queries' weights are first added in 64-bit fixed point, whose
+// sums do not depend on the order, and then once to acc.
+#include "attn_weights.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 16;    // selected rows in shared memory
+constexpr int kHeads = 16;
+constexpr int kSlots = 64;   // selected positions a CTA takes
+
+template <typename TK>
+__global__ void __launch_bounds__(kThreads) attn_weights_simt_kernel(WeightArgs a) {
+  extern __shared__ float smem[];
+  const int D = a.d, DP = D + 1;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  float* ks = smem;                  // [kKeys][D + 1]
+  float* qs = ks + kKeys * DP;       // [kHeads][D]
+  float* red = qs + kHeads * D;      // [kHeads][kKeys]
+  __shared__ int pos_s[kKeys], row_s[kKeys];
+  RowInfo r;
+  if (!query_row_info(a.seqs, t, r, a.status)) return;
+  const TK* q = static_cast<const TK*>(a.q) + (int64_t)t * a.h * D;
+  const TK* kv = static_cast<const TK*>(a.kv);
+  const int hh = tid / kKeys, kk = tid % kKeys;
+  const int lo = blockIdx.y * kSlots, hi = min(a.top_k, lo + kSlots);
+  for (int i0 = lo; i0 < hi; i0 += kKeys) {
+    __syncthreads();
+    if (tid < kKeys) {
+      const int v = i0 + tid < hi ? a.idx[(int64_t)t * a.top_k + i0 + tid] : -1;
+      int row = -1;
+      if (v >= 0 && v <= r.pos) row = key_row(a.seqs, r.b, r.k0, v);
+      if (row < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+      pos_s[tid] = v;
+      row_s[tid] = row;
+    }
+    __syncthreads();
+    for (int i = tid; i < kKeys * D; i += kThreads) {
+      const int k = i / D, c = i - k * D;
+      ks[k * DP + c] = row_s[k] >= 0 ? to_f32(kv[(int64_t)row_s[k] * D + c]) : 0.f;
+    }
+    float w = 0.f;
+    for (int h0 = 0; h0 < a.h; h0 += kHeads) {
+      __syncthreads();
+      const int n = min(kHeads, a.h - h0) * D;
+      for (int i = tid; i < n; i += kThreads) qs[i] = to_f32(q[(int64_t)h0 * D + i]);
+      __syncthreads();
+      if (h0 + hh < a.h) {
+        const float lse = a.lse[(int64_t)t * a.h + h0 + hh];
+        float dot = 0.f;
+        for (int c = 0; c < D; ++c) dot = fmaf(qs[hh * D + c], ks[kk * DP + c], dot);
+        // lse = -inf: the attention had no valid entry, so nothing received weight
+        if (lse != -INFINITY) w += exp2f(fmaf(dot, a.scale_log2, -lse * kLog2e));
+      }
+    }
+    red[hh * kKeys + kk] = w;
+    __syncthreads();
+    if (tid < kKeys && row_s[tid] >= 0) {
+      float s = 0.f;
+      for (int j = 0; j < kHeads; ++j) s += red[j * kKeys + tid];
+      add_weight(a, r.b, pos_s[tid], s);
+    }
+  }
+}
+
+// acc += the fixed-point sums of the positions a sequence holds.
+__global__ void __launch_bounds__(256) attn_weights_finish_kernel(WeightArgs a, int per) {
+  const int b = blockIdx.x / per, j = blockIdx.x - b * per;
+  const int L = min(__ldg(a.seqs.cu_k + b + 1) - __ldg(a.seqs.cu_k + b), a.seqs.max_k_len);
+  const float unit = (float)(1.0 / a.fx_scale);
+  for (int s = j * 256 + threadIdx.x; s < L; s += per * 256) {
+    const long long v = a.fx[(int64_t)b * a.seqs.max_k_len + s];
+    if (v) a.acc[(int64_t)b * a.ld_acc + s] += (float)v * unit;
+  }
+}
+
+template <typename TK>
+int launch_typed(const WeightArgs& a, cudaStream_t stream) {
+  const size_t smem = sizeof(float) * ((size_t)kKeys * (a.d + 1) + (size_t)kHeads * a.d +
+                                       kHeads * kKeys);
+  auto kern = attn_weights_simt_kernel<TK>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return check_launch("attn_weights_simt: smem attribute");
+  dim3 grid((unsigned)a.seqs.total_q, (unsigned)((a.top_k + kSlots - 1) / kSlots));
+  DSA_LAUNCH("attn_weights_simt", stream, kern<<<grid, kThreads, smem, stream>>>(a));
+  return check_launch("attn_weights_simt");
+}
+
+}  // namespace
+
+int launch_attn_weights_simt(const WeightArgs& a, cudaStream_t stream) {
+  return a.kv_dtype == DSA_F32 ? launch_typed<float>(a, stream)
+                               : launch_typed<__nv_bfloat16>(a, stream);
+}
+
+int launch_attn_weights(const WeightArgs& a, cudaStream_t stream) {
+  if (a.fx) {
+    const cudaError_t e = cudaMemsetAsync(
+        a.fx, 0, (size_t)a.seqs.B * a.seqs.max_k_len * sizeof(long long), stream);
+    if (e != cudaSuccess)
+      return set_error(DSA_ERR_CUDA, "attn_weights clear: %s", cudaGetErrorString(e));
+  }
+  const int rc = launch_attn_weights_simt(a, stream);
+  if (rc != DSA_OK || !a.fx) return rc;
+  const int64_t want = (a.seqs.max_k_len + 1023) / 1024, most = 0x7fffffff / a.seqs.B;
+  const int per = (int)(want < 64 ? (want < most ? want : most) : (64 < most ? 64 : most));
+  DSA_LAUNCH("attn_weights_finish", stream,
+             attn_weights_finish_kernel<<<(unsigned)per * a.seqs.B, 256, 0, stream>>>(a, per));
+  return check_launch("attn_weights_finish");
+}
+
+}  // namespace dsa

@@ -9,7 +9,10 @@
 #include <string>
 #include <vector>
 
+#include "attn_weights.cuh"
 #include "dsa_internal.cuh"
+#include "evict.cuh"
+#include "prefix_attn.cuh"
 #include "tc_sm100.cuh"
 
 namespace dsa {
@@ -389,6 +392,70 @@ int run_sfa(const dsa_problem* p, const void* q, const void* kv, const int32_t* 
   return launch_sfa_simt(sa, s);
 }
 
+// ----------------------------------------------------------------------------
+// Shared-prefix attention.
+
+PrefixArgs prefix_args(const dsa_problem* p, int prefix_len) {
+  PrefixArgs a{};
+  a.seqs = seqs_of(p);
+  a.max_q_len = p->max_q_len;
+  a.h = p->h;
+  a.d_c = p->d_c;
+  a.d_rope = p->d_rope;
+  a.kv_dtype = p->kv_dtype;
+  a.out_dtype = p->out_dtype;
+  a.scale_log2 = scale_of(p) * kLog2e;
+  a.prefix_len = prefix_len;
+  return a;
+}
+
+// Pieces a row's keys are cut into, so that few rows still fill the SMs (three blocks fit one):
+// at least 128 keys a piece.  It depends on the rows alone where the keys' number is unknown
+// (prefix_len < 0: the most that any prefix asks for), so the workspace does not grow with the prefix.
+int prefix_simt_splits(const dsa_problem* p, int64_t prefix_len) {
+  const int64_t blocks = (int64_t)p->num_seqs * prefix_simt_blocks(p->max_q_len, p->h);
+  if (blocks == 0) return 1;
+  int64_t s = 3 * (int64_t)num_sms() / blocks;
+  if (prefix_len >= 0) {
+    const int64_t most = (prefix_len + p->max_k_len + 127) / 128;
+    if (s > most) s = most;
+  }
+  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+// Partial outputs and their (max, sum) for `pieces` pieces of every row.
+size_t carve_prefix(const dsa_problem* p, int pieces, void* ws, PrefixArgs* a) {
+  Carve c;
+  const size_t rows = (size_t)p->total_q * p->h;
+  const size_t o = c.take(pieces > 1 ? pieces * rows * p->d_c * 4 : 0);
+  const size_t m = c.take(pieces > 1 ? pieces * rows * 8 : 0);
+  if (a) {
+    a->part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o);
+    a->part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + m);
+  }
+  return c.off;
+}
+size_t ws_prefix(const dsa_problem* p) {
+  return carve_prefix(p, prefix_simt_splits(p, -1), nullptr, nullptr);
+}
+
+// ----------------------------------------------------------------------------
+// Accumulated attention weight and eviction.
+
+// Fixed-point sums where a sequence may have several queries.
+size_t carve_weights(const dsa_problem* p, void* ws, long long** fx) {
+  Carve c;
+  const bool need = p->max_q_len > 1;
+  const size_t o = c.take(need ? (size_t)p->num_seqs * p->max_k_len * 8 : 0);
+  if (fx) *fx = need ? reinterpret_cast<long long*>(static_cast<char*>(ws) + o) : nullptr;
+  return c.off;
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 }  // namespace
 }  // namespace dsa
 
@@ -432,6 +499,15 @@ int dsa_workspace_size(const dsa_problem* p, int op, size_t* bytes) {
       DSA_TRY(check_problem(p, true, true));
       *bytes = ws_fused_forward(p);
       break;
+    case DSA_OP_PREFIX_MLA_ATTN:
+      DSA_TRY(check_problem(p, false, true));
+      *bytes = ws_prefix(p);
+      break;
+    case DSA_OP_ATTN_WEIGHTS:
+      DSA_TRY(check_problem(p, false, true));
+      *bytes = carve_weights(p, nullptr, nullptr);
+      break;
+    case DSA_OP_EVICT: DSA_TRY(check_problem(p, false, false)); *bytes = kStatusBytes; break;
     default: return set_error(DSA_ERR_INVALID_ARG, "unknown op %d", op);
   }
   return DSA_OK;
@@ -513,6 +589,158 @@ int dsa_fused_forward(const dsa_problem* p, const void* q_idx, const void* k_idx
   // the kernels run back to back: each may start while the one before it finishes
   DSA_TRY(run_fused_indexer(p, q_idx, k_idx, w, q_scale, k_scale, idx, vals_out, ws, s));
   return run_sfa(p, q, kv, idx, out, lse, ws, sc.sfa, s);
+}
+
+int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* prefix_kv,
+                        const int32_t* prefix_table, const void* q, const void* kv, void* out,
+                        float* lse, void* ws, size_t ws_bytes, void* stream) {
+  DSA_TRY(check_problem(p, false, true));
+  if (prefix_len < 0) return set_error(DSA_ERR_INVALID_ARG, "prefix_len = %d", prefix_len);
+  if ((int64_t)prefix_len + p->max_k_len >= (int64_t(1) << 30))
+    return set_error(DSA_ERR_UNSUPPORTED, "prefix_len + max_k_len >= 2^30");
+  if (prefix_len > 0) {
+    if ((prefix_kv != nullptr) == (prefix_table != nullptr))
+      return set_error(DSA_ERR_INVALID_ARG, "one of prefix_kv and prefix_table is needed");
+    if (prefix_table && p->page_size == 0)
+      return set_error(DSA_ERR_INVALID_ARG, "prefix_table needs paged caches");
+    DSA_TRY(check_ptr(prefix_kv, "prefix_kv", true));
+    if (((uintptr_t)prefix_table & 3u) != 0)
+      return set_error(DSA_ERR_INVALID_ARG, "prefix_table is not 4-byte aligned");
+  }
+  DSA_TRY(check_ptr(q, "q", p->total_q == 0));
+  DSA_TRY(check_ptr(kv, "kv"));
+  DSA_TRY(check_ptr(out, "out", p->total_q == 0));
+  DSA_TRY(check_ptr(lse, "lse", true));
+  if ((int64_t)p->total_q * p->h >= (int64_t(1) << 31) ||
+      (int64_t)p->num_seqs * prefix_simt_blocks(p->max_q_len, p->h) >= (int64_t(1) << 31))
+    return set_error(DSA_ERR_UNSUPPORTED, "too many (token, head) rows");
+  DSA_TRY(check_ws(ws, ws_bytes, ws_prefix(p)));
+  if (p->total_q == 0) return DSA_OK;
+  PrefixArgs a = prefix_args(p, prefix_len);
+  a.prefix_kv = prefix_len > 0 ? prefix_kv : nullptr;
+  a.prefix_table = prefix_len > 0 ? prefix_table : nullptr;
+  a.q = q;
+  a.kv = kv;
+  a.out = out;
+  a.lse = lse;
+  a.status = static_cast<uint32_t*>(ws);
+  a.splits = prefix_simt_splits(p, prefix_len);
+  carve_prefix(p, a.splits, ws, &a);
+  return launch_prefix_simt(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void* kv,
+                                const int32_t* idx, const float* lse, float* acc, int64_t ld_acc,
+                                void* ws, size_t ws_bytes, void* stream) {
+  DSA_TRY(check_problem(p, false, true));
+  const bool none = p->total_q == 0;
+  DSA_TRY(check_ptr(q, "q", none));
+  DSA_TRY(check_ptr(kv, "kv"));
+  DSA_TRY(check_ptr(idx, "idx", none));
+  DSA_TRY(check_ptr(lse, "lse", none));
+  if (!acc || ((uintptr_t)acc & 3u) != 0)
+    return set_error(DSA_ERR_INVALID_ARG, "acc is NULL or not 4-byte aligned");
+  if (ld_acc < p->max_k_len) return set_error(DSA_ERR_INVALID_ARG, "ld_acc < max_k_len");
+  DSA_TRY(check_ws(ws, ws_bytes, carve_weights(p, nullptr, nullptr)));
+  if (none) return DSA_OK;
+  WeightArgs a{};
+  a.seqs = seqs_of(p);
+  a.h = p->h;
+  a.d = p->d_c + p->d_rope;
+  a.top_k = p->top_k;
+  a.kv_dtype = p->kv_dtype;
+  a.scale_log2 = scale_of(p) * kLog2e;
+  a.q = q;
+  a.kv = kv;
+  a.idx = idx;
+  a.lse = lse;
+  a.acc = acc;
+  a.ld_acc = ld_acc;
+  a.status = static_cast<uint32_t*>(ws);
+  carve_weights(p, ws, &a.fx);
+  // the sum of a position's weights is below 2 · h · max_q_len <= 2^ceil: the rest of 62 bits are
+  // binary places
+  int ceil = 0;
+  while ((int64_t(1) << ceil) < 2 * (int64_t)p->h * p->max_q_len) ++ceil;
+  a.fx_scale = (double)(int64_t(1) << (62 - ceil));
+  return launch_attn_weights(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t budget, int32_t sink,
+              int32_t recent, int32_t* kept, int32_t* cu_k_out, float* acc_out, int64_t ld_acc_out,
+              const void* kv, void* kv_out, const void* k_idx, void* k_idx_out,
+              const void* k_scale, void* k_scale_out, const int32_t* table_out,
+              int32_t max_pages_out, int32_t num_pages_out, int64_t rows_out, void* ws,
+              size_t ws_bytes, void* stream) {
+  DSA_TRY(check_problem(p, k_idx || k_scale, kv != nullptr));
+  if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
+    return set_error(DSA_ERR_INVALID_ARG, "budget = %d, sink = %d, recent = %d", budget, sink, recent);
+  if ((int64_t)p->num_seqs * budget >= (int64_t(1) << 40))
+    return set_error(DSA_ERR_UNSUPPORTED, "num_seqs * budget too large");
+  const void* need[4] = {acc, kept, cu_k_out, acc};
+  const char* names[4] = {"acc", "kept", "cu_k_out", "acc"};
+  for (int i = 0; i < 3; ++i)
+    if (!need[i] || ((uintptr_t)need[i] & 3u) != 0)
+      return set_error(DSA_ERR_INVALID_ARG, "%s is NULL or not 4-byte aligned", names[i]);
+  if (ld_acc < p->max_k_len) return set_error(DSA_ERR_INVALID_ARG, "ld_acc < max_k_len");
+  if (acc_out) {
+    if (((uintptr_t)acc_out & 3u) != 0 || ld_acc_out < budget)
+      return set_error(DSA_ERR_INVALID_ARG, "acc_out is not 4-byte aligned or ld_acc_out < budget");
+    if (overlap(acc, ld_acc * p->num_seqs * 4, acc_out, ld_acc_out * p->num_seqs * 4))
+      return set_error(DSA_ERR_INVALID_ARG, "acc_out overlaps acc");
+  }
+  EvictArgs a{};
+  const int kvb = (p->d_c + p->d_rope) * (p->kv_dtype == DSA_BF16 ? 2 : 4);
+  const int ixb = p->d_idx * (p->idx_dtype == DSA_F32 ? 4 : p->idx_dtype == DSA_BF16 ? 2 : 1);
+  const int scb = p->idx_dtype == DSA_FP8_E4M3 ? 4 : p->idx_dtype == DSA_MXFP8_E4M3 ? p->d_idx / 32 : 0;
+  if (k_scale && scb == 0)
+    return set_error(DSA_ERR_INVALID_ARG, "k_scale goes with FP8 or MXFP8 index keys");
+  const void* src[3] = {kv, k_idx, k_scale};
+  void* dst[3] = {kv_out, k_idx_out, k_scale_out};
+  const int bytes[3] = {kvb, ixb, scb};
+  const char* cache[3] = {"kv", "k_idx", "k_scale"};
+  if (table_out) {
+    if (p->page_size == 0) return set_error(DSA_ERR_INVALID_ARG, "table_out needs paged caches");
+    if (((uintptr_t)table_out & 3u) != 0 || max_pages_out < 1 || num_pages_out < 1)
+      return set_error(DSA_ERR_INVALID_ARG, "table_out is not 4-byte aligned, or max_pages_out = %d, num_pages_out = %d",
+                       max_pages_out, num_pages_out);
+    if ((int64_t)num_pages_out * p->page_size >= (int64_t(1) << 31))
+      return set_error(DSA_ERR_UNSUPPORTED, "num_pages_out * page_size >= 2^31");
+  } else if (rows_out < 0 || rows_out >= (int64_t(1) << 31)) {
+    return set_error(DSA_ERR_INVALID_ARG, "rows_out = %lld", (long long)rows_out);
+  }
+  const Seqs seqs = seqs_of(p);
+  for (int i = 0; i < 3; ++i) {
+    if ((src[i] != nullptr) != (dst[i] != nullptr))
+      return set_error(DSA_ERR_INVALID_ARG, "%s and %s_out go together", cache[i], cache[i]);
+    if (!src[i]) continue;
+    DSA_TRY(check_ptr(src[i], cache[i]));
+    DSA_TRY(check_ptr(dst[i], cache[i]));
+    const int64_t n_out = table_out ? (int64_t)num_pages_out * p->page_size : rows_out;
+    if (!(table_out && src[i] == dst[i]) &&
+        overlap(src[i], seqs.cache_rows() * bytes[i], dst[i], n_out * bytes[i]))
+      return set_error(DSA_ERR_INVALID_ARG, "%s_out overlaps %s", cache[i], cache[i]);
+    a.src[i] = src[i];
+    a.dst[i] = dst[i];
+    a.row_bytes[i] = bytes[i];
+  }
+  DSA_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  a.seqs = seqs;
+  a.acc = acc;
+  a.ld_acc = ld_acc;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.kept = kept;
+  a.cu_k_out = cu_k_out;
+  a.acc_out = acc_out;
+  a.ld_acc_out = ld_acc_out;
+  a.table_out = table_out;
+  a.max_pages_out = max_pages_out;
+  a.num_pages_out = num_pages_out;
+  a.rows_out = rows_out;
+  a.status = static_cast<uint32_t*>(ws);
+  return launch_evict(a, static_cast<cudaStream_t>(stream));
 }
 
 int dsa_clear_status(void* ws, void* stream) {

@@ -26,6 +26,9 @@ constexpr int kRowSyncWord = 256;
 constexpr int kPieceWord = kRowSyncWord + 2 * 128 * 8;
 constexpr int kPieceRows = (int)(kStatusBytes / 4 - kPieceWord) / 2;
 
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Sequence layout as the kernels see it.
