@@ -436,7 +436,9 @@ size_t carve_prefix(const dsa_problem* p, int pieces, void* ws, PrefixArgs* a) {
   return c.off;
 }
 size_t ws_prefix(const dsa_problem* p) {
-  return carve_prefix(p, prefix_simt_splits(p, -1), nullptr, nullptr);
+  const PrefixArgs a = prefix_args(p, 0);
+  return carve_prefix(p, prefix_tc_eligible(a) ? prefix_tc_most_pieces(a) : prefix_simt_splits(p, -1),
+                      nullptr, nullptr);
 }
 
 // ----------------------------------------------------------------------------
@@ -596,6 +598,8 @@ int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* pr
                         float* lse, void* ws, size_t ws_bytes, void* stream) {
   DSA_TRY(check_problem(p, false, true));
   if (prefix_len < 0) return set_error(DSA_ERR_INVALID_ARG, "prefix_len = %d", prefix_len);
+  if (p->total_q > 0 && p->max_q_len < 1)
+    return set_error(DSA_ERR_INVALID_ARG, "max_q_len = %d with total_q = %d", p->max_q_len, p->total_q);
   if ((int64_t)prefix_len + p->max_k_len >= (int64_t(1) << 30))
     return set_error(DSA_ERR_UNSUPPORTED, "prefix_len + max_k_len >= 2^30");
   if (prefix_len > 0) {
@@ -624,6 +628,10 @@ int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* pr
   a.out = out;
   a.lse = lse;
   a.status = static_cast<uint32_t*>(ws);
+  if (prefix_tc_eligible(a)) {
+    carve_prefix(p, prefix_tc_pieces(a), ws, &a);
+    return launch_prefix_tc(a, static_cast<cudaStream_t>(stream));
+  }
   a.splits = prefix_simt_splits(p, prefix_len);
   carve_prefix(p, a.splits, ws, &a);
   return launch_prefix_simt(a, static_cast<cudaStream_t>(stream));

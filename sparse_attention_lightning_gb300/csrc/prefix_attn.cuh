@@ -27,13 +27,14 @@ struct SeqInfo {
 };
 
 // Sequence b's rows; false (and flagged) when cu_q/cu_k are inconsistent with the descriptor.
-__device__ __forceinline__ bool seq_info(const Seqs& s, int b, SeqInfo& i, uint32_t* status) {
+__device__ __forceinline__ bool prefix_seq(const PrefixArgs& a, int b, SeqInfo& i) {
+  const Seqs& s = a.seqs;
   const int q0 = __ldg(s.cu_q + b), q1 = __ldg(s.cu_q + b + 1);
   const int k0 = __ldg(s.cu_k + b), k1 = __ldg(s.cu_k + b + 1);
   i = SeqInfo{b, q0, q1 - q0, k0, k1 - k0};
   const bool ok = q0 >= 0 && q1 >= q0 && q1 <= s.total_q && k0 >= 0 && k1 >= k0 &&
-                  k1 <= s.total_k && i.T <= i.L && i.L <= s.max_k_len;
-  if (!ok) atomicOr(status, DSA_FLAG_BAD_SEQS);
+                  k1 <= s.total_k && i.T <= i.L && i.L <= s.max_k_len && i.T <= a.max_q_len;
+  if (!ok) atomicOr(a.status, DSA_FLAG_BAD_SEQS);
   return ok;
 }
 
@@ -59,6 +60,13 @@ __device__ __forceinline__ const void* prefix_key(const PrefixArgs& a, int b, in
 inline int prefix_simt_blocks(int max_q_len, int h) {
   return (int)(((int64_t)max_q_len * h + 15) / 16);
 }
+
+// tcgen05 path (bf16, 64 <= D <= 576, d_c <= 512): the pieces it cuts rows into for a prefix length,
+// and for any (the workspace's size).
+bool prefix_tc_eligible(const PrefixArgs& a);
+int prefix_tc_pieces(const PrefixArgs& a);
+int prefix_tc_most_pieces(const PrefixArgs& a);
+int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream);
 
 int launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream);
 int launch_prefix_merge(const PrefixArgs& a, int pieces, cudaStream_t stream);

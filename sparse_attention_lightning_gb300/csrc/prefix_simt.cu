@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
   __shared__ uint32_t okmask;
 
   SeqInfo s;
-  if (!seq_info(a.seqs, b, s, a.status)) return;
+  if (!prefix_seq(a, b, s)) return;
   const int64_t r0 = (int64_t)blk * kRows, nrow = (int64_t)s.T * H;
   if (r0 >= nrow) return;
   const int R = (int)min((int64_t)kRows, nrow - r0);
@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(PrefixArgs a, int pie
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   RowInfo ri;
-  if (!query_row_info(a.seqs, (int)(row / a.h), ri, a.status)) return;
+  SeqInfo si;  // the pieces of a row whose sequence is inconsistent were not written
+  if (!query_row_info(a.seqs, (int)(row / a.h), ri, a.status) || !prefix_seq(a, ri.b, si)) return;
   float M = -INFINITY;
   for (int j = 0; j < pieces; ++j) {
     const float2 v = a.part_ml[j * rows + row];

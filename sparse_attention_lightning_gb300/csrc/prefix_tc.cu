@@ -1,0 +1,639 @@
+// Dense attention over the MLA latent cache for a batch that shares a prefix, on tcgen05 tensor
+// cores (bf16, 64 <= D <= 576, d_c <= 512, any number of heads).
+//
+//   S[r, x] = scale · q[r,:]·key_x,  out[r,:] = Σ_x softmax(S[r,:])_x · key_x[0:d_c]
+//
+// All heads of all queries attend over the same latent keys, so the MMA's M = 128 rows are any 128
+// (token, head) rows.  Rows of different sequences share a block where only the prefix is attended
+// (few rows a sequence): the prefix is then computed once for the batch, 128 rows at a time,
+// and each sequence's own keys in blocks of its own rows, and the pieces are merged.  Where a
+// sequence fills blocks by itself, its blocks run over prefix and suffix as one key axis.
+//
+// Why value halves.  A 128 x 512 fp32 output accumulator is all of the tensor memory.  So a CTA
+// accumulates at most 256 output columns, and d_c = 512 takes two CTAs a block, each with the
+// whole logits: 576 + 256 columns of MMA instead of 576 + 512 split in two (544), but no exchange of
+// partial logits between SMs (that link moves ~12 B a clock: 16 KB for a 64-key chunk would
+// take longer than the duplicate MMAs).  The twin CTA finds the keys in L2.
+//
+// Tensor memory: O (256 columns) | two logit buffers (64 each; P, as bf16 pairs, overwrites the
+// first half of its own logits) | the first 256 query columns (128).  Shared memory: the other query
+// columns (80 KB) and two rings of [64 keys x 64 columns] tiles: the CTA's own value columns are
+// held until P·V (3 chunks of 32 KB), the others only until the logits (6 tiles of 8 KB).
+//
+// Per chunk of 64 keys: the producer thread loads tiles by TMA; the MMA thread issues
+// S(g) = Q·Kᵀ (M=128, N=64, K=D), then O += P(g-1)·V (M=128, N=256, K=64; P from tensor memory);
+// four softmax warps, a thread a row, take the running max (it moves only when a row's max grows
+// by more than 2^8; O is then rescaled), the sum in fp32 of the unrounded p, and write P.
+// Every wait is bounded (DSA_FLAG_TIMEOUT).
+#include "prefix_attn.cuh"
+#include "tc_sm100.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128;                 // rows of a block
+constexpr int kN = 64;                  // keys of a chunk
+constexpr int kTile = kN * 128;         // 8 KB: 64 keys x 64 columns
+constexpr int kQTile = kM * 128;        // 16 KB: 128 rows x 64 columns
+constexpr int kQTmemTiles = 4;          // query column tiles in tensor memory
+constexpr int kQSmemTiles = 5;
+constexpr int kVSlots = 3, kKSlots = 6;
+constexpr int kVSlot = 4 * kTile;
+constexpr int kThreads = 192;           // producer, MMA, 4 softmax warps
+constexpr int kBarBytes = 512;
+constexpr int kSmem = kQSmemTiles * kQTile + kVSlots * kVSlot + kKSlots * kTile + kBarBytes + 1024;
+constexpr int kOCol = 0, kSCol = 256, kQCol = 384;
+constexpr float kRescaleLog2 = 8.0f;
+static_assert(kSmem <= 232448, "shared memory");
+
+struct Params {
+  PrefixArgs a;
+  int nblk;        // blocks of a sequence
+  int fblk;        // blocks of all rows end to end (prefix items), 0: one key axis
+  int sp, ss;      // pieces of the prefix alone / of a sequence's keys
+  int halves;      // value column halves
+  int prefix_items;
+  int chunk_rows;  // cache rows a tile is loaded in
+};
+
+struct Item {
+  int half, piece, b;        // b < 0: prefix only
+  int64_t row0;              // first flat (token, head) row
+  int rows;
+  int c0, c1;                // chunks [c0, c1) of the item's key axis
+  int ncp;                   // prefix chunks on the axis
+  int k0, pos0;              // suffix: first key row, position of the block's first token
+  int hoff;                  // head of the block's first row
+};
+
+// False: nothing to do (a block past its sequence's rows, an inconsistent sequence).
+__device__ __forceinline__ bool item_at(const Params& p, int i, Item& it) {
+  const int pch = (p.a.prefix_len + kN - 1) / kN;
+  if (i < p.prefix_items) {
+    it.half = i % p.halves;
+    i /= p.halves;
+    it.row0 = (int64_t)(i % p.fblk) * kM;
+    it.piece = i / p.fblk;
+    it.b = -1;
+    it.rows = (int)min((int64_t)kM, (int64_t)p.a.seqs.total_q * p.a.h - it.row0);
+    it.ncp = pch;
+    it.c0 = (int)((int64_t)pch * it.piece / p.sp);
+    it.c1 = (int)((int64_t)pch * (it.piece + 1) / p.sp);
+    it.k0 = it.pos0 = it.hoff = 0;
+    return true;
+  }
+  i -= p.prefix_items;
+  it.half = i % p.halves;
+  i /= p.halves;
+  const int blocks = p.a.seqs.B * p.nblk;
+  const int blk = i % blocks;
+  const int split = i / blocks;
+  it.b = blk / p.nblk;
+  SeqInfo s;
+  if (!prefix_seq(p.a, it.b, s)) return false;
+  const int64_t r0 = (int64_t)(blk - it.b * p.nblk) * kM, nrow = (int64_t)s.T * p.a.h;
+  if (r0 >= nrow) return false;
+  it.row0 = (int64_t)s.q0 * p.a.h + r0;
+  it.rows = (int)min((int64_t)kM, nrow - r0);
+  it.ncp = p.fblk ? 0 : pch;
+  it.k0 = s.k0;
+  it.pos0 = s.L - s.T + (int)(r0 / p.a.h);
+  it.hoff = (int)(r0 % p.a.h);
+  const int last = s.L - s.T + (int)((r0 + it.rows - 1) / p.a.h);
+  const int n = it.ncp + last / kN + 1;
+  it.c0 = (int)((int64_t)n * split / p.ss);
+  it.c1 = (int)((int64_t)n * (split + 1) / p.ss);
+  it.piece = (p.fblk ? p.sp : 0) + split;
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 64 consecutive tensor-memory columns of this warp's 32 lanes (two loads, one wait each).
+__device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
+  uint32_t r[32];
+  tmem_ld32(taddr, r);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
+  tmem_ld32(taddr + 32, r);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[32 + i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Zero the infinities and NaNs among 8 bf16 values; whether there were any.
+__device__ __forceinline__ bool finite8(uint4& v) {
+  uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((u[i] & 0x7f80u) == 0x7f80u) { u[i] &= 0xffff0000u; any = true; }
+    if ((u[i] & 0x7f800000u) == 0x7f800000u) { u[i] &= 0xffffu; any = true; }
+  }
+  v = make_uint4(u[0], u[1], u[2], u[3]);
+  return any;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap kmap) {
+  Item it;
+  if (!item_at(p, blockIdx.x, it)) return;
+  const PrefixArgs& a = p.a;
+  const int64_t rows_all = (int64_t)a.seqs.total_q * a.h;
+  const int nch = it.c1 - it.c0;
+  const bool split = (p.fblk ? p.sp + p.ss : p.ss) > 1;
+  if (nch == 0) {  // a piece without keys
+    if (split && it.half == 0)
+      for (int i = threadIdx.x; i < it.rows; i += kThreads)
+        a.part_ml[(int64_t)it.piece * rows_all + it.row0 + i] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* qs = smem;                               // [5][128][128 B]
+  uint8_t* vs = qs + kQSmemTiles * kQTile;          // [3][4][64][128 B]
+  uint8_t* ks = vs + kVSlots * kVSlot;              // [6][64][128 B]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ks + kKSlots * kTile);
+  uint64_t* v_full = bars;            // [3]
+  uint64_t* v_empty = bars + 3;       // [3]
+  uint64_t* k_full = bars + 6;        // [6]
+  uint64_t* k_empty = bars + 12;      // [6]
+  uint64_t* s_full = bars + 18;       // [2] logits of the buffer's chunk complete
+  uint64_t* p_full = bars + 20;       // [2] its 4 softmax warps have written P
+  uint64_t* pv_done = bars + 22;      // [2] its P·V complete
+  uint64_t* q_full = bars + 24;       // the query tiles in shared memory
+  uint64_t* qt_full = bars + 25;      // the query columns in tensor memory (4 warps)
+  uint64_t* drain = bars + 26;
+  uint64_t* badkeys = bars + 27;      // [3] keys of a chunk on pages outside the cache, a bit each
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 31);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.d_c + a.d_rope;
+  const int ntile = (D + 63) / 64;
+  const int vcol0 = it.half * 256;
+  const int ncol = min(256, a.d_c - vcol0);         // this CTA's output columns (a multiple of 16)
+  const int vt0 = it.half * 4, nvt = (ncol + 63) / 64;
+  const int nkt = ntile - nvt;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kVSlots; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
+    for (int i = 0; i < kKSlots; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(qt_full, 4);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+  tc_fence_before();
+  cta_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (lane == 0) {
+      const int nqs = max(ntile - kQTmemTiles, 0);
+      if (nqs) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(nqs * kQTile));
+        for (int j = 0; j < nqs; ++j)
+          tma_load_2d(qs + j * kQTile, &qmap, q_full, (kQTmemTiles + j) * 64, (int)it.row0);
+      }
+      int kt = 0, g = 0;
+      for (; g < nch; ++g) {
+        const int c = it.c0 + g, vslot = g % kVSlots;
+        if (!mbar_wait(&v_empty[vslot], ((g / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
+          break;
+        // the cache rows of the chunk's keys: one run, or one a page
+        const bool pre = c < it.ncp;
+        const int x0 = (pre ? c : c - it.ncp) * kN;
+        const CUtensorMap* map = pre ? &pmap : &kmap;
+        const bool paged = a.seqs.paged();
+        int run[kN / 16];
+        uint64_t bad = 0;
+        const int cr = p.chunk_rows, nrun = kN / cr;
+        if (!paged) {
+          run[0] = pre ? x0 : it.k0 + x0;
+        } else {
+          const int sh = __ffs(a.seqs.page_size) - 1;
+          const int pages = pre ? (a.prefix_len + a.seqs.page_size - 1) >> sh : a.seqs.max_pages;
+          const int32_t* table = pre ? a.prefix_table : a.seqs.block_table + (int64_t)it.b * a.seqs.max_pages;
+#pragma unroll
+          for (int j = 0; j < kN / 16; ++j) {
+            if (j >= nrun) break;
+            const int x = x0 + j * cr, slot = x >> sh;
+            const int pg = slot < pages ? __ldg(table + slot) : -1;
+            const bool ok = (unsigned)pg < (unsigned)a.seqs.num_pages;
+            // keys of a page outside the cache are masked; page 0 stands in for their rows
+            if (!ok) bad |= (cr == 64 ? ~0ull : ((1ull << cr) - 1)) << (j * cr);
+            run[j] = ok ? (pg << sh) | (x & (a.seqs.page_size - 1)) : 0;
+          }
+        }
+        badkeys[vslot] = bad;
+        mbar_arrive_expect_tx(&v_full[vslot], (uint32_t)(nvt * kTile));
+        for (int t = 0; t < nvt; ++t)
+#pragma unroll
+          for (int j = 0; j < kN / 16; ++j) {
+            if (j >= nrun) break;
+            tma_load_2d(vs + vslot * kVSlot + t * kTile + j * cr * 128, map, &v_full[vslot],
+                        (vt0 + t) * 64, run[j]);
+          }
+        bool stop = false;
+        for (int t = 0; t < ntile; ++t) {
+          if (t >= vt0 && t < vt0 + nvt) continue;
+          const int slot = kt % kKSlots;
+          if (!mbar_wait(&k_empty[slot], ((kt / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+            stop = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&k_full[slot], kTile);
+#pragma unroll
+          for (int j = 0; j < kN / 16; ++j) {
+            if (j >= nrun) break;
+            tma_load_2d(ks + slot * kTile + j * cr * 128, map, &k_full[slot], t * 64, run[j]);
+          }
+          ++kt;
+        }
+        if (stop) { ++g; break; }
+      }
+      // every copy issued has landed before the CTA may exit
+      if (nqs) mbar_wait_drain(q_full, 0);
+      for (int i = max(0, g - kVSlots); i < g; ++i)
+        mbar_wait_drain(&v_full[i % kVSlots], (i / kVSlots) & 1);
+      for (int i = max(0, kt - kKSlots); i < kt; ++i)
+        mbar_wait_drain(&k_full[i % kKSlots], (i / kKSlots) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16(kM, kN);
+      const uint32_t idesc_pv = idesc_bf16(kM, ncol, false, true);
+      const uint32_t q0 = smem_u32(qs), v0 = smem_u32(vs), k0 = smem_u32(ks);
+      bool stop = !mbar_wait(qt_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+      if (!stop && ntile > kQTmemTiles)
+        stop = !mbar_wait(q_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+      tc_fence_after();
+      int kt = 0;
+      // one tile's K-steps of the logits
+      auto qk_tile = [&](uint32_t d, int t, uint32_t tile, bool first) {
+        const int steps = min(4, (D - t * 64) / 16);
+        const uint64_t b0 = sdesc_sw128(tile, 16, 1024);
+        if (t < kQTmemTiles) {
+          for (int i = 0; i < steps; ++i)
+            mma_bf16_ts(d, tmem + kQCol + t * 32 + i * 8, b0 + (uint64_t)(i * 2), idesc_s,
+                        first && i == 0 ? 0u : 1u);
+        } else {
+          const uint64_t a0 = sdesc_sw128(q0 + (t - kQTmemTiles) * kQTile, 16, 1024);
+          for (int i = 0; i < steps; ++i)
+            mma_bf16(d, a0 + (uint64_t)(i * 2), b0 + (uint64_t)(i * 2), idesc_s,
+                     first && i == 0 ? 0u : 1u);
+        }
+      };
+      auto pv = [&](int g) -> bool {
+        if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) return false;
+        tc_fence_after();
+        const uint32_t vb = v0 + (g % kVSlots) * kVSlot;
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+          mma_bf16_ts(tmem + kOCol, tmem + kSCol + (g & 1) * kN + kk * 8,
+                      sdesc_sw128(vb + kk * 2048, kTile, 1024), idesc_pv, (g > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&v_empty[g % kVSlots]);
+        mma_commit(&pv_done[g & 1]);
+        return true;
+      };
+      for (int g = 0; g < nch && !stop; ++g) {
+        // the buffer's last P (chunk g - 2) has been read
+        if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g - 2) >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
+          break;
+        if (!mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + kSCol + (g & 1) * kN;
+        for (int t = 0; t < nvt; ++t)
+          qk_tile(d, vt0 + t, v0 + (g % kVSlots) * kVSlot + t * kTile, t == 0);
+        for (int t = 0; t < ntile; ++t) {
+          if (t >= vt0 && t < vt0 + nvt) continue;
+          const int slot = kt % kKSlots;
+          if (!mbar_wait(&k_full[slot], (kt / kKSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+            stop = true;
+            break;
+          }
+          qk_tile(d, t, k0 + slot * kTile, false);
+          mma_commit(&k_empty[slot]);
+          ++kt;
+        }
+        if (stop) break;
+        mma_commit(&s_full[g & 1]);
+        if (g > 0 && !pv(g - 1)) stop = true;
+      }
+      if (!stop && !*abort_flag) pv(nch - 1);
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+  } else {
+    // ---------------- softmax: thread = row ----------------
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int64_t flat = it.row0 + min(r, it.rows - 1);  // rows past the block repeat its last
+    // this row's last visible suffix position
+    const int pos = it.pos0 + (it.hoff + min(r, it.rows - 1)) / a.h;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + flat * D);
+      for (int t = 0; t < min(ntile, kQTmemTiles); ++t) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = t * 8 + i;  // 16-byte piece
+          const uint4 v = e * 8 < D ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+        tmem_st32(lane_base + kQCol + t * 32, w);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qt_full);
+    }
+    float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum relative to it
+    bool stop = false;
+    for (int g = 0; g < nch; ++g) {
+      const int c = it.c0 + g;
+      // keys of the chunk this row sees, and the block's first row
+      const bool pre = c < it.ncp;
+      const int x0 = (pre ? c : c - it.ncp) * kN;
+      const int lim = pre ? min(kN, a.prefix_len - x0) : max(0, min(kN, pos + 1 - x0));
+      const int lim0 = pre ? lim : max(0, min(kN, it.pos0 + 1 - x0));
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag, a.status,
+                                             DSA_FLAG_TIMEOUT))) { stop = true; break; }
+      tc_fence_after();
+      uint64_t bad = 0;
+      if (a.seqs.paged()) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag,
+                                               a.status, DSA_FLAG_TIMEOUT))) { stop = true; break; }
+        bad = *const_cast<volatile uint64_t*>(&badkeys[g % kVSlots]);
+      }
+      const uint32_t sbuf = lane_base + kSCol + (g & 1) * kN;
+      float s[kN];
+      load_row(sbuf, s);
+      if (lim0 < kN || bad) {
+        // some row does not see some key.  Its p is 0, but 0 times an infinity or a NaN in the
+        // key's value columns would not be: those are zeroed in the tile, which the logits have read
+        // already (a row that does see such a key has a NaN logit)
+        if (!a.seqs.paged() &&
+            !__all_sync(0xffffffffu, mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag,
+                                               a.status, DSA_FLAG_TIMEOUT))) { stop = true; break; }
+        bool any = false;
+        uint8_t* vt = vs + (g % kVSlots) * kVSlot;
+        for (int i = r; i < nvt * kN * 8; i += kM) {  // 16-byte pieces; swizzled order does not matter
+          const int key = (i >> 3) & (kN - 1);
+          if (key < lim0 && !((bad >> key) & 1)) continue;
+          uint4* at = reinterpret_cast<uint4*>(vt) + i;
+          uint4 v = *at;
+          if (finite8(v)) { *at = v; any = true; }
+        }
+        if (any) fence_proxy_async_smem();
+        const uint64_t in = (lim >= kN ? ~0ull : (1ull << lim) - 1);
+        if ((bad & in) && it.half == 0) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+        const uint64_t see = in & ~bad;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (!((see >> i) & 1)) s[i] = -INFINITY;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+      const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const bool grow = mc > m + kRescaleLog2;  // the first keys always (m = -inf)
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m_new = grow ? mc : m;
+        const float factor = grow ? ex2(m - m_new) : 1.f;
+        l *= factor;
+        if (g > 0) {
+          // O holds the chunks before g at the old reference: rescale it once P·V(g - 1) is in
+          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
+                                                 a.status, DSA_FLAG_TIMEOUT))) { stop = true; break; }
+          tc_fence_after();
+          __syncwarp();
+          for (int b = 0; b < (ncol + 31) / 32; ++b) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + kOCol + 32 * b, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+            tmem_st32(lane_base + kOCol + 32 * b, o);
+          }
+        }
+        m = m_new;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;  // nothing visible so far
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t pk[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float p0 = ex2(fmaf(s[2 * i], a.scale_log2, -ref));
+        const float p1 = ex2(fmaf(s[2 * i + 1], a.scale_log2, -ref));
+        sum[(2 * i) & 3] += p0;
+        sum[(2 * i + 1) & 3] += p1;
+        pk[i] = bf16x2(p0, p1);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      __syncwarp();
+      tmem_st32(sbuf, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[g & 1]);
+    }
+    if (!stop)
+      stop = !__all_sync(0xffffffffu, mbar_wait(&pv_done[(nch - 1) & 1], ((nch - 1) >> 1) & 1, abort_flag,
+                                                a.status, DSA_FLAG_TIMEOUT));
+    if (!stop) {
+      tc_fence_after();
+      const bool live = r < it.rows;
+      const float inv = split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      for (int b = 0; b < (ncol + 31) / 32; ++b) {
+        uint32_t o[32];
+        __syncwarp();  // the load is the whole warp's
+        tmem_ld32(lane_base + kOCol + 32 * b, o);
+        const int n = live ? min(32, ncol - 32 * b) : 0;  // 16 or 32 columns
+        const int64_t at = flat * a.d_c + vcol0 + 32 * b;
+        if (split || a.out_dtype == DSA_F32) {
+          float* dst = split ? a.part_o + (int64_t)it.piece * rows_all * a.d_c + at
+                             : static_cast<float*>(a.out) + at;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (4 * i < n)
+              reinterpret_cast<float4*>(dst)[i] =
+                  make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                              __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (8 * i < n) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                              __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+      }
+      if (live && it.half == 0) {
+        if (split) a.part_ml[(int64_t)it.piece * rows_all + flat] = make_float2(m, l);
+        else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  cta_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// How the rows and their keys are cut (all from the descriptor's sizes and the prefix's length).
+struct Plan {
+  int nblk, fblk, sp, ss, halves;
+  int pieces() const { return fblk ? sp + ss : ss; }
+};
+
+// Most pieces a row is cut into: about four waves of CTAs.
+int most_pieces(int64_t blocks, int halves) {
+  const int64_t s = 4 * (int64_t)num_sms() / (blocks * halves > 0 ? blocks * halves : 1);
+  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+constexpr size_t kMostPartial = size_t(1) << 30;
+size_t partial_bytes(const PrefixArgs& a, int pieces) {
+  return pieces > 1 ? (size_t)pieces * a.seqs.total_q * a.h * (a.d_c * 4 + 8) : 0;
+}
+
+Plan blocks_of(const PrefixArgs& a) {
+  Plan pl{};
+  pl.halves = (a.d_c + 255) / 256;
+  pl.nblk = (int)(((int64_t)a.max_q_len * a.h + kM - 1) / kM);
+  pl.fblk = (int)(((int64_t)a.seqs.total_q * a.h + kM - 1) / kM);
+  return pl;
+}
+
+// Time model in units of a chunk: a CTA's start and end cost about four chunks, a wave ends
+// with its longest CTA, and merging costs a launch (about three chunks) and the partial outputs' traffic.
+Plan plan_of(const PrefixArgs& a) {
+  Plan pl = blocks_of(a);
+  const int sms = num_sms();
+  const int64_t seq_blocks = (int64_t)a.seqs.B * pl.nblk;
+  const double pch = (a.prefix_len + kN - 1) / kN;
+  const double sch = 0.5 + (double)a.seqs.total_k / a.seqs.B / kN;  // a sequence's own chunks, on average
+  const double row_cost = (double)a.seqs.total_q * a.h * a.d_c * 8 / 4e6;  // partials of a piece: us at 4 TB/s
+  const double start = 4;
+  double best = 1e30;
+  Plan out = pl;
+  // one key axis
+  for (int s = 1; s <= most_pieces(seq_blocks, pl.halves); ++s) {
+    const double len = (pch + sch) / s;
+    if (s > 1 && (len < 2 || partial_bytes(a, s) > kMostPartial)) break;
+    const int64_t items = seq_blocks * pl.halves * s;
+    const double waves = (double)((items + sms - 1) / sms);
+    const double cost = waves * (ceil(len) + start) + (s > 1 ? 3 + s * row_cost : 0);
+    if (cost < best) {
+      best = cost;
+      out.fblk = 0; out.sp = 0; out.ss = s;
+    }
+  }
+  // the prefix by blocks of all rows, the sequences' own keys apart
+  if (a.prefix_len > 0 && pl.fblk < seq_blocks) {
+    for (int s = 1; s <= most_pieces(pl.fblk, pl.halves); ++s) {
+      const double len = pch / s;
+      if (s > 1 && len < 2) break;
+      int ss = (int)(sch / (len > 2 ? len : 2) + 0.5);
+      const int most = most_pieces(seq_blocks, pl.halves);
+      ss = ss < 1 ? 1 : ss > most ? most : ss;
+      if (partial_bytes(a, s + ss) > kMostPartial) break;
+      const double work = pl.halves * (pl.fblk * (pch + s * start) + seq_blocks * (sch + ss * start));
+      const double longest = ceil(len) + start;
+      const double items = (double)pl.halves * pl.fblk * s;
+      const double waves = ceil(items / sms) * longest;
+      const double cost = (work / sms > waves ? work / sms + 0.3 * longest : waves) + 3 + (s + ss) * row_cost;
+      if (cost < best) {
+        best = cost;
+        out.fblk = pl.fblk; out.sp = s; out.ss = ss;
+      }
+    }
+  }
+  return out;
+}
+
+}  // namespace
+
+bool prefix_tc_eligible(const PrefixArgs& a) {
+  const int D = a.d_c + a.d_rope;
+  return a.kv_dtype == DSA_BF16 && a.d_c <= 512 && D >= 64 && D <= 576;
+}
+
+// Pieces the workspace has room for, whatever the prefix's length.
+int prefix_tc_most_pieces(const PrefixArgs& a) {
+  const Plan pl = blocks_of(a);
+  const int64_t seq_blocks = (int64_t)a.seqs.B * pl.nblk;
+  if (pl.fblk == 0 || seq_blocks == 0) return 1;
+  const int one = most_pieces(seq_blocks, pl.halves);
+  const int two = pl.fblk < seq_blocks ? most_pieces(pl.fblk, pl.halves) + one : 1;
+  int n = one > two ? one : two;
+  while (n > 1 && partial_bytes(a, n) > kMostPartial) --n;
+  return n;
+}
+
+int prefix_tc_pieces(const PrefixArgs& a) { return plan_of(a).pieces(); }
+
+int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
+  const Plan pl = plan_of(a);
+  Params p{};
+  p.a = a;
+  p.nblk = pl.nblk;
+  p.fblk = pl.fblk;
+  p.sp = pl.sp;
+  p.ss = pl.ss;
+  p.halves = pl.halves;
+  p.prefix_items = pl.fblk * pl.sp * pl.halves;
+  p.chunk_rows = a.seqs.paged() && a.seqs.page_size < kN ? a.seqs.page_size : kN;
+  const int64_t items = p.prefix_items + (int64_t)a.seqs.B * pl.nblk * pl.ss * pl.halves;
+  if (items > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "prefix attention: grid too large");
+  const uint64_t D = a.d_c + a.d_rope;
+  CUtensorMap qmap, pmap, kmap;
+  int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, D, (uint64_t)a.seqs.total_q * a.h,
+                        D * 2, 64, kM);
+  if (rc == DSA_OK)
+    rc = make_tmap_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, D, (uint64_t)a.seqs.cache_rows(),
+                      D * 2, 64, (uint32_t)p.chunk_rows);
+  pmap = kmap;
+  if (rc == DSA_OK && a.prefix_kv)
+    rc = make_tmap_2d(&pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.prefix_kv, D, (uint64_t)a.prefix_len,
+                      D * 2, 64, (uint32_t)p.chunk_rows);
+  if (rc != DSA_OK) return rc;
+  if (cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return check_launch("prefix_tc: smem attribute");
+  DSA_LAUNCH("prefix_tc", stream,
+             prefix_tc_kernel<<<(unsigned)items, kThreads, kSmem, stream>>>(p, qmap, pmap, kmap));
+  rc = check_launch("prefix_tc");
+  if (rc != DSA_OK || pl.pieces() == 1) return rc;
+  return launch_prefix_merge(a, pl.pieces(), stream);
+}
+
+}  // namespace dsa
