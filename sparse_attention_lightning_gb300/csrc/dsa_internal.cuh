@@ -151,6 +151,10 @@ int check_launch(const char* what);
 int make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
                  uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
                  bool swizzle = true);
+// 16-bit rows as [tiles][rows][64 columns] (rows of tiles · 64 elements): a box is box_tiles tiles of
+// box_rows rows, each tile as make_tmap_2d's box of 64 columns would store it.
+int make_tmap_tiles(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t tiles,
+                    uint64_t rows, uint64_t row_bytes, uint32_t box_tiles, uint32_t box_rows);
 int num_sms();
 
 #define DSA_LAUNCH(name, stream, ...)   \

@@ -16,14 +16,18 @@
 // take longer than the duplicate MMAs).  The twin CTA finds the keys in L2.
 //
 // Tensor memory: O (256 columns) | two logit buffers (64 each; P, as bf16 pairs, overwrites the
-// first half of its own logits) | the first 256 query columns (128).  Shared memory: the other query
-// columns (80 KB) and two rings of [64 keys x 64 columns] tiles: the CTA's own value columns are
-// held until P·V (3 chunks of 32 KB), the others only until the logits (6 tiles of 8 KB).
+// first half of its own logits) | the query columns that match the CTA's value tiles (128).  Shared
+// memory: the other query columns (80 KB) and 18 tiles of [64 keys x 64 columns]: the CTA's own value
+// columns ("V tiles") are held until P·V (3 chunks of 32 KB for d_c = 512), the others ("K tiles")
+// only until the logits.
 //
 // Per chunk of 64 keys: the producer thread loads tiles by TMA; the MMA thread issues
-// S(g) = Q·Kᵀ (M=128, N=64, K=D), then O += P(g-1)·V (M=128, N=256, K=64; P from tensor memory);
+// S(g) = Q·Kᵀ (M=128, N=64, K=D) and O += P(g-1)·V (M=128, N=256, K=64; P from tensor memory);
 // four softmax warps, a thread a row, take the running max (it moves only when a row's max grows
 // by more than 2^8; O is then rescaled), the sum in fp32 of the unrounded p, and write P.
+// Order of the MMAs: S over the K tiles (their buffers are refilled meanwhile), over half the V tiles, P·V
+// of the chunk before, the other half: softmax has the first part to finish in, and the last part hides the
+// wait for P·V before the next chunk overwrites its P.
 // Every wait is bounded (DSA_FLAG_TIMEOUT).
 #include "prefix_attn.cuh"
 #include "tc_sm100.cuh"
@@ -39,11 +43,11 @@ constexpr int kTile = kN * 128;         // 8 KB: 64 keys x 64 columns
 constexpr int kQTile = kM * 128;        // 16 KB: 128 rows x 64 columns
 constexpr int kQTmemTiles = 4;          // query column tiles in tensor memory
 constexpr int kQSmemTiles = 5;
-constexpr int kVSlots = 3, kKSlots = 6;
-constexpr int kVSlot = 4 * kTile;
+constexpr int kTiles = 18;              // key tiles in flight
+constexpr int kVSlots = 3, kKSlots = 3; // at most: chunks whose V, K tiles are in flight
 constexpr int kThreads = 192;           // producer, MMA, 4 softmax warps
 constexpr int kBarBytes = 512;
-constexpr int kSmem = kQSmemTiles * kQTile + kVSlots * kVSlot + kKSlots * kTile + kBarBytes + 1024;
+constexpr int kSmem = kQSmemTiles * kQTile + kTiles * kTile + kBarBytes + 1024;
 constexpr int kOCol = 0, kSCol = 256, kQCol = 384;
 constexpr float kRescaleLog2 = 8.0f;
 static_assert(kSmem <= 232448, "shared memory");
@@ -131,6 +135,13 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Zero the infinities and NaNs among 8 bf16 values; whether there were any.
 __device__ __forceinline__ bool finite8(uint4& v) {
   uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -144,9 +155,28 @@ __device__ __forceinline__ bool finite8(uint4& v) {
   return any;
 }
 
+// Box of kN (or a page's) rows x 64 columns x 4 column tiles into four consecutive tiles.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+struct Maps {
+  CUtensorMap q;           // [rows, D], box 128 x 64
+  CUtensorMap pre, key;    // prefix and cache rows, box chunk_rows x 64
+  CUtensorMap pre4, key4;  // the same as [tiles][rows][64], box 4 x chunk_rows x 64
+};
+
+// FIXED: 512 + 64 columns (4 V tiles and 5 K tiles in both halves), everything unrolled and the tiles
+// loaded four at a time; otherwise any widths.  One thread issues all MMAs and one all copies, and
+// their scalar code is what counts: with the counts known only at run time the issue took 4,600 clocks a
+// chunk where the tensor pipe needs 1,980 (36 MMAs of N = 64 and 4 of N = 256).
+template <bool FIXED>
 __global__ void __launch_bounds__(kThreads, 1)
-prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
-                 const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap kmap) {
+prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   Item it;
   if (!item_at(p, blockIdx.x, it)) return;
   const PrefixArgs& a = p.a;
@@ -163,13 +193,12 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* qs = smem;                               // [5][128][128 B]
-  uint8_t* vs = qs + kQSmemTiles * kQTile;          // [3][4][64][128 B]
-  uint8_t* ks = vs + kVSlots * kVSlot;              // [6][64][128 B]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ks + kKSlots * kTile);
+  uint8_t* vs = qs + kQSmemTiles * kQTile;          // [vslots][nvt][64][128 B], then the K tiles
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vs + kTiles * kTile);
   uint64_t* v_full = bars;            // [3]
   uint64_t* v_empty = bars + 3;       // [3]
-  uint64_t* k_full = bars + 6;        // [6]
-  uint64_t* k_empty = bars + 12;      // [6]
+  uint64_t* k_full = bars + 6;        // [3][2] the two parts of a chunk's K tiles
+  uint64_t* k_empty = bars + 12;      // [3][2]
   uint64_t* s_full = bars + 18;       // [2] logits of the buffer's chunk complete
   uint64_t* p_full = bars + 20;       // [2] its 4 softmax warps have written P
   uint64_t* pv_done = bars + 22;      // [2] its P·V complete
@@ -184,13 +213,21 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
   const int D = a.d_c + a.d_rope;
   const int ntile = (D + 63) / 64;
   const int vcol0 = it.half * 256;
-  const int ncol = min(256, a.d_c - vcol0);         // this CTA's output columns (a multiple of 16)
-  const int vt0 = it.half * 4, nvt = (ncol + 63) / 64;
-  const int nkt = ntile - nvt;
+  const int ncol = FIXED ? 256 : min(256, a.d_c - vcol0);         // this CTA's output columns (a multiple of 16)
+  const int vt0 = it.half * 4, nvt = FIXED ? 4 : (ncol + 63) / 64;
+  const int nkt = FIXED ? 5 : ntile - nvt;          // at most 8
+  const int nka = FIXED ? 4 : (nkt + 1) / 2;        // the K tiles' first part
+  // 3 chunks of V tiles always fit beside one of K tiles (3·4 + 5, or nvt < 4: 3·3 + 8 of 18)
+  const int kslots = FIXED ? 1 : nkt ? min(kKSlots, (kTiles - kVSlots * nvt) / nkt) : 0;
+  uint8_t* ks = vs + kVSlots * nvt * kTile;         // [kslots][nkt][64][128 B]
+  // Column tile of K tile j, and where the query columns that match a tile are: V tile j in tensor
+  // memory at tile j; K tile j after them while there is room (4 tiles), then in shared memory.
+  auto ktile = [&](int j) { return j < vt0 ? j : j + nvt; };
+  const int nkq = FIXED ? 0 : min(nkt, kQTmemTiles - nvt);      // K tiles whose query columns are in tensor memory
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kVSlots; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
-    for (int i = 0; i < kKSlots; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < 2 * kKSlots; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
@@ -210,22 +247,21 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 
   if (warp == 0) {
     // ---------------- producer ----------------
-    if (lane == 0) {
-      const int nqs = max(ntile - kQTmemTiles, 0);
+    if (elect_one()) {
+      const int nqs = nkt - nkq;
       if (nqs) {
         mbar_arrive_expect_tx(q_full, (uint32_t)(nqs * kQTile));
         for (int j = 0; j < nqs; ++j)
-          tma_load_2d(qs + j * kQTile, &qmap, q_full, (kQTmemTiles + j) * 64, (int)it.row0);
+          tma_load_2d(qs + j * kQTile, &maps.q, q_full, ktile(nkq + j) * 64, (int)it.row0);
       }
-      int kt = 0, g = 0;
+      int g = 0, kn = 0;  // chunks whose V tiles, half-chunks whose K tiles have been issued
       for (; g < nch; ++g) {
         const int c = it.c0 + g, vslot = g % kVSlots;
-        if (!mbar_wait(&v_empty[vslot], ((g / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
-          break;
         // the cache rows of the chunk's keys: one run, or one a page
         const bool pre = c < it.ncp;
         const int x0 = (pre ? c : c - it.ncp) * kN;
-        const CUtensorMap* map = pre ? &pmap : &kmap;
+        const CUtensorMap* map = pre ? &maps.pre : &maps.key;
+        const CUtensorMap* map4 = pre ? &maps.pre4 : &maps.key4;
         const bool paged = a.seqs.paged();
         int run[kN / 16];
         uint64_t bad = 0;
@@ -247,103 +283,197 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             run[j] = ok ? (pg << sh) | (x & (a.seqs.page_size - 1)) : 0;
           }
         }
-        badkeys[vslot] = bad;
-        mbar_arrive_expect_tx(&v_full[vslot], (uint32_t)(nvt * kTile));
-        for (int t = 0; t < nvt; ++t)
+        auto load = [&](uint8_t* dst, uint64_t* bar, int tile) {
 #pragma unroll
           for (int j = 0; j < kN / 16; ++j) {
             if (j >= nrun) break;
-            tma_load_2d(vs + vslot * kVSlot + t * kTile + j * cr * 128, map, &v_full[vslot],
-                        (vt0 + t) * 64, run[j]);
+            tma_load_2d(dst + j * cr * 128, map, bar, tile * 64, run[j]);
           }
+        };
+        auto load4 = [&](uint8_t* dst, uint64_t* bar, int tile) {
+#pragma unroll
+          for (int j = 0; j < kN / 16; ++j) {
+            if (j >= nrun) break;
+            if (cr == kN) {
+              tma_load_3d(dst, map4, bar, 0, run[j], tile);
+            } else {  // a page's rows of each tile: the tiles are kTile apart, not the box's size
+              for (int t = 0; t < 4; ++t) tma_load_2d(dst + t * kTile + j * cr * 128, map, bar, (tile + t) * 64, run[j]);
+            }
+          }
+        };
+        // K tiles first: the MMAs start with them
         bool stop = false;
-        for (int t = 0; t < ntile; ++t) {
-          if (t >= vt0 && t < vt0 + nvt) continue;
-          const int slot = kt % kKSlots;
-          if (!mbar_wait(&k_empty[slot], ((kt / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+        for (int h = 0; h < 2; ++h) {
+          const int j0 = h ? nka : 0, j1 = h ? nkt : nka;
+          if (j0 == j1) continue;
+          const int slot = g % kslots, bar = slot * 2 + h;
+          if (!mbar_wait(&k_empty[bar], ((g / kslots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
             stop = true;
             break;
           }
-          mbar_arrive_expect_tx(&k_full[slot], kTile);
-#pragma unroll
-          for (int j = 0; j < kN / 16; ++j) {
-            if (j >= nrun) break;
-            tma_load_2d(ks + slot * kTile + j * cr * 128, map, &k_full[slot], t * 64, run[j]);
+          mbar_arrive_expect_tx(&k_full[bar], (uint32_t)((j1 - j0) * kTile));
+          if (FIXED && h == 0) {
+            load4(ks, &k_full[0], 4 - vt0);
+          } else {
+            for (int j = j0; j < j1; ++j) load(ks + (slot * nkt + j) * kTile, &k_full[bar], ktile(j));
           }
-          ++kt;
+          kn = 2 * g + h + 1;
         }
-        if (stop) { ++g; break; }
+        if (stop || !mbar_wait(&v_empty[vslot], ((g / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
+          break;
+        badkeys[vslot] = bad;
+        mbar_arrive_expect_tx(&v_full[vslot], (uint32_t)(nvt * kTile));
+        if (FIXED) {
+          load4(vs + vslot * 4 * kTile, &v_full[vslot], vt0);
+        } else {
+          for (int t = 0; t < nvt; ++t) load(vs + (vslot * nvt + t) * kTile, &v_full[vslot], vt0 + t);
+        }
       }
       // every copy issued has landed before the CTA may exit
       if (nqs) mbar_wait_drain(q_full, 0);
       for (int i = max(0, g - kVSlots); i < g; ++i)
         mbar_wait_drain(&v_full[i % kVSlots], (i / kVSlots) & 1);
-      for (int i = max(0, kt - kKSlots); i < kt; ++i)
-        mbar_wait_drain(&k_full[i % kKSlots], (i / kKSlots) & 1);
+      for (int i = max(0, kn - 2 * kslots); i < kn; ++i) {
+        const int c = i >> 1, h = i & 1;
+        if (h && nka == nkt) continue;
+        mbar_wait_drain(&k_full[(c % kslots) * 2 + h], (c / kslots) & 1);
+      }
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    // elect.sync and unrolled K-steps keep the operands in uniform registers: an M=128, N=64, K=16
+    // MMA with A in tensor memory then issues every 33 clocks (the pipe's own rate), with A in shared
+    // memory every 49 (6 KB of operands at 128 B a clock); under lane == 0 and a counted loop it was 164.
+    if (elect_one()) {
       const uint32_t idesc_s = idesc_bf16(kM, kN);
       const uint32_t idesc_pv = idesc_bf16(kM, ncol, false, true);
       const uint32_t q0 = smem_u32(qs), v0 = smem_u32(vs), k0 = smem_u32(ks);
       bool stop = !mbar_wait(qt_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-      if (!stop && ntile > kQTmemTiles)
-        stop = !mbar_wait(q_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+      if (!stop && nkt > nkq) stop = !mbar_wait(q_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
       tc_fence_after();
-      int kt = 0;
-      // one tile's K-steps of the logits
-      auto qk_tile = [&](uint32_t d, int t, uint32_t tile, bool first) {
-        const int steps = min(4, (D - t * 64) / 16);
+      const uint64_t qd = sdesc_sw128(q0, 16, 1024);
+      const bool full = D % 64 == 0;  // every tile has 4 K-steps
+      // the logits' K-steps of one tile: A = tile qt of the query in tensor memory, or (qt >= 4) tile
+      // qt - 4 of it in shared memory
+      auto qk_tile = [&](uint32_t d, int qt, int t, uint32_t tile, bool first) {
+        const int steps = full ? 4 : min(4, (D - t * 64) / 16);
         const uint64_t b0 = sdesc_sw128(tile, 16, 1024);
-        if (t < kQTmemTiles) {
-          for (int i = 0; i < steps; ++i)
-            mma_bf16_ts(d, tmem + kQCol + t * 32 + i * 8, b0 + (uint64_t)(i * 2), idesc_s,
-                        first && i == 0 ? 0u : 1u);
+        if (qt < kQTmemTiles) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < steps)
+              mma_bf16_ts(d, tmem + kQCol + qt * 32 + i * 8, b0 + (uint64_t)(i * 2), idesc_s,
+                          first && i == 0 ? 0u : 1u);
         } else {
-          const uint64_t a0 = sdesc_sw128(q0 + (t - kQTmemTiles) * kQTile, 16, 1024);
-          for (int i = 0; i < steps; ++i)
-            mma_bf16(d, a0 + (uint64_t)(i * 2), b0 + (uint64_t)(i * 2), idesc_s,
-                     first && i == 0 ? 0u : 1u);
+          const uint64_t a0 = qd + (uint64_t)((qt - kQTmemTiles) * (kQTile >> 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < steps)
+              mma_bf16(d, a0 + (uint64_t)(i * 2), b0 + (uint64_t)(i * 2), idesc_s, first && i == 0 ? 0u : 1u);
         }
       };
       auto pv = [&](int g) -> bool {
         if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) return false;
         tc_fence_after();
-        const uint32_t vb = v0 + (g % kVSlots) * kVSlot;
+        const uint64_t vd = sdesc_sw128(v0 + (g % kVSlots) * nvt * kTile, kTile, 1024);
+        const uint32_t pa = tmem + kSCol + (g & 1) * kN;
 #pragma unroll
         for (int kk = 0; kk < kN / 16; ++kk)
-          mma_bf16_ts(tmem + kOCol, tmem + kSCol + (g & 1) * kN + kk * 8,
-                      sdesc_sw128(vb + kk * 2048, kTile, 1024), idesc_pv, (g > 0 || kk > 0) ? 1u : 0u);
+          mma_bf16_ts(tmem + kOCol, pa + kk * 8, vd + (uint64_t)(kk * 128), idesc_pv, (g > 0 || kk > 0) ? 1u : 0u);
         mma_commit(&v_empty[g % kVSlots]);
         mma_commit(&pv_done[g & 1]);
         return true;
       };
+      if constexpr (FIXED) {
+        const uint64_t kd = sdesc_sw128(k0, 16, 1024);
+        int vslot = 0, vphase = 0;           // of chunk g
+        uint64_t pvd = 0;                    // V tiles of chunk g - 1, as P·V reads them
+        uint64_t* pv_empty = nullptr;
+        auto pv_fixed = [&](int g) -> bool {
+          if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) return false;
+          tc_fence_after();
+          const uint32_t pa = tmem + kSCol + (g & 1) * kN;
+          const uint32_t acc = g > 0;
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_bf16_ts(tmem + kOCol, pa + kk * 8, pvd + (uint64_t)(kk * 128), idesc_pv, kk ? 1u : acc);
+          mma_commit(pv_empty);
+          mma_commit(&pv_done[g & 1]);
+          return true;
+        };
+        for (int g = 0; g < nch && !stop; ++g) {
+          if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
+            break;
+          const uint32_t d = tmem + kSCol + (g & 1) * kN;
+          if (!mbar_wait(&k_full[0], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_bf16(d, qd + (uint64_t)(j * (kQTile >> 4) + i * 2), kd + (uint64_t)(j * (kTile >> 4) + i * 2),
+                       idesc_s, j || i ? 1u : 0u);
+          mma_commit(&k_empty[0]);
+          if (!mbar_wait(&k_full[1], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_bf16(d, qd + (uint64_t)(4 * (kQTile >> 4) + i * 2), kd + (uint64_t)(4 * (kTile >> 4) + i * 2),
+                     idesc_s, 1u);
+          mma_commit(&k_empty[1]);
+          if (!mbar_wait(&v_full[vslot], vphase, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+          tc_fence_after();
+          const uint64_t vd = sdesc_sw128(v0 + vslot * (4 * kTile), 16, 1024);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_bf16_ts(d, tmem + kQCol + t * 32 + i * 8, vd + (uint64_t)(t * (kTile >> 4) + i * 2), idesc_s, 1u);
+          if (g > 0 && !pv_fixed(g - 1)) { stop = true; break; }
+#pragma unroll
+          for (int t = 2; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_bf16_ts(d, tmem + kQCol + t * 32 + i * 8, vd + (uint64_t)(t * (kTile >> 4) + i * 2), idesc_s, 1u);
+          mma_commit(&s_full[g & 1]);
+          pvd = sdesc_sw128(v0 + vslot * (4 * kTile), kTile, 1024);
+          pv_empty = &v_empty[vslot];
+          if (++vslot == kVSlots) { vslot = 0; vphase ^= 1; }
+          if (g == nch - 1 && !pv_fixed(g)) stop = true;
+        }
+      } else {
       for (int g = 0; g < nch && !stop; ++g) {
+        const int kslot = nkt ? g % kslots : 0;
         // the buffer's last P (chunk g - 2) has been read
         if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g - 2) >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
           break;
-        if (!mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
-        tc_fence_after();
         const uint32_t d = tmem + kSCol + (g & 1) * kN;
-        for (int t = 0; t < nvt; ++t)
-          qk_tile(d, vt0 + t, v0 + (g % kVSlots) * kVSlot + t * kTile, t == 0);
-        for (int t = 0; t < ntile; ++t) {
-          if (t >= vt0 && t < vt0 + nvt) continue;
-          const int slot = kt % kKSlots;
-          if (!mbar_wait(&k_full[slot], (kt / kKSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+        const uint32_t kb = k0 + kslot * nkt * kTile;
+        for (int h = 0; h < 2; ++h) {
+          const int j0 = h ? nka : 0, j1 = h ? nkt : nka;
+          if (j0 == j1) continue;
+          const int bar = kslot * 2 + h;
+          if (!mbar_wait(&k_full[bar], (g / kslots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
             stop = true;
             break;
           }
-          qk_tile(d, t, k0 + slot * kTile, false);
-          mma_commit(&k_empty[slot]);
-          ++kt;
+          tc_fence_after();
+          for (int j = j0; j < j1; ++j)
+            qk_tile(d, j < nkq ? nvt + j : kQTmemTiles + j - nkq, ktile(j), kb + j * kTile, j == 0);
+          mma_commit(&k_empty[bar]);
         }
-        if (stop) break;
+        if (stop || !mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
+          break;
+        tc_fence_after();
+        const uint32_t vb = v0 + (g % kVSlots) * nvt * kTile;
+        const int mid = nvt / 2;
+        for (int t = 0; t < mid; ++t) qk_tile(d, t, vt0 + t, vb + t * kTile, nkt == 0 && t == 0);
+        if (g > 0 && !pv(g - 1)) { stop = true; break; }
+        for (int t = mid; t < nvt; ++t) qk_tile(d, t, vt0 + t, vb + t * kTile, nkt == 0 && t == 0);
         mma_commit(&s_full[g & 1]);
-        if (g > 0 && !pv(g - 1)) stop = true;
+        if (g == nch - 1 && !pv(g)) stop = true;
       }
-      if (!stop && !*abort_flag) pv(nch - 1);
+      }
       mma_commit(drain);
       mbar_wait_drain(drain, 0);
     }
@@ -357,12 +487,12 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
     const int pos = it.pos0 + (it.hoff + min(r, it.rows - 1)) / a.h;
     {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + flat * D);
-      for (int t = 0; t < min(ntile, kQTmemTiles); ++t) {
+      for (int t = 0; t < nvt + nkq; ++t) {
+        const int col = (t < nvt ? vt0 + t : ktile(t - nvt)) * 8;  // first 16-byte piece of the tile
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int e = t * 8 + i;  // 16-byte piece
-          const uint4 v = e * 8 < D ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = (col + i) * 8 < D ? __ldg(src + col + i) : make_uint4(0u, 0u, 0u, 0u);
           w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
         tmem_st32(lane_base + kQCol + t * 32, w);
@@ -400,7 +530,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             !__all_sync(0xffffffffu, mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag,
                                                a.status, DSA_FLAG_TIMEOUT))) { stop = true; break; }
         bool any = false;
-        uint8_t* vt = vs + (g % kVSlots) * kVSlot;
+        uint8_t* vt = vs + (g % kVSlots) * nvt * kTile;
         for (int i = r; i < nvt * kN * 8; i += kM) {  // 16-byte pieces; swizzled order does not matter
           const int key = (i >> 3) & (kN - 1);
           if (key < lim0 && !((bad >> key) & 1)) continue;
@@ -615,22 +745,26 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   p.chunk_rows = a.seqs.paged() && a.seqs.page_size < kN ? a.seqs.page_size : kN;
   const int64_t items = p.prefix_items + (int64_t)a.seqs.B * pl.nblk * pl.ss * pl.halves;
   if (items > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "prefix attention: grid too large");
-  const uint64_t D = a.d_c + a.d_rope;
-  CUtensorMap qmap, pmap, kmap;
-  int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, D, (uint64_t)a.seqs.total_q * a.h,
-                        D * 2, 64, kM);
-  if (rc == DSA_OK)
-    rc = make_tmap_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, D, (uint64_t)a.seqs.cache_rows(),
-                      D * 2, 64, (uint32_t)p.chunk_rows);
-  pmap = kmap;
-  if (rc == DSA_OK && a.prefix_kv)
-    rc = make_tmap_2d(&pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.prefix_kv, D, (uint64_t)a.prefix_len,
-                      D * 2, 64, (uint32_t)p.chunk_rows);
+  const uint64_t D = a.d_c + a.d_rope, keys = (uint64_t)a.seqs.cache_rows();
+  const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const bool fixed = a.d_c == 512 && a.d_rope == 64;
+  Maps m;
+  int rc = make_tmap_2d(&m.q, bf, a.q, D, (uint64_t)a.seqs.total_q * a.h, D * 2, 64, kM);
+  if (rc == DSA_OK) rc = make_tmap_2d(&m.key, bf, a.kv, D, keys, D * 2, 64, (uint32_t)p.chunk_rows);
+  m.key4 = m.key;
+  if (rc == DSA_OK && fixed && p.chunk_rows == kN) rc = make_tmap_tiles(&m.key4, bf, a.kv, D / 64, keys, D * 2, 4, kN);
+  m.pre = m.key;
+  m.pre4 = m.key4;
+  if (a.prefix_kv) {
+    const uint64_t n = (uint64_t)a.prefix_len;
+    if (rc == DSA_OK) rc = make_tmap_2d(&m.pre, bf, a.prefix_kv, D, n, D * 2, 64, (uint32_t)p.chunk_rows);
+    if (rc == DSA_OK && fixed) rc = make_tmap_tiles(&m.pre4, bf, a.prefix_kv, D / 64, n, D * 2, 4, kN);
+  }
   if (rc != DSA_OK) return rc;
-  if (cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+  auto kern = fixed ? prefix_tc_kernel<true> : prefix_tc_kernel<false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return check_launch("prefix_tc: smem attribute");
-  DSA_LAUNCH("prefix_tc", stream,
-             prefix_tc_kernel<<<(unsigned)items, kThreads, kSmem, stream>>>(p, qmap, pmap, kmap));
+  DSA_LAUNCH("prefix_tc", stream, kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p, m));
   rc = check_launch("prefix_tc");
   if (rc != DSA_OK || pl.pieces() == 1) return rc;
   return launch_prefix_merge(a, pl.pieces(), stream);
