@@ -4,7 +4,8 @@
 //   acc[b, idx[t,i]] += Σ_h exp(scale · q[t,h,:]·kv[row_i,:] − lse[t,h])
 //
 // A query's weights are probabilities (the lse is the attention's), so the sum needs no running
-// max.  One CTA = one query × 64 of its selected positions; the CUDA cores compute in fp32.
+// max.  One CTA = one query × 64 of its selected positions; the CUDA cores compute in fp32
+// (the generic path: any type and width).
 //
 // Order.  Where no sequence has more than one query, a position receives additions of one value
 // only (a repeated index adds the same weight again), so plain fp32 atomics give the same bytes
@@ -112,7 +113,8 @@ int launch_attn_weights(const WeightArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess)
       return set_error(DSA_ERR_CUDA, "attn_weights clear: %s", cudaGetErrorString(e));
   }
-  const int rc = launch_attn_weights_simt(a, stream);
+  const int rc = attn_weights_tc_eligible(a) ? launch_attn_weights_tc(a, stream)
+                                             : launch_attn_weights_simt(a, stream);
   if (rc != DSA_OK || !a.fx) return rc;
   const int64_t want = (a.seqs.max_k_len + 1023) / 1024, most = 0x7fffffff / a.seqs.B;
   const int per = (int)(want < 64 ? (want < most ? want : most) : (64 < most ? 64 : most));

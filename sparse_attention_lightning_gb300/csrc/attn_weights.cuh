@@ -36,6 +36,10 @@ __device__ __forceinline__ void add_weight(const WeightArgs& a, int b, int pos, 
   }
 }
 
+// tcgen05 path (bf16, 64 <= D <= 576, up to 128 heads).
+bool attn_weights_tc_eligible(const WeightArgs& a);
+int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream);
+
 int launch_attn_weights(const WeightArgs& a, cudaStream_t stream);
 
 }  // namespace dsa
