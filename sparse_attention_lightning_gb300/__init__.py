@@ -12,6 +12,7 @@ fused_forward, indexer_prolog, add_rmsnorm, prefix_mla_attn, accumulate_attn_wei
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple, Optional, Sequence, Tuple
 
@@ -73,6 +74,8 @@ class Problem:
             self.out_dtype, self.sm_scale, self.cu_q.data_ptr(), self.cu_k.data_ptr(),
             self.page_size, self.block_table.shape[1] if self.page_size else 0, self.num_pages,
             self.block_table.data_ptr() if self.page_size else None)
+        self._ref = ctypes.byref(self.c)
+        self._ws_sizes = {}
 
     @classmethod
     def from_config(cls, cfg, cu_q: torch.Tensor, cu_k: torch.Tensor, sm_scale: float = 0.0,
@@ -345,66 +348,84 @@ def fused_forward(P: Problem, q_idx, k_idx, w, q, kv, q_scale=None, k_scale=None
 
 
 # ---------------------------------------------------------------------------
-# Operators around the caches.
+# Operators around the caches.  Their small calls cost as much on the host as on the GPU, so the
+# checks are written out (no objects built, nothing looked up twice).
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_TORCH_DT = {_abi.DSA_F32: (torch.float32,), _abi.DSA_BF16: (torch.bfloat16,),
+             _abi.DSA_FP8_E4M3: _CODES}
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), _CODES
 
 _op_ws = {}
 
 
-def _op_workspace(ws: Optional[Workspace], device: torch.device, nbytes: int) -> Workspace:
+def _op_workspace(ws: Optional[Workspace], index: int, stream: int, nbytes: int) -> Workspace:
     """The caller's workspace, grown as needed, or this device's and stream's own: calls on two
     streams do not share scratch.  A default workspace that grows keeps its earlier buffers
     alive, so a captured graph that refers to one stays valid; while a stream is being captured none
     is allocated (its memory would belong to the graph)."""
     if ws is not None:
-        if ws.device.type != device.type or ws.buf.device != device:
-            raise ValueError(f"the workspace is on {ws.buf.device}, the tensors on {device}")
+        if ws.buf.get_device() != index:
+            raise ValueError(f"the workspace is on {ws.buf.device}, the tensors on cuda:{index}")
         if ws.nbytes < nbytes and torch.cuda.is_current_stream_capturing():
             raise ValueError(f"a captured call needs a workspace of {nbytes} bytes beforehand")
         return ws.ensure(nbytes)
-    key = (device.index, _stream(device))
-    held = _op_ws.setdefault(key, [])
-    if not held or held[-1].nbytes < nbytes:
+    held = _op_ws.get((index, stream))
+    if held is None or held[-1].nbytes < nbytes:
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("a captured call needs its workspace beforehand: pass ws, or make the "
                              "call once on this stream before capturing it")
-        grown = max(nbytes, 2 * held[-1].nbytes if held else 0)
-        held.append(Workspace(device, grown))
+        if held is None:
+            held = _op_ws[index, stream] = []
+        held.append(Workspace(torch.device("cuda", index),
+                              max(nbytes, 2 * held[-1].nbytes if held else 0)))
     return held[-1]
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _want(t, name: str, dtypes, shape, index: int) -> None:
+    """A contiguous CUDA tensor of a dtype, shape and device."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-class _on:
-    """Makes a device current for a launch (nothing to do where it is already)."""
-
-    __slots__ = ("dev", "prev")
-
-    def __init__(self, dev: torch.device):
-        self.dev = dev
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev.index:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev.index:
-            torch.cuda.set_device(self.prev)
-        return False
+def _there(t, index: int) -> None:
+    """A tensor of a Problem is on the call's device."""
+    if t.get_device() != index:
+        raise ValueError(f"the problem's offsets are on {t.device}, the tensors on cuda:{index}")
 
 
-def _rows_2d(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(rows, row stride in elements) of a tensor [..., d] whose rows are evenly spaced."""
+def _on_device(f):
+    """Runs a call with its first tensor's device current (nothing to do where it is already)."""
+    def call(*args, **kw):
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                if t.is_cuda and t.get_device() != _current_device():
+                    with torch.cuda.device(t.get_device()):
+                        return f(*args, **kw)
+                break
+        return f(*args, **kw)
+    return functools.wraps(f)(call)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride in elements of a tensor [..., d] whose rows are evenly spaced."""
     d = t.shape[-1]
+    if t.is_contiguous():
+        return d
     if d > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    rows = t.numel() // d if d else 0
-    if t.dim() == 1 or rows <= 1:
-        return rows, d
     step, n = None, 1
     for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
@@ -414,11 +435,14 @@ def _rows_2d(t: torch.Tensor, name: str) -> Tuple[int, int]:
         elif stride != step * n:
             raise ValueError(f"{name}'s rows must be evenly spaced")
         n *= size
+    if step is None:
+        return d
     if step < d:
         raise ValueError(f"{name}'s rows overlap")
-    return rows, step
+    return step
 
 
+@_on_device
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 eps: float = 1e-6, quant: Optional[str] = None, want_y: Optional[bool] = None,
                 h=None, y=None, codes=None, scale=None):
@@ -431,52 +455,73 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     codes with E8M0 scale [..., d/32] uint8: on rows of d_idx elements the k_idx and k_scale
     of the indexer.  None for a part not computed.
     """
-    if quant not in (None, "e4m3", "mxfp8"):
-        raise ValueError(f"quant is {quant!r}, expected None, 'e4m3' or 'mxfp8'")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    dtype, shape, index = x.dtype, x.shape, x.get_device()
+    if dtype is torch.bfloat16:
+        dt = _abi.DSA_BF16
+    elif dtype is torch.float32:
+        dt = _abi.DSA_F32
+    else:
+        raise ValueError(f"x has dtype {dtype}")
+    if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least 1")
-    dt = _DT.get(x.dtype)
-    if dt not in (_abi.DSA_F32, _abi.DSA_BF16):
-        raise ValueError(f"x has dtype {x.dtype}")
-    shape, d, dev = tuple(x.shape), x.shape[-1], x.device
-    rows, ld_x = _rows_2d(x, "x")
-    _need(weight, "weight", dt, (d,))
-    ld_r = 0
+    d = shape[-1]
+    ld_x = _row_stride(x, "x")
+    _want(weight, "weight", (dtype,), (d,), index)
+    ld_r = res_ptr = h_ptr = y_ptr = codes_ptr = scale_ptr = code = 0
     if residual is not None:
-        if residual.dtype != x.dtype or residual.shape != x.shape or not residual.is_cuda:
+        if residual.dtype != dtype or residual.shape != shape or residual.get_device() != index:
             raise ValueError("residual must have x's shape, dtype and device")
-        ld_r = _rows_2d(residual, "residual")[1]
+        ld_r, res_ptr = _row_stride(residual, "residual"), residual.data_ptr()
         if h is None:
-            h = torch.empty(shape, dtype=x.dtype, device=dev)
-        _need(h, "h", dt, shape)
+            h = torch.empty(shape, dtype=dtype, device=x.device)
+        else:
+            _want(h, "h", (dtype,), shape, index)
+        h_ptr = h.data_ptr()
     elif h is not None:
         raise ValueError("h needs a residual")
-    if y is None and (quant is None if want_y is None else want_y or quant is None):
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
-    _need(y, "y", dt, shape, optional=True)
-    code = 0
+    if y is not None:
+        _want(y, "y", (dtype,), shape, index)
+        y_ptr = y.data_ptr()
+    elif quant is None or want_y:
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+        y_ptr = y.data_ptr()
     if quant is not None:
-        code = _NAME_DT[quant]
-        mx = code == _abi.DSA_MXFP8_E4M3
-        if mx and d % 32:
-            raise ValueError(f"mxfp8 needs a last dimension that is a multiple of 32, not {d}")
-        sshape = shape[:-1] + (d // 32,) if mx else shape[:-1]
+        if quant == "mxfp8":
+            if d % 32:
+                raise ValueError(f"mxfp8 needs a last dimension that is a multiple of 32, not {d}")
+            code, sdt, sshape = _abi.DSA_MXFP8_E4M3, torch.uint8, shape[:-1] + (d // 32,)
+        elif quant == "e4m3":
+            code, sdt, sshape = _abi.DSA_FP8_E4M3, torch.float32, shape[:-1]
+        else:
+            raise ValueError(f"quant is {quant!r}, expected None, 'e4m3' or 'mxfp8'")
         if codes is None:
-            codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+            codes = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        else:
+            _want(codes, "codes", _CODES, shape, index)
         if scale is None:
-            scale = torch.empty(sshape, dtype=torch.uint8 if mx else torch.float32, device=dev)
-        _need(codes, "codes", _abi.DSA_FP8_E4M3, shape)
-        _need(scale, "scale", _abi.DSA_FP8_E4M3 if mx else _abi.DSA_F32, sshape)
+            scale = torch.empty(sshape, dtype=sdt, device=x.device)
+        else:
+            _want(scale, "scale", (sdt,), sshape, index)
+        codes_ptr, scale_ptr = codes.data_ptr(), scale.data_ptr()
     elif codes is not None or scale is not None:
         raise ValueError("codes and scale need quant")
-    _same_device(dev, weight=weight, residual=residual, h=h, y=y, codes=codes, scale=scale)
-    with _on(dev):
-        _abi.check(lib().dsa_add_rmsnorm(rows, d, dt, code, eps, x.data_ptr(), ld_x,
-                                         _ptr(residual), ld_r, weight.data_ptr(), _ptr(h), _ptr(y),
-                                         _ptr(codes), _ptr(scale), _stream(dev)))
+    rc = lib().dsa_add_rmsnorm(x.numel() // d, d, dt, code, eps, x.data_ptr(), ld_x, res_ptr, ld_r,
+                               weight.data_ptr(), h_ptr, y_ptr, codes_ptr, scale_ptr,
+                               _raw_stream(index))
+    if rc:
+        _abi.check(rc)
     return y, h, codes, scale
+
+
+def _ws_bytes(P: Problem, op: int) -> int:
+    """P's workspace size for an op on the current device, asked for once."""
+    key = (op, _current_device(), _abi.lib())
+    n = P._ws_sizes.get(key)
+    if n is None:
+        n = P._ws_sizes[key] = P.workspace_size(op)
+    return n
 
 
 def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
@@ -488,38 +533,56 @@ def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
     P describes the sequences behind the prefix.  The prefix is prefix_kv [prefix_len, D], or, in a
     paged cache, the pages prefix_table [>= ceil(prefix_len / page_size)] int32 of kv; without
     either there is none."""
-    _need(q, "q", P.kv_dtype, (P.total_q, P.h, P.d))
-    _need(kv, "kv", P.kv_dtype, (P.cache_rows, P.d))
-    dev = kv.device
-    if prefix_kv is not None and prefix_table is not None:
-        raise ValueError("prefix_kv and prefix_table exclude each other")
-    n = 0
+    return _prefix_mla_attn(kv, P, q, prefix_kv, prefix_table, prefix_len, out, lse, want_lse, ws)
+
+
+@_on_device
+def _prefix_mla_attn(kv, P, q, prefix_kv, prefix_table, prefix_len, out, lse, want_lse, ws):
+    if not kv.is_cuda:
+        raise ValueError("kv must be a CUDA tensor")
+    index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
+    TQ, H, D = P.total_q, P.h, P.d
+    _want(q, "q", dts, (TQ, H, D), index)
+    _want(kv, "kv", dts, (P.cache_rows, D), index)
+    _there(P.cu_q, index)
+    n = pre_ptr = table_ptr = 0
     if prefix_kv is not None:
+        if prefix_table is not None:
+            raise ValueError("prefix_kv and prefix_table exclude each other")
+        if prefix_kv.dim() != 2:
+            raise ValueError(f"prefix_kv has shape {tuple(prefix_kv.shape)}")
+        _want(prefix_kv, "prefix_kv", dts, (prefix_kv.shape[0], D), index)
         n = prefix_kv.shape[0] if prefix_len is None else int(prefix_len)
-        if prefix_kv.dim() != 2 or not 0 <= n <= prefix_kv.shape[0]:
-            raise ValueError(f"prefix_len is {n}, prefix_kv {tuple(prefix_kv.shape)}")
-        _need(prefix_kv, "prefix_kv", P.kv_dtype, (prefix_kv.shape[0], P.d))
+        if not 0 <= n <= prefix_kv.shape[0]:
+            raise ValueError(f"prefix_len is {n}, prefix_kv has {prefix_kv.shape[0]} rows")
+        pre_ptr = prefix_kv.data_ptr() if n else 0
     elif prefix_table is not None:
         if not P.page_size:
             raise ValueError("prefix_table needs paged caches")
         if prefix_len is None:
             raise ValueError("prefix_table needs prefix_len")
         n = int(prefix_len)
-        if not prefix_table.is_cuda or prefix_table.dtype != torch.int32 \
-                or prefix_table.dim() != 1 or not prefix_table.is_contiguous() \
-                or n < 0 or prefix_table.numel() * P.page_size < n:
-            raise ValueError("prefix_table must be a contiguous int32 CUDA tensor that covers prefix_len")
+        if prefix_table.dim() != 1 or n < 0 or prefix_table.numel() * P.page_size < n:
+            raise ValueError("prefix_table must be an int32 tensor [pages] that covers prefix_len")
+        _want(prefix_table, "prefix_table", _I32, prefix_table.shape, index)
+        table_ptr = prefix_table.data_ptr() if n else 0
     elif prefix_len:
         raise ValueError("prefix_len needs prefix_kv or prefix_table")
-    out, lse = _attn_out(P, out, lse, dev, want_lse)
-    _same_device(dev, q=q, prefix_kv=prefix_kv, prefix_table=prefix_table, out=out, lse=lse,
-                 cu_q=P.cu_q)
-    with _on(dev):
-        ws = _op_workspace(ws, dev, P.workspace_size(_abi.OP_PREFIX_MLA_ATTN))
-        _abi.check(lib().dsa_prefix_mla_attn(
-            ctypes.byref(P.c), n, _ptr(prefix_kv) if n else None, _ptr(prefix_table) if n else None,
-            q.data_ptr(), kv.data_ptr(), out.data_ptr(), _ptr(lse), ws.ptr, ws.nbytes,
-            _stream(dev)))
+    if out is None:
+        out = torch.empty((TQ, H, P.d_c), dtype=_TORCH_OUT[P.out_dtype], device=kv.device)
+    else:
+        _want(out, "out", _TORCH_DT[P.out_dtype], (TQ, H, P.d_c), index)
+    if lse is not None:
+        _want(lse, "lse", _F32, (TQ, H), index)
+    elif want_lse:
+        lse = torch.empty((TQ, H), dtype=torch.float32, device=kv.device)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, _ws_bytes(P, _abi.OP_PREFIX_MLA_ATTN))
+    rc = lib().dsa_prefix_mla_attn(P._ref, n, pre_ptr, table_ptr, q.data_ptr(), kv.data_ptr(),
+                                   out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                                   ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
     return out, lse
 
 
@@ -527,32 +590,41 @@ def accumulate_attn_weights(P: Problem, q, kv, idx, lse, acc, ws: Optional[Works
     """Add the attention weight every selected position received, summed over heads and queries,
     to acc [B, >= max_k_len] f32 in place (dsa_accumulate_attn_weights); returns acc.  idx and lse
     are those of sparse_mla_attn or fused_forward on the same q and kv."""
-    _need(q, "q", P.kv_dtype, (P.total_q, P.h, P.d))
-    _need(kv, "kv", P.kv_dtype, (P.cache_rows, P.d))
-    _need(idx, "idx", None, (P.total_q, P.top_k))
-    if idx.dtype != torch.int32:
-        raise ValueError(f"idx has dtype {idx.dtype}")
-    _need(lse, "lse", _abi.DSA_F32, (P.total_q, P.h))
-    ld = _acc_stride(P, acc, "acc", P.max_k_len)
-    dev = kv.device
-    _same_device(dev, q=q, idx=idx, lse=lse, acc=acc, cu_q=P.cu_q)
-    with _on(dev):
-        ws = _op_workspace(ws, dev, P.workspace_size(_abi.OP_ATTN_WEIGHTS))
-        _abi.check(lib().dsa_accumulate_attn_weights(
-            ctypes.byref(P.c), q.data_ptr(), kv.data_ptr(), idx.data_ptr(), lse.data_ptr(),
-            acc.data_ptr(), ld, ws.ptr, ws.nbytes, _stream(dev)))
+    return _accumulate(kv, P, q, idx, lse, acc, ws)
+
+
+@_on_device
+def _accumulate(kv, P, q, idx, lse, acc, ws):
+    if not kv.is_cuda:
+        raise ValueError("kv must be a CUDA tensor")
+    index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
+    TQ, H, D = P.total_q, P.h, P.d
+    _want(q, "q", dts, (TQ, H, D), index)
+    _want(kv, "kv", dts, (P.cache_rows, D), index)
+    _want(idx, "idx", _I32, (TQ, P.top_k), index)
+    _want(lse, "lse", _F32, (TQ, H), index)
+    ld = _acc_stride(P, acc, "acc", P.max_k_len, index)
+    _there(P.cu_q, index)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, _ws_bytes(P, _abi.OP_ATTN_WEIGHTS))
+    rc = lib().dsa_accumulate_attn_weights(P._ref, q.data_ptr(), kv.data_ptr(), idx.data_ptr(),
+                                           lse.data_ptr(), acc.data_ptr(), ld, ws.buf.data_ptr(),
+                                           ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
     return acc
 
 
-def _acc_stride(P: Problem, acc, name: str, width: int) -> int:
+def _acc_stride(P: Problem, acc, name: str, width: int, index: int) -> int:
     """Row stride of an accumulator [B, >= width] f32 (rows contiguous, any stride between)."""
-    if not acc.is_cuda or acc.dtype != torch.float32 or acc.dim() != 2 \
-            or acc.shape[0] != P.c.num_seqs or acc.shape[1] < width \
-            or (acc.shape[1] > 1 and acc.stride(1) != 1) \
-            or (acc.shape[0] > 1 and acc.stride(0) < acc.shape[1]):
-        raise ValueError(f"{name} must be a float32 CUDA tensor [{P.c.num_seqs}, >= {width}] with "
+    B = P.c.num_seqs
+    if acc.dtype is not torch.float32 or acc.dim() != 2 or acc.get_device() != index \
+            or acc.shape[0] != B or acc.shape[1] < width \
+            or not (acc.is_contiguous() or ((acc.shape[1] == 1 or acc.stride(1) == 1)
+                                            and (B == 1 or acc.stride(0) >= acc.shape[1]))):
+        raise ValueError(f"{name} must be a float32 tensor [{B}, >= {width}] on cuda:{index} with "
                          "contiguous rows")
-    return acc.stride(0) if acc.shape[0] > 1 else acc.shape[1]
+    return acc.stride(0) if B > 1 else acc.shape[1]
 
 
 class Eviction(NamedTuple):
@@ -578,79 +650,84 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
     the result; allocated where None) or, with block_table_out [B, pages] int32, paged with P's
     page size (the *_out tensors are then required; they may be the source's pool, on other pages).
     acc_out [B, >= budget] receives the kept positions' acc and zeros behind them."""
-    budget, sink, recent = int(budget), int(sink), int(recent)
+    return _evict(acc, P, int(budget), int(sink), int(recent), (kv, k_idx, k_scale),
+                  (kv_out, k_idx_out, k_scale_out), block_table_out, kept, cu_k_out, acc_out, ws)
+
+
+@_on_device
+def _evict(acc, P, budget, sink, recent, src, dst, table, kept, cu_k_out, acc_out, ws):
+    if not acc.is_cuda:
+        raise ValueError("acc must be a CUDA tensor")
     if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
         raise ValueError(f"budget = {budget}, sink = {sink}, recent = {recent}: 1 <= budget and "
                          "sink + recent <= budget are needed")
-    B, dev = P.c.num_seqs, acc.device
-    ld = _acc_stride(P, acc, "acc", P.max_k_len)
-    k_lens = [min(n, budget) for n in P.k_lens]
+    B, dev, index = P.c.num_seqs, acc.device, acc.get_device()
+    ld = _acc_stride(P, acc, "acc", P.max_k_len, index)
+    _there(P.cu_k, index)
+    k_lens = [n if n < budget else budget for n in P.k_lens]
     rows = sum(k_lens)
-    max_pages = num_pages = 0
-    if block_table_out is not None:
+    max_pages = num_pages = table_ptr = 0
+    if table is not None:
         if not P.page_size:
             raise ValueError("block_table_out needs paged caches")
-        if not block_table_out.is_cuda or block_table_out.dtype != torch.int32 \
-                or block_table_out.dim() != 2 or block_table_out.shape[0] != B \
-                or not block_table_out.is_contiguous() \
-                or block_table_out.shape[1] * P.page_size < max(k_lens):
-            raise ValueError("block_table_out must be a contiguous int32 CUDA tensor [B, pages] that covers "
-                             "the kept positions")
-        max_pages = block_table_out.shape[1]
+        if table.dim() != 2 or table.shape[0] != B or table.shape[1] * P.page_size < max(k_lens):
+            raise ValueError("block_table_out must be an int32 tensor [B, pages] that covers the kept "
+                             "positions")
+        _want(table, "block_table_out", _I32, table.shape, index)
+        max_pages, table_ptr = table.shape[1], table.data_ptr()
     mx = P.idx_dtype == _abi.DSA_MXFP8_E4M3
-    codes = _abi.DSA_FP8_E4M3 if mx else P.idx_dtype
-    if k_scale is not None and not mx and P.idx_dtype != _abi.DSA_FP8_E4M3:
+    d_idx = P.d_idx
+    if src[2] is not None and not mx and P.idx_dtype != _abi.DSA_FP8_E4M3:
         raise ValueError("k_scale goes with FP8 or MXFP8 index keys")
-    moved = {}
-    rows_out = None
-    for name, src, dst, code, tail in (
-            ("kv", kv, kv_out, P.kv_dtype, (P.d,)),
-            ("k_idx", k_idx, k_idx_out, codes, (P.c.d_idx,)),
-            ("k_scale", k_scale, k_scale_out, _abi.DSA_FP8_E4M3 if mx else _abi.DSA_F32,
-             (P.c.d_idx // 32,) if mx else ())):
-        if src is None:
-            if dst is not None:
+    specs = (("kv", _TORCH_DT[P.kv_dtype], (P.d,)),
+             ("k_idx", _CODES if mx else _TORCH_DT[P.idx_dtype], (d_idx,)),
+             ("k_scale", _U8, (d_idx // 32,)) if mx else ("k_scale", _F32, ()))
+    moved, ptrs, rows_out = [], [], None
+    for s, o, (name, dts, tail) in zip(src, dst, specs):
+        if s is None:
+            if o is not None:
                 raise ValueError(f"{name}_out needs {name}")
-            moved[name] = None
+            moved.append(None)
+            ptrs += (0, 0)
             continue
-        _need(src, name, code, (P.cache_rows,) + tail)
-        if dst is None:
-            if block_table_out is not None:
+        _want(s, name, dts, (P.cache_rows,) + tail, index)
+        if o is None:
+            if table is not None:
                 raise ValueError(f"a paged destination needs {name}_out")
-            dst = torch.empty((rows,) + tail, dtype=src.dtype, device=dev)
-        n = dst.shape[0]
-        _need(dst, name + "_out", code, (n,) + tail)
-        if n < rows or (rows_out is not None and n != rows_out) \
-                or (block_table_out is not None and n % P.page_size):
+            o = torch.empty((rows,) + tail, dtype=s.dtype, device=dev)
+        elif o.dim() != 1 + len(tail):
+            raise ValueError(f"{name}_out has shape {tuple(o.shape)}")
+        else:
+            _want(o, name + "_out", dts, (o.shape[0],) + tail, index)
+        n = o.shape[0]
+        if n < rows or (rows_out is not None and n != rows_out) or (table is not None and n % P.page_size):
             raise ValueError(f"{name}_out has {n} rows: all destinations need the same number, at "
                              f"least {rows}, whole pages where they are paged")
         rows_out = n
-        moved[name] = dst
-    if block_table_out is not None:
-        num_pages = (rows_out if rows_out is not None else P.cache_rows) // P.page_size
+        moved.append(o)
+        ptrs += (s.data_ptr(), o.data_ptr())
+    if table is not None:
+        num_pages = (P.cache_rows if rows_out is None else rows_out) // P.page_size
     if kept is None:
-        kept = torch.empty(B, budget, dtype=torch.int32, device=dev)
+        kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
+    else:
+        _want(kept, "kept", _I32, (B, budget), index)
     if cu_k_out is None:
-        cu_k_out = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        cu_k_out = torch.empty((B + 1,), dtype=torch.int32, device=dev)
+    else:
+        _want(cu_k_out, "cu_k_out", _I32, (B + 1,), index)
     if acc_out is None:
-        acc_out = torch.empty(B, budget, dtype=torch.float32, device=dev)
-    for name, t, shape in (("kept", kept, (B, budget)), ("cu_k_out", cu_k_out, (B + 1,))):
-        _need(t, name, None, shape)
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} has dtype {t.dtype}")
-    ld_out = _acc_stride(P, acc_out, "acc_out", budget)
-    _same_device(dev, kv=kv, k_idx=k_idx, k_scale=k_scale, kept=kept, cu_k_out=cu_k_out,
-                 acc_out=acc_out, block_table_out=block_table_out, cu_k=P.cu_k,
-                 **{k + "_out": v for k, v in moved.items()})
-    with _on(dev):
-        ws = _op_workspace(ws, dev, P.workspace_size(_abi.OP_EVICT))
-        _abi.check(lib().dsa_evict(
-            ctypes.byref(P.c), acc.data_ptr(), ld, budget, sink, recent, kept.data_ptr(),
-            cu_k_out.data_ptr(), acc_out.data_ptr(), ld_out, _ptr(kv), _ptr(moved["kv"]),
-            _ptr(k_idx), _ptr(moved["k_idx"]), _ptr(k_scale), _ptr(moved["k_scale"]),
-            _ptr(block_table_out), max_pages, num_pages, rows_out or 0, ws.ptr, ws.nbytes,
-            _stream(dev)))
-    return Eviction(kept, cu_k_out, k_lens, acc_out, moved["kv"], moved["k_idx"], moved["k_scale"])
+        acc_out, ld_out = torch.empty((B, budget), dtype=torch.float32, device=dev), budget
+    else:
+        ld_out = _acc_stride(P, acc_out, "acc_out", budget, index)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, _ws_bytes(P, _abi.OP_EVICT))
+    rc = lib().dsa_evict(P._ref, acc.data_ptr(), ld, budget, sink, recent, kept.data_ptr(),
+                         cu_k_out.data_ptr(), acc_out.data_ptr(), ld_out, *ptrs, table_ptr, max_pages,
+                         num_pages, rows_out or 0, ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return Eviction(kept, cu_k_out, k_lens, acc_out, *moved)
 
 
 class trace:

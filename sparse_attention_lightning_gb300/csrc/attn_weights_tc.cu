@@ -248,12 +248,13 @@ int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   const int64_t grid = (int64_t)a.seqs.total_q * p.splits;
   if (grid > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "attention weights: grid too large");
   CUtensorMap qmap;
-  const int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, (uint64_t)a.d,
+  int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, (uint64_t)a.d,
                               (uint64_t)a.seqs.total_q * a.h, (uint64_t)a.d * 2, 64, (uint32_t)p.n);
   if (rc != DSA_OK) return rc;
   const int smem = kSlots * kTile + p.ntile * p.n * 128 + kMetaBytes + 1024;
-  if (cudaFuncSetAttribute(attn_weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return check_launch("attn_weights_tc: smem attribute");
+  static int allowed[64];
+  rc = allow_smem(attn_weights_tc_kernel, smem, allowed, "attn_weights_tc: smem attribute");
+  if (rc != DSA_OK) return rc;
   DSA_LAUNCH("attn_weights_tc", stream,
              attn_weights_tc_kernel<<<(unsigned)grid, kThreads, smem, stream>>>(p, qmap));
   return check_launch("attn_weights_tc");

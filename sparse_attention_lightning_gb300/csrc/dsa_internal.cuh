@@ -157,6 +157,20 @@ int make_tmap_tiles(CUtensorMap* m, CUtensorMapDataType dt, const void* base, ui
                     uint64_t rows, uint64_t row_bytes, uint32_t box_tiles, uint32_t box_rows);
 int num_sms();
 
+// Allow `kern` `bytes` of dynamic shared memory; asked of the runtime once for a kernel (its slot:
+// one static array a kernel), device and size.
+template <typename K>
+inline int allow_smem(K kern, int bytes, int (&slot)[64], const char* what) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && slot[dev] >= bytes) return DSA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return check_launch(what);
+  if (keep) slot[dev] = bytes;
+  return DSA_OK;
+}
+
 #define DSA_LAUNCH(name, stream, ...)   \
   do {                                  \
     ::dsa::trace_pre(name, stream);     \

@@ -762,8 +762,9 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   }
   if (rc != DSA_OK) return rc;
   auto kern = fixed ? prefix_tc_kernel<true> : prefix_tc_kernel<false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return check_launch("prefix_tc: smem attribute");
+  static int allowed[2][64];
+  rc = allow_smem(kern, kSmem, allowed[fixed], "prefix_tc: smem attribute");
+  if (rc != DSA_OK) return rc;
   DSA_LAUNCH("prefix_tc", stream, kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p, m));
   rc = check_launch("prefix_tc");
   if (rc != DSA_OK || pl.pieces() == 1) return rc;
