@@ -354,7 +354,8 @@ int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void*
  * positions keep their order and move to the caches' *_out tensors:
  *   kept[b, 0..n_b-1] = the kept positions, ascending; kept[b, n_b..budget-1] = -1
  *   cu_k_out[b] = Σ_{b' < b} n_b'                           (num_seqs + 1 entries)
- *   acc_out[b, i] = acc[b, kept[b, i]] for i < n_b, 0 for n_b <= i < ld_acc_out
+ *   acc_out[b, i] = acc[b, kept[b, i]] for i < n_b, 0 for n_b <= i < budget (columns at or past
+ *     budget stay as they were)
  *   kv_out, k_idx_out, k_scale_out: row of position i of sequence b in the destination =
  *     the source's row of position kept[b, i].
  * The destination is packed (sequence b at rows cu_k_out[b] ..; rows_out rows in all), or, with

@@ -649,7 +649,8 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
     The destination is packed (kv_out, k_idx_out, k_scale_out with at least sum(k_lens) rows of
     the result; allocated where None) or, with block_table_out [B, pages] int32, paged with P's
     page size (the *_out tensors are then required; they may be the source's pool, on other pages).
-    acc_out [B, >= budget] receives the kept positions' acc and zeros behind them."""
+    acc_out [B, >= budget] receives the kept positions' acc and zeros behind them up to column
+    budget."""
     return _evict(acc, P, int(budget), int(sink), int(recent), (kv, k_idx, k_scale),
                   (kv_out, k_idx_out, k_scale_out), block_table_out, kept, cu_k_out, acc_out, ws)
 

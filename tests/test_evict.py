@@ -275,7 +275,7 @@ def _check_eviction(P, keys, r, out, acc, budget, sink, recent, page):
 @pytest.mark.parametrize("idx_dtype", ["e4m3", "mxfp8", "bf16"])
 @pytest.mark.parametrize("k_lens,budget,sink,recent", [
     ([1], 1, 0, 0), ([1, 40, 17], 100, 3, 5), ([50, 200, 64], 64, 0, 0), ([3000, 1, 65, 1024], 65, 60, 5),
-    ([5000, 1025, 999], 1000, 7, 40), ([2100], 1, 1, 0), ([130, 129], 128, 0, 128)])
+    ([5000, 1025, 999], 1000, 7, 40), ([60000, 49153, 31], 20000, 5, 9), ([2100], 1, 1, 0), ([130, 129], 128, 0, 128)])
 def test_evict_matches_definition(k_lens, budget, sink, recent, idx_dtype, page):
     import sparse_attention_lightning_gb300 as dsa
     P, keys, caches, out = _caches(k_lens, idx_dtype, page, seed=budget, budget=budget)
@@ -321,7 +321,12 @@ def test_evict_strided_acc_and_parts():
     wide = torch.full((2, 160), 5.0).cuda()
     r = dsa.evict(P, acc, 100, 1, 2, kv=caches["kv"], acc_out=wide)
     assert r.k_idx is None and r.acc is wide
-    _check_eviction(P, {"kv": keys["kv"]}, r._replace(acc=wide), out, acc, 100, 1, 2, 0)
+    assert (wide[:, 100:] == 5.0).all()  # columns past the budget stay as they were
+    _check_eviction(P, {"kv": keys["kv"]}, r._replace(acc=wide[:, :100]), out, acc, 100, 1, 2, 0)
+    part = torch.full((2, 130), 5.0).cuda()  # a part of wider rows
+    r = dsa.evict(P, acc, 100, 1, 2, acc_out=part[:, 20:120])
+    assert (part[:, :20] == 5.0).all() and (part[:, 120:] == 5.0).all()
+    assert torch.equal(r.acc, wide[:, :100])
     r = dsa.evict(P, acc, 100)
     assert r.kv is None and r.kept[1, 80:].eq(-1).all()
     with pytest.raises(ValueError):
