@@ -2,16 +2,22 @@
 //
 //   w[i] = Σ_h exp(scale · q[t,h,:]·kv[row_i,:] − lse[t,h])
 //
-// The sum runs over heads, so the selected keys are the MMA's M = 128 (a tensor-memory lane a key) and the
-// heads its N: a thread holds one key's logits of all heads and adds their exponentials without any
-// exchange.  The query's heads stay in shared memory (D x 128 heads: 144 KB); gathered rows come
-// through a ring of four [128 keys x 64 columns] tiles.
+// Bound by the gather (1152 B a selected row from anywhere in the cache), so shared memory is left to it: the
+// query's heads are the MMA's M = 128 and live in tensor memory (288 columns), and three chunks of 64
+// gathered rows (216 KB) are in flight on an SM.  (With the keys as M and the query in shared memory, 64 KB
+// were: 34 us for the decode step below.)  The sum over heads is then one
+// over lanes: a thread takes one head's 64 exponentials, 62 shuffles a warp transpose and add them, and
+// the four warps' sums meet in shared memory.
 //
-// Bound by the gather: 1152 B a selected row, and ~2,300 clocks of MMA and ~1,500 of exponentials per 128 keys that
-// overlap with it.  Four producer warps copy with cp.async, eight lanes a 128-byte row piece, straight
-// into the swizzled operand layout (64 KB in flight an SM); one thread issues the MMAs; four warps
-// take the exponentials from two logit buffers in turn.  A CTA takes one query and a share of its
-// selected positions, so that few queries still fill the SMs.  Every wait is bounded (DSA_FLAG_TIMEOUT).
+// Per chunk of 64 selected rows: four producer warps gather them by TMA, four rows x 128 bytes a copy, into the
+// swizzled operand layout; one thread issues S = Q·Kᵀ (M=128, N=64, K=D, A from tensor memory: 33 clocks a
+// K-step); four warps take the exponentials from two logit buffers in turn.  The query block comes through
+// the same ring as one or two chunks of 64 heads and is copied to tensor memory from there: read row by row
+// from global memory (a thread a head, 1152 bytes apart) it took 16,000 clocks before the first MMA.
+// Every CTA takes one contiguous, equal share of all queries' chunks, so that few queries fill the SMs;
+// where a share crosses queries, the query block is loaded again.  Every wait is bounded (DSA_FLAG_TIMEOUT).
+// Decode step of 32 queries x 2048 rows of 1152 B, 128 heads: 24 us, 75.5 MB gathered at about the measured copy
+// rate once it has started; the start (launch, row lookup, first indices, query) is about 5 us.
 #include "attn_weights.cuh"
 #include "tc_sm100.cuh"
 
@@ -20,18 +26,18 @@ namespace {
 
 using namespace tc;
 
-constexpr int kM = 128;               // keys of a chunk
-constexpr int kTile = kM * 128;       // 16 KB
-constexpr int kSlots = 4;
-constexpr int kProducers = 4;         // warps
+constexpr int kN = 64;                 // selected rows of a chunk
+constexpr int kTile = kN * 128;        // 8 KB: 64 rows x 64 columns
+constexpr int kMaxTiles = 9;
+constexpr int kStages = 3;
+constexpr int kProducers = 4;          // warps
 constexpr int kThreads = 32 * (kProducers + 1 + 4);
-constexpr int kMetaBytes = 1024;      // barriers, lse
+constexpr int kMetaBytes = 4096 + 256; // barriers, the warps' sums
+constexpr int kSCol = 0, kQCol = 128;  // tensor memory: 2 x 64 logit columns, 288 query columns
 
 struct Params {
   WeightArgs a;
-  int splits;   // CTAs of a query
   int chunks;   // of a query
-  int n;        // MMA N: heads rounded up to 16
   int ntile;    // column tiles
 };
 
@@ -45,218 +51,352 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Rows r0..r3, 64 columns from column c, to four consecutive 128-byte rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int c, int r0, int r1,
+                                            int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
+      : "memory");
 }
-__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+
+// The k-th piece of this CTA's share: chunks [c0, c1) of query row t; false past the end.
+struct Piece {
+  int t, c0, c1;
+};
+__device__ __forceinline__ bool piece_at(const Params& p, int k, Piece& pc) {
+  const int64_t tot = (int64_t)p.a.seqs.total_q * p.chunks;
+  const int64_t x0 = tot * blockIdx.x / gridDim.x, x1 = tot * (blockIdx.x + 1) / gridDim.x;
+  const int64_t t = x0 / p.chunks + k, r0 = t * p.chunks;
+  if (r0 >= x1) return false;
+  pc.t = (int)t;
+  pc.c0 = k == 0 ? (int)(x0 - r0) : 0;
+  pc.c1 = (int)min((int64_t)p.chunks, x1 - r0);
+  return true;
+}
+
+// query_row_info by a whole warp: a 32-way search over cu_q (one round of loads up to 32 sequences).
+__device__ __forceinline__ bool warp_row_info(const Seqs& s, int t, int lane, RowInfo& r, uint32_t* status) {
+  int lo = 0, hi = s.B;  // the last b with cu_q[b] <= t is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int probe = lo + lane * step;
+    const bool le = probe < hi && (lane == 0 || __ldg(s.cu_q + probe) <= t);
+    const int m = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += m * step;
+    hi = min(hi, lo + step);
+  }
+  const int q0 = __ldg(s.cu_q + lo), q1 = __ldg(s.cu_q + lo + 1);
+  const int k0 = __ldg(s.cu_k + lo), k1 = __ldg(s.cu_k + lo + 1);
+  const int T = q1 - q0, L = k1 - k0;
+  if (!(t >= q0 && t < q1 && T <= L && k0 >= 0 && k1 <= s.total_k && L <= s.max_k_len && q1 <= s.total_q)) {
+    atomicOr(status, DSA_FLAG_BAD_SEQS);
+    return false;
+  }
+  r = RowInfo{lo, L - T + (t - q0), k0, L};
+  return true;
+}
+
+// v[i] of all lanes added up for i = 0..31: lane l gets the sum of v[l] (31 shuffles: each step a lane
+// keeps the half its bit selects).  The tree is the same for every i.
+__device__ __forceinline__ float transpose_add(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o];
+      const float keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
+attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kvmap) {
   const WeightArgs& a = p.a;
-  const int t = blockIdx.x / p.splits, split = blockIdx.x - t * p.splits;
-  const int c0 = (int)((int64_t)p.chunks * split / p.splits);
-  const int nch = (int)((int64_t)p.chunks * (split + 1) / p.splits) - c0;
-  RowInfo ri;
-  if (!query_row_info(a.seqs, t, ri, a.status) || nch == 0) return;
-
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* ring = smem;                                   // [4][128][128 B]
-  uint8_t* qs = ring + kSlots * kTile;                    // [ntile][n][128 B]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(qs + p.ntile * p.n * 128);
-  uint64_t* a_full = bars;          // [4] 128 producer threads (cp.async completion)
-  uint64_t* a_empty = bars + 4;     // [4]
-  uint64_t* s_full = bars + 8;      // [2]
-  uint64_t* s_empty = bars + 10;    // [2] 4 warps
-  uint64_t* q_full = bars + 12;
-  uint64_t* drain = bars + 13;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 15);
-  float* lse2 = reinterpret_cast<float*>(bars + 16);      // [128] lse in log2 units, +inf: no weight
+  uint8_t* ring = smem;                                   // [3][ntile][64][128 B]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kStages * p.ntile * kTile);
+  uint64_t* k_full = bars;          // [3] 4 producer warps, and their bytes
+  uint64_t* k_empty = bars + 3;     // [3]
+  uint64_t* s_full = bars + 6;      // [2]
+  uint64_t* s_empty = bars + 8;     // [2] 4 warps
+  uint64_t* q_full = bars + 10;     // 4 warps have stored the query
+  uint64_t* drain = bars + 11;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 13);
+  uint64_t* red_full = bars + 14;   // [2] 4 warps have stored a chunk's sums
+  // [4][4][64] the warps' sums, by chunk: a warp may be up to two chunks ahead of the threads that read them
+  float* red = reinterpret_cast<float*>(bars + 16);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) { mbar_init(&a_full[i], 32 * kProducers); mbar_init(&a_empty[i], 1); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(&k_full[i], kProducers); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4); }
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 4);
+    mbar_init(&red_full[0], 4);
+    mbar_init(&red_full[1], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (threadIdx.x < 128) {
-    float v = INFINITY;
-    if ((int)threadIdx.x < a.h) {
-      v = a.lse[(int64_t)t * a.h + threadIdx.x];
-      v = v == -INFINITY ? INFINITY : v * kLog2e;
-    }
-    lse2[threadIdx.x] = v;
-  }
-  if (warp == kProducers) { tmem_alloc(tmem_slot, 256); tmem_relinquish(); }
+  if (warp == kProducers) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
   tc_fence_before();
   cta_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int D = a.d;
+  const int stage_bytes = p.ntile * kTile;
+  const int qchunks = a.h > 64 ? 2 : 1;  // ring chunks of a query block
 
   if (warp < kProducers) {
-    // ---------------- producers: 8 lanes a row piece of 128 bytes, 4 rows a step and warp ----------------
-    const int piece = lane & 7, rsub = warp * 4 + (lane >> 3);
-    const __nv_bfloat16* kv = static_cast<const __nv_bfloat16*>(a.kv);
-    // this thread's 8 cache rows of chunk c (row 0 in place of entries that are skipped: their weight
-    // is dropped)
-    int row[8];
-    auto load_rows = [&](int c) {
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const int i = c * kM + g * 16 + rsub;
-        const int v = i < a.top_k ? __ldg(a.idx + (int64_t)t * a.top_k + i) : -1;
-        int r = -1;
-        if (v >= 0 && v <= ri.pos) r = key_row(a.seqs, ri.b, ri.k0, v);
-        row[g] = r < 0 ? 0 : r;
-      }
-    };
-    load_rows(c0);
-    int n = 0;
+    // ---------------- producers: 16 rows of a chunk each, four rows x 128 bytes a copy ----------------
+    int slot = 0, phase = 1, n = 0;
     bool stop = false;
-    for (int c = 0; c < nch && !stop; ++c) {
-      const char* src[8];
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        if (!dsa_check(row[g] < a.seqs.cache_rows(), a.status)) row[g] = 0;
-        src[g] = reinterpret_cast<const char*>(kv + (int64_t)row[g] * D) + piece * 16;
-      }
-      if (c + 1 < nch) load_rows(c0 + c + 1);
-      for (int tile = 0; tile < p.ntile; ++tile, ++n) {
-        const int slot = n % kSlots;
-        if (!__all_sync(0xffffffffu, mbar_wait(&a_empty[slot], ((n / kSlots) & 1) ^ 1, abort_flag, a.status,
-                                               DSA_FLAG_TIMEOUT))) { stop = true; break; }
-        const uint32_t dst = smem_u32(ring + slot * kTile) + rsub * 128;
-        if (tile * 64 + piece * 8 < D) {  // D is a multiple of 16: a piece is inside or outside
-#pragma unroll
-          for (int g = 0; g < 8; ++g)
-            // rows g·16 + rsub: their place in the 8-row swizzle is rsub's
-            cp_async16(dst + g * 2048 + ((piece ^ (rsub & 7)) * 16), src[g] + tile * 128);
+    Piece pc;
+    for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
+      RowInfo ri;
+      // lanes 0..15: this warp's entries, read two chunks ahead, and their pages, one chunk ahead
+      auto load_idx = [&](int c) {
+        const int i = c * kN + warp * 16 + lane;
+        return lane < 16 && i < a.top_k ? __ldg(a.idx + (int64_t)pc.t * a.top_k + i) : -1;
+      };
+      int v0 = load_idx(pc.c0), v1 = load_idx(pc.c0 + 1);
+      if (!warp_row_info(a.seqs, pc.t, lane, ri, a.status)) continue;
+      // the query block, 64 heads a chunk of the ring
+      for (int c = 0; c < qchunks && !stop; ++c, ++n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+          stop = true;
+          break;
         }
-        cp_async_arrive_noinc(&a_full[slot]);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&k_full[slot], (uint32_t)((p.ntile + 3 - warp) / kProducers * kTile));
+          for (int t = warp; t < p.ntile; t += kProducers)
+            tma_load_2d(ring + slot * stage_bytes + t * kTile, &qmap, &k_full[slot], t * 64, pc.t * a.h + c * kN);
+        }
+        __syncwarp();
+        if (++slot == kStages) { slot = 0; phase ^= 1; }
+      }
+      if (stop) break;
+      const bool paged = a.seqs.paged();
+      const int sh = paged ? __ffs(a.seqs.page_size) - 1 : 0;
+      const int32_t* table = a.seqs.block_table + (int64_t)ri.b * a.seqs.max_pages;
+      auto load_page = [&](int v) { return paged && v >= 0 && v <= ri.pos ? __ldg(table + (v >> sh)) : 0; };
+      int pg = load_page(v0);
+      for (int c = pc.c0; c < pc.c1; ++c, ++n) {
+        int row = -1;
+        if (v0 >= 0 && v0 <= ri.pos) {
+          if (!paged) row = ri.k0 + v0;
+          else if ((unsigned)pg < (unsigned)a.seqs.num_pages) row = (pg << sh) | (v0 & (a.seqs.page_size - 1));
+        }
+        if (!dsa_check(row < a.seqs.cache_rows(), a.status)) row = -1;
+        v0 = v1;
+        pg = load_page(v0);
+        v1 = load_idx(c + 2);
+        // Four entries a copy.  Skipped entries repeat another of their four (their weight is dropped), and four
+        // skipped ones copy nothing: standing in for padding with one fixed row made every SM ask for the same
+        // lines (43 us instead of 21 for 86 queries, half of whose 500 entries were padding).
+        const unsigned ok = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+        const unsigned four = (ok >> (lane & 12)) & 15u;
+        const int other = __shfl_sync(0xffffffffu, row, (lane & 12) + (four ? __ffs(four) - 1 : 0));
+        if (row < 0) row = other;
+        const int copies = __popc((ok | ok >> 1 | ok >> 2 | ok >> 3) & 0x1111u);
+        int r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __shfl_sync(0xffffffffu, row, i);
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+          stop = true;
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&k_full[slot], (uint32_t)(copies * p.ntile * 512));
+          uint8_t* dst = ring + slot * stage_bytes + warp * 16 * 128;
+#pragma unroll
+          for (int t = 0; t < kMaxTiles; ++t) {
+            if (t >= p.ntile) break;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if ((ok >> (4 * g)) & 15u)
+                tma_gather4(dst + t * kTile + g * 512, &kvmap, &k_full[slot], t * 64, r[4 * g], r[4 * g + 1],
+                          r[4 * g + 2], r[4 * g + 3]);
+          }
+        }
+        __syncwarp();
+        if (++slot == kStages) { slot = 0; phase ^= 1; }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // landed before the CTA may exit
+    // every copy issued has landed before the CTA may exit
+    for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_drain(&k_full[i % kStages], (i / kStages) & 1);
   } else if (warp == kProducers) {
-    // ---------------- the query's heads, MMA issue ----------------
-    if (elect_one()) {
-      mbar_arrive_expect_tx(q_full, (uint32_t)(p.ntile * p.n * 128));
-      for (int j = 0; j < p.ntile; ++j)
-        tma_load_2d(qs + j * p.n * 128, &qmap, q_full, j * 64, t * a.h);
-      const uint32_t idesc = idesc_bf16(kM, p.n);
-      const uint64_t ad0 = sdesc_sw128(smem_u32(ring), 16, 1024), bd0 = sdesc_sw128(smem_u32(qs), 16, 1024);
-      const uint32_t bstep = (uint32_t)(p.n * 128) >> 4;
-      bool stop = !mbar_wait(q_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-      uint32_t slot = 0, phase = 0;
-      for (int c = 0; c < nch && !stop; ++c) {
-        if (!mbar_wait(&s_empty[c & 1], ((c >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
-        const uint32_t d = tmem + (c & 1) * 128;
-        uint64_t bd = bd0;
-        for (int tile = 0; tile < p.ntile; ++tile) {
-          if (!mbar_wait(&a_full[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT)) { stop = true; break; }
-          fence_proxy_async_smem();  // the cp.async writes, seen by the tensor core
+    // ---------------- MMA issue: the warp walks the pieces, one lane issues ----------------
+    const uint32_t idesc = idesc_bf16(128, kN);
+    const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+    int slot = 0, phase = 0, n = 0, qn = 0;
+    bool stop = false;
+    Piece pc;
+    for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
+      RowInfo ri;
+      if (!warp_row_info(a.seqs, pc.t, lane, ri, a.status)) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(q_full, qn & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) break;
+      ++qn;
+      for (int c = 0; c < qchunks; ++c) {  // the query has left the ring for tensor memory
+        if (lane == 0) mbar_arrive(&k_empty[slot]);
+        if (++slot == kStages) { slot = 0; phase ^= 1; }
+      }
+      for (int c = pc.c0; c < pc.c1; ++c, ++n) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&s_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) &&
+                            mbar_wait(&k_full[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+          stop = true;
+          break;
+        }
+        if (elect_one()) {
           tc_fence_after();
-          const uint64_t ad = ad0 + (uint64_t)(slot * (kTile >> 4));
-          if (tile * 64 + 64 <= D) {
+          const uint32_t d = tmem + kSCol + (n & 1) * kN;
+          const uint64_t kd = kd0 + (uint64_t)(slot * (stage_bytes >> 4));
+#pragma unroll
+          for (int t = 0; t < kMaxTiles; ++t) {
+            if (t * 64 >= D) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_bf16(d, ad + (uint64_t)(i * 2), bd + (uint64_t)(i * 2), idesc, tile || i ? 1u : 0u);
-          } else {
-            for (int i = 0; i < (D - tile * 64) / 16; ++i)
-              mma_bf16(d, ad + (uint64_t)(i * 2), bd + (uint64_t)(i * 2), idesc, tile || i ? 1u : 0u);
+              if (t * 64 + i * 16 < D)
+                mma_bf16_ts(d, tmem + kQCol + t * 32 + i * 8, kd + (uint64_t)(t * (kTile >> 4) + i * 2), idesc,
+                            t || i ? 1u : 0u);
           }
-          mma_commit(&a_empty[slot]);
-          bd += bstep;
-          if (++slot == kSlots) { slot = 0; phase ^= 1; }
+          mma_commit(&k_empty[slot]);
+          mma_commit(&s_full[n & 1]);
         }
-        if (!stop) mma_commit(&s_full[c & 1]);
+        __syncwarp();
+        if (++slot == kStages) { slot = 0; phase ^= 1; }
       }
+    }
+    if (elect_one()) {
       mma_commit(drain);
       mbar_wait_drain(drain, 0);
-      mbar_wait_drain(q_full, 0);
     }
+    __syncwarp();
   } else {
-    // ---------------- weights: thread = key ----------------
-    const int quarter = warp & 3;
+    // ---------------- weights: thread = head ----------------
+    const int quarter = warp & 3, h = quarter * 32 + lane;
+    const int et = threadIdx.x - 32 * (kProducers + 1);  // 0..127
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    for (int c = 0; c < nch; ++c) {
-      const int i = (c0 + c) * kM + quarter * 32 + lane;
-      const int v = i < a.top_k ? __ldg(a.idx + (int64_t)t * a.top_k + i) : -1;
-      const bool valid = v >= 0 && v <= ri.pos && key_row(a.seqs, ri.b, ri.k0, v) >= 0;
-      if (!valid && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[c & 1], (c >> 1) & 1, abort_flag, a.status,
-                                             DSA_FLAG_TIMEOUT))) break;
-      tc_fence_after();
-      float w[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int h0 = 0; h0 < a.h; h0 += 32) {
-        uint32_t s[32];
-        __syncwarp();
-        tmem_ld32(lane_base + (c & 1) * 128 + h0, s);
+    int n = 0, slot = 0, phase = 0;
+    bool stop = false;
+    Piece pc;
+    for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
+      RowInfo ri;
+      if (!warp_row_info(a.seqs, pc.t, lane, ri, a.status)) continue;
+      // this warp's 32 heads of the query block, from the ring to tensor memory (the previous piece's
+      // logits are complete: its last chunk has been read)
+      const int qc = quarter >> 1;
+      int qslot = slot + qc, qphase = phase;
+      if (qslot >= kStages) { qslot -= kStages; qphase ^= 1; }
+      if (qc < qchunks) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_full[qslot], qphase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) break;
+        const int r = (quarter & 1) * 32 + lane;  // row of the chunk
+        const uint8_t* from = ring + qslot * stage_bytes + r * 128;
+#pragma unroll 3
+        for (int t = 0; t < p.ntile; ++t) {
+          uint32_t w[32];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(lse2 + h0 + j);
-          const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // +inf: no such head, or it attended to nothing; whatever its logit is, it adds nothing
-            const float x = ex2(fmaf(__uint_as_float(s[j + e]), a.scale_log2, -l[e]));
-            w[e] += l[e] == INFINITY ? 0.f : x;
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + t * kTile + ((i ^ (r & 7)) * 16));
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
           }
+          tmem_st32(lane_base + kQCol + t * 32, w);
         }
       }
+      slot += qchunks + pc.c1 - pc.c0;  // the piece's place in the ring is passed
+      phase ^= (slot / kStages) & 1;
+      slot %= kStages;
+      const int64_t flat = (int64_t)pc.t * a.h + min(h, a.h - 1);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[c & 1]);
-      if (valid) add_weight(a, ri.b, v, (w[0] + w[1]) + (w[2] + w[3]));
+      if (lane == 0) mbar_arrive(q_full);
+      const float lse = h < a.h ? a.lse[flat] : -INFINITY;
+      const bool dead = lse == -INFINITY;  // no such head, or it attended to nothing: it adds nothing
+      const float lse2 = dead ? 0.f : lse * kLog2e;
+      for (int c = pc.c0; c < pc.c1; ++c, ++n) {
+        // threads 0..63 add up and store one selected position each
+        int pos = -1;
+        if (et < kN) {
+          const int i = c * kN + et;
+          const int v = i < a.top_k ? __ldg(a.idx + (int64_t)pc.t * a.top_k + i) : -1;
+          if (v >= 0 && v <= ri.pos && key_row(a.seqs, ri.b, ri.k0, v) >= 0) pos = v;
+          else if (v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (n >> 1) & 1, abort_flag, a.status,
+                                               DSA_FLAG_TIMEOUT))) { stop = true; break; }
+        tc_fence_after();
+        float* mine = red + (n & 3) * 256 + quarter * 64;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t s[32];
+          __syncwarp();
+          tmem_ld32(lane_base + kSCol + (n & 1) * kN + half * 32, s);
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[n & 1]);
+          }
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e = ex2(fmaf(__uint_as_float(s[i]), a.scale_log2, -lse2));
+            x[i] = dead ? 0.f : e;
+          }
+          mine[half * 32 + lane] = transpose_add(x, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&red_full[n & 1]);
+        if (et >= kN) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(&red_full[n & 1], (n >> 1) & 1, abort_flag, a.status,
+                                               DSA_FLAG_TIMEOUT))) { stop = true; break; }
+        if (pos >= 0) {
+          const float* r = red + (n & 3) * 256 + et;
+          add_weight(a, ri.b, pos, (r[0] + r[64]) + (r[128] + r[192]));
+        }
+      }
     }
   }
   tc_fence_before();
   cta_sync();
   if (warp == kProducers) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 }  // namespace
 
 bool attn_weights_tc_eligible(const WeightArgs& a) {
-  return a.kv_dtype == DSA_BF16 && a.d >= 64 && a.d <= 576 && a.h <= 128;
+  return a.kv_dtype == DSA_BF16 && a.d >= 64 && a.d <= 64 * kMaxTiles && a.h <= 128;
 }
 
 int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
-  p.n = (a.h + 15) / 16 * 16;
   p.ntile = (a.d + 63) / 64;
-  p.chunks = (a.top_k + kM - 1) / kM;
-  // CTAs of a query: fewest waves of its chunks, with about one and a half chunks' time for a CTA's start
-  const int sms = num_sms();
-  double best = 1e30;
-  p.splits = 1;
-  for (int s = 1; s <= p.chunks; ++s) {
-    const int64_t ctas = (int64_t)a.seqs.total_q * s;
-    const double cost = (double)((ctas + sms - 1) / sms) * ((p.chunks + s - 1) / s + 1.5);
-    if (cost < best) { best = cost; p.splits = s; }
-  }
-  const int64_t grid = (int64_t)a.seqs.total_q * p.splits;
-  if (grid > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "attention weights: grid too large");
-  CUtensorMap qmap;
+  p.chunks = (a.top_k + kN - 1) / kN;
+  const int64_t tot = (int64_t)a.seqs.total_q * p.chunks;
+  const int grid = (int)(tot < num_sms() ? tot : num_sms());
+  const int smem = kStages * p.ntile * kTile + kMetaBytes + 1024;
+  CUtensorMap qmap, kvmap;
   int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, (uint64_t)a.d,
-                              (uint64_t)a.seqs.total_q * a.h, (uint64_t)a.d * 2, 64, (uint32_t)p.n);
+                        (uint64_t)a.seqs.total_q * a.h, (uint64_t)a.d * 2, 64, kN);
   if (rc != DSA_OK) return rc;
-  const int smem = kSlots * kTile + p.ntile * p.n * 128 + kMetaBytes + 1024;
+  rc = make_tmap_2d(&kvmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, (uint64_t)a.d,
+                        (uint64_t)a.seqs.cache_rows(), (uint64_t)a.d * 2, 64, 1);
+  if (rc != DSA_OK) return rc;
   static int allowed[64];
   rc = allow_smem(attn_weights_tc_kernel, smem, allowed, "attn_weights_tc: smem attribute");
   if (rc != DSA_OK) return rc;
-  DSA_LAUNCH("attn_weights_tc", stream,
-             attn_weights_tc_kernel<<<(unsigned)grid, kThreads, smem, stream>>>(p, qmap));
+  DSA_LAUNCH("attn_weights_tc", stream, attn_weights_tc_kernel<<<grid, kThreads, smem, stream>>>(p, qmap, kvmap));
   return check_launch("attn_weights_tc");
 }
 
