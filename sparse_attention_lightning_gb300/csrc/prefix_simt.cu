@@ -19,6 +19,7 @@ constexpr int kRows = 16;
 
 template <typename TK, typename TO, int KC>
 __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int nblk) {
+  griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   extern __shared__ float smem[];
   const int D = a.d_c + a.d_rope, DP = D + 1, dc = a.d_c, H = a.h;
   const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk, split = blockIdx.y;
@@ -126,44 +127,80 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
   if (tid < R) a.part_ml[(int64_t)split * rows + flat0 + tid] = make_float2(m_s[tid], l_s[tid]);
 }
 
-// out = Σ_j w_j O_j / Σ_j w_j l_j, w_j = 2^(m_j - max m) over the row's pieces, in piece order.
-// Four rows a block, 32 threads a row; a piece without keys has l = 0 and its O is not read.
+// out = Σ_j w_j O_j / Σ_j w_j l_j, w_j = 2^(m_j - max m) over the row's pieces, O added in piece order.  A block a
+// row, four columns a thread.  All it costs is latency: the row is looked up before the pieces' grid has
+// ended, each lane takes two pieces' (max, sum), and eight pieces' outputs are loaded before the first is
+// added.  (One load after another, for 9 pieces of 64 rows: 12 us; so: 4.)  A piece without keys has l = 0
+// and its O is not read.
+constexpr int kMaxPieces = 128;
 template <typename TO>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(PrefixArgs a, int pieces) {
-  const int64_t rows = (int64_t)a.seqs.total_q * a.h;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(128, 8) prefix_merge_kernel(PrefixArgs a, int pieces) {
+  const int64_t rows = (int64_t)a.seqs.total_q * a.h, row = blockIdx.x;
   const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
   RowInfo ri;
   SeqInfo si;  // the pieces of a row whose sequence is inconsistent were not written
-  if (!query_row_info(a.seqs, (int)(row / a.h), ri, a.status) || !prefix_seq(a, ri.b, si)) return;
-  float M = -INFINITY;
-  for (int j = 0; j < pieces; ++j) {
-    const float2 v = a.part_ml[j * rows + row];
+  const bool ok = query_row_info(a.seqs, (int)(row / a.h), ri, a.status) && prefix_seq(a, ri.b, si);
+  griddep_wait();
+  if (!ok) return;
+  float m[kMaxPieces / 32], w[kMaxPieces / 32], M = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxPieces / 32; ++i) {
+    const int j = i * 32 + lane;
+    const float2 v = j < pieces ? __ldcg(a.part_ml + j * rows + row) : make_float2(-INFINITY, 0.f);
+    m[i] = v.x;
+    w[i] = v.y;
     if (v.y != 0.f) M = fmaxf(M, v.x);
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  for (int j = 0; j < pieces; ++j) {
-    const float2 v = a.part_ml[j * rows + row];
-    if (v.y != 0.f) l = fmaf(exp2f(v.x - ref), v.y, l);
+#pragma unroll
+  for (int i = 0; i < kMaxPieces / 32; ++i) {
+    const float f = w[i] == 0.f ? 0.f : exp2f(m[i] - ref);
+    l = fmaf(f, w[i], l);
+    w[i] = f;
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   TO* o = static_cast<TO*>(a.out) + row * a.d_c;
-  for (int c = lane * 4; c < a.d_c; c += 128) {
+  const float* po = a.part_o + row * a.d_c;
+  const int64_t stride = rows * a.d_c;
+  for (int c0 = 0; c0 < a.d_c; c0 += 512) {
+    const int c = c0 + (int)threadIdx.x * 4;
+    const bool in = c < a.d_c;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < pieces; ++j) {
-      const float2 v = a.part_ml[j * rows + row];
-      if (v.y == 0.f) continue;
-      const float w = exp2f(v.x - ref);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + (j * rows + row) * a.d_c + c);
-      s.x = fmaf(w, x.x, s.x); s.y = fmaf(w, x.y, s.y);
-      s.z = fmaf(w, x.z, s.z); s.w = fmaf(w, x.w, s.w);
+#pragma unroll
+    for (int i = 0; i < kMaxPieces / 32; ++i) {
+      if (i * 32 >= pieces) break;
+      for (int j0 = 0; j0 < 32 && i * 32 + j0 < pieces; j0 += 8) {
+        float4 x[8];
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[j] = __shfl_sync(0xffffffffu, w[i], j0 + j);  // 0 past the last piece
+          x[j] = in && f[j] != 0.f
+                     ? __ldcg(reinterpret_cast<const float4*>(po + (i * 32 + j0 + j) * stride + c))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s.x = fmaf(f[j], x[j].x, s.x); s.y = fmaf(f[j], x[j].y, s.y);
+          s.z = fmaf(f[j], x[j].z, s.z); s.w = fmaf(f[j], x[j].w, s.w);
+        }
+      }
     }
-    store_f32(o + c, s.x * inv); store_f32(o + c + 1, s.y * inv);
-    store_f32(o + c + 2, s.z * inv); store_f32(o + c + 3, s.w * inv);
+    if (!in) continue;
+    if (sizeof(TO) == 4) {
+      *reinterpret_cast<float4*>(o + c) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * inv, s.y * inv);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(s.z * inv, s.w * inv);
+      *reinterpret_cast<uint2*>(o + c) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
   }
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+  if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 template <typename TK, typename TO, int KC>
@@ -202,13 +239,10 @@ int launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream) {
 
 int launch_prefix_merge(const PrefixArgs& a, int pieces, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.seqs.total_q * a.h;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  if (a.out_dtype == DSA_F32)
-    DSA_LAUNCH("prefix_merge", stream,
-               prefix_merge_kernel<float><<<grid, 128, 0, stream>>>(a, pieces));
-  else
-    DSA_LAUNCH("prefix_merge", stream,
-               prefix_merge_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a, pieces));
+  auto kern = a.out_dtype == DSA_F32 ? prefix_merge_kernel<float> : prefix_merge_kernel<__nv_bfloat16>;
+  cudaError_t e = cudaSuccess;
+  DSA_LAUNCH("prefix_merge", stream, e = launch_pdl(kern, dim3((unsigned)rows), dim3(128), 0, stream, a, pieces));
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "prefix_merge: %s", cudaGetErrorString(e));
   return check_launch("prefix_merge");
 }
 

@@ -177,6 +177,7 @@ struct Maps {
 template <bool FIXED>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   Item it;
   if (!item_at(p, blockIdx.x, it)) return;
   const PrefixArgs& a = p.a;
@@ -197,8 +198,8 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   uint64_t* bars = reinterpret_cast<uint64_t*>(vs + kTiles * kTile);
   uint64_t* v_full = bars;            // [3]
   uint64_t* v_empty = bars + 3;       // [3]
-  uint64_t* k_full = bars + 6;        // [3][2] the two parts of a chunk's K tiles
-  uint64_t* k_empty = bars + 12;      // [3][2]
+  uint64_t* k_full = bars + 6;        // [3][2] the two parts of a chunk's K tiles; FIXED: [5] a K tile
+  uint64_t* k_empty = bars + 12;
   uint64_t* s_full = bars + 18;       // [2] logits of the buffer's chunk complete
   uint64_t* p_full = bars + 20;       // [2] its 4 softmax warps have written P
   uint64_t* pv_done = bars + 22;      // [2] its P·V complete
@@ -208,6 +209,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   uint64_t* badkeys = bars + 27;      // [3] keys of a chunk on pages outside the cache, a bit each
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 31);
+  uint64_t* q_staged = bars + 32;     // query tiles on their way to tensor memory
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = a.d_c + a.d_rope;
@@ -223,7 +225,10 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   // Column tile of K tile j, and where the query columns that match a tile are: V tile j in tensor
   // memory at tile j; K tile j after them while there is room (4 tiles), then in shared memory.
   auto ktile = [&](int j) { return j < vt0 ? j : j + nvt; };
-  const int nkq = FIXED ? 0 : min(nkt, kQTmemTiles - nvt);      // K tiles whose query columns are in tensor memory
+  const int nkq = FIXED ? 0 : min(nkt, kQTmemTiles - nvt);  // K tiles whose query columns are in tensor memory
+  // The query tiles for tensor memory come by TMA into key tiles that no chunk uses yet (FIXED: those of
+  // chunks 1 and 2; otherwise the first, and no key is loaded before they have left).
+  uint8_t* qstage = vs + (FIXED ? 4 * kTile : 0);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kVSlots; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
@@ -234,6 +239,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_staged, 1);
     mbar_init(qt_full, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -248,14 +254,19 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   if (warp == 0) {
     // ---------------- producer ----------------
     if (elect_one()) {
-      const int nqs = nkt - nkq;
+      const int nqs = nkt - nkq, nqt = nvt + nkq;
+      mbar_arrive_expect_tx(q_staged, (uint32_t)(nqt * kQTile));
+      for (int t = 0; t < nqt; ++t)
+        tma_load_2d(qstage + t * kQTile, &maps.q, q_staged, (t < nvt ? vt0 + t : ktile(t - nvt)) * 64, (int)it.row0);
       if (nqs) {
         mbar_arrive_expect_tx(q_full, (uint32_t)(nqs * kQTile));
         for (int j = 0; j < nqs; ++j)
           tma_load_2d(qs + j * kQTile, &maps.q, q_full, ktile(nkq + j) * 64, (int)it.row0);
       }
-      int g = 0, kn = 0;  // chunks whose V tiles, half-chunks whose K tiles have been issued
-      for (; g < nch; ++g) {
+      int g = 0, kn = 0;  // chunks whose V tiles, half-chunks (FIXED: tiles) whose K tiles have been issued
+      auto stage_free = [&]() { return mbar_wait(qt_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT); };
+      const int stop_at = FIXED || stage_free() ? nch : 0;
+      for (; g < stop_at; ++g) {
         const int c = it.c0 + g, vslot = g % kVSlots;
         // the cache rows of the chunk's keys: one run, or one a page
         const bool pre = c < it.ncp;
@@ -303,6 +314,15 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         };
         // K tiles first: the MMAs start with them
         bool stop = false;
+        if constexpr (FIXED) {
+          for (int j = 0; j < 5; ++j) {
+            if (!mbar_wait(&k_empty[j], (g & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) { stop = true; break; }
+            mbar_arrive_expect_tx(&k_full[j], kTile);
+            load(ks + j * kTile, &k_full[j], ktile(j));
+            ++kn;
+          }
+          if (g == 1 && !stop) stop = !stage_free();
+        } else
         for (int h = 0; h < 2; ++h) {
           const int j0 = h ? nka : 0, j1 = h ? nkt : nka;
           if (j0 == j1) continue;
@@ -312,11 +332,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
             break;
           }
           mbar_arrive_expect_tx(&k_full[bar], (uint32_t)((j1 - j0) * kTile));
-          if (FIXED && h == 0) {
-            load4(ks, &k_full[0], 4 - vt0);
-          } else {
-            for (int j = j0; j < j1; ++j) load(ks + (slot * nkt + j) * kTile, &k_full[bar], ktile(j));
-          }
+          for (int j = j0; j < j1; ++j) load(ks + (slot * nkt + j) * kTile, &k_full[bar], ktile(j));
           kn = 2 * g + h + 1;
         }
         if (stop || !mbar_wait(&v_empty[vslot], ((g / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
@@ -330,9 +346,13 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         }
       }
       // every copy issued has landed before the CTA may exit
+      mbar_wait_drain(q_staged, 0);
       if (nqs) mbar_wait_drain(q_full, 0);
       for (int i = max(0, g - kVSlots); i < g; ++i)
         mbar_wait_drain(&v_full[i % kVSlots], (i / kVSlots) & 1);
+      if constexpr (FIXED) {
+        for (int i = max(0, kn - 5); i < kn; ++i) mbar_wait_drain(&k_full[i % 5], (i / 5) & 1);
+      } else
       for (int i = max(0, kn - 2 * kslots); i < kn; ++i) {
         const int c = i >> 1, h = i & 1;
         if (h && nka == nkt) continue;
@@ -405,22 +425,18 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
           if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
             break;
           const uint32_t d = tmem + kSCol + (g & 1) * kN;
-          if (!mbar_wait(&k_full[0], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
-          tc_fence_after();
+          // a barrier a tile: each is refilled while the others and the V tiles are multiplied
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 5; ++j) {
+            if (!mbar_wait(&k_full[j], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) { stop = true; break; }
+            tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               mma_bf16(d, qd + (uint64_t)(j * (kQTile >> 4) + i * 2), kd + (uint64_t)(j * (kTile >> 4) + i * 2),
                        idesc_s, j || i ? 1u : 0u);
-          mma_commit(&k_empty[0]);
-          if (!mbar_wait(&k_full[1], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_bf16(d, qd + (uint64_t)(4 * (kQTile >> 4) + i * 2), kd + (uint64_t)(4 * (kTile >> 4) + i * 2),
-                     idesc_s, 1u);
-          mma_commit(&k_empty[1]);
+            mma_commit(&k_empty[j]);
+          }
+          if (stop) break;
           if (!mbar_wait(&v_full[vslot], vphase, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
           tc_fence_after();
           const uint64_t vd = sdesc_sw128(v0 + vslot * (4 * kTile), 16, 1024);
@@ -486,13 +502,13 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
     // this row's last visible suffix position
     const int pos = it.pos0 + (it.hoff + min(r, it.rows - 1)) / a.h;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + flat * D);
-      for (int t = 0; t < nvt + nkq; ++t) {
-        const int col = (t < nvt ? vt0 + t : ktile(t - nvt)) * 8;  // first 16-byte piece of the tile
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(q_staged, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT));
+      for (int t = 0; ok && t < nvt + nkq; ++t) {
+        const uint8_t* from = qstage + t * kQTile + r * 128;
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 v = (col + i) * 8 < D ? __ldg(src + col + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = *reinterpret_cast<const uint4*>(from + ((i ^ (r & 7)) * 16));
           w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
         tmem_st32(lane_base + kQCol + t * 32, w);
