@@ -12,7 +12,6 @@ fused_forward, indexer_prolog, add_rmsnorm, prefix_mla_attn, accumulate_attn_wei
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 from typing import NamedTuple, Optional, Sequence, Tuple
 
@@ -406,17 +405,10 @@ def _there(t, index: int) -> None:
         raise ValueError(f"the problem's offsets are on {t.device}, the tensors on cuda:{index}")
 
 
-def _on_device(f):
-    """Runs a call with its first tensor's device current (nothing to do where it is already)."""
-    def call(*args, **kw):
-        for t in args:
-            if isinstance(t, torch.Tensor):
-                if t.is_cuda and t.get_device() != _current_device():
-                    with torch.cuda.device(t.get_device()):
-                        return f(*args, **kw)
-                break
+def _elsewhere(index: int, f, *args, **kw):
+    """A call whose tensors are on another device than the current one: made with that one current."""
+    with torch.cuda.device(index):
         return f(*args, **kw)
-    return functools.wraps(f)(call)
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -442,7 +434,6 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return step
 
 
-@_on_device
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 eps: float = 1e-6, quant: Optional[str] = None, want_y: Optional[bool] = None,
                 h=None, y=None, codes=None, scale=None):
@@ -466,6 +457,8 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
         raise ValueError(f"x has dtype {dtype}")
     if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least 1")
+    if index != _current_device():
+        return _elsewhere(index, add_rmsnorm, x, weight, residual, eps, quant, want_y, h, y, codes, scale)
     d = shape[-1]
     ld_x = _row_stride(x, "x")
     _want(weight, "weight", (dtype,), (d,), index)
@@ -516,11 +509,10 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
 
 
 def _ws_bytes(P: Problem, op: int) -> int:
-    """P's workspace size for an op on the current device, asked for once."""
-    key = (op, _current_device(), _abi.lib())
-    n = P._ws_sizes.get(key)
+    """P's workspace size for an op (on P's device, which is current), asked for once."""
+    n = P._ws_sizes.get(op)
     if n is None:
-        n = P._ws_sizes[key] = P.workspace_size(op)
+        n = P._ws_sizes[op] = P.workspace_size(op)
     return n
 
 
@@ -533,14 +525,12 @@ def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
     P describes the sequences behind the prefix.  The prefix is prefix_kv [prefix_len, D], or, in a
     paged cache, the pages prefix_table [>= ceil(prefix_len / page_size)] int32 of kv; without
     either there is none."""
-    return _prefix_mla_attn(kv, P, q, prefix_kv, prefix_table, prefix_len, out, lse, want_lse, ws)
-
-
-@_on_device
-def _prefix_mla_attn(kv, P, q, prefix_kv, prefix_table, prefix_len, out, lse, want_lse, ws):
     if not kv.is_cuda:
         raise ValueError("kv must be a CUDA tensor")
     index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
+    if index != _current_device():
+        return _elsewhere(index, prefix_mla_attn, P, q, kv, prefix_kv, prefix_table, prefix_len, out, lse,
+                          want_lse, ws)
     TQ, H, D = P.total_q, P.h, P.d
     _want(q, "q", dts, (TQ, H, D), index)
     _want(kv, "kv", dts, (P.cache_rows, D), index)
@@ -590,14 +580,11 @@ def accumulate_attn_weights(P: Problem, q, kv, idx, lse, acc, ws: Optional[Works
     """Add the attention weight every selected position received, summed over heads and queries,
     to acc [B, >= max_k_len] f32 in place (dsa_accumulate_attn_weights); returns acc.  idx and lse
     are those of sparse_mla_attn or fused_forward on the same q and kv."""
-    return _accumulate(kv, P, q, idx, lse, acc, ws)
-
-
-@_on_device
-def _accumulate(kv, P, q, idx, lse, acc, ws):
     if not kv.is_cuda:
         raise ValueError("kv must be a CUDA tensor")
     index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
+    if index != _current_device():
+        return _elsewhere(index, accumulate_attn_weights, P, q, kv, idx, lse, acc, ws)
     TQ, H, D = P.total_q, P.h, P.d
     _want(q, "q", dts, (TQ, H, D), index)
     _want(kv, "kv", dts, (P.cache_rows, D), index)
@@ -651,14 +638,13 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
     page size (the *_out tensors are then required; they may be the source's pool, on other pages).
     acc_out [B, >= budget] receives the kept positions' acc and zeros behind them up to column
     budget."""
-    return _evict(acc, P, int(budget), int(sink), int(recent), (kv, k_idx, k_scale),
-                  (kv_out, k_idx_out, k_scale_out), block_table_out, kept, cu_k_out, acc_out, ws)
-
-
-@_on_device
-def _evict(acc, P, budget, sink, recent, src, dst, table, kept, cu_k_out, acc_out, ws):
     if not acc.is_cuda:
         raise ValueError("acc must be a CUDA tensor")
+    if acc.get_device() != _current_device():
+        return _elsewhere(acc.get_device(), evict, P, acc, budget, sink, recent, kv, k_idx, k_scale, kv_out,
+                          k_idx_out, k_scale_out, block_table_out, kept, cu_k_out, acc_out, ws)
+    budget, sink, recent, table = int(budget), int(sink), int(recent), block_table_out
+    src, dst = (kv, k_idx, k_scale), (kv_out, k_idx_out, k_scale_out)
     if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
         raise ValueError(f"budget = {budget}, sink = {sink}, recent = {recent}: 1 <= budget and "
                          "sink + recent <= budget are needed")
