@@ -51,6 +51,7 @@ constexpr int kSmem = kQSmemTiles * kQTile + kTiles * kTile + kBarBytes + 1024;
 constexpr int kOCol = 0, kSCol = 256, kQCol = 384;
 constexpr float kRescaleLog2 = 8.0f;
 static_assert(kSmem <= 232448, "shared memory");
+static_assert(kM * (256 * 4 + 16) <= kTiles * kTile, "the output leaves through the key tiles");
 
 struct Params {
   PrefixArgs a;
@@ -547,12 +548,18 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
                                                a.status, DSA_FLAG_TIMEOUT))) { stop = true; break; }
         bool any = false;
         uint8_t* vt = vs + (g % kVSlots) * nvt * kTile;
-        for (int i = r; i < nvt * kN * 8; i += kM) {  // 16-byte pieces; swizzled order does not matter
-          const int key = (i >> 3) & (kN - 1);
-          if (key < lim0 && !((bad >> key) & 1)) continue;
-          uint4* at = reinterpret_cast<uint4*>(vt) + i;
-          uint4 v = *at;
-          if (finite8(v)) { *at = v; any = true; }
+        for (int i0 = r; i0 < nvt * kN * 8; i0 += 4 * kM) {  // 16-byte pieces, four loads in flight; a row of the
+          uint4 v[4];                                       // tile is a key, in whatever order its pieces are
+          bool look[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kM, key = (i >> 3) & (kN - 1);
+            look[j] = i < nvt * kN * 8 && (key >= lim0 || ((bad >> key) & 1));
+            if (look[j]) v[j] = reinterpret_cast<const uint4*>(vt)[i];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (look[j] && finite8(v[j])) { reinterpret_cast<uint4*>(vt)[i0 + j * kM] = v[j]; any = true; }
         }
         if (any) fence_proxy_async_smem();
         const uint64_t in = (lim >= kN ? ~0ull : (1ull << lim) - 1);
@@ -610,25 +617,28 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
                                                 a.status, DSA_FLAG_TIMEOUT));
     if (!stop) {
       tc_fence_after();
+      // O goes out through the key tiles (all of them have been multiplied): a thread writes its row there and
+      // sends it with one bulk copy.  Stored from registers, 16 bytes of 32 different rows at a time, the
+      // rows took 2.5 us.  Rows are 16 bytes more than their length apart, which spreads them over the banks.
       const bool live = r < it.rows;
       const float inv = split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      const bool f32 = split || a.out_dtype == DSA_F32;
+      const int row_bytes = ncol * (f32 ? 4 : 2);
+      uint8_t* mine = vs + r * (row_bytes + 16);
       for (int b = 0; b < (ncol + 31) / 32; ++b) {
         uint32_t o[32];
         __syncwarp();  // the load is the whole warp's
         tmem_ld32(lane_base + kOCol + 32 * b, o);
-        const int n = live ? min(32, ncol - 32 * b) : 0;  // 16 or 32 columns
-        const int64_t at = flat * a.d_c + vcol0 + 32 * b;
-        if (split || a.out_dtype == DSA_F32) {
-          float* dst = split ? a.part_o + (int64_t)it.piece * rows_all * a.d_c + at
-                             : static_cast<float*>(a.out) + at;
+        const int n = min(32, ncol - 32 * b);  // 16 or 32 columns
+        if (f32) {
+          float4* dst = reinterpret_cast<float4*>(mine) + 8 * b;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (4 * i < n)
-              reinterpret_cast<float4*>(dst)[i] =
-                  make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                              __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+              dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                   __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+          uint4* dst = reinterpret_cast<uint4*>(mine) + 4 * b;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (8 * i < n) {
@@ -641,10 +651,21 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
             }
         }
       }
+      fence_proxy_async_smem();  // our writes, seen by the bulk copy
+      if (live) {
+        const int64_t at = flat * a.d_c + vcol0;
+        void* dst = split ? static_cast<void*>(a.part_o + (int64_t)it.piece * rows_all * a.d_c + at)
+                    : f32 ? static_cast<void*>(static_cast<float*>(a.out) + at)
+                          : static_cast<void*>(static_cast<__nv_bfloat16*>(a.out) + at);
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         reinterpret_cast<uint64_t>(dst)), "r"(smem_u32(mine)), "r"(row_bytes)
+                     : "memory");
+      }
       if (live && it.half == 0) {
         if (split) a.part_ml[(int64_t)it.piece * rows_all + flat] = make_float2(m, l);
         else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
   tc_fence_before();
