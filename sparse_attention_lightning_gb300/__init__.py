@@ -75,6 +75,7 @@ class Problem:
             self.block_table.data_ptr() if self.page_size else None)
         self._ref = ctypes.byref(self.c)
         self._ws_sizes = {}
+        self._row_specs = None
 
     @classmethod
     def from_config(cls, cfg, cu_q: torch.Tensor, cu_k: torch.Tensor, sm_scale: float = 0.0,
@@ -413,13 +414,14 @@ def _elsewhere(index: int, f, *args, **kw):
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Row stride in elements of a tensor [..., d] whose rows are evenly spaced."""
-    d = t.shape[-1]
     if t.is_contiguous():
-        return d
-    if d > 1 and t.stride(-1) != 1:
+        return t.shape[-1]
+    shape, strides = t.shape, t.stride()
+    d = shape[-1]
+    if d > 1 and strides[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     step, n = None, 1
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(shape[-2::-1], strides[-2::-1]):
         if size == 1:
             continue
         if step is None:
@@ -662,22 +664,24 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
                              "positions")
         _want(table, "block_table_out", _I32, table.shape, index)
         max_pages, table_ptr = table.shape[1], table.data_ptr()
-    mx = P.idx_dtype == _abi.DSA_MXFP8_E4M3
-    d_idx = P.d_idx
-    if src[2] is not None and not mx and P.idx_dtype != _abi.DSA_FP8_E4M3:
+    specs = P._row_specs
+    if specs is None:  # of a row of each cache: name, dtypes, shape of the cache, shape of a row
+        mx, n = P.idx_dtype == _abi.DSA_MXFP8_E4M3, P.cache_rows
+        tails = ((P.d,), (P.d_idx,), (P.d_idx // 32,) if mx else ())
+        dts = (_TORCH_DT[P.kv_dtype], _CODES if mx else _TORCH_DT[P.idx_dtype], _U8 if mx else _F32)
+        specs = P._row_specs = tuple((name, dt, (n,) + tail, tail) for name, dt, tail in
+                                     zip(("kv", "k_idx", "k_scale"), dts, tails))
+    if k_scale is not None and P.idx_dtype not in (_abi.DSA_FP8_E4M3, _abi.DSA_MXFP8_E4M3):
         raise ValueError("k_scale goes with FP8 or MXFP8 index keys")
-    specs = (("kv", _TORCH_DT[P.kv_dtype], (P.d,)),
-             ("k_idx", _CODES if mx else _TORCH_DT[P.idx_dtype], (d_idx,)),
-             ("k_scale", _U8, (d_idx // 32,)) if mx else ("k_scale", _F32, ()))
     moved, ptrs, rows_out = [], [], None
-    for s, o, (name, dts, tail) in zip(src, dst, specs):
+    for s, o, (name, dts, whole, tail) in zip(src, dst, specs):
         if s is None:
             if o is not None:
                 raise ValueError(f"{name}_out needs {name}")
             moved.append(None)
             ptrs += (0, 0)
             continue
-        _want(s, name, dts, (P.cache_rows,) + tail, index)
+        _want(s, name, dts, whole, index)
         if o is None:
             if table is not None:
                 raise ValueError(f"a paged destination needs {name}_out")

@@ -424,14 +424,14 @@ PrefixArgs prefix_args(const dsa_problem* p, int prefix_len) {
 }
 
 // Pieces a row's keys are cut into, so that few rows still fill the SMs (three blocks fit one):
-// at least 128 keys a piece.  It depends on the rows alone where the keys' number is unknown
+// at least 64 keys a piece.  It depends on the rows alone where the keys' number is unknown
 // (prefix_len < 0: the most that any prefix asks for), so the workspace does not grow with the prefix.
 int prefix_simt_splits(const dsa_problem* p, int64_t prefix_len) {
   const int64_t blocks = (int64_t)p->num_seqs * prefix_simt_blocks(p->max_q_len, p->h);
   if (blocks == 0) return 1;
   int64_t s = 3 * (int64_t)num_sms() / blocks;
   if (prefix_len >= 0) {
-    const int64_t most = (prefix_len + p->max_k_len + 127) / 128;
+    const int64_t most = (prefix_len + p->max_k_len + 63) / 64;
     if (s > most) s = most;
   }
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);

@@ -9,6 +9,12 @@
 // One CTA = 16 of a sequence's (token, head) rows × one share of their keys: every row attends
 // over the same latent keys, so a key loaded to shared memory serves 16 rows.  This is the
 // generic fp32/bf16 path (all dims); it computes in fp32.
+//
+// Bound by latency (few rows) and by shared-memory loads.  16 threads take a row: two keys each for the
+// logits, four columns in 64 each for the values, both by 16-byte loads (a row of keys is four floats longer
+// than its columns, which spreads it over the banks); max and sum stay within the 16, so a chunk of 32
+// keys needs two block barriers.  One thread a dot, scalar loads and the softmax through shared memory took
+// 45 us for 3 sequences of up to 40 tokens x 8 heads over 256 + 130 keys of 80 columns; this way it is 16.
 #include "prefix_attn.cuh"
 
 namespace dsa {
@@ -17,21 +23,42 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 16;
 
-template <typename TK, typename TO, int KC>
+// 16 bytes of keys or queries as floats.
+__device__ __forceinline__ void widen16(const uint4& v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void widen16(const uint4& v, float (&f)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+template <typename TK>
+__device__ __forceinline__ void copy16(float* dst, const TK* src) {
+  constexpr int V = 16 / (int)sizeof(TK);
+  float f[V];
+  widen16(src ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u), f);
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    *reinterpret_cast<float4*>(dst + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+}
+
+// KC keys a step (16 or 32); NJ: 64-column groups of the values (d_c <= 64 · NJ).
+template <typename TK, typename TO, int KC, int NJ>
 __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int nblk) {
   griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
-  extern __shared__ float smem[];
-  const int D = a.d_c + a.d_rope, DP = D + 1, dc = a.d_c, H = a.h;
+  extern __shared__ __align__(16) float smem[];
+  constexpr int V = 16 / (int)sizeof(TK);
+  const int D = a.d_c + a.d_rope, DP = D + 4, dc = a.d_c, H = a.h;
   const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk, split = blockIdx.y;
   const int tid = threadIdx.x;
   float* qs = smem;                 // [kRows][D]
-  float* ks = qs + kRows * D;       // [KC][D + 1]
-  float* acc = ks + KC * DP;        // [kRows][dc]
-  float* P = acc + kRows * dc;      // [kRows][KC]
-  float* m_s = P + kRows * KC;      // [kRows]
-  float* l_s = m_s + kRows;
-  float* al_s = l_s + kRows;
-  __shared__ uint32_t okmask;
+  float* ks = qs + kRows * D;       // [KC][D + 4]
+  float* P = ks + KC * DP;          // [kRows][KC]
+  __shared__ const TK* keys[KC];    // null: masked
 
   SeqInfo s;
   if (!prefix_seq(a, b, s)) return;
@@ -45,86 +72,112 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
   const int nch = (nvis + KC - 1) / KC;
   const int c0 = (int)((int64_t)nch * split / a.splits), c1 = (int)((int64_t)nch * (split + 1) / a.splits);
 
-  const TK* q = static_cast<const TK*>(a.q) + flat0 * D;
-  for (int i = tid; i < R * D; i += kThreads) qs[i] = to_f32(q[i]);
-  for (int i = tid; i < R * dc; i += kThreads) acc[i] = 0.f;
-  if (tid < kRows) { m_s[tid] = -INFINITY; l_s[tid] = 0.f; }
+  // a thread's row (rows past the block repeat its last) and place among the row's 16 threads
+  const int row = tid >> 4, place = tid & 15;
+  const int r = min(row, R - 1), vis = visible(r);
+  const TK* q = static_cast<const TK*>(a.q) + (flat0 + r) * D;
+  for (int i = place * V; i < D; i += 16 * V) copy16(qs + row * D + i, q + i);
+  float m = -INFINITY, l = 0.f;
+  float4 acc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 
   for (int c = c0; c < c1; ++c) {
     const int x0 = c * KC, cn = min(KC, nvis - x0);
     __syncthreads();
-    if (tid < 32) {
+    if (tid < KC) {
+      const void* k = tid < cn ? prefix_key(a, s.b, s.k0, x0 + tid) : nullptr;
       // a key on a page outside the cache is skipped (and reported)
-      const bool in = tid < cn;
-      const bool ok = in && prefix_key(a, s.b, s.k0, x0 + tid) != nullptr;
-      if (in && !ok) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
-      const unsigned bal = __ballot_sync(0xffffffffu, ok);
-      if (tid == 0) okmask = bal;
-    }
-    for (int i = tid; i < KC * D; i += kThreads) {
-      const int k = i / D, col = i - k * D;
-      const TK* src = k < cn ? static_cast<const TK*>(prefix_key(a, s.b, s.k0, x0 + k)) : nullptr;
-      ks[k * DP + col] = src ? to_f32(src[col]) : 0.f;
+      if (tid < cn && !k) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+      keys[tid] = static_cast<const TK*>(k);
     }
     __syncthreads();
-    const uint32_t ok = okmask;
-    for (int i = tid; i < kRows * KC; i += kThreads) {
-      const int r = i / KC, k = i - r * KC;
-      if (r >= R) continue;
-      const float* qr = qs + r * D;
-      const float* kr = ks + k * DP;
-      float dot = 0.f;
-      for (int e = 0; e < D; ++e) dot = fmaf(qr[e], kr[e], dot);
-      P[i] = ((ok >> k) & 1u) && x0 + k < visible(r) ? dot * a.scale_log2 : -INFINITY;
+    {
+      // 256 / KC threads load a key
+      constexpr int kT = kThreads / KC;
+      const int k = tid / kT;
+      const TK* src = keys[k];
+      for (int i = (tid % kT) * V; i < D; i += kT * V) copy16(ks + k * DP + i, src ? src + i : nullptr);
     }
     __syncthreads();
-    for (int r = tid >> 5; r < R; r += kThreads / 32) {  // a warp per row, KC <= 32
-      const int lane = tid & 31;
-      const bool in = lane < KC && ((ok >> lane) & 1u) && x0 + lane < visible(r);
-      const float v = in ? P[r * KC + lane] : -INFINITY;
-      float mx = v;
+    float dot[KC / 16];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float m_old = m_s[r], m_new = fmaxf(m_old, mx);
-      const float ref = m_new == -INFINITY ? 0.f : m_new;  // nothing visible so far
-      const float e = in ? exp2f(v - ref) : 0.f;
-      if (lane < KC) P[r * KC + lane] = e;
-      float sum = e;
+    for (int j = 0; j < KC / 16; ++j) dot[j] = 0.f;
+    const float* qr = qs + row * D;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(qr + e);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) {
-        const float alpha = exp2f(m_old - ref);
-        al_s[r] = alpha;
-        l_s[r] = l_s[r] * alpha + sum;
-        m_s[r] = m_new;
+      for (int j = 0; j < KC / 16; ++j) {
+        const float4 y = *reinterpret_cast<const float4*>(ks + (place + 16 * j) * DP + e);
+        dot[j] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[j]))));
       }
     }
-    __syncthreads();
-    for (int i = tid; i < R * dc; i += kThreads) {
-      const int r = i / dc, col = i - r * dc;
-      const float* pr = P + r * KC;
-      // only keys the row sees: a masked key's values (whatever they are) add nothing
-      const int n = min(cn, visible(r) - x0);
-      float v = acc[i] * al_s[r];
-      for (int k = 0; k < n; ++k) v = fmaf(pr[k], ks[k * DP + col], v);
-      acc[i] = v;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < KC / 16; ++j) {
+      const int k = place + 16 * j;
+      dot[j] = keys[k] && x0 + k < vis ? dot[j] * a.scale_log2 : -INFINITY;
+      mx = fmaxf(mx, dot[j]);
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float m_new = fmaxf(m, mx), ref = m_new == -INFINITY ? 0.f : m_new;  // -inf: nothing visible so far
+    float sum = 0.f;
+    __syncwarp();  // the last chunk's P has been read
+#pragma unroll
+    for (int j = 0; j < KC / 16; ++j) {
+      const float e = exp2f(dot[j] - ref);
+      P[row * KC + place + 16 * j] = e;
+      sum += e;
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float alpha = exp2f(m - ref);
+    l = fmaf(l, alpha, sum);
+    m = m_new;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      acc[j].x *= alpha; acc[j].y *= alpha; acc[j].z *= alpha; acc[j].w *= alpha;
+    }
+    // only keys the row sees: a masked key's values (whatever they are) add nothing
+    const int n = min(cn, vis - x0);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float pk = P[row * KC + k];
+      const float* v = ks + k * DP + place * 4;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (place * 4 + 64 * j < dc) {
+          const float4 y = *reinterpret_cast<const float4*>(v + 64 * j);
+          acc[j].x = fmaf(pk, y.x, acc[j].x); acc[j].y = fmaf(pk, y.y, acc[j].y);
+          acc[j].z = fmaf(pk, y.z, acc[j].z); acc[j].w = fmaf(pk, y.w, acc[j].w);
+        }
     }
   }
-  __syncthreads();
-  if (a.splits == 1) {
-    TO* o = static_cast<TO*>(a.out) + flat0 * dc;
-    for (int i = tid; i < R * dc; i += kThreads) {
-      const float l = l_s[i / dc];
-      store_f32(o + i, l == 0.f ? 0.f : acc[i] / l);
+  if (row >= R) return;
+  const int64_t rows = (int64_t)a.seqs.total_q * H, flat = flat0 + row;
+  const bool last = a.splits == 1;
+  const float inv = last ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int col = place * 4 + 64 * j;
+    if (col >= dc) continue;
+    const float f[4] = {acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv};
+    if (last) {
+      TO* o = static_cast<TO*>(a.out) + flat * dc + col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_f32(o + i, f[i]);
+    } else {
+      *reinterpret_cast<float4*>(a.part_o + ((int64_t)split * rows + flat) * dc + col) =
+          make_float4(f[0], f[1], f[2], f[3]);
     }
-    if (a.lse && tid < R)
-      a.lse[flat0 + tid] = l_s[tid] == 0.f ? -INFINITY : (m_s[tid] + log2f(l_s[tid])) * kLn2;
-    return;
   }
-  const int64_t rows = (int64_t)a.seqs.total_q * H;
-  float* o = a.part_o + ((int64_t)split * rows + flat0) * dc;
-  for (int i = tid; i < R * dc; i += kThreads) o[i] = acc[i];
-  if (tid < R) a.part_ml[(int64_t)split * rows + flat0 + tid] = make_float2(m_s[tid], l_s[tid]);
+  if (place == 0) {
+    if (!last) a.part_ml[(int64_t)split * rows + flat] = make_float2(m, l);
+    else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
 }
 
 // out = Σ_j w_j O_j / Σ_j w_j l_j, w_j = 2^(m_j - max m) over the row's pieces, O added in piece order.  A block a
@@ -203,26 +256,27 @@ __global__ void __launch_bounds__(128, 8) prefix_merge_kernel(PrefixArgs a, int 
   if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
-template <typename TK, typename TO, int KC>
+template <typename TK, typename TO, int KC, int NJ>
 int launch_typed(const PrefixArgs& a, cudaStream_t stream) {
   const int D = a.d_c + a.d_rope;
-  const size_t smem = sizeof(float) * ((size_t)kRows * D + (size_t)KC * (D + 1) +
-                                       (size_t)kRows * a.d_c + kRows * KC + 3 * kRows);
-  auto kern = prefix_simt_kernel<TK, TO, KC>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return check_launch("prefix_simt: smem attribute");
+  const int smem = (int)sizeof(float) * (kRows * D + KC * (D + 4) + kRows * KC);
+  auto kern = prefix_simt_kernel<TK, TO, KC, NJ>;
+  static int allowed[64];
+  const int rc = smem <= 40960 ? DSA_OK : allow_smem(kern, smem, allowed, "prefix_simt: smem attribute");
+  if (rc != DSA_OK) return rc;
   const int nblk = prefix_simt_blocks(a.max_q_len, a.h);
   dim3 grid((unsigned)(a.seqs.B * nblk), (unsigned)a.splits);
   DSA_LAUNCH("prefix_simt", stream, kern<<<grid, kThreads, smem, stream>>>(a, nblk));
   return check_launch("prefix_simt");
 }
 
+// 32 keys a step (16 where rows are wider than 1024: they would not fit the shared memory).
 template <typename TK, typename TO>
 int launch_dims(const PrefixArgs& a, cudaStream_t stream) {
-  // 32 keys a step where they fit the shared memory beside the widest rows, else 16
-  return a.d_c + a.d_rope <= 640 ? launch_typed<TK, TO, 32>(a, stream)
-                                 : launch_typed<TK, TO, 16>(a, stream);
+  if (a.d_c + a.d_rope > 1024) return launch_typed<TK, TO, 16, 16>(a, stream);
+  return a.d_c <= 64    ? launch_typed<TK, TO, 32, 1>(a, stream)
+         : a.d_c <= 512 ? launch_typed<TK, TO, 32, 8>(a, stream)
+                        : launch_typed<TK, TO, 32, 16>(a, stream);
 }
 
 }  // namespace
