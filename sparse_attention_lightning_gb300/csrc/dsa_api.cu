@@ -643,7 +643,7 @@ int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* pr
   a.lse = lse;
   a.status = static_cast<uint32_t*>(ws);
   if (prefix_tc_eligible(a)) {
-    carve_prefix(p, prefix_tc_pieces(a), ws, &a);
+    carve_prefix(p, prefix_tc_most_pieces(a), ws, &a);
     return launch_prefix_tc(a, static_cast<cudaStream_t>(stream));
   }
   a.splits = prefix_simt_splits(p, prefix_len);

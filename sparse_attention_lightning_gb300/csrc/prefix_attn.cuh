@@ -57,18 +57,26 @@ __device__ __forceinline__ const void* prefix_key(const PrefixArgs& a, int b, in
   return row < 0 ? nullptr : base + row * bytes;
 }
 
+// Which pieces of part_o and part_ml a row has.
+constexpr int kMaxLines = 192;
+struct PrefixMerge {
+  int pieces;        // of every row (table = 0); otherwise the number of piece slots
+  int table = 0;     // pieces go by line: the block of 128 rows that attended together
+  int fblk, nblk;    // blocks over the prefix alone (0: none; one key axis), blocks of a sequence
+  int base;          // slot of a sequence block's first piece
+  uint8_t np[kMaxLines];  // pieces of a line, the prefix's blocks first
+};
+
 inline int prefix_simt_blocks(int max_q_len, int h) {
   return (int)(((int64_t)max_q_len * h + 15) / 16);
 }
 
-// tcgen05 path (bf16, 64 <= D <= 576, d_c <= 512): the pieces it cuts rows into for a prefix length,
-// and for any (the workspace's size).
+// tcgen05 path (bf16, 64 <= D <= 576, d_c <= 512): the most pieces it cuts rows into (the workspace's size).
 bool prefix_tc_eligible(const PrefixArgs& a);
-int prefix_tc_pieces(const PrefixArgs& a);
 int prefix_tc_most_pieces(const PrefixArgs& a);
 int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream);
 
 int launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream);
-int launch_prefix_merge(const PrefixArgs& a, int pieces, cudaStream_t stream);
+int launch_prefix_merge(const PrefixArgs& a, const PrefixMerge& m, cudaStream_t stream);
 
 }  // namespace dsa

@@ -187,19 +187,27 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
 // and its O is not read.
 constexpr int kMaxPieces = 128;
 template <typename TO>
-__global__ void __launch_bounds__(128, 8) prefix_merge_kernel(PrefixArgs a, int pieces) {
+__global__ void __launch_bounds__(128, 8) prefix_merge_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixMerge mg) {
   const int64_t rows = (int64_t)a.seqs.total_q * a.h, row = blockIdx.x;
   const int lane = threadIdx.x & 31;
   RowInfo ri;
   SeqInfo si;  // the pieces of a row whose sequence is inconsistent were not written
   const bool ok = query_row_info(a.seqs, (int)(row / a.h), ri, a.status) && prefix_seq(a, ri.b, si);
+  // its pieces: slots [0, n0) and [base, base + n1)
+  int n0 = mg.pieces, n1 = 0, pieces = mg.pieces;
+  if (mg.table && ok) {
+    const int line = mg.fblk + ri.b * mg.nblk + (int)((row - (int64_t)si.q0 * a.h) >> 7);
+    n0 = mg.fblk ? mg.np[row >> 7] : 0;
+    n1 = mg.np[line];
+    pieces = mg.base + n1;
+  }
   griddep_wait();
-  if (!ok) return;
+  if (!ok || (mg.table && !mg.fblk && n1 == 1)) return;  // (a line that was not cut wrote its output)
   float m[kMaxPieces / 32], w[kMaxPieces / 32], M = -INFINITY, l = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxPieces / 32; ++i) {
     const int j = i * 32 + lane;
-    const float2 v = j < pieces ? __ldcg(a.part_ml + j * rows + row) : make_float2(-INFINITY, 0.f);
+    const float2 v = j < n0 || (j >= mg.base && j < mg.base + n1) ? __ldcg(a.part_ml + j * rows + row) : make_float2(-INFINITY, 0.f);
     m[i] = v.x;
     w[i] = v.y;
     if (v.y != 0.f) M = fmaxf(M, v.x);
@@ -288,14 +296,16 @@ int launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream) {
                     : (of ? launch_dims<__nv_bfloat16, float>(a, stream)
                           : launch_dims<__nv_bfloat16, __nv_bfloat16>(a, stream));
   if (rc != DSA_OK || a.splits == 1) return rc;
-  return launch_prefix_merge(a, a.splits, stream);
+  PrefixMerge m{};
+  m.pieces = m.base = a.splits;
+  return launch_prefix_merge(a, m, stream);
 }
 
-int launch_prefix_merge(const PrefixArgs& a, int pieces, cudaStream_t stream) {
+int launch_prefix_merge(const PrefixArgs& a, const PrefixMerge& m, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.seqs.total_q * a.h;
   auto kern = a.out_dtype == DSA_F32 ? prefix_merge_kernel<float> : prefix_merge_kernel<__nv_bfloat16>;
   cudaError_t e = cudaSuccess;
-  DSA_LAUNCH("prefix_merge", stream, e = launch_pdl(kern, dim3((unsigned)rows), dim3(128), 0, stream, a, pieces));
+  DSA_LAUNCH("prefix_merge", stream, e = launch_pdl(kern, dim3((unsigned)rows), dim3(128), 0, stream, a, m));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "prefix_merge: %s", cudaGetErrorString(e));
   return check_launch("prefix_merge");
 }

@@ -61,10 +61,24 @@ struct Params {
   int halves;      // value column halves
   int prefix_items;
   int chunk_rows;  // cache rows a tile is loaded in
+  int nseg;        // cuts: segments (0: every line in equal pieces, sp or ss)
+  int ns;          // cuts: length of a line of a sequence's block, as the segments count it
+};
+
+// One CTA's (with halves, two CTAs') part of a line: the key chunks [a, b) of a block of rows.  Lines: the
+// blocks of all rows over the prefix (fblk of them), then the sequences' blocks.
+struct Seg {
+  uint32_t a, b;
+  uint16_t line, piece;
+};
+constexpr int kMaxSegs = 288;
+struct Cuts {
+  Seg seg[kMaxSegs];
 };
 
 struct Item {
   int half, piece, b;        // b < 0: prefix only
+  bool split;                // the rows have other pieces: partial outputs
   int64_t row0;              // first flat (token, head) row
   int rows;
   int c0, c1;                // chunks [c0, c1) of the item's key axis
@@ -74,28 +88,40 @@ struct Item {
 };
 
 // False: nothing to do (a block past its sequence's rows, an inconsistent sequence).
-__device__ __forceinline__ bool item_at(const Params& p, int i, Item& it) {
+__device__ __forceinline__ bool item_at(const Params& p, const Cuts& cuts, int i, Item& it) {
   const int pch = (p.a.prefix_len + kN - 1) / kN;
-  if (i < p.prefix_items) {
-    it.half = i % p.halves;
-    i /= p.halves;
-    it.row0 = (int64_t)(i % p.fblk) * kM;
-    it.piece = i / p.fblk;
+  it.half = i % p.halves;
+  i /= p.halves;
+  int line, split = 0;  // line: block, counted over the prefix's, then the sequences'
+  Seg sg{};
+  if (p.nseg) {
+    sg = cuts.seg[i];
+    line = sg.line;
+    it.piece = sg.piece;
+  } else if (i < p.prefix_items) {
+    line = i % p.fblk;
+    it.piece = split = i / p.fblk;
+  } else {
+    i -= p.prefix_items;
+    const int blocks = p.a.seqs.B * p.nblk;
+    line = p.fblk + i % blocks;
+    split = i / blocks;
+    it.piece = split + (p.fblk ? p.sp : 0);
+  }
+  if (line < p.fblk) {
+    it.split = true;
+    it.row0 = (int64_t)line * kM;
     it.b = -1;
     it.rows = (int)min((int64_t)kM, (int64_t)p.a.seqs.total_q * p.a.h - it.row0);
     it.ncp = pch;
-    it.c0 = (int)((int64_t)pch * it.piece / p.sp);
-    it.c1 = (int)((int64_t)pch * (it.piece + 1) / p.sp);
+    it.c0 = p.nseg ? (int)sg.a : (int)((int64_t)pch * split / p.sp);
+    it.c1 = p.nseg ? (int)sg.b : (int)((int64_t)pch * (split + 1) / p.sp);
     it.k0 = it.pos0 = it.hoff = 0;
     return true;
   }
-  i -= p.prefix_items;
-  it.half = i % p.halves;
-  i /= p.halves;
-  const int blocks = p.a.seqs.B * p.nblk;
-  const int blk = i % blocks;
-  const int split = i / blocks;
+  const int blk = line - p.fblk;
   it.b = blk / p.nblk;
+  it.split = p.fblk || (p.nseg ? sg.a > 0 || (int)sg.b < p.ns : p.ss > 1);
   SeqInfo s;
   if (!prefix_seq(p.a, it.b, s)) return false;
   const int64_t r0 = (int64_t)(blk - it.b * p.nblk) * kM, nrow = (int64_t)s.T * p.a.h;
@@ -108,9 +134,8 @@ __device__ __forceinline__ bool item_at(const Params& p, int i, Item& it) {
   it.hoff = (int)(r0 % p.a.h);
   const int last = s.L - s.T + (int)((r0 + it.rows - 1) / p.a.h);
   const int n = it.ncp + last / kN + 1;
-  it.c0 = (int)((int64_t)n * split / p.ss);
-  it.c1 = (int)((int64_t)n * (split + 1) / p.ss);
-  it.piece = (p.fblk ? p.sp : 0) + split;
+  it.c0 = p.nseg ? (int)((int64_t)n * sg.a / p.ns) : (int)((int64_t)n * split / p.ss);
+  it.c1 = p.nseg ? (int)((int64_t)n * sg.b / p.ns) : (int)((int64_t)n * (split + 1) / p.ss);
   return true;
 }
 
@@ -177,14 +202,15 @@ struct Maps {
 // chunk where the tensor pipe needs 1,980 (36 MMAs of N = 64 and 4 of N = 256).
 template <bool FIXED>
 __global__ void __launch_bounds__(kThreads, 1)
-prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps,
+                 const __grid_constant__ Cuts cuts) {
   griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   Item it;
-  if (!item_at(p, blockIdx.x, it)) return;
+  if (!item_at(p, cuts, blockIdx.x, it)) return;
   const PrefixArgs& a = p.a;
   const int64_t rows_all = (int64_t)a.seqs.total_q * a.h;
   const int nch = it.c1 - it.c0;
-  const bool split = (p.fblk ? p.sp + p.ss : p.ss) > 1;
+  const bool split = it.split;
   if (nch == 0) {  // a piece without keys
     if (split && it.half == 0)
       for (int i = threadIdx.x; i < it.rows; i += kThreads)
@@ -676,10 +702,13 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   }
 }
 
-// How the rows and their keys are cut (all from the descriptor's sizes and the prefix's length).
+// How the rows and their keys are cut (all from the descriptor's sizes and the prefix's length): into
+// equal pieces (sp, ss), or into segments.
 struct Plan {
   int nblk, fblk, sp, ss, halves;
-  int pieces() const { return fblk ? sp + ss : ss; }
+  int nseg = 0, ns = 0;
+  PrefixMerge merge;
+  Cuts cuts;
 };
 
 // Most pieces a row is cut into: about four waves of CTAs.
@@ -693,59 +722,158 @@ size_t partial_bytes(const PrefixArgs& a, int pieces) {
   return pieces > 1 ? (size_t)pieces * a.seqs.total_q * a.h * (a.d_c * 4 + 8) : 0;
 }
 
-Plan blocks_of(const PrefixArgs& a) {
-  Plan pl{};
+void blocks_of(const PrefixArgs& a, Plan& pl) {
   pl.halves = (a.d_c + 255) / 256;
   pl.nblk = (int)(((int64_t)a.max_q_len * a.h + kM - 1) / kM);
   pl.fblk = (int)(((int64_t)a.seqs.total_q * a.h + kM - 1) / kM);
-  return pl;
+}
+
+constexpr double kStart = 4;   // a CTA's start and end, in chunks
+constexpr int kShort = 3;      // chunks of the shortest segment (but for a line's own length)
+
+// Cut the lines, laid end to end, into one share a machine (an SM, or one a half) of at most C chunks' time.
+// False if they do not fit.  `round` counts a machine's segments.
+bool cut(int fblk, int pch, int lines, int ns, int machines, double C, Seg* seg, uint8_t* round, uint8_t* np,
+         int& nseg) {
+  int m = 0, r = 0, n = 0;
+  double used = 0;
+  for (int line = 0; line < lines; ++line) {
+    const int len = line < fblk ? pch : ns;
+    int at = 0, k = 0;
+    while (at < len) {
+      int take = (int)(C - used - kStart);
+      if (take >= len - at) take = len - at;
+      else if (len - at - take < kShort) take = len - at - kShort;
+      if (take < kShort && take < len - at) {
+        if (r == 0 || ++m >= machines) return false;
+        used = 0;
+        r = 0;
+        continue;
+      }
+      if (n >= kMaxSegs || k >= 64) return false;
+      seg[n] = Seg{(uint32_t)at, (uint32_t)(at + take), (uint16_t)line, (uint16_t)k++};
+      round[n++] = (uint8_t)r++;
+      used += take + kStart;
+      at += take;
+    }
+    np[line] = (uint8_t)k;
+  }
+  nseg = n;
+  return true;
+}
+
+// Segments of equal shares, in launch order: every machine's first, then the others, longest first (a
+// machine that ends its first segment early then takes what its own share had left, or as much).  Returns
+// the time in chunks, or 1e30.
+double cut_equal(const PrefixArgs& a, int fblk, Plan& pl) {
+  const int pch = (a.prefix_len + kN - 1) / kN;
+  const int sch = (int)(((int64_t)a.seqs.total_k / a.seqs.B + kN - 1) / kN);
+  const int64_t lines = fblk + (int64_t)a.seqs.B * pl.nblk;
+  const int ns = (fblk ? 0 : pch) + (sch > 0 ? sch : 1), machines = num_sms() / pl.halves;
+  if (lines > kMaxLines) return 1e30;
+  const double total = (double)fblk * (pch + kStart) + (double)(lines - fblk) * (ns + kStart);
+  if (total < 8.0 * machines) return 1e30;  // little to balance
+  Seg seg[kMaxSegs];
+  uint8_t round[kMaxSegs];
+  int n = 0;
+  double C = total / machines + kStart * 0.8;
+  bool fits = false;
+  for (int i = 0; i < 16 && !fits; ++i, C *= 1.015)
+    fits = cut(fblk, pch, (int)lines, ns, machines, C, seg, round, pl.merge.np, n);
+  // segments of a sequence's block are the same parts of its own length: with very different lengths, equal
+  // pieces in several waves even out better
+  if (!fits || (double)a.seqs.max_k_len / kN - sch > 0.2 * C) return 1e30;
+  int most[2] = {0, 0}, order[kMaxSegs], k = 0;
+  for (int i = 0; i < (int)lines; ++i) {
+    int& x = most[i < fblk ? 0 : 1];
+    if (pl.merge.np[i] > x) x = pl.merge.np[i];
+  }
+  if (most[0] + most[1] > prefix_tc_most_pieces(a)) return 1e30;
+  for (int i = 0; i < n; ++i)
+    if (round[i] == 0) order[k++] = i;
+  const int first = k;
+  for (int i = 0; i < n; ++i) {
+    if (round[i] == 0) continue;
+    int j = k++;
+    for (; j > first && seg[order[j - 1]].b - seg[order[j - 1]].a < seg[i].b - seg[i].a; --j) order[j] = order[j - 1];
+    order[j] = i;
+  }
+  for (int i = 0; i < n; ++i) {
+    Seg& t = pl.cuts.seg[i];
+    t = seg[order[i]];
+    if (t.line >= fblk) t.piece = (uint16_t)(t.piece + most[0]);
+  }
+  pl.nseg = n;
+  pl.ns = ns;
+  pl.merge.table = 1;
+  pl.merge.fblk = fblk;
+  pl.merge.nblk = pl.nblk;
+  pl.merge.base = most[0];
+  pl.merge.pieces = most[0] + most[1];
+  return C;
 }
 
 // Time model in units of a chunk: a CTA's start and end cost about four chunks, a wave ends
 // with its longest CTA, and merging costs a launch (about three chunks) and the partial outputs' traffic.
-Plan plan_of(const PrefixArgs& a) {
-  Plan pl = blocks_of(a);
+void plan_of(const PrefixArgs& a, Plan& out) {
+  blocks_of(a, out);
+  const int halves = out.halves, fblk = out.fblk;
   const int sms = num_sms();
-  const int64_t seq_blocks = (int64_t)a.seqs.B * pl.nblk;
+  const int64_t seq_blocks = (int64_t)a.seqs.B * out.nblk;
   const double pch = (a.prefix_len + kN - 1) / kN;
   const double sch = 0.5 + (double)a.seqs.total_k / a.seqs.B / kN;  // a sequence's own chunks, on average
   const double row_cost = (double)a.seqs.total_q * a.h * a.d_c * 8 / 4e6;  // partials of a piece: us at 4 TB/s
-  const double start = 4;
   double best = 1e30;
-  Plan out = pl;
   // one key axis
-  for (int s = 1; s <= most_pieces(seq_blocks, pl.halves); ++s) {
+  for (int s = 1; s <= most_pieces(seq_blocks, halves); ++s) {
     const double len = (pch + sch) / s;
     if (s > 1 && (len < 2 || partial_bytes(a, s) > kMostPartial)) break;
-    const int64_t items = seq_blocks * pl.halves * s;
+    const int64_t items = seq_blocks * halves * s;
     const double waves = (double)((items + sms - 1) / sms);
-    const double cost = waves * (ceil(len) + start) + (s > 1 ? 3 + s * row_cost : 0);
+    const double cost = waves * (ceil(len) + kStart) + (s > 1 ? 3 + s * row_cost : 0);
     if (cost < best) {
       best = cost;
       out.fblk = 0; out.sp = 0; out.ss = s;
     }
   }
   // the prefix by blocks of all rows, the sequences' own keys apart
-  if (a.prefix_len > 0 && pl.fblk < seq_blocks) {
-    for (int s = 1; s <= most_pieces(pl.fblk, pl.halves); ++s) {
-      const double len = pch / s;
-      if (s > 1 && len < 2) break;
-      int ss = (int)(sch / (len > 2 ? len : 2) + 0.5);
-      const int most = most_pieces(seq_blocks, pl.halves);
-      ss = ss < 1 ? 1 : ss > most ? most : ss;
-      if (partial_bytes(a, s + ss) > kMostPartial) break;
-      const double work = pl.halves * (pl.fblk * (pch + s * start) + seq_blocks * (sch + ss * start));
-      const double longest = ceil(len) + start;
-      const double items = (double)pl.halves * pl.fblk * s;
-      const double waves = ceil(items / sms) * longest;
-      const double cost = (work / sms > waves ? work / sms + 0.3 * longest : waves) + 3 + (s + ss) * row_cost;
-      if (cost < best) {
-        best = cost;
-        out.fblk = pl.fblk; out.sp = s; out.ss = ss;
-      }
+  const bool apart = a.prefix_len > 0 && fblk < seq_blocks;
+  for (int s = 1; apart && s <= most_pieces(fblk, halves); ++s) {
+    const double len = pch / s;
+    if (s > 1 && len < 2) break;
+    int ss = (int)(sch / (len > 2 ? len : 2) + 0.5);
+    const int most = most_pieces(seq_blocks, halves);
+    ss = ss < 1 ? 1 : ss > most ? most : ss;
+    if (partial_bytes(a, s + ss) > kMostPartial) break;
+    const double work = halves * (fblk * (pch + s * kStart) + seq_blocks * (sch + ss * kStart));
+    const double longest = ceil(len) + kStart;
+    const double items = (double)halves * fblk * s;
+    const double waves = ceil(items / sms) * longest;
+    const double cost = (work / sms > waves ? work / sms + 0.3 * longest : waves) + 3 + (s + ss) * row_cost;
+    if (cost < best) {
+      best = cost;
+      out.fblk = fblk; out.sp = s; out.ss = ss;
     }
   }
-  return out;
+  out.merge.table = 0;
+  out.merge.base = 0;
+  out.merge.pieces = out.fblk ? out.sp + out.ss : out.ss;
+  // equal shares, cut anywhere
+  for (int f = 0; f <= (apart ? 1 : 0); ++f) {
+    Plan t;
+    t.halves = halves;
+    t.nblk = out.nblk;
+    const double time = cut_equal(a, f ? fblk : 0, t);
+    if (time >= 1e30) continue;
+    const double lines = (double)seq_blocks + (f ? fblk : 0);
+    const double cost = time + 3 + (f ? 2 : 1) * (t.nseg / lines) * row_cost;
+    if (cost < best) {
+      best = cost;
+      t.fblk = f ? fblk : 0;
+      t.sp = t.ss = 0;
+      out = t;
+    }
+  }
 }
 
 }  // namespace
@@ -757,7 +885,8 @@ bool prefix_tc_eligible(const PrefixArgs& a) {
 
 // Pieces the workspace has room for, whatever the prefix's length.
 int prefix_tc_most_pieces(const PrefixArgs& a) {
-  const Plan pl = blocks_of(a);
+  Plan pl;
+  blocks_of(a, pl);
   const int64_t seq_blocks = (int64_t)a.seqs.B * pl.nblk;
   if (pl.fblk == 0 || seq_blocks == 0) return 1;
   const int one = most_pieces(seq_blocks, pl.halves);
@@ -767,10 +896,9 @@ int prefix_tc_most_pieces(const PrefixArgs& a) {
   return n;
 }
 
-int prefix_tc_pieces(const PrefixArgs& a) { return plan_of(a).pieces(); }
-
 int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
-  const Plan pl = plan_of(a);
+  Plan pl;
+  plan_of(a, pl);
   Params p{};
   p.a = a;
   p.nblk = pl.nblk;
@@ -778,9 +906,12 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   p.sp = pl.sp;
   p.ss = pl.ss;
   p.halves = pl.halves;
-  p.prefix_items = pl.fblk * pl.sp * pl.halves;
+  p.nseg = pl.nseg;
+  p.ns = pl.ns;
+  p.prefix_items = pl.fblk * pl.sp;
   p.chunk_rows = a.seqs.paged() && a.seqs.page_size < kN ? a.seqs.page_size : kN;
-  const int64_t items = p.prefix_items + (int64_t)a.seqs.B * pl.nblk * pl.ss * pl.halves;
+  const int64_t items =
+      (pl.nseg ? pl.nseg : p.prefix_items + (int64_t)a.seqs.B * pl.nblk * pl.ss) * pl.halves;
   if (items > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "prefix attention: grid too large");
   const uint64_t D = a.d_c + a.d_rope, keys = (uint64_t)a.seqs.cache_rows();
   const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -802,10 +933,10 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   static int allowed[2][64];
   rc = allow_smem(kern, kSmem, allowed[fixed], "prefix_tc: smem attribute");
   if (rc != DSA_OK) return rc;
-  DSA_LAUNCH("prefix_tc", stream, kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p, m));
+  DSA_LAUNCH("prefix_tc", stream, kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p, m, pl.cuts));
   rc = check_launch("prefix_tc");
-  if (rc != DSA_OK || pl.pieces() == 1) return rc;
-  return launch_prefix_merge(a, pl.pieces(), stream);
+  if (rc != DSA_OK || pl.merge.pieces == 1) return rc;
+  return launch_prefix_merge(a, pl.merge, stream);
 }
 
 }  // namespace dsa
