@@ -1,7 +1,7 @@
 // Accumulated attention weight: what its kernels and its host code share.
 #pragma once
 
-#include "dsa_internal.cuh"
+#include "cache_ops.cuh"
 
 namespace dsa {
 

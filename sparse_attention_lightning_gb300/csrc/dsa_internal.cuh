@@ -26,9 +26,6 @@ constexpr int kRowSyncWord = 256;
 constexpr int kPieceWord = kRowSyncWord + 2 * 128 * 8;
 constexpr int kPieceRows = (int)(kStatusBytes / 4 - kPieceWord) / 2;
 
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
-
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Sequence layout as the kernels see it.
@@ -151,25 +148,7 @@ int check_launch(const char* what);
 int make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
                  uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
                  bool swizzle = true);
-// 16-bit rows as [tiles][rows][64 columns] (rows of tiles · 64 elements): a box is box_tiles tiles of
-// box_rows rows, each tile as make_tmap_2d's box of 64 columns would store it.
-int make_tmap_tiles(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t tiles,
-                    uint64_t rows, uint64_t row_bytes, uint32_t box_tiles, uint32_t box_rows);
 int num_sms();
-
-// Allow `kern` `bytes` of dynamic shared memory; asked of the runtime once for a kernel (its slot:
-// one static array a kernel), device and size.
-template <typename K>
-inline int allow_smem(K kern, int bytes, int (&slot)[64], const char* what) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const bool keep = dev >= 0 && dev < 64;
-  if (keep && slot[dev] >= bytes) return DSA_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return check_launch(what);
-  if (keep) slot[dev] = bytes;
-  return DSA_OK;
-}
 
 #define DSA_LAUNCH(name, stream, ...)   \
   do {                                  \

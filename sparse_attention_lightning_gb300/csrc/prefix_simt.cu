@@ -182,12 +182,13 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
 
 // out = Σ_j w_j O_j / Σ_j w_j l_j, w_j = 2^(m_j - max m) over the row's pieces, O added in piece order.  A block a
 // row, four columns a thread.  All it costs is latency: the row is looked up before the pieces' grid has
-// ended, each lane takes two pieces' (max, sum), and eight pieces' outputs are loaded before the first is
-// added.  (One load after another, for 9 pieces of 64 rows: 12 us; so: 4.)  A piece without keys has l = 0
-// and its O is not read.
+// ended, each lane takes up to four pieces' (max, sum), four pieces' outputs are loaded before the first is
+// added, and 16 blocks fit an SM (with eight loads in flight and 8 blocks, 4096 rows took 2 us more).  One load
+// after another, 9 pieces of 64 rows took 12 us; so they take 4.  A piece without keys has l = 0 and its O is
+// not read.
 constexpr int kMaxPieces = 128;
 template <typename TO>
-__global__ void __launch_bounds__(128, 8) prefix_merge_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixMerge mg) {
+__global__ void __launch_bounds__(128, 16) prefix_merge_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixMerge mg) {
   const int64_t rows = (int64_t)a.seqs.total_q * a.h, row = blockIdx.x;
   const int lane = threadIdx.x & 31;
   RowInfo ri;
@@ -234,18 +235,18 @@ __global__ void __launch_bounds__(128, 8) prefix_merge_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < kMaxPieces / 32; ++i) {
       if (i * 32 >= pieces) break;
-      for (int j0 = 0; j0 < 32 && i * 32 + j0 < pieces; j0 += 8) {
-        float4 x[8];
-        float f[8];
+      for (int j0 = 0; j0 < 32 && i * 32 + j0 < pieces; j0 += 4) {
+        float4 x[4];
+        float f[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           f[j] = __shfl_sync(0xffffffffu, w[i], j0 + j);  // 0 past the last piece
           x[j] = in && f[j] != 0.f
                      ? __ldcg(reinterpret_cast<const float4*>(po + (i * 32 + j0 + j) * stride + c))
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           s.x = fmaf(f[j], x[j].x, s.x); s.y = fmaf(f[j], x[j].y, s.y);
           s.z = fmaf(f[j], x[j].z, s.z); s.w = fmaf(f[j], x[j].w, s.w);
         }
