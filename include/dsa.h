@@ -335,7 +335,8 @@ int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* pr
  * For every query row t of sequence b and every valid entry i of idx[t, :]:
  *   acc[b, idx[t,i]] += Σ_h exp(sm_scale · q[t,h,:]·kv[row of idx[t,i], :] − lse[t,h])
  * with idx and lse those of dsa_sparse_mla_attn on the same q and kv.  Entries that attention
- * skips add nothing (an entry outside [0, pos(t)] or on a page outside the cache sets
+ * skips add nothing (rows of a sequence whose cu_q/cu_k are inconsistent, or that has more than max_q_len
+ * queries, set DSA_FLAG_BAD_SEQS; an entry outside [0, pos(t)] or on a page outside the cache sets
  * DSA_FLAG_BAD_INDEX); neither do heads whose lse is -inf; a repeated entry adds as often
  * as it appears.  The result does not depend on the order of the additions: the same call gives the
  * same bytes.
@@ -369,7 +370,7 @@ int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void*
  * the call reads: a packed *_out that overlaps its source is refused; with pages, source and
  * destination may be one pool, in which the destination's pages must not be the sources'.
  * acc [num_seqs, ld_acc >= max_k_len] f32; acc_out [num_seqs, ld_acc_out >= budget] f32 or NULL,
- * not overlapping acc; 1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
+ * not overlapping acc; cu_k_out not overlapping p's cu_k; 1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
  */
 int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t budget, int32_t sink,
               int32_t recent, int32_t* kept, int32_t* cu_k_out, float* acc_out, int64_t ld_acc_out,

@@ -32,6 +32,10 @@ __global__ void __launch_bounds__(kThreads) attn_weights_simt_kernel(WeightArgs 
   __shared__ int pos_s[kKeys], row_s[kKeys];
   RowInfo r;
   if (!query_row_info(a.seqs, t, r, a.status)) return;
+  if (__ldg(a.seqs.cu_q + r.b + 1) - __ldg(a.seqs.cu_q + r.b) > a.max_q_len) {
+    atomicOr(a.status, DSA_FLAG_BAD_SEQS);  // the order of additions and fx_scale rest on max_q_len
+    return;
+  }
   const TK* q = static_cast<const TK*>(a.q) + (int64_t)t * a.h * D;
   const TK* kv = static_cast<const TK*>(a.kv);
   const int hh = tid / kKeys, kk = tid % kKeys;

@@ -7,7 +7,7 @@ namespace dsa {
 
 struct WeightArgs {
   Seqs seqs;
-  int h, d, top_k, kv_dtype;
+  int h, d, top_k, kv_dtype, max_q_len;
   float scale_log2;     // softmax scale · log2(e)
   const void* q;
   const void* kv;

@@ -77,7 +77,8 @@ __device__ __forceinline__ bool piece_at(const Params& p, int k, Piece& pc) {
 }
 
 // query_row_info by a whole warp: a 32-way search over cu_q (one round of loads up to 32 sequences).
-__device__ __forceinline__ bool warp_row_info(const Seqs& s, int t, int lane, RowInfo& r, uint32_t* status) {
+__device__ __forceinline__ bool warp_row_info(const WeightArgs& a, int t, int lane, RowInfo& r) {
+  const Seqs& s = a.seqs;
   int lo = 0, hi = s.B;  // the last b with cu_q[b] <= t is in [lo, hi)
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -90,8 +91,9 @@ __device__ __forceinline__ bool warp_row_info(const Seqs& s, int t, int lane, Ro
   const int q0 = __ldg(s.cu_q + lo), q1 = __ldg(s.cu_q + lo + 1);
   const int k0 = __ldg(s.cu_k + lo), k1 = __ldg(s.cu_k + lo + 1);
   const int T = q1 - q0, L = k1 - k0;
-  if (!(t >= q0 && t < q1 && T <= L && k0 >= 0 && k1 <= s.total_k && L <= s.max_k_len && q1 <= s.total_q)) {
-    atomicOr(status, DSA_FLAG_BAD_SEQS);
+  if (!(t >= q0 && t < q1 && T <= L && k0 >= 0 && k1 <= s.total_k && L <= s.max_k_len && q1 <= s.total_q &&
+        T <= a.max_q_len)) {  // (the order of additions and fx_scale rest on max_q_len)
+    atomicOr(a.status, DSA_FLAG_BAD_SEQS);
     return false;
   }
   r = RowInfo{lo, L - T + (t - q0), k0, L};
@@ -167,7 +169,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
         return lane < 16 && i < a.top_k ? __ldg(a.idx + (int64_t)pc.t * a.top_k + i) : -1;
       };
       int v0 = load_idx(pc.c0), v1 = load_idx(pc.c0 + 1);
-      if (!warp_row_info(a.seqs, pc.t, lane, ri, a.status)) continue;
+      if (!warp_row_info(a, pc.t, lane, ri)) continue;
       // the query block, 64 heads a chunk of the ring
       for (int c = 0; c < qchunks && !stop; ++c, ++n) {
         if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
@@ -241,7 +243,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
     Piece pc;
     for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
       RowInfo ri;
-      if (!warp_row_info(a.seqs, pc.t, lane, ri, a.status)) continue;
+      if (!warp_row_info(a, pc.t, lane, ri)) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(q_full, qn & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) break;
       ++qn;
       for (int c = 0; c < qchunks; ++c) {  // the query has left the ring for tensor memory
@@ -290,7 +292,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
     Piece pc;
     for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
       RowInfo ri;
-      if (!warp_row_info(a.seqs, pc.t, lane, ri, a.status)) continue;
+      if (!warp_row_info(a, pc.t, lane, ri)) continue;
       // this warp's 32 heads of the query block, from the ring to tensor memory (the previous piece's
       // logits are complete: its last chunk has been read)
       const int qc = quarter >> 1;

@@ -656,6 +656,8 @@ int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void*
                                 void* ws, size_t ws_bytes, void* stream) {
   DSA_TRY(check_problem(p, false, true));
   const bool none = p->total_q == 0;
+  if (!none && p->max_q_len < 1)
+    return set_error(DSA_ERR_INVALID_ARG, "max_q_len = %d with total_q = %d", p->max_q_len, p->total_q);
   DSA_TRY(check_ptr(q, "q", none));
   DSA_TRY(check_ptr(kv, "kv"));
   DSA_TRY(check_ptr(idx, "idx", none));
@@ -668,6 +670,7 @@ int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void*
   WeightArgs a{};
   a.seqs = seqs_of(p);
   a.h = p->h;
+  a.max_q_len = p->max_q_len;
   a.d = p->d_c + p->d_rope;
   a.top_k = p->top_k;
   a.kv_dtype = p->kv_dtype;
@@ -705,6 +708,9 @@ int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t bu
     if (!need[i] || ((uintptr_t)need[i] & 3u) != 0)
       return set_error(DSA_ERR_INVALID_ARG, "%s is NULL or not 4-byte aligned", names[i]);
   if (ld_acc < p->max_k_len) return set_error(DSA_ERR_INVALID_ARG, "ld_acc < max_k_len");
+  const int64_t offsets = ((int64_t)p->num_seqs + 1) * 4;
+  if (overlap(cu_k_out, offsets, p->cu_k, offsets))
+    return set_error(DSA_ERR_INVALID_ARG, "cu_k_out overlaps cu_k");
   if (acc_out) {
     if (((uintptr_t)acc_out & 3u) != 0 || ld_acc_out < budget)
       return set_error(DSA_ERR_INVALID_ARG, "acc_out is not 4-byte aligned or ld_acc_out < budget");

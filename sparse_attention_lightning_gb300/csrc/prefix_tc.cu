@@ -300,12 +300,13 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         const int x0 = (pre ? c : c - it.ncp) * kN;
         const CUtensorMap* map = pre ? &maps.pre : &maps.key;
         const CUtensorMap* map4 = pre ? &maps.pre4 : &maps.key4;
-        const bool paged = a.seqs.paged();
+        const bool paged = a.seqs.paged() && !(pre && a.prefix_kv);  // a paged cache's prefix may be packed
         int run[kN / 16];
         uint64_t bad = 0;
         const int cr = p.chunk_rows, nrun = kN / cr;
         if (!paged) {
-          run[0] = pre ? x0 : it.k0 + x0;
+#pragma unroll
+          for (int j = 0; j < kN / 16; ++j) run[j] = (pre ? x0 : it.k0 + x0) + j * cr;
         } else {
           const int sh = __ffs(a.seqs.page_size) - 1;
           const int pages = pre ? (a.prefix_len + a.seqs.page_size - 1) >> sh : a.seqs.max_pages;

@@ -70,6 +70,7 @@ def test_evict_argument_checks():
     assert call(p, table=A, mp=1, np_=1 << 27) == unsup
     assert call(p, table=A, mp=1, np_=4, kvo=5 * A + 160) == bad    # neither the same pool nor apart
     assert call(rows=-1) == bad
+    assert call(cu=8192 + 8) == bad                                # the offsets it reads
     assert call(ws=None) == _abi.DSA_ERR_WORKSPACE and call(wsb=64) == _abi.DSA_ERR_WORKSPACE
 
 
@@ -193,6 +194,20 @@ def test_weights_repeats_padding_and_empty_heads():
         ref, tol = s.reference(lse, before)
         bad = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, s.idx.cuda(), lse, before.clone(), ws=ws)
         assert ws.status() == _abi.DSA_FLAG_BAD_INDEX
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weights_inconsistent_offsets_are_reported(dtype):
+    import sparse_attention_lightning_gb300 as dsa
+    s = Weights([2, 2, 1], [40, 50, 9], 16, 64, 16, 64, dtype, seed=5)
+    lse = s.attention()
+    ref = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, s.idx.cuda(), lse, torch.zeros(3, 50).cuda())
+    ws = dsa.Workspace()
+    s.prob.cu_q.copy_(torch.tensor([0, 2, 5, 5], dtype=torch.int32))  # 3 queries, max_q_len = 2
+    got = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, s.idx.cuda(), lse, torch.zeros(3, 50).cuda(), ws=ws)
+    assert ws.status() == _abi.DSA_FLAG_BAD_SEQS
+    assert torch.equal(got[0], ref[0]) and (got[1:] == 0).all()
 
 
 @pytest.mark.gpu

@@ -310,6 +310,45 @@ def test_streams_graphs_and_refusals():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+@pytest.mark.parametrize("dtype,dims", [(BF, FULL), (BF, SMALL), (F32, SMALL)])
+def test_packed_prefix_of_a_paged_cache(dtype, dims, page):
+    s = Setup([1, 5, 1], [40, 300, 3], 16, P=333, dtype=dtype, page=page, seed=12, **dims)
+    s.prefix = dict(prefix_kv=s.pre.cuda())
+    s.check(*s.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_lens,k_lens,h,P", [
+    ([1] * 20, [50 + 7 * i for i in range(20)], 128, 4100),  # one key axis, lines cut anywhere
+    ([3] * 60, [20] * 60, 20, 4000),                         # blocks over the prefix, and the sequences'
+    ([40, 1], [40, 700], 128, 6000),                         # a prefill chunk beside a decode row
+    ([0, 200, 0, 1], [5, 333, 1, 64], 128, 3000),            # many blocks of one sequence
+])
+def test_shares_cut_anywhere(q_lens, k_lens, h, P):
+    """Enough work that every SM gets an equal share of the laid-out lines."""
+    s = Setup(q_lens, k_lens, h, P=P, dtype=BF, seed=h + P, spread=2.0, **FULL)
+    out, lse = s.run()
+    n = sum(q_lens)
+    s.check(out, lse, rows=set(range(0, n, max(1, n // 12))) | {n - 1})
+    again, lse2 = s.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+def test_a_longer_sequence_than_max_q_len_is_reported():
+    import sparse_attention_lightning_gb300 as dsa
+    for dtype, h in ((BF, 16), (F32, 8)):
+        s = Setup([2, 2], [30, 30], h, P=40, dtype=dtype, seed=13, **SMALL)
+        out0, lse0 = s.run()
+        ws = dsa.Workspace()
+        out, lse = torch.full_like(out0, 7.0), torch.full_like(lse0, 7.0)
+        s.prob.cu_q.copy_(torch.tensor([0, 1, 4], dtype=torch.int32))  # T_1 = 3, max_q_len = 2
+        s.run(out=out, lse=lse, ws=ws)
+        assert ws.status() == _abi.DSA_FLAG_BAD_SEQS and (out[1:] == 7.0).all() and (lse[1:] == 7.0).all()
+
+
+@pytest.mark.gpu
 def test_prefix_len_takes_part_of_the_rows():
     s = Setup([1, 2], [3, 4], 16, P=200, dtype=BF, seed=11, **FULL)
     out, lse = s.run(prefix_len=77)
