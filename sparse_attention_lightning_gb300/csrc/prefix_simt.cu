@@ -182,13 +182,13 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
 
 // out = Σ_j w_j O_j / Σ_j w_j l_j, w_j = 2^(m_j - max m) over the row's pieces, O added in piece order.  A block a
 // row, four columns a thread.  All it costs is latency: the row is looked up before the pieces' grid has
-// ended, each lane takes up to four pieces' (max, sum), four pieces' outputs are loaded before the first is
-// added, and 16 blocks fit an SM (with eight loads in flight and 8 blocks, 4096 rows took 2 us more).  One load
-// after another, 9 pieces of 64 rows took 12 us; so they take 4.  A piece without keys has l = 0 and its O is
-// not read.
+// ended, each lane takes up to four pieces' (max, sum), and U pieces' outputs are loaded before the first is
+// added: 8 where all blocks run at once, 4 (and twice the blocks on an SM) for more rows: 4096 rows of 2 to 4 pieces
+// take 2 us less that way, 64 rows of 9 pieces 1 us more.  One load after another, those 64 rows took 12 us;
+// so they take 4.  A piece without keys has l = 0 and its O is not read.
 constexpr int kMaxPieces = 128;
-template <typename TO>
-__global__ void __launch_bounds__(128, 16) prefix_merge_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixMerge mg) {
+template <typename TO, int U>
+__global__ void __launch_bounds__(128, 64 / U) prefix_merge_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixMerge mg) {
   const int64_t rows = (int64_t)a.seqs.total_q * a.h, row = blockIdx.x;
   const int lane = threadIdx.x & 31;
   RowInfo ri;
@@ -235,18 +235,18 @@ __global__ void __launch_bounds__(128, 16) prefix_merge_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < kMaxPieces / 32; ++i) {
       if (i * 32 >= pieces) break;
-      for (int j0 = 0; j0 < 32 && i * 32 + j0 < pieces; j0 += 4) {
-        float4 x[4];
-        float f[4];
+      for (int j0 = 0; j0 < 32 && i * 32 + j0 < pieces; j0 += U) {
+        float4 x[U];
+        float f[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < U; ++j) {
           f[j] = __shfl_sync(0xffffffffu, w[i], j0 + j);  // 0 past the last piece
           x[j] = in && f[j] != 0.f
                      ? __ldcg(reinterpret_cast<const float4*>(po + (i * 32 + j0 + j) * stride + c))
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < U; ++j) {
           s.x = fmaf(f[j], x[j].x, s.x); s.y = fmaf(f[j], x[j].y, s.y);
           s.z = fmaf(f[j], x[j].z, s.z); s.w = fmaf(f[j], x[j].w, s.w);
         }
@@ -304,7 +304,10 @@ int launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream) {
 
 int launch_prefix_merge(const PrefixArgs& a, const PrefixMerge& m, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.seqs.total_q * a.h;
-  auto kern = a.out_dtype == DSA_F32 ? prefix_merge_kernel<float> : prefix_merge_kernel<__nv_bfloat16>;
+  const bool few = rows <= 8 * (int64_t)num_sms();
+  auto kern = a.out_dtype == DSA_F32
+                  ? (few ? prefix_merge_kernel<float, 8> : prefix_merge_kernel<float, 4>)
+                  : (few ? prefix_merge_kernel<__nv_bfloat16, 8> : prefix_merge_kernel<__nv_bfloat16, 4>);
   cudaError_t e = cudaSuccess;
   DSA_LAUNCH("prefix_merge", stream, e = launch_pdl(kern, dim3((unsigned)rows), dim3(128), 0, stream, a, m));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "prefix_merge: %s", cudaGetErrorString(e));
