@@ -196,14 +196,18 @@ struct Maps {
   CUtensorMap pre4, key4;  // the same as [tiles][rows][64], box 4 x chunk_rows x 64
 };
 
-// FIXED: 512 + 64 columns (4 V tiles and 5 K tiles in both halves), everything unrolled and the tiles
-// loaded four at a time; otherwise any widths.  One thread issues all MMAs and one all copies, and
-// their scalar code is what counts: with the counts known only at run time the issue took 4,600 clocks a
-// chunk where the tensor pipe needs 1,980 (36 MMAs of N = 64 and 4 of N = 256).
-template <bool FIXED>
+// NK > 0: 512 value columns and NK K tiles in both halves (d_rope = 64: 5, d_rope = 0: 4), everything unrolled, V
+// tiles loaded four at a time, a barrier a K tile.  NK = 0: any widths, a barrier a chunk's K tiles.  One thread issues
+// all MMAs and one all copies, and their scalar code is what counts: with the counts known only at run time
+// (and divided by, for a slot and a phase) the issue took 4,600 clocks a chunk of 512 + 64 columns where
+// the tensor pipe needs 1,980 (36 MMAs of N = 64 and 4 of N = 256); unrolled it takes 2,170.  Without
+// divisions the general form takes 2,530 for 512 + 0 columns (NK = 4: 2,130), 1,950 for 256 + 32, 1,430 for 128 + 64
+// and 1,340 for 64 + 16, the last two bound by softmax; a barrier a K tile there cost 100 to 700 clocks more.
+template <int NK>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps,
                  const __grid_constant__ Cuts cuts) {
+  constexpr bool FIXED = NK > 0;
   griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   Item it;
   if (!item_at(p, cuts, blockIdx.x, it)) return;
@@ -225,7 +229,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   uint64_t* bars = reinterpret_cast<uint64_t*>(vs + kTiles * kTile);
   uint64_t* v_full = bars;            // [3]
   uint64_t* v_empty = bars + 3;       // [3]
-  uint64_t* k_full = bars + 6;        // [3][2] the two parts of a chunk's K tiles; FIXED: [5] a K tile
+  uint64_t* k_full = bars + 6;        // [3] a chunk's K tiles; NK > 0: [NK] a K tile
   uint64_t* k_empty = bars + 12;
   uint64_t* s_full = bars + 18;       // [2] logits of the buffer's chunk complete
   uint64_t* p_full = bars + 20;       // [2] its 4 softmax warps have written P
@@ -244,8 +248,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   const int vcol0 = it.half * 256;
   const int ncol = FIXED ? 256 : min(256, a.d_c - vcol0);         // this CTA's output columns (a multiple of 16)
   const int vt0 = it.half * 4, nvt = FIXED ? 4 : (ncol + 63) / 64;
-  const int nkt = FIXED ? 5 : ntile - nvt;          // at most 8
-  const int nka = FIXED ? 4 : (nkt + 1) / 2;        // the K tiles' first part
+  const int nkt = FIXED ? NK : ntile - nvt;          // at most 8
   // 3 chunks of V tiles always fit beside one of K tiles (3·4 + 5, or nvt < 4: 3·3 + 8 of 18)
   const int kslots = FIXED ? 1 : nkt ? min(kKSlots, (kTiles - kVSlots * nvt) / nkt) : 0;
   uint8_t* ks = vs + kVSlots * nvt * kTile;         // [kslots][nkt][64][128 B]
@@ -253,7 +256,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
   // memory at tile j; K tile j after them while there is room (4 tiles), then in shared memory.
   auto ktile = [&](int j) { return j < vt0 ? j : j + nvt; };
   const int nkq = FIXED ? 0 : min(nkt, kQTmemTiles - nvt);  // K tiles whose query columns are in tensor memory
-  // The query tiles for tensor memory come by TMA into key tiles that no chunk uses yet (FIXED: those of
+  // The query tiles for tensor memory come by TMA into key tiles that no chunk uses yet (NK > 0: those of
   // chunks 1 and 2; otherwise the first, and no key is loaded before they have left).
   uint8_t* qstage = vs + (FIXED ? 4 * kTile : 0);
 
@@ -290,7 +293,8 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         for (int j = 0; j < nqs; ++j)
           tma_load_2d(qs + j * kQTile, &maps.q, q_full, ktile(nkq + j) * 64, (int)it.row0);
       }
-      int g = 0, kn = 0;  // chunks whose V tiles, half-chunks (FIXED: tiles) whose K tiles have been issued
+      int g = 0, kn = 0;  // chunks whose V tiles, chunks (NK > 0: tiles) whose K tiles have been issued
+      int kslot = 0, kphase = 0;
       auto stage_free = [&]() { return mbar_wait(qt_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT); };
       const int stop_at = FIXED || stage_free() ? nch : 0;
       for (; g < stop_at; ++g) {
@@ -343,25 +347,21 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         // K tiles first: the MMAs start with them
         bool stop = false;
         if constexpr (FIXED) {
-          for (int j = 0; j < 5; ++j) {
+          for (int j = 0; j < NK; ++j) {
             if (!mbar_wait(&k_empty[j], (g & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) { stop = true; break; }
             mbar_arrive_expect_tx(&k_full[j], kTile);
             load(ks + j * kTile, &k_full[j], ktile(j));
             ++kn;
           }
           if (g == 1 && !stop) stop = !stage_free();
-        } else
-        for (int h = 0; h < 2; ++h) {
-          const int j0 = h ? nka : 0, j1 = h ? nkt : nka;
-          if (j0 == j1) continue;
-          const int slot = g % kslots, bar = slot * 2 + h;
-          if (!mbar_wait(&k_empty[bar], ((g / kslots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
-            stop = true;
-            break;
+        } else if (nkt) {
+          stop = !mbar_wait(&k_empty[kslot], kphase ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+          if (!stop) {
+            mbar_arrive_expect_tx(&k_full[kslot], (uint32_t)(nkt * kTile));
+            for (int j = 0; j < nkt; ++j) load(ks + (kslot * nkt + j) * kTile, &k_full[kslot], ktile(j));
+            ++kn;
+            if (++kslot == kslots) { kslot = 0; kphase ^= 1; }
           }
-          mbar_arrive_expect_tx(&k_full[bar], (uint32_t)((j1 - j0) * kTile));
-          for (int j = j0; j < j1; ++j) load(ks + (slot * nkt + j) * kTile, &k_full[bar], ktile(j));
-          kn = 2 * g + h + 1;
         }
         if (stop || !mbar_wait(&v_empty[vslot], ((g / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
           break;
@@ -379,12 +379,9 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
       for (int i = max(0, g - kVSlots); i < g; ++i)
         mbar_wait_drain(&v_full[i % kVSlots], (i / kVSlots) & 1);
       if constexpr (FIXED) {
-        for (int i = max(0, kn - 5); i < kn; ++i) mbar_wait_drain(&k_full[i % 5], (i / 5) & 1);
-      } else
-      for (int i = max(0, kn - 2 * kslots); i < kn; ++i) {
-        const int c = i >> 1, h = i & 1;
-        if (h && nka == nkt) continue;
-        mbar_wait_drain(&k_full[(c % kslots) * 2 + h], (c / kslots) & 1);
+        for (int i = max(0, kn - NK); i < kn; ++i) mbar_wait_drain(&k_full[i % NK], (i / NK) & 1);
+      } else {
+        for (int i = max(0, kn - kslots); i < kn; ++i) mbar_wait_drain(&k_full[i % kslots], (i / kslots) & 1);
       }
     }
   } else if (warp == 1) {
@@ -400,38 +397,6 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
       if (!stop && nkt > nkq) stop = !mbar_wait(q_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
       tc_fence_after();
       const uint64_t qd = sdesc_sw128(q0, 16, 1024);
-      const bool full = D % 64 == 0;  // every tile has 4 K-steps
-      // the logits' K-steps of one tile: A = tile qt of the query in tensor memory, or (qt >= 4) tile
-      // qt - 4 of it in shared memory
-      auto qk_tile = [&](uint32_t d, int qt, int t, uint32_t tile, bool first) {
-        const int steps = full ? 4 : min(4, (D - t * 64) / 16);
-        const uint64_t b0 = sdesc_sw128(tile, 16, 1024);
-        if (qt < kQTmemTiles) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < steps)
-              mma_bf16_ts(d, tmem + kQCol + qt * 32 + i * 8, b0 + (uint64_t)(i * 2), idesc_s,
-                          first && i == 0 ? 0u : 1u);
-        } else {
-          const uint64_t a0 = qd + (uint64_t)((qt - kQTmemTiles) * (kQTile >> 4));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < steps)
-              mma_bf16(d, a0 + (uint64_t)(i * 2), b0 + (uint64_t)(i * 2), idesc_s, first && i == 0 ? 0u : 1u);
-        }
-      };
-      auto pv = [&](int g) -> bool {
-        if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) return false;
-        tc_fence_after();
-        const uint64_t vd = sdesc_sw128(v0 + (g % kVSlots) * nvt * kTile, kTile, 1024);
-        const uint32_t pa = tmem + kSCol + (g & 1) * kN;
-#pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk)
-          mma_bf16_ts(tmem + kOCol, pa + kk * 8, vd + (uint64_t)(kk * 128), idesc_pv, (g > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&v_empty[g % kVSlots]);
-        mma_commit(&pv_done[g & 1]);
-        return true;
-      };
       if constexpr (FIXED) {
         const uint64_t kd = sdesc_sw128(k0, 16, 1024);
         int vslot = 0, vphase = 0;           // of chunk g
@@ -455,7 +420,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
           const uint32_t d = tmem + kSCol + (g & 1) * kN;
           // a barrier a tile: each is refilled while the others and the V tiles are multiplied
 #pragma unroll
-          for (int j = 0; j < 5; ++j) {
+          for (int j = 0; j < NK; ++j) {
             if (!mbar_wait(&k_full[j], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) { stop = true; break; }
             tc_fence_after();
 #pragma unroll
@@ -486,37 +451,76 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
           if (g == nch - 1 && !pv_fixed(g)) stop = true;
         }
       } else {
-      for (int g = 0; g < nch && !stop; ++g) {
-        const int kslot = nkt ? g % kslots : 0;
-        // the buffer's last P (chunk g - 2) has been read
-        if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g - 2) >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
-          break;
-        const uint32_t d = tmem + kSCol + (g & 1) * kN;
-        const uint32_t kb = k0 + kslot * nkt * kTile;
-        for (int h = 0; h < 2; ++h) {
-          const int j0 = h ? nka : 0, j1 = h ? nkt : nka;
-          if (j0 == j1) continue;
-          const int bar = kslot * 2 + h;
-          if (!mbar_wait(&k_full[bar], (g / kslots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
-            stop = true;
-            break;
+        // The logits' K-steps of one tile: A = tile qt of the query in tensor memory, or (qt >= 4) tile qt - 4 of
+        // it in shared memory; the last tile may have fewer than four steps.
+        const int tail = D % 64 / 16;
+        uint32_t acc = 0;
+        auto qk_tile = [&](uint32_t d, int qt, int t, uint64_t b0) {
+          const uint64_t a0 = qd + (uint64_t)((qt - kQTmemTiles) * (kQTile >> 4));
+          const uint32_t at = tmem + kQCol + qt * 32;
+          if (tail == 0 || t + 1 < ntile) {
+            if (qt < kQTmemTiles) {
+              mma_bf16_ts(d, at, b0, idesc_s, acc);
+#pragma unroll
+              for (int i = 1; i < 4; ++i) mma_bf16_ts(d, at + i * 8, b0 + (uint64_t)(i * 2), idesc_s, 1u);
+            } else {
+              mma_bf16(d, a0, b0, idesc_s, acc);
+#pragma unroll
+              for (int i = 1; i < 4; ++i) mma_bf16(d, a0 + (uint64_t)(i * 2), b0 + (uint64_t)(i * 2), idesc_s, 1u);
+            }
+          } else {
+            for (int i = 0; i < tail; ++i) {
+              if (qt < kQTmemTiles) mma_bf16_ts(d, at + i * 8, b0 + (uint64_t)(i * 2), idesc_s, i ? 1u : acc);
+              else mma_bf16(d, a0 + (uint64_t)(i * 2), b0 + (uint64_t)(i * 2), idesc_s, i ? 1u : acc);
+            }
           }
+          acc = 1;
+        };
+        const uint64_t kd = sdesc_sw128(k0, 16, 1024), vd = sdesc_sw128(v0, 16, 1024);
+        const uint64_t pvd = sdesc_sw128(v0, kTile, 1024);
+        int kslot = 0, kphase = 0, vslot = 0, vphase = 0, pslot = 0;  // pslot: V slot of chunk g - 1
+        auto pv = [&](int g) -> bool {
+          if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) return false;
           tc_fence_after();
-          for (int j = j0; j < j1; ++j)
-            qk_tile(d, j < nkq ? nvt + j : kQTmemTiles + j - nkq, ktile(j), kb + j * kTile, j == 0);
-          mma_commit(&k_empty[bar]);
+          const uint64_t b0 = pvd + (uint64_t)(pslot * nvt * (kTile >> 4));
+          const uint32_t pa = tmem + kSCol + (g & 1) * kN;
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_bf16_ts(tmem + kOCol, pa + kk * 8, b0 + (uint64_t)(kk * 128), idesc_pv, (g > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&v_empty[pslot]);
+          mma_commit(&pv_done[g & 1]);
+          return true;
+        };
+        // P·V waits for softmax (~800 clocks after its logits): with few column tiles the next logits come whole
+        // before it, or softmax would wait for them in turn (64 + 16 columns: 1,535 clocks a chunk with
+        // P·V in their middle, 1,340 so)
+        const int mid = ntile > 5 ? nvt / 2 : nvt;
+        for (int g = 0; g < nch && !stop; ++g) {
+          // the buffer's last P (chunk g - 2) has been read
+          if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
+            break;
+          const uint32_t d = tmem + kSCol + (g & 1) * kN;
+          acc = 0;
+          if (nkt) {
+            if (!mbar_wait(&k_full[kslot], kphase, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+            tc_fence_after();
+            uint64_t b0 = kd + (uint64_t)(kslot * nkt * (kTile >> 4));
+            for (int j = 0; j < nkt; ++j, b0 += kTile >> 4)
+              qk_tile(d, j < nkq ? nvt + j : kQTmemTiles + j - nkq, ktile(j), b0);
+            mma_commit(&k_empty[kslot]);
+            if (++kslot == kslots) { kslot = 0; kphase ^= 1; }
+          }
+          if (!mbar_wait(&v_full[vslot], vphase, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+          tc_fence_after();
+          uint64_t b0 = vd + (uint64_t)(vslot * nvt * (kTile >> 4));
+          for (int t = 0; t < mid; ++t, b0 += kTile >> 4) qk_tile(d, t, vt0 + t, b0);
+          if (g > 0 && !pv(g - 1)) { stop = true; break; }
+          for (int t = mid; t < nvt; ++t, b0 += kTile >> 4) qk_tile(d, t, vt0 + t, b0);
+          mma_commit(&s_full[g & 1]);
+          pslot = vslot;
+          if (++vslot == kVSlots) { vslot = 0; vphase ^= 1; }
+          if (g == nch - 1 && !pv(g)) stop = true;
         }
-        if (stop || !mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
-          break;
-        tc_fence_after();
-        const uint32_t vb = v0 + (g % kVSlots) * nvt * kTile;
-        const int mid = nvt / 2;
-        for (int t = 0; t < mid; ++t) qk_tile(d, t, vt0 + t, vb + t * kTile, nkt == 0 && t == 0);
-        if (g > 0 && !pv(g - 1)) { stop = true; break; }
-        for (int t = mid; t < nvt; ++t) qk_tile(d, t, vt0 + t, vb + t * kTile, nkt == 0 && t == 0);
-        mma_commit(&s_full[g & 1]);
-        if (g == nch - 1 && !pv(g)) stop = true;
-      }
       }
       mma_commit(drain);
       mbar_wait_drain(drain, 0);
@@ -916,7 +920,8 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   if (items > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "prefix attention: grid too large");
   const uint64_t D = a.d_c + a.d_rope, keys = (uint64_t)a.seqs.cache_rows();
   const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const bool fixed = a.d_c == 512 && a.d_rope == 64;
+  const int nk = a.d_c == 512 && (a.d_rope == 64 || a.d_rope == 0) ? (a.d_rope ? 5 : 4) : 0;
+  const bool fixed = nk > 0;
   Maps m;
   int rc = make_tmap_2d(&m.q, bf, a.q, D, (uint64_t)a.seqs.total_q * a.h, D * 2, 64, kM);
   if (rc == DSA_OK) rc = make_tmap_2d(&m.key, bf, a.kv, D, keys, D * 2, 64, (uint32_t)p.chunk_rows);
@@ -930,9 +935,9 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
     if (rc == DSA_OK && fixed) rc = make_tmap_tiles(&m.pre4, bf, a.prefix_kv, D / 64, n, D * 2, 4, kN);
   }
   if (rc != DSA_OK) return rc;
-  auto kern = fixed ? prefix_tc_kernel<true> : prefix_tc_kernel<false>;
-  static int allowed[2][64];
-  rc = allow_smem(kern, kSmem, allowed[fixed], "prefix_tc: smem attribute");
+  auto kern = nk == 5 ? prefix_tc_kernel<5> : nk == 4 ? prefix_tc_kernel<4> : prefix_tc_kernel<0>;
+  static int allowed[6][64];
+  rc = allow_smem(kern, kSmem, allowed[nk], "prefix_tc: smem attribute");
   if (rc != DSA_OK) return rc;
   DSA_LAUNCH("prefix_tc", stream, kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p, m, pl.cuts));
   rc = check_launch("prefix_tc");
