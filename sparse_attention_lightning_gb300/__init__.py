@@ -351,8 +351,8 @@ def fused_forward(P: Problem, q_idx, k_idx, w, q, kv, q_scale=None, k_scale=None
 # Operators around the caches.  Their small calls cost as much on the host as on the GPU, so the
 # checks are written out (no objects built, nothing looked up twice).
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA: nothing is called then
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _TORCH_DT = {_abi.DSA_F32: (torch.float32,), _abi.DSA_BF16: (torch.bfloat16,),
              _abi.DSA_FP8_E4M3: _CODES}

@@ -197,6 +197,24 @@ def test_weights_repeats_padding_and_empty_heads():
 
 
 @pytest.mark.gpu
+def test_checked_build_raises_no_flag():
+    """The kernels' own checks of gather rows and accumulator slots, in the build that has them."""
+    import sparse_attention_lightning_gb300 as dsa
+    from sparse_attention_lightning_gb300 import build
+    build.build(checked=True)
+    for q_lens, dtype, page in (([1, 1], BF, 0), ([4, 9], BF, 16), ([4, 9], F32, 0)):
+        s = Weights(q_lens, [200, 90], 16, 64, 16, 50, dtype, page, seed=6)
+        lse = s.attention()
+        ref = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, s.idx.cuda(), lse, torch.zeros(2, 200).cuda())
+        ws = dsa.Workspace()
+        with _abi.using(_abi.CHECKED_LIB_PATH):
+            got = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, s.idx.cuda(), lse,
+                                              torch.zeros(2, 200).cuda(), ws=ws)
+            assert ws.status() == 0
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_weights_inconsistent_offsets_are_reported(dtype):
     import sparse_attention_lightning_gb300 as dsa
