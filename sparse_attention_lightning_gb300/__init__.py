@@ -74,8 +74,12 @@ class Problem:
             self.page_size, self.block_table.shape[1] if self.page_size else 0, self.num_pages,
             self.block_table.data_ptr() if self.page_size else None)
         self._ref = ctypes.byref(self.c)
+        # what the operators around the caches check a call's tensors against
         self._ws_sizes = {}
         self._row_specs = None
+        tq = self.c.total_q
+        self._shapes = ((tq, h, self.d), (self.cache_rows, self.d), (tq, h, d_c), (tq, h), (tq, top_k))
+        self._device = self.cu_q.get_device()
 
     @classmethod
     def from_config(cls, cfg, cu_q: torch.Tensor, cu_k: torch.Tensor, sm_scale: float = 0.0,
@@ -388,6 +392,8 @@ def _want(t, name: str, dtypes, shape, index: int) -> None:
     """A contiguous CUDA tensor of a dtype, shape and device."""
     if t is None:
         raise ValueError(f"{name} is required")
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -396,14 +402,13 @@ def _want(t, name: str, dtypes, shape, index: int) -> None:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _there(t, index: int) -> None:
-    """A tensor of a Problem is on the call's device."""
-    if t.get_device() != index:
-        raise ValueError(f"the problem's offsets are on {t.device}, the tensors on cuda:{index}")
+def _there(P: Problem, index: int) -> None:
+    """A Problem's tensors are on the call's device."""
+    if P._device != index:
+        raise ValueError(f"the problem's offsets are on cuda:{P._device}, the tensors on cuda:{index}")
 
 
 def _elsewhere(index: int, f, *args, **kw):
@@ -462,13 +467,16 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     if index != _current_device():
         return _elsewhere(index, add_rmsnorm, x, weight, residual, eps, quant, want_y, h, y, codes, scale)
     d = shape[-1]
-    ld_x = _row_stride(x, "x")
-    _want(weight, "weight", (dtype,), (d,), index)
+    ld_x = d if x.is_contiguous() else _row_stride(x, "x")
+    if weight.dtype is not dtype or weight.shape != (d,) or weight.get_device() != index \
+            or not weight.is_contiguous():
+        _want(weight, "weight", (dtype,), (d,), index)
     ld_r = res_ptr = h_ptr = y_ptr = codes_ptr = scale_ptr = code = 0
     if residual is not None:
         if residual.dtype != dtype or residual.shape != shape or residual.get_device() != index:
             raise ValueError("residual must have x's shape, dtype and device")
-        ld_r, res_ptr = _row_stride(residual, "residual"), residual.data_ptr()
+        ld_r = d if residual.is_contiguous() else _row_stride(residual, "residual")
+        res_ptr = residual.data_ptr()
         if h is None:
             h = torch.empty(shape, dtype=dtype, device=x.device)
         else:
@@ -533,20 +541,21 @@ def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
     if index != _current_device():
         return _elsewhere(index, prefix_mla_attn, P, q, kv, prefix_kv, prefix_table, prefix_len, out, lse,
                           want_lse, ws)
-    TQ, H, D = P.total_q, P.h, P.d
-    _want(q, "q", dts, (TQ, H, D), index)
-    _want(kv, "kv", dts, (P.cache_rows, D), index)
-    _there(P.cu_q, index)
+    q_shape, kv_shape, out_shape, lse_shape, _ = P._shapes
+    _want(q, "q", dts, q_shape, index)
+    _want(kv, "kv", dts, kv_shape, index)
+    _there(P, index)
     n = pre_ptr = table_ptr = 0
     if prefix_kv is not None:
         if prefix_table is not None:
             raise ValueError("prefix_kv and prefix_table exclude each other")
         if prefix_kv.dim() != 2:
             raise ValueError(f"prefix_kv has shape {tuple(prefix_kv.shape)}")
-        _want(prefix_kv, "prefix_kv", dts, (prefix_kv.shape[0], D), index)
-        n = prefix_kv.shape[0] if prefix_len is None else int(prefix_len)
-        if not 0 <= n <= prefix_kv.shape[0]:
-            raise ValueError(f"prefix_len is {n}, prefix_kv has {prefix_kv.shape[0]} rows")
+        rows = prefix_kv.shape[0]
+        _want(prefix_kv, "prefix_kv", dts, (rows, kv_shape[1]), index)
+        n = rows if prefix_len is None else int(prefix_len)
+        if not 0 <= n <= rows:
+            raise ValueError(f"prefix_len is {n}, prefix_kv has {rows} rows")
         pre_ptr = prefix_kv.data_ptr() if n else 0
     elif prefix_table is not None:
         if not P.page_size:
@@ -561,13 +570,13 @@ def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
     elif prefix_len:
         raise ValueError("prefix_len needs prefix_kv or prefix_table")
     if out is None:
-        out = torch.empty((TQ, H, P.d_c), dtype=_TORCH_OUT[P.out_dtype], device=kv.device)
+        out = torch.empty(out_shape, dtype=_TORCH_OUT[P.out_dtype], device=kv.device)
     else:
-        _want(out, "out", _TORCH_DT[P.out_dtype], (TQ, H, P.d_c), index)
+        _want(out, "out", _TORCH_DT[P.out_dtype], out_shape, index)
     if lse is not None:
-        _want(lse, "lse", _F32, (TQ, H), index)
+        _want(lse, "lse", _F32, lse_shape, index)
     elif want_lse:
-        lse = torch.empty((TQ, H), dtype=torch.float32, device=kv.device)
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=kv.device)
     stream = _raw_stream(index)
     ws = _op_workspace(ws, index, stream, _ws_bytes(P, _abi.OP_PREFIX_MLA_ATTN))
     rc = lib().dsa_prefix_mla_attn(P._ref, n, pre_ptr, table_ptr, q.data_ptr(), kv.data_ptr(),
@@ -587,13 +596,13 @@ def accumulate_attn_weights(P: Problem, q, kv, idx, lse, acc, ws: Optional[Works
     index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
     if index != _current_device():
         return _elsewhere(index, accumulate_attn_weights, P, q, kv, idx, lse, acc, ws)
-    TQ, H, D = P.total_q, P.h, P.d
-    _want(q, "q", dts, (TQ, H, D), index)
-    _want(kv, "kv", dts, (P.cache_rows, D), index)
-    _want(idx, "idx", _I32, (TQ, P.top_k), index)
-    _want(lse, "lse", _F32, (TQ, H), index)
+    q_shape, kv_shape, _, lse_shape, idx_shape = P._shapes
+    _want(q, "q", dts, q_shape, index)
+    _want(kv, "kv", dts, kv_shape, index)
+    _want(idx, "idx", _I32, idx_shape, index)
+    _want(lse, "lse", _F32, lse_shape, index)
     ld = _acc_stride(P, acc, "acc", P.max_k_len, index)
-    _there(P.cu_q, index)
+    _there(P, index)
     stream = _raw_stream(index)
     ws = _op_workspace(ws, index, stream, _ws_bytes(P, _abi.OP_ATTN_WEIGHTS))
     rc = lib().dsa_accumulate_attn_weights(P._ref, q.data_ptr(), kv.data_ptr(), idx.data_ptr(),
@@ -652,7 +661,7 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
                          "sink + recent <= budget are needed")
     B, dev, index = P.c.num_seqs, acc.device, acc.get_device()
     ld = _acc_stride(P, acc, "acc", P.max_k_len, index)
-    _there(P.cu_k, index)
+    _there(P, index)
     k_lens = [n if n < budget else budget for n in P.k_lens]
     rows = sum(k_lens)
     max_pages = num_pages = table_ptr = 0

@@ -4,7 +4,7 @@
 //   acc[b, idx[t,i]] += Σ_h exp(scale · q[t,h,:]·kv[row_i,:] − lse[t,h])
 //
 // A query's weights are probabilities (the lse is the attention's), so the sum needs no running
-// max.  One CTA = one query × 64 of its selected positions; the CUDA cores compute in fp32
+// max.  One CTA = one query × 16 of its selected positions; the CUDA cores compute in fp32
 // (the generic path: any type and width).
 //
 // Order.  Where no sequence has more than one query, a position receives additions of one value
@@ -17,19 +17,36 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 16;    // selected rows in shared memory
-constexpr int kHeads = 16;
-constexpr int kSlots = 64;   // selected positions a CTA takes
+constexpr int kKeys = 16;    // selected positions a CTA takes
+constexpr int kHeads = 16;   // heads at a time
 
+// 16 bytes of TK as floats to shared memory (zeros where src is null).
+__device__ __forceinline__ void copy16(float* dst, const float* src) {
+  const float4 v = src ? __ldg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  *reinterpret_cast<float4*>(dst) = v;
+}
+__device__ __forceinline__ void copy16(float* dst, const __nv_bfloat16* src) {
+  const uint4 v = src ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<float4*>(dst + 4 * i) =
+        make_float4(__uint_as_float(u[2 * i] << 16), __uint_as_float(u[2 * i] & 0xffff0000u),
+                    __uint_as_float(u[2 * i + 1] << 16), __uint_as_float(u[2 * i + 1] & 0xffff0000u));
+}
+
+// A thread a (head, key) pair, 16 x 16 of them; rows are four floats longer than their columns in shared
+// memory, which spreads 16-byte loads over the banks.
 template <typename TK>
 __global__ void __launch_bounds__(kThreads) attn_weights_simt_kernel(WeightArgs a) {
-  extern __shared__ float smem[];
-  const int D = a.d, DP = D + 1;
+  extern __shared__ __align__(16) float smem[];
+  constexpr int V = 16 / (int)sizeof(TK);
+  const int D = a.d, DP = D + 4;
   const int t = blockIdx.x, tid = threadIdx.x;
-  float* ks = smem;                  // [kKeys][D + 1]
-  float* qs = ks + kKeys * DP;       // [kHeads][D]
-  float* red = qs + kHeads * D;      // [kHeads][kKeys]
-  __shared__ int pos_s[kKeys], row_s[kKeys];
+  float* ks = smem;                  // [kKeys][D + 4]
+  float* qs = ks + kKeys * DP;       // [kHeads][D + 4]
+  float* red = qs + kHeads * DP;     // [kHeads][kKeys]
+  __shared__ int row_s[kKeys];
   RowInfo r;
   if (!query_row_info(a.seqs, t, r, a.status)) return;
   if (__ldg(a.seqs.cu_q + r.b + 1) - __ldg(a.seqs.cu_q + r.b) > a.max_q_len) {
@@ -39,43 +56,48 @@ __global__ void __launch_bounds__(kThreads) attn_weights_simt_kernel(WeightArgs 
   const TK* q = static_cast<const TK*>(a.q) + (int64_t)t * a.h * D;
   const TK* kv = static_cast<const TK*>(a.kv);
   const int hh = tid / kKeys, kk = tid % kKeys;
-  const int lo = blockIdx.y * kSlots, hi = min(a.top_k, lo + kSlots);
-  for (int i0 = lo; i0 < hi; i0 += kKeys) {
+  int pos = -1;  // threads 0..15: their key's position
+  if (tid < kKeys) {
+    const int i = blockIdx.y * kKeys + tid;
+    const int v = i < a.top_k ? a.idx[(int64_t)t * a.top_k + i] : -1;
+    int row = -1;
+    if (v >= 0 && v <= r.pos) row = key_row(a.seqs, r.b, r.k0, v);
+    if (row < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+    if (!dsa_check(row < a.seqs.cache_rows(), a.status)) row = -1;
+    pos = row < 0 ? -1 : v;
+    row_s[tid] = row;
+  }
+  if (!__syncthreads_or(pos >= 0)) return;  // padding only
+  {
+    const int row = row_s[hh];  // 16 threads a key
+    for (int i = kk * V; i < D; i += 16 * V)
+      copy16(ks + hh * DP + i, row >= 0 ? kv + (int64_t)row * D + i : static_cast<const TK*>(nullptr));
+  }
+  float w = 0.f;
+  for (int h0 = 0; h0 < a.h; h0 += kHeads) {
     __syncthreads();
-    if (tid < kKeys) {
-      const int v = i0 + tid < hi ? a.idx[(int64_t)t * a.top_k + i0 + tid] : -1;
-      int row = -1;
-      if (v >= 0 && v <= r.pos) row = key_row(a.seqs, r.b, r.k0, v);
-      if (row < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
-      pos_s[tid] = v;
-      row_s[tid] = row;
-    }
+    const bool head = h0 + hh < a.h;
+    for (int i = kk * V; i < D; i += 16 * V)
+      copy16(qs + hh * DP + i, head ? q + (int64_t)(h0 + hh) * D + i : static_cast<const TK*>(nullptr));
+    const float lse = head ? a.lse[(int64_t)t * a.h + h0 + hh] : -INFINITY;
     __syncthreads();
-    for (int i = tid; i < kKeys * D; i += kThreads) {
-      const int k = i / D, c = i - k * D;
-      ks[k * DP + c] = row_s[k] >= 0 ? to_f32(kv[(int64_t)row_s[k] * D + c]) : 0.f;
+    float dot = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(qs + hh * DP + c);
+      const float4 y = *reinterpret_cast<const float4*>(ks + kk * DP + c);
+      dot = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot))));
     }
-    float w = 0.f;
-    for (int h0 = 0; h0 < a.h; h0 += kHeads) {
-      __syncthreads();
-      const int n = min(kHeads, a.h - h0) * D;
-      for (int i = tid; i < n; i += kThreads) qs[i] = to_f32(q[(int64_t)h0 * D + i]);
-      __syncthreads();
-      if (h0 + hh < a.h) {
-        const float lse = a.lse[(int64_t)t * a.h + h0 + hh];
-        float dot = 0.f;
-        for (int c = 0; c < D; ++c) dot = fmaf(qs[hh * D + c], ks[kk * DP + c], dot);
-        // lse = -inf: the attention had no valid entry, so nothing received weight
-        if (lse != -INFINITY) w += exp2f(fmaf(dot, a.scale_log2, -lse * kLog2e));
-      }
-    }
-    red[hh * kKeys + kk] = w;
-    __syncthreads();
-    if (tid < kKeys && row_s[tid] >= 0) {
-      float s = 0.f;
-      for (int j = 0; j < kHeads; ++j) s += red[j * kKeys + tid];
-      add_weight(a, r.b, pos_s[tid], s);
-    }
+    // lse = -inf: the attention had no valid entry, so nothing received weight
+    if (lse != -INFINITY) w += exp2f(fmaf(dot, a.scale_log2, -lse * kLog2e));
+  }
+  red[hh * kKeys + kk] = w;
+  __syncthreads();
+  if (pos >= 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) s += red[j * kKeys + tid];
+    add_weight(a, r.b, pos, s);
   }
 }
 
@@ -92,13 +114,12 @@ __global__ void __launch_bounds__(256) attn_weights_finish_kernel(WeightArgs a, 
 
 template <typename TK>
 int launch_typed(const WeightArgs& a, cudaStream_t stream) {
-  const size_t smem = sizeof(float) * ((size_t)kKeys * (a.d + 1) + (size_t)kHeads * a.d +
-                                       kHeads * kKeys);
+  const size_t smem = sizeof(float) * ((size_t)(kKeys + kHeads) * (a.d + 4) + kHeads * kKeys);
   auto kern = attn_weights_simt_kernel<TK>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return check_launch("attn_weights_simt: smem attribute");
-  dim3 grid((unsigned)a.seqs.total_q, (unsigned)((a.top_k + kSlots - 1) / kSlots));
+  dim3 grid((unsigned)a.seqs.total_q, (unsigned)((a.top_k + kKeys - 1) / kKeys));
   DSA_LAUNCH("attn_weights_simt", stream, kern<<<grid, kThreads, smem, stream>>>(a));
   return check_launch("attn_weights_simt");
 }
