@@ -402,8 +402,15 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         int vslot = 0, vphase = 0;           // of chunk g
         uint64_t pvd = 0;                    // V tiles of chunk g - 1, as P·V reads them
         uint64_t* pv_empty = nullptr;
-        auto pv_fixed = [&](int g) -> bool {
-          if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) return false;
+        // A barrier is tested before the MMAs that come ahead of its use are issued, so that the test's own latency
+        // passes beside them (a wait that finds its barrier complete still takes ~100 clocks, and eight of them
+        // a chunk were the issuing thread's time); only where it was not complete yet is it waited for.
+        auto test = [&](uint64_t* bar, uint32_t parity) { return mbar_test(smem_u32(bar), parity); };
+        auto sure = [&](bool ready, uint64_t* bar, uint32_t parity) {
+          return ready || mbar_wait(bar, parity, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+        };
+        auto pv_fixed = [&](int g, bool ready) -> bool {
+          if (!sure(ready, &p_full[g & 1], (g >> 1) & 1)) return false;
           tc_fence_after();
           const uint32_t pa = tmem + kSCol + (g & 1) * kN;
           const uint32_t acc = g > 0;
@@ -415,30 +422,32 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
           return true;
         };
         for (int g = 0; g < nch && !stop; ++g) {
+          bool ready = test(&k_full[0], g & 1);
           if (g >= 2 && !mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))
             break;
           const uint32_t d = tmem + kSCol + (g & 1) * kN;
           // a barrier a tile: each is refilled while the others and the V tiles are multiplied
 #pragma unroll
           for (int j = 0; j < NK; ++j) {
-            if (!mbar_wait(&k_full[j], g & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) { stop = true; break; }
+            if (!sure(ready, &k_full[j], g & 1)) { stop = true; break; }
             tc_fence_after();
+            ready = j + 1 < NK ? test(&k_full[j + 1], g & 1) : test(&v_full[vslot], vphase);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               mma_bf16(d, qd + (uint64_t)(j * (kQTile >> 4) + i * 2), kd + (uint64_t)(j * (kTile >> 4) + i * 2),
                        idesc_s, j || i ? 1u : 0u);
             mma_commit(&k_empty[j]);
           }
-          if (stop) break;
-          if (!mbar_wait(&v_full[vslot], vphase, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
+          if (stop || !sure(ready, &v_full[vslot], vphase)) break;
           tc_fence_after();
+          ready = g > 0 && test(&p_full[(g - 1) & 1], ((g - 1) >> 1) & 1);
           const uint64_t vd = sdesc_sw128(v0 + vslot * (4 * kTile), 16, 1024);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               mma_bf16_ts(d, tmem + kQCol + t * 32 + i * 8, vd + (uint64_t)(t * (kTile >> 4) + i * 2), idesc_s, 1u);
-          if (g > 0 && !pv_fixed(g - 1)) { stop = true; break; }
+          if (g > 0 && !pv_fixed(g - 1, ready)) { stop = true; break; }
 #pragma unroll
           for (int t = 2; t < 4; ++t)
 #pragma unroll
@@ -448,7 +457,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
           pvd = sdesc_sw128(v0 + vslot * (4 * kTile), kTile, 1024);
           pv_empty = &v_empty[vslot];
           if (++vslot == kVSlots) { vslot = 0; vphase ^= 1; }
-          if (g == nch - 1 && !pv_fixed(g)) stop = true;
+          if (g == nch - 1 && !pv_fixed(g, false)) stop = true;
         }
       } else {
         // The logits' K-steps of one tile: A = tile qt of the query in tensor memory, or (qt >= 4) tile qt - 4 of
