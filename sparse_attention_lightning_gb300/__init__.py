@@ -357,6 +357,7 @@ def fused_forward(P: Problem, q_idx, k_idx, w, q, kv, q_scale=None, k_scale=None
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA: nothing is called then
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _TORCH_DT = {_abi.DSA_F32: (torch.float32,), _abi.DSA_BF16: (torch.bfloat16,),
              _abi.DSA_FP8_E4M3: _CODES}
@@ -366,26 +367,26 @@ _op_ws = {}
 
 
 def _op_workspace(ws: Optional[Workspace], index: int, stream: int, nbytes: int) -> Workspace:
-    """The caller's workspace, grown as needed, or this device's and stream's own: calls on two
-    streams do not share scratch.  A default workspace that grows keeps its earlier buffers
-    alive, so a captured graph that refers to one stays valid; while a stream is being captured none
-    is allocated (its memory would belong to the graph)."""
+    """The caller's workspace, grown as needed (its earlier buffers stay alive, a captured graph may
+    refer to them), or this device's and stream's own: calls on two streams do not share scratch.  A
+    captured call has to bring its workspace: graphs captured on one stream may be replayed on two, and
+    memory allocated while capturing would belong to the graph."""
     if ws is not None:
         if ws.buf.get_device() != index:
             raise ValueError(f"the workspace is on {ws.buf.device}, the tensors on cuda:{index}")
-        if ws.nbytes < nbytes and torch.cuda.is_current_stream_capturing():
-            raise ValueError(f"a captured call needs a workspace of {nbytes} bytes beforehand")
-        return ws.ensure(nbytes)
+        if ws.nbytes < nbytes:
+            if _capturing():
+                raise ValueError(f"a captured call needs a workspace of {nbytes} bytes beforehand")
+            ws.__dict__.setdefault("_earlier", []).append(ws.buf)
+            ws.ensure(nbytes)
+        return ws
+    if _capturing():
+        raise ValueError(f"a captured call needs a workspace of its own: ws=Workspace(nbytes={nbytes})")
     held = _op_ws.get((index, stream))
-    if held is None or held[-1].nbytes < nbytes:
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("a captured call needs its workspace beforehand: pass ws, or make the "
-                             "call once on this stream before capturing it")
-        if held is None:
-            held = _op_ws[index, stream] = []
-        held.append(Workspace(torch.device("cuda", index),
-                              max(nbytes, 2 * held[-1].nbytes if held else 0)))
-    return held[-1]
+    if held is None or held.nbytes < nbytes:
+        size = max(nbytes, 2 * held.nbytes if held else 0)
+        held = _op_ws[index, stream] = Workspace(torch.device("cuda", index), size)
+    return held
 
 
 def _want(t, name: str, dtypes, shape, index: int) -> None:

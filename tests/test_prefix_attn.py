@@ -357,3 +357,34 @@ def test_prefix_len_takes_part_of_the_rows():
     out, lse = s.run(prefix_len=0)
     s.P, s.pre = 0, s.pre[:0]
     s.check(out, lse)
+
+
+@pytest.mark.gpu
+def test_a_captured_call_brings_its_workspace():
+    """Graphs captured on one stream may be replayed on two, so none may use the stream's own scratch; and
+    a workspace that grows later leaves a captured graph the buffer it was captured with."""
+    import sparse_attention_lightning_gb300 as dsa
+    s = Setup([1, 1], [30, 60], 16, P=2000, dtype=BF, seed=14, **FULL)
+    q = s.q.cuda()
+    ws = dsa.Workspace(nbytes=s.prob.workspace_size(_abi.OP_PREFIX_MLA_ATTN))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ref, ref_lse = dsa.prefix_mla_attn(s.prob, q, s.kv, **s.prefix)  # the stream has its own scratch now
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError, match="of its own"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            dsa.prefix_mla_attn(s.prob, q, s.kv, **s.prefix)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, lse = dsa.prefix_mla_attn(s.prob, q, s.kv, ws=ws, **s.prefix)
+    held = ws.buf.data_ptr()
+    big = Setup([1] * 9, [60] * 9, 128, P=2000, dtype=BF, seed=15, **FULL)
+    assert big.prob.workspace_size(_abi.OP_PREFIX_MLA_ATTN) > ws.nbytes
+    big.check(*big.run(ws=ws), rows={0, 8})
+    assert ws.buf.data_ptr() != held
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    assert all((j == 255).all() for j in junk)
