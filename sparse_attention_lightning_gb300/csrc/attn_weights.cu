@@ -101,8 +101,15 @@ __global__ void __launch_bounds__(kThreads) attn_weights_simt_kernel(WeightArgs 
   }
 }
 
+// Zero the fixed-point sums.  The kernel that adds to them is set up meanwhile, and gathers its first rows.
+__global__ void __launch_bounds__(256) attn_weights_clear_kernel(long long* fx, int64_t n) {
+  griddep_launch();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) fx[i] = 0;
+}
+
 // acc += the fixed-point sums of the positions a sequence holds.
 __global__ void __launch_bounds__(256) attn_weights_finish_kernel(WeightArgs a, int per) {
+  griddep_wait();
   const int b = blockIdx.x / per, j = blockIdx.x - b * per;
   const int L = min(__ldg(a.seqs.cu_k + b + 1) - __ldg(a.seqs.cu_k + b), a.seqs.max_k_len);
   const float unit = (float)(1.0 / a.fx_scale);
@@ -133,18 +140,21 @@ int launch_attn_weights_simt(const WeightArgs& a, cudaStream_t stream) {
 
 int launch_attn_weights(const WeightArgs& a, cudaStream_t stream) {
   if (a.fx) {
-    const cudaError_t e = cudaMemsetAsync(
-        a.fx, 0, (size_t)a.seqs.B * a.seqs.max_k_len * sizeof(long long), stream);
-    if (e != cudaSuccess)
-      return set_error(DSA_ERR_CUDA, "attn_weights clear: %s", cudaGetErrorString(e));
+    const int64_t n = (int64_t)a.seqs.B * a.seqs.max_k_len, blocks = (n + 1023) / 1024;
+    const unsigned grid = (unsigned)(blocks < 1 ? 1 : blocks < 4 * num_sms() ? blocks : 4 * num_sms());
+    DSA_LAUNCH("attn_weights_clear", stream, attn_weights_clear_kernel<<<grid, 256, 0, stream>>>(a.fx, n));
+    const int rc = check_launch("attn_weights_clear");
+    if (rc != DSA_OK) return rc;
   }
   const int rc = attn_weights_tc_eligible(a) ? launch_attn_weights_tc(a, stream)
                                              : launch_attn_weights_simt(a, stream);
   if (rc != DSA_OK || !a.fx) return rc;
   const int64_t want = (a.seqs.max_k_len + 1023) / 1024, most = 0x7fffffff / a.seqs.B;
   const int per = (int)(want < 64 ? (want < most ? want : most) : (64 < most ? 64 : most));
+  cudaError_t e = cudaSuccess;
   DSA_LAUNCH("attn_weights_finish", stream,
-             attn_weights_finish_kernel<<<(unsigned)per * a.seqs.B, 256, 0, stream>>>(a, per));
+             e = launch_pdl(attn_weights_finish_kernel, dim3((unsigned)per * a.seqs.B), dim3(256), 0, stream, a, per));
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn_weights_finish: %s", cudaGetErrorString(e));
   return check_launch("attn_weights_finish");
 }
 

@@ -119,6 +119,7 @@ __device__ __forceinline__ float transpose_add(float (&v)[32], int lane) {
 __global__ void __launch_bounds__(kThreads, 1)
 attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
                        const __grid_constant__ CUtensorMap kvmap) {
+  griddep_launch();  // the kernel that adds the sums to acc may be set up; it waits for this grid to end
   const WeightArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -320,6 +321,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
+      griddep_wait();  // the sums are zero (and written: the kernels behind this one wait for it alone)
       const float lse = h < a.h ? a.lse[flat] : -INFINITY;
       const bool dead = lse == -INFINITY;  // no such head, or it attended to nothing: it adds nothing
       const float lse2 = dead ? 0.f : lse * kLog2e;
@@ -365,6 +367,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
         }
       }
     }
+    griddep_wait();
   }
   tc_fence_before();
   cta_sync();
@@ -398,7 +401,14 @@ int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   static int allowed[64];
   rc = allow_smem(attn_weights_tc_kernel, smem, allowed, "attn_weights_tc: smem attribute");
   if (rc != DSA_OK) return rc;
-  DSA_LAUNCH("attn_weights_tc", stream, attn_weights_tc_kernel<<<grid, kThreads, smem, stream>>>(p, qmap, kvmap));
+  cudaError_t e = cudaSuccess;
+  if (a.fx) {
+    DSA_LAUNCH("attn_weights_tc", stream,
+               e = launch_pdl(attn_weights_tc_kernel, dim3(grid), dim3(kThreads), smem, stream, p, qmap, kvmap));
+  } else {
+    DSA_LAUNCH("attn_weights_tc", stream, attn_weights_tc_kernel<<<grid, kThreads, smem, stream>>>(p, qmap, kvmap));
+  }
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn_weights_tc: %s", cudaGetErrorString(e));
   return check_launch("attn_weights_tc");
 }
 
