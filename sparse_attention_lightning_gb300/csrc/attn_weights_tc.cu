@@ -83,13 +83,13 @@ __device__ __forceinline__ bool warp_row_info(const WeightArgs& a, int t, int la
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int probe = lo + lane * step;
-    const bool le = probe < hi && (lane == 0 || __ldg(s.cu_q + probe) <= t);
+    const bool le = probe < hi && (lane == 0 || s.cu_q[probe] <= t);
     const int m = 31 - __clz(__ballot_sync(0xffffffffu, le));
     lo += m * step;
     hi = min(hi, lo + step);
   }
-  const int q0 = __ldg(s.cu_q + lo), q1 = __ldg(s.cu_q + lo + 1);
-  const int k0 = __ldg(s.cu_k + lo), k1 = __ldg(s.cu_k + lo + 1);
+  const int q0 = s.cu_q[lo], q1 = s.cu_q[lo + 1];
+  const int k0 = s.cu_k[lo], k1 = s.cu_k[lo + 1];
   const int T = q1 - q0, L = k1 - k0;
   if (!(t >= q0 && t < q1 && T <= L && k0 >= 0 && k1 <= s.total_k && L <= s.max_k_len && q1 <= s.total_q &&
         T <= a.max_q_len)) {  // (the order of additions and fx_scale rest on max_q_len)
@@ -119,7 +119,11 @@ __device__ __forceinline__ float transpose_add(float (&v)[32], int lane) {
 __global__ void __launch_bounds__(kThreads, 1)
 attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
                        const __grid_constant__ CUtensorMap kvmap) {
-  griddep_launch();  // the kernel that adds the sums to acc may be set up; it waits for this grid to end
+  // With sums, the kernel before this one clears them (waited for ahead of the first addition), and the one behind
+  // it, which adds them to acc, may be set up meanwhile: it waits for this grid to end.  A caller's next
+  // kernel may not: it may read what comes before it without waiting.
+  if (p.a.fx) griddep_launch();
+  else griddep_wait();
   const WeightArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -167,7 +171,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
       // lanes 0..15: this warp's entries, read two chunks ahead, and their pages, one chunk ahead
       auto load_idx = [&](int c) {
         const int i = c * kN + warp * 16 + lane;
-        return lane < 16 && i < a.top_k ? __ldg(a.idx + (int64_t)pc.t * a.top_k + i) : -1;
+        return lane < 16 && i < a.top_k ? a.idx[(int64_t)pc.t * a.top_k + i] : -1;
       };
       int v0 = load_idx(pc.c0), v1 = load_idx(pc.c0 + 1);
       if (!warp_row_info(a, pc.t, lane, ri)) continue;
@@ -189,7 +193,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
       const bool paged = a.seqs.paged();
       const int sh = paged ? __ffs(a.seqs.page_size) - 1 : 0;
       const int32_t* table = a.seqs.block_table + (int64_t)ri.b * a.seqs.max_pages;
-      auto load_page = [&](int v) { return paged && v >= 0 && v <= ri.pos ? __ldg(table + (v >> sh)) : 0; };
+      auto load_page = [&](int v) { return paged && v >= 0 && v <= ri.pos ? table[v >> sh] : 0; };
       int pg = load_page(v0);
       for (int c = pc.c0; c < pc.c1; ++c, ++n) {
         int row = -1;
@@ -330,8 +334,8 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
         int pos = -1;
         if (et < kN) {
           const int i = c * kN + et;
-          const int v = i < a.top_k ? __ldg(a.idx + (int64_t)pc.t * a.top_k + i) : -1;
-          if (v >= 0 && v <= ri.pos && key_row(a.seqs, ri.b, ri.k0, v) >= 0) pos = v;
+          const int v = i < a.top_k ? a.idx[(int64_t)pc.t * a.top_k + i] : -1;
+          if (v >= 0 && v <= ri.pos && cache_row(a.seqs, ri.b, ri.k0, v) >= 0) pos = v;
           else if (v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (n >> 1) & 1, abort_flag, a.status,
@@ -402,12 +406,8 @@ int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   rc = allow_smem(attn_weights_tc_kernel, smem, allowed, "attn_weights_tc: smem attribute");
   if (rc != DSA_OK) return rc;
   cudaError_t e = cudaSuccess;
-  if (a.fx) {
-    DSA_LAUNCH("attn_weights_tc", stream,
-               e = launch_pdl(attn_weights_tc_kernel, dim3(grid), dim3(kThreads), smem, stream, p, qmap, kvmap));
-  } else {
-    DSA_LAUNCH("attn_weights_tc", stream, attn_weights_tc_kernel<<<grid, kThreads, smem, stream>>>(p, qmap, kvmap));
-  }
+  DSA_LAUNCH("attn_weights_tc", stream,
+             e = launch_pdl(attn_weights_tc_kernel, dim3(grid), dim3(kThreads), smem, stream, p, qmap, kvmap));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn_weights_tc: %s", cudaGetErrorString(e));
   return check_launch("attn_weights_tc");
 }

@@ -8,6 +8,20 @@ namespace dsa {
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Kernels launched with launch_pdl read what the kernels before them wrote by ordinary loads, behind
+// griddep_wait(): the read-only path (__ldg) is for data that nobody changes while the grid runs, and its loads may
+// be moved ahead of the wait.  Those that begin an operator wait at their very start (the launch itself
+// then passes beside the kernel before: a call of 20 to 140 us is 2 to 3 us shorter in a row of calls), and let only
+// their own operator's next kernel start early, as a caller's next one may read its inputs ahead of its wait.
+
+// key_row by ordinary loads.
+__device__ __forceinline__ int cache_row(const Seqs& s, int b, int k0, int pos) {
+  if (!s.paged()) return k0 + pos;
+  const int sh = __ffs(s.page_size) - 1;
+  const int pg = s.block_table[(int64_t)b * s.max_pages + (pos >> sh)];
+  return (unsigned)pg < (unsigned)s.num_pages ? (pg << sh) | (pos & (s.page_size - 1)) : -1;
+}
+
 // 16-bit rows as [tiles][rows][64 columns] (rows of tiles · 64 elements): a box is box_tiles tiles of
 // box_rows rows, each tile as make_tmap_2d's box of 64 columns would store it.
 int make_tmap_tiles(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t tiles,

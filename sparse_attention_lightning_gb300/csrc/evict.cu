@@ -27,7 +27,7 @@ constexpr int kBins = 2048;
 constexpr int kSmemKeys = 49152;
 
 __device__ __forceinline__ int seq_keep(const EvictArgs& a, int b, int& L) {
-  const int k0 = __ldg(a.seqs.cu_k + b), k1 = __ldg(a.seqs.cu_k + b + 1);
+  const int k0 = a.seqs.cu_k[b], k1 = a.seqs.cu_k[b + 1];
   L = k1 - k0;
   if (k0 < 0 || L < 0 || k1 > a.seqs.total_k || L > a.seqs.max_k_len) {
     atomicOr(a.status, DSA_FLAG_BAD_SEQS);
@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(kSel) evict_select_kernel(EvictArgs a) {
   __shared__ int warp_sums[32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  griddep_launch();  // the move may be set up meanwhile; it waits for this grid to end
+  griddep_wait();
+  if (a.moves) griddep_launch();  // the move may be set up meanwhile; it waits for this grid to end
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int L;
   const int n = seq_keep(a, b, L);
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kSel) evict_select_kernel(EvictArgs a) {
   }
   const float* acc = a.acc + (int64_t)b * a.ld_acc;
   const int lo = a.sink, hi = L - a.recent;
-  auto key = [&](int i) { return SMEM ? keys[i] : order_key(__ldg(acc + i)); };
+  auto key = [&](int i) { return SMEM ? keys[i] : order_key(acc[i]); };
   int need = a.budget - a.sink - a.recent;
   const bool any = need > 0;
   uint32_t prefix = 0;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kSel) evict_select_kernel(EvictArgs a) {
       for (int i = lo + tid; i < hi; i += kFly * kSel) {
         float f[kFly];
 #pragma unroll
-        for (int j = 0; j < kFly; ++j) f[j] = i + j * kSel < hi ? __ldg(acc + i + j * kSel) : 0.f;
+        for (int j = 0; j < kFly; ++j) f[j] = i + j * kSel < hi ? acc[i + j * kSel] : 0.f;
 #pragma unroll
         for (int j = 0; j < kFly; ++j)
           if (i + j * kSel < hi) {
@@ -252,20 +253,23 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
 
 }  // namespace
 
-int launch_evict(const EvictArgs& a, cudaStream_t stream) {
+int launch_evict(EvictArgs a, cudaStream_t stream) {
+  a.moves = a.row_bytes[0] || a.row_bytes[1] || a.row_bytes[2] || a.acc_out;
+  cudaError_t e = cudaSuccess;
   if (a.seqs.max_k_len <= kSmemKeys) {
     const int smem = a.seqs.max_k_len * 4;
     static int allowed[64];
     const int rc = smem + 16384 <= 49152 ? DSA_OK
                                          : allow_smem(evict_select_kernel<true>, kSmemKeys * 4, allowed, "evict_select: smem attribute");
     if (rc != DSA_OK) return rc;
-    DSA_LAUNCH("evict_select", stream, evict_select_kernel<true><<<a.seqs.B, kSel, smem, stream>>>(a));
+    DSA_LAUNCH("evict_select", stream, e = launch_pdl(evict_select_kernel<true>, dim3(a.seqs.B), dim3(kSel), smem, stream, a));
   } else {
-    DSA_LAUNCH("evict_select", stream, evict_select_kernel<false><<<a.seqs.B, kSel, 0, stream>>>(a));
+    DSA_LAUNCH("evict_select", stream, e = launch_pdl(evict_select_kernel<false>, dim3(a.seqs.B), dim3(kSel), 0, stream, a));
   }
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "evict_select: %s", cudaGetErrorString(e));
   const int rc = check_launch("evict_select");
   if (rc != DSA_OK) return rc;
-  if (!a.row_bytes[0] && !a.row_bytes[1] && !a.row_bytes[2] && !a.acc_out) return DSA_OK;
+  if (!a.moves) return DSA_OK;
   // row slots a block, blocks an SM: as many row slots as fit kMoveSmem (rows are at most 6 KB)
   const int64_t total = (int64_t)a.seqs.B * a.budget;
   const int rb = a.row_bytes[0] + a.row_bytes[1];
@@ -276,7 +280,6 @@ int launch_evict(const EvictArgs& a, cudaStream_t stream) {
   static int allowed[64];
   const int rc2 = smem <= 40960 ? DSA_OK : allow_smem(evict_move_kernel, kMoveSmem, allowed, "evict_move: smem attribute");
   if (rc2 != DSA_OK) return rc2;
-  cudaError_t e = cudaSuccess;
   DSA_LAUNCH("evict_move", stream,
              e = launch_pdl(evict_move_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(thr / kMoveLanes * 32), smem,
                             stream, a));

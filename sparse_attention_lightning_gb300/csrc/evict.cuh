@@ -21,8 +21,9 @@ struct EvictArgs {
   int max_pages_out, num_pages_out;
   int64_t rows_out;
   uint32_t* status;
+  bool moves;            // there is something to move (set by launch_evict)
 };
 
-int launch_evict(const EvictArgs& a, cudaStream_t stream);
+int launch_evict(EvictArgs a, cudaStream_t stream);
 
 }  // namespace dsa

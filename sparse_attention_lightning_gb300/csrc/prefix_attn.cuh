@@ -29,8 +29,8 @@ struct SeqInfo {
 // Sequence b's rows; false (and flagged) when cu_q/cu_k are inconsistent with the descriptor.
 __device__ __forceinline__ bool prefix_seq(const PrefixArgs& a, int b, SeqInfo& i) {
   const Seqs& s = a.seqs;
-  const int q0 = __ldg(s.cu_q + b), q1 = __ldg(s.cu_q + b + 1);
-  const int k0 = __ldg(s.cu_k + b), k1 = __ldg(s.cu_k + b + 1);
+  const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
+  const int k0 = s.cu_k[b], k1 = s.cu_k[b + 1];
   i = SeqInfo{b, q0, q1 - q0, k0, k1 - k0};
   const bool ok = q0 >= 0 && q1 >= q0 && q1 <= s.total_q && k0 >= 0 && k1 >= k0 &&
                   k1 <= s.total_k && i.T <= i.L && i.L <= s.max_k_len && i.T <= a.max_q_len;
@@ -44,13 +44,13 @@ __device__ __forceinline__ const void* prefix_key(const PrefixArgs& a, int b, in
   int64_t row;
   const char* base = static_cast<const char*>(a.kv);
   if (x >= a.prefix_len) {
-    row = key_row(a.seqs, b, k0, x - a.prefix_len);
+    row = cache_row(a.seqs, b, k0, x - a.prefix_len);
   } else if (a.prefix_kv) {
     base = static_cast<const char*>(a.prefix_kv);
     row = x;
   } else {
     const int sh = __ffs(a.seqs.page_size) - 1;
-    const int pg = __ldg(a.prefix_table + (x >> sh));
+    const int pg = a.prefix_table[x >> sh];
     row = (unsigned)pg < (unsigned)a.seqs.num_pages
               ? ((int64_t)pg << sh) | (x & (a.seqs.page_size - 1)) : -1;
   }

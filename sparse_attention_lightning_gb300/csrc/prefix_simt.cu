@@ -40,7 +40,7 @@ template <typename TK>
 __device__ __forceinline__ void copy16(float* dst, const TK* src) {
   constexpr int V = 16 / (int)sizeof(TK);
   float f[V];
-  widen16(src ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u), f);
+  widen16(src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u), f);
 #pragma unroll
   for (int i = 0; i < V; i += 4)
     *reinterpret_cast<float4*>(dst + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
@@ -49,7 +49,8 @@ __device__ __forceinline__ void copy16(float* dst, const TK* src) {
 // KC keys a step (16 or 32); NJ: 64-column groups of the values (d_c <= 64 · NJ).
 template <typename TK, typename TO, int KC, int NJ>
 __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int nblk) {
-  griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
+  griddep_wait();
+  if (a.splits > 1) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   extern __shared__ __align__(16) float smem[];
   constexpr int V = 16 / (int)sizeof(TK);
   const int D = a.d_c + a.d_rope, DP = D + 4, dc = a.d_c, H = a.h;
@@ -275,7 +276,9 @@ int launch_typed(const PrefixArgs& a, cudaStream_t stream) {
   if (rc != DSA_OK) return rc;
   const int nblk = prefix_simt_blocks(a.max_q_len, a.h);
   dim3 grid((unsigned)(a.seqs.B * nblk), (unsigned)a.splits);
-  DSA_LAUNCH("prefix_simt", stream, kern<<<grid, kThreads, smem, stream>>>(a, nblk));
+  cudaError_t e = cudaSuccess;
+  DSA_LAUNCH("prefix_simt", stream, e = launch_pdl(kern, grid, dim3(kThreads), smem, stream, a, nblk));
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "prefix_simt: %s", cudaGetErrorString(e));
   return check_launch("prefix_simt");
 }
 

@@ -63,6 +63,7 @@ struct Params {
   int chunk_rows;  // cache rows a tile is loaded in
   int nseg;        // cuts: segments (0: every line in equal pieces, sp or ss)
   int ns;          // cuts: length of a line of a sequence's block, as the segments count it
+  bool merged;     // a merge of pieces follows
 };
 
 // One CTA's (with halves, two CTAs') part of a line: the key chunks [a, b) of a block of rows.  Lines: the
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps,
                  const __grid_constant__ Cuts cuts) {
   constexpr bool FIXED = NK > 0;
-  griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
+  griddep_wait();
+  if (p.merged) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   Item it;
   if (!item_at(p, cuts, blockIdx.x, it)) return;
   const PrefixArgs& a = p.a;
@@ -319,7 +321,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
           for (int j = 0; j < kN / 16; ++j) {
             if (j >= nrun) break;
             const int x = x0 + j * cr, slot = x >> sh;
-            const int pg = slot < pages ? __ldg(table + slot) : -1;
+            const int pg = slot < pages ? table[slot] : -1;
             const bool ok = (unsigned)pg < (unsigned)a.seqs.num_pages;
             // keys of a page outside the cache are masked; page 0 stands in for their rows
             if (!ok) bad |= (cr == 64 ? ~0ull : ((1ull << cr) - 1)) << (j * cr);
@@ -922,6 +924,7 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   p.halves = pl.halves;
   p.nseg = pl.nseg;
   p.ns = pl.ns;
+  p.merged = pl.merge.pieces > 1;
   p.prefix_items = pl.fblk * pl.sp;
   p.chunk_rows = a.seqs.paged() && a.seqs.page_size < kN ? a.seqs.page_size : kN;
   const int64_t items =
@@ -948,9 +951,12 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   static int allowed[6][64];
   rc = allow_smem(kern, kSmem, allowed[nk], "prefix_tc: smem attribute");
   if (rc != DSA_OK) return rc;
-  DSA_LAUNCH("prefix_tc", stream, kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p, m, pl.cuts));
+  cudaError_t e = cudaSuccess;
+  DSA_LAUNCH("prefix_tc", stream,
+             e = launch_pdl(kern, dim3((unsigned)items), dim3(kThreads), kSmem, stream, p, m, pl.cuts));
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "prefix_tc: %s", cudaGetErrorString(e));
   rc = check_launch("prefix_tc");
-  if (rc != DSA_OK || pl.merge.pieces == 1) return rc;
+  if (rc != DSA_OK || !p.merged) return rc;
   return launch_prefix_merge(a, pl.merge, stream);
 }
 

@@ -16,7 +16,7 @@
 #include <cuda_fp8.h>
 #include <float.h>
 
-#include "dsa_internal.cuh"
+#include "cache_ops.cuh"
 
 namespace dsa {
 namespace {
@@ -111,6 +111,7 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&f)[V]) {
 template <typename T, int V, int C, bool BLOCK>
 __global__ void __launch_bounds__(!BLOCK ? 256 : C == 4 ? 512 : 1024) add_rmsnorm_kernel(NormParams p) {
   using Raw = typename Vec<T, V>::Raw;
+  griddep_wait();
   const int nthr = BLOCK ? (int)blockDim.x : p.lanes;
   const int me = BLOCK ? (int)threadIdx.x : (int)threadIdx.x & (p.lanes - 1);
   const int64_t row = BLOCK ? (int64_t)blockIdx.x
@@ -134,18 +135,20 @@ __global__ void __launch_bounds__(!BLOCK ? 256 : C == 4 ? 512 : 1024) add_rmsnor
     }
   };
   float ss = 0.f, mx = 0.f;
-  auto stats = [&](int v, const float (&f)[V]) {
+  auto stats = [&](const float (&f)[V], const Raw& rw) {
 #pragma unroll
     for (int i = 0; i < V; ++i) ss = fmaf(f[i], f[i], ss);
     if (e4m3) {
       float w[V];
-      Vec<T, V>::get(__ldg(wr + v), w);
+      Vec<T, V>::get(rw, w);
 #pragma unroll
       for (int i = 0; i < V; ++i) mx = fmaxf(mx, fabsf(f[i] * w[i]));
     }
   };
 
+  // the weight's vectors are read ahead of the stores, which the compiler would not move loads across
   float hv[C > 0 ? C : 1][V];
+  Raw rw[C > 0 ? C : 1];
   if constexpr (C > 0) {
     Raw rx[C], rs[C];
 #pragma unroll
@@ -163,6 +166,11 @@ __global__ void __launch_bounds__(!BLOCK ? 256 : C == 4 ? 512 : 1024) add_rmsnor
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int v = me + c * nthr;
+      if (v < p.nvec) rw[c] = wr[v];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int v = me + c * nthr;
       if (v < p.nvec) {
         Vec<T, V>::get(rx[c], hv[c]);
         if (rr) {
@@ -171,13 +179,13 @@ __global__ void __launch_bounds__(!BLOCK ? 256 : C == 4 ? 512 : 1024) add_rmsnor
 #pragma unroll
           for (int i = 0; i < V; ++i) hv[c][i] += g[i];
         }
-        stats(v, hv[c]);
+        stats(hv[c], rw[c]);
       }
     }
   } else {
     for (int v = me; v < p.nvec; v += nthr) {
       load_h(v, hv[0]);
-      stats(v, hv[0]);
+      stats(hv[0], wr[v]);
     }
   }
 
@@ -213,11 +221,11 @@ __global__ void __launch_bounds__(!BLOCK ? 256 : C == 4 ? 512 : 1024) add_rmsnor
 
   Raw* ho = p.h ? reinterpret_cast<Raw*>(static_cast<T*>(p.h) + r * p.d) : nullptr;
   Raw* yo = p.y ? reinterpret_cast<Raw*>(static_cast<T*>(p.y) + r * p.d) : nullptr;
-  auto finish = [&](int v, const float (&f)[V], bool in) {
+  auto finish = [&](int v, const float (&f)[V], const Raw& rw, bool in) {
     float y[V];
     if (in) {
       float w[V];
-      Vec<T, V>::get(__ldg(wr + v), w);
+      Vec<T, V>::get(rw, w);
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = f[i] * rstd * w[i];
       if (live) {
@@ -256,13 +264,16 @@ __global__ void __launch_bounds__(!BLOCK ? 256 : C == 4 ? 512 : 1024) add_rmsnor
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int v = me + c * nthr;
-      finish(v, hv[c], v < p.nvec);
+      finish(v, hv[c], rw[c], v < p.nvec);
     }
   } else {
     for (int v0 = 0; v0 < p.nvec; v0 += nthr) {  // whole warps take part in the group shuffles
       const int v = v0 + me;
-      if (v < p.nvec) load_h(v, hv[0]);
-      finish(v, hv[0], v < p.nvec);
+      if (v < p.nvec) {
+        load_h(v, hv[0]);
+        rw[0] = wr[v];
+      }
+      finish(v, hv[0], rw[0], v < p.nvec);
     }
   }
 }
@@ -277,9 +288,8 @@ cudaError_t launch(NormParams p, cudaStream_t s) {
     p.lanes = lanes;
     const int rows = 256 / lanes;
     const unsigned grid = (unsigned)((p.rows + rows - 1) / rows);
-    if (p.nvec <= lanes) add_rmsnorm_kernel<T, V, 1, false><<<grid, 256, 0, s>>>(p);
-    else add_rmsnorm_kernel<T, V, 4, false><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.nvec <= lanes) return launch_pdl(add_rmsnorm_kernel<T, V, 1, false>, dim3(grid), dim3(256), 0, s, p);
+    return launch_pdl(add_rmsnorm_kernel<T, V, 4, false>, dim3(grid), dim3(256), 0, s, p);
   }
   // few rows: as many threads as there are vectors (latency); many rows: 4 vectors a thread
   const bool few = p.rows <= 4 * num_sms();
@@ -288,11 +298,10 @@ cudaError_t launch(NormParams p, cudaStream_t s) {
   const int thr = C ? ((p.nvec + C - 1) / C + 31) / 32 * 32 : 1024;
   const unsigned grid = (unsigned)p.rows;
   switch (C) {
-    case 1: add_rmsnorm_kernel<T, V, 1, true><<<grid, thr, 0, s>>>(p); break;
-    case 4: add_rmsnorm_kernel<T, V, 4, true><<<grid, thr, 0, s>>>(p); break;
-    default: add_rmsnorm_kernel<T, V, 0, true><<<grid, thr, 0, s>>>(p); break;
+    case 1: return launch_pdl(add_rmsnorm_kernel<T, V, 1, true>, dim3(grid), dim3(thr), 0, s, p);
+    case 4: return launch_pdl(add_rmsnorm_kernel<T, V, 4, true>, dim3(grid), dim3(thr), 0, s, p);
+    default: return launch_pdl(add_rmsnorm_kernel<T, V, 0, true>, dim3(grid), dim3(thr), 0, s, p);
   }
-  return cudaGetLastError();
 }
 
 bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -466,3 +466,87 @@ def test_a_layer_that_evicts(quant):
     # while a cache holds no more positions than top_k, dense and sparse attention agree
     dense, dl = dsa.prefix_mla_attn(P2, d["q"], r.kv)
     assert (dl - l2).min() >= -2e-3  # the dense sum has every key
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,q_lens", [(0, [1, 1, 1]), (64, [2, 1, 2])])
+def test_kernels_behind_one_another(page, q_lens):
+    """Each operator right behind the one that writes its input, no wait between them on the host, in a stream and as
+    a captured graph that joins a copy on another stream: the same bytes as with a device-wide wait after each."""
+    import sparse_attention_lightning_gb300 as dsa
+    from sparse_attention_lightning_gb300 import workloads as W
+    dims = dict(h_idx=64, d_idx=128, h=128, d_c=512, d_rope=64, top_k=256)
+    cfg = W.custom(q_lens, [900, 300, 2000], idx_dtype="e4m3", kv_dtype="bf16", **dims)
+    d = {k: v.cuda() for k, v in W.make_case(cfg, 8).tensors().items()}
+    g = torch.Generator().manual_seed(3)
+    kw, rows = {}, cfg.total_k
+    if page:
+        n = [-(-L // page) for L in cfg.k_lens]
+        order = torch.randperm(sum(n), generator=g).to(torch.int32)
+        table = torch.full((3, max(n)), -1, dtype=torch.int32)
+        for b in range(3):
+            table[b, :n[b]] = order[sum(n[:b]):sum(n[:b + 1])]
+        kw, rows = dict(block_table=table.cuda(), page_size=page, num_pages=sum(n)), sum(n) * page
+    P = dsa.Problem.from_config(cfg, d["cu_q"], d["cu_k"], **kw)
+    kv0 = (torch.randn(rows, 576, generator=g) / 24).to(BF).cuda()
+    proj0 = torch.randn(rows, 128, generator=g).to(BF).cuda()
+    prompt = (torch.randn(500, 576, generator=g) / 24).to(BF).cuda()
+    gamma, wide = torch.full((128,), 0.1, dtype=BF).cuda(), torch.full((576,), 0.04, dtype=BF).cuda()
+    small = W.custom(q_lens, [min(L, 400) for L in cfg.k_lens], idx_dtype="e4m3", kv_dtype="bf16", **dims)
+    cu_small = torch.zeros(4, dtype=torch.int32, device="cuda")
+    P2 = dsa.Problem.from_config(small, d["cu_q"], cu_small)
+    ws = [dsa.Workspace(nbytes=n) for n in (P.workspace_size(_abi.OP_FUSED_FORWARD), P.workspace_size(_abi.OP_ATTN_WEIGHTS),
+                                            16384, P2.workspace_size(_abi.OP_PREFIX_MLA_ATTN))]
+    kv, proj = kv0.clone(), proj0.clone()
+
+    def step(i, wait):
+        proj.copy_(proj0).mul_(1 + i)
+        _, _, k_idx, k_scale = dsa.add_rmsnorm(proj, gamma, quant="e4m3")
+        wait()
+        y, kv_new, _, _ = dsa.add_rmsnorm(kv, wide, residual=kv0)
+        wait()
+        out, lse, idx, _ = dsa.fused_forward(P, d["q_idx"], k_idx, d["w"], d["q"], y, d["q_scale"], k_scale, ws=ws[0])
+        wait()
+        acc = torch.zeros(3, P.max_k_len, device="cuda")
+        dsa.accumulate_attn_weights(P, d["q"], y, idx, lse, acc, ws=ws[1])
+        wait()
+        r = dsa.evict(P, acc, 400, sink=4, recent=32, kv=y, k_idx=k_idx, k_scale=k_scale, cu_k_out=cu_small,
+                      ws=ws[2]) if not page else None
+        wait()
+        if r is None:
+            out2, lse2 = dsa.prefix_mla_attn(P, d["q"], y, prompt, ws=ws[3])
+        else:
+            out2, lse2 = dsa.prefix_mla_attn(P2, d["q"], r.kv, prompt, ws=ws[3])
+        wait()
+        # the output's rows, normalised by the next launch
+        y2, _, _, _ = dsa.add_rmsnorm(out2, wide[:512])
+        kv.copy_(kv_new)
+        wait()
+        return [k_idx, k_scale, out, lse, idx, acc, out2, lse2, y2] + ([] if r is None else [r.kept, r.kv, r.acc])
+
+    def same(got, want):
+        return all(torch.equal(x.view(torch.uint8) if x.element_size() == 1 else x,
+                               y.view(torch.uint8) if y.element_size() == 1 else y) for x, y in zip(got, want))
+
+    want = [step(i, torch.cuda.synchronize) for i in range(6)]
+    kv.copy_(kv0)
+    got = [step(i, lambda: None) for i in range(6)]
+    torch.cuda.synchronize()
+    assert all(same(x, y) for x, y in zip(got, want))
+    assert not torch.equal(want[0][8], want[1][8])  # the steps differ
+    # captured, behind a copy on a stream that joins
+    kv.zero_()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kv.copy_(kv0)
+        main.wait_stream(side)
+        got = [step(i, lambda: None) for i in range(2)]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(x, y) for x, y in zip(got, want))
+    assert all(w.status() == 0 for w in ws)
