@@ -8,9 +8,10 @@
 //   E4M3:  scale = max|y| / 448 a row, codes = E4M3(y / scale)
 //   MXFP8: 2^e a group of 32, the smallest with max|y| <= 448·2^e, codes = E4M3(y / 2^e)
 //
-// Bound by memory: a row is read once and held in registers as 16-byte vectors between the
-// statistics and the output.  Rows of at most 4 vectors a lane of a warp's share take 8, 16 or 32
-// lanes each (several rows a warp: indexer keys are 128 wide); longer rows take a block.  Both
+// Bound by memory (8192 x 7168 bf16 with a residual: 470 MB in 68 us, 6.9 TB/s), for few rows by the
+// launch: a row is read once and held in registers as 16-byte vectors between the
+// statistics and the output.  Short rows take 8, 16 or 32 lanes each (several rows a warp: indexer
+// keys are 128 wide); longer rows take a block.  Rows without 16-byte alignment go element by element.  Both
 // statistics a row needs (the sum of squares and max |h·w|, from which max |y| follows by the
 // factor rsqrt(...)) are reduced together, so a row costs one reduction.
 #include <cuda_fp8.h>
@@ -282,7 +283,11 @@ template <typename T, int V>
 cudaError_t launch(NormParams p, cudaStream_t s) {
   p.nvec = p.d / V;
   constexpr int kMinLanes = V == 1 ? 32 : 8;  // a group of 32 stays inside a row's lanes
-  if (p.nvec <= 128) {
+  const bool few = p.rows <= 4 * num_sms();
+  // Lanes of a warp for rows of up to 32 vectors, and of up to 128 where there are many (64 rows x 512 bf16: a block
+  // 1.6 us, a warp 2.0; 2,000 rows: 2.8 and 2.5; 16384 rows x 101 fp32: 14.7 and 8.8); as few lanes as there are
+  // vectors (65536 rows x 128 bf16 to MXFP8: 16 lanes 9.7 us, 32 lanes 18.1, a block a row 34.8).
+  if (p.nvec <= 32 || (p.nvec <= 128 && !few)) {
     int lanes = kMinLanes;
     while (lanes < 32 && lanes < p.nvec) lanes *= 2;
     p.lanes = lanes;
@@ -291,16 +296,21 @@ cudaError_t launch(NormParams p, cudaStream_t s) {
     if (p.nvec <= lanes) return launch_pdl(add_rmsnorm_kernel<T, V, 1, false>, dim3(grid), dim3(256), 0, s, p);
     return launch_pdl(add_rmsnorm_kernel<T, V, 4, false>, dim3(grid), dim3(256), 0, s, p);
   }
-  // few rows: as many threads as there are vectors (latency); many rows: 4 vectors a thread
-  const bool few = p.rows <= 4 * num_sms();
-  // (512 threads at most: 128 registers each); longer rows are read twice, the second time from L2
-  const int C = p.nvec <= 1024 && few ? 1 : p.nvec <= 2048 ? 4 : 0;
+  // A block a row.  Few rows: as many threads as there are vectors (64 rows x 1024 bf16: 1.6 us, 4 vectors a thread 2.2);
+  // many: 4 vectors a thread (512 threads at most, 128 registers each; 8192 rows x 7168: 68 us, 1 vector 89).  Single elements
+  // 8 a thread up to 4096, and up to 8192 where there are few rows (4096 rows x 3001 fp32: 46 us, read twice 73; x 5001: 93
+  // and 92); longer rows are read twice, the second time from L2.
+  const int C = p.nvec <= 1024 && few ? 1
+                : p.nvec <= 2048      ? 4
+                : V == 1 && p.nvec <= (few ? 8192 : 4096) ? 8 : 0;
   const int thr = C ? ((p.nvec + C - 1) / C + 31) / 32 * 32 : 1024;
-  const unsigned grid = (unsigned)p.rows;
+  const dim3 grid((unsigned)p.rows);
+  if constexpr (V == 1)
+    if (C == 8) return launch_pdl(add_rmsnorm_kernel<T, V, 8, true>, grid, dim3(thr), 0, s, p);
   switch (C) {
-    case 1: return launch_pdl(add_rmsnorm_kernel<T, V, 1, true>, dim3(grid), dim3(thr), 0, s, p);
-    case 4: return launch_pdl(add_rmsnorm_kernel<T, V, 4, true>, dim3(grid), dim3(thr), 0, s, p);
-    default: return launch_pdl(add_rmsnorm_kernel<T, V, 0, true>, dim3(grid), dim3(thr), 0, s, p);
+    case 1: return launch_pdl(add_rmsnorm_kernel<T, V, 1, true>, grid, dim3(thr), 0, s, p);
+    case 4: return launch_pdl(add_rmsnorm_kernel<T, V, 4, true>, grid, dim3(thr), 0, s, p);
+    default: return launch_pdl(add_rmsnorm_kernel<T, V, 0, true>, grid, dim3(thr), 0, s, p);
   }
 }
 

@@ -117,6 +117,37 @@ def test_odd_lengths(d, dtype, quant):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("quant", [None, "e4m3", "mxfp8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [5, 620])
+@pytest.mark.parametrize("d", [37, 129, 513, 1025, 2049, 3001, 4096, 4097, 8191, 8192, 8193])
+def test_single_elements_and_few_or_many_rows(d, rows, dtype, quant):
+    """Rows that start between 16-byte boundaries (a slice of a wider tensor), each way of sharing them out."""
+    import sparse_attention_lightning_gb300 as dsa
+    if quant == "mxfp8":
+        d = d // 32 * 32
+    g = torch.Generator().manual_seed(d + rows)
+    x, r = (torch.randn(rows, d + 5, generator=g).to(dtype).cuda()[:, 3:3 + d] for _ in range(2))
+    w = torch.randn(d, generator=g).to(dtype).cuda()
+    y, h, codes, scale = dsa.add_rmsnorm(x, w, r, EPS, quant, want_y=True)
+    _check(x, w, r, EPS, quant, y, h, codes, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [None, "e4m3", "mxfp8"])
+@pytest.mark.parametrize("rows", [4, 620])
+@pytest.mark.parametrize("d", [32, 160, 256, 288, 512, 1024, 1056])
+def test_vectors_and_few_or_many_rows(d, rows, quant):
+    import sparse_attention_lightning_gb300 as dsa
+    for dtype in (torch.bfloat16, torch.float32):
+        g = torch.Generator().manual_seed(d + rows)
+        x, r = (torch.randn(rows, d, generator=g).to(dtype).cuda() for _ in range(2))
+        w = torch.randn(d, generator=g).to(dtype).cuda()
+        y, h, codes, scale = dsa.add_rmsnorm(x, w, r, EPS, quant, want_y=True)
+        _check(x, w, r, EPS, quant, y, h, codes, scale)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("off", [0, 8, 3])
 def test_strided_slice_and_shapes(off):
     """A slice of a wider projection (aligned and not), leading dimensions, index-key rows."""
