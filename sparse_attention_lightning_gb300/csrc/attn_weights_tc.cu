@@ -14,8 +14,8 @@
 // K-step); four warps take the exponentials from two logit buffers in turn.  The query block comes through
 // the same ring as one or two chunks of 64 heads and is copied to tensor memory from there: read row by row
 // from global memory (a thread a head, 1152 bytes apart) it took 16,000 clocks before the first MMA.
-// Every CTA takes one contiguous, equal share of all queries' chunks, so that few queries fill the SMs;
-// where a share crosses queries, the query block is loaded again.  Every wait is bounded (DSA_FLAG_TIMEOUT).
+// Every CTA takes a contiguous share of all queries' chunks, so that few queries fill the SMs;
+// where a share crosses queries, the query block is loaded again (see the launcher).  Every wait is bounded (DSA_FLAG_TIMEOUT).
 // Decode step of 32 queries x 2048 rows of 1152 B, 128 heads: 21.6 us, 75.5 MB gathered at about the measured copy
 // rate once it has started; the start (launch, row lookup, first indices, query) is about 5 us.
 #include "attn_weights.cuh"
@@ -37,8 +37,10 @@ constexpr int kSCol = 0, kQCol = 128;  // tensor memory: 2 x 64 logit columns, 2
 
 struct Params {
   WeightArgs a;
-  int chunks;   // of a query
-  int ntile;    // column tiles
+  uint32_t chunks; // of a query
+  int ntile;       // column tiles
+  uint32_t split;  // units a query's chunks are split into
+  uint32_t per;    // consecutive units of a CTA
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -61,26 +63,28 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
-// The k-th piece of this CTA's share: chunks [c0, c1) of query row t; false past the end.
+// The k-th piece of this CTA's units: chunks [c0, c1) of query row t; false past the end.
 struct Piece {
   int t, c0, c1;
 };
 __device__ __forceinline__ bool piece_at(const Params& p, int k, Piece& pc) {
-  const int64_t tot = (int64_t)p.a.seqs.total_q * p.chunks;
-  const int64_t x0 = tot * blockIdx.x / gridDim.x, x1 = tot * (blockIdx.x + 1) / gridDim.x;
-  const int64_t t = x0 / p.chunks + k, r0 = t * p.chunks;
+  // (32 bits: the launcher keeps the units below 2^31; 64-bit divisions took 0.6 us ahead of the first copy)
+  const uint32_t tot = (uint32_t)p.a.seqs.total_q * p.split;
+  const uint32_t x0 = blockIdx.x * (uint32_t)p.per, x1 = min(x0 + p.per, tot);
+  const uint32_t t = x0 / p.split + k, r0 = t * p.split;
   if (r0 >= x1) return false;
   pc.t = (int)t;
-  pc.c0 = k == 0 ? (int)(x0 - r0) : 0;
-  pc.c1 = (int)min((int64_t)p.chunks, x1 - r0);
+  pc.c0 = k == 0 ? (int)((x0 - r0) * p.chunks / p.split) : 0;
+  pc.c1 = (int)(min((uint32_t)p.split, x1 - r0) * p.chunks / p.split);
   return true;
 }
 
-// query_row_info by a whole warp: a 32-way search over cu_q (one round of loads up to 32 sequences).
+// query_row_info by a whole warp: a 32-way search over cu_q, whose last round loads all that is needed of
+// the sequence (one round of loads up to 32 sequences).
 __device__ __forceinline__ bool warp_row_info(const WeightArgs& a, int t, int lane, RowInfo& r) {
   const Seqs& s = a.seqs;
   int lo = 0, hi = s.B;  // the last b with cu_q[b] <= t is in [lo, hi)
-  while (hi - lo > 1) {
+  while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32;
     const int probe = lo + lane * step;
     const bool le = probe < hi && (lane == 0 || s.cu_q[probe] <= t);
@@ -88,15 +92,21 @@ __device__ __forceinline__ bool warp_row_info(const WeightArgs& a, int t, int la
     lo += m * step;
     hi = min(hi, lo + step);
   }
-  const int q0 = s.cu_q[lo], q1 = s.cu_q[lo + 1];
-  const int k0 = s.cu_k[lo], k1 = s.cu_k[lo + 1];
+  const int b = min(lo + lane, hi - 1);
+  int q0 = s.cu_q[b], q1 = s.cu_q[b + 1], k0 = s.cu_k[b], k1 = s.cu_k[b + 1];
+  const unsigned le = __ballot_sync(0xffffffffu, lo + lane < hi && (lane == 0 || q0 <= t));
+  const int m = 31 - __clz(le);
+  q0 = __shfl_sync(0xffffffffu, q0, m);
+  q1 = __shfl_sync(0xffffffffu, q1, m);
+  k0 = __shfl_sync(0xffffffffu, k0, m);
+  k1 = __shfl_sync(0xffffffffu, k1, m);
   const int T = q1 - q0, L = k1 - k0;
   if (!(t >= q0 && t < q1 && T <= L && k0 >= 0 && k1 <= s.total_k && L <= s.max_k_len && q1 <= s.total_q &&
         T <= a.max_q_len)) {  // (the order of additions and fx_scale rest on max_q_len)
     atomicOr(a.status, DSA_FLAG_BAD_SEQS);
     return false;
   }
-  r = RowInfo{lo, L - T + (t - q0), k0, L};
+  r = RowInfo{lo + m, L - T + (t - q0), k0, L};
   return true;
 }
 
@@ -174,8 +184,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
         return lane < 16 && i < a.top_k ? a.idx[(int64_t)pc.t * a.top_k + i] : -1;
       };
       int v0 = load_idx(pc.c0), v1 = load_idx(pc.c0 + 1);
-      if (!warp_row_info(a, pc.t, lane, ri)) continue;
-      // the query block, 64 heads a chunk of the ring
+      // the query block, 64 heads a chunk of the ring (ahead of the row's lookup: it is consumed in any case)
       for (int c = 0; c < qchunks && !stop; ++c, ++n) {
         if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
           stop = true;
@@ -190,6 +199,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
         if (++slot == kStages) { slot = 0; phase ^= 1; }
       }
       if (stop) break;
+      if (!warp_row_info(a, pc.t, lane, ri)) continue;
       const bool paged = a.seqs.paged();
       const int sh = paged ? __ffs(a.seqs.page_size) - 1 : 0;
       const int32_t* table = a.seqs.block_table + (int64_t)ri.b * a.seqs.max_pages;
@@ -248,14 +258,14 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
     Piece pc;
     for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
       RowInfo ri;
-      if (!warp_row_info(a, pc.t, lane, ri)) continue;
+      const bool ok = warp_row_info(a, pc.t, lane, ri);
       if (!__all_sync(0xffffffffu, mbar_wait(q_full, qn & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) break;
       ++qn;
       for (int c = 0; c < qchunks; ++c) {  // the query has left the ring for tensor memory
         if (lane == 0) mbar_arrive(&k_empty[slot]);
         if (++slot == kStages) { slot = 0; phase ^= 1; }
       }
-      for (int c = pc.c0; c < pc.c1; ++c, ++n) {
+      for (int c = pc.c0; ok && c < pc.c1; ++c, ++n) {
         if (!__all_sync(0xffffffffu,
                         mbar_wait(&s_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) &&
                             mbar_wait(&k_full[slot], phase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
@@ -297,7 +307,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
     Piece pc;
     for (int k = 0; !stop && piece_at(p, k, pc); ++k) {
       RowInfo ri;
-      if (!warp_row_info(a, pc.t, lane, ri)) continue;
+      const bool ok = warp_row_info(a, pc.t, lane, ri);
       // this warp's 32 heads of the query block, from the ring to tensor memory (the previous piece's
       // logits are complete: its last chunk has been read)
       const int qc = quarter >> 1;
@@ -318,7 +328,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
           tmem_st32(lane_base + kQCol + t * 32, w);
         }
       }
-      slot += qchunks + pc.c1 - pc.c0;  // the piece's place in the ring is passed
+      slot += qchunks + (ok ? pc.c1 - pc.c0 : 0);  // the piece's place in the ring is passed
       phase ^= (slot / kStages) & 1;
       slot %= kStages;
       const int64_t flat = (int64_t)pc.t * a.h + min(h, a.h - 1);
@@ -329,7 +339,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
       const float lse = h < a.h ? a.lse[flat] : -INFINITY;
       const bool dead = lse == -INFINITY;  // no such head, or it attended to nothing: it adds nothing
       const float lse2 = dead ? 0.f : lse * kLog2e;
-      for (int c = pc.c0; c < pc.c1; ++c, ++n) {
+      for (int c = pc.c0; ok && c < pc.c1; ++c, ++n) {
         // threads 0..63 add up and store one selected position each
         int pos = -1;
         if (et < kN) {
@@ -391,9 +401,25 @@ int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.ntile = (a.d + 63) / 64;
-  p.chunks = (a.top_k + kN - 1) / kN;
-  const int64_t tot = (int64_t)a.seqs.total_q * p.chunks;
-  const int grid = (int)(tot < num_sms() ? tot : num_sms());
+  // Shares.  A query block costs about two chunks each time a CTA loads one (it comes through the ring).  So queries
+  // are split into units, and a CTA takes `per` consecutive ones: the fewest chunks and query blocks a CTA.
+  // (Contiguous equal shares of all chunks: 32 queries x 32 chunks on 152 SMs are 7 chunks and two queries for 31 of
+  // them, which end 3 us behind the others; 4 CTAs a query with 8 chunks each end together.)
+  const int64_t chunks = (a.top_k + kN - 1) / kN;
+  int64_t best = -1;
+  for (int64_t s = 1; s <= chunks; ++s) {
+    const int64_t units = a.seqs.total_q * s, n = (units + num_sms() - 1) / num_sms();
+    if (s > 1 && units >= int64_t(1) << 30) break;
+    const int64_t blocks = s % n == 0 ? 1 : n % s == 0 ? n / s : (n - 2) / s + 2;
+    const int64_t cost = (n * chunks + s - 1) / s + 2 * blocks;
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.split = (uint32_t)s;
+      p.per = (uint32_t)n;
+    }
+  }
+  p.chunks = (uint32_t)chunks;
+  const int grid = (int)(((int64_t)a.seqs.total_q * p.split + p.per - 1) / p.per);
   const int smem = kStages * p.ntile * kTile + kMetaBytes + 1024;
   CUtensorMap qmap, kvmap;
   int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, (uint64_t)a.d,
