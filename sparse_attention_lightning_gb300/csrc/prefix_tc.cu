@@ -88,6 +88,12 @@ struct Item {
   int hoff;                  // head of the block's first row
 };
 
+// floor(n · a / of), a <= of (in 32 bits where it fits: with 64-bit divisions here 64 sequences' call took 0.6 us more).
+__device__ __forceinline__ int part(int n, uint32_t a, int of) {
+  if (n < 65536 && of < 65536) return (int)((uint32_t)n * a / (uint32_t)of);
+  return (int)((int64_t)n * a / of);
+}
+
 // False: nothing to do (a block past its sequence's rows, an inconsistent sequence).
 __device__ __forceinline__ bool item_at(const Params& p, const Cuts& cuts, int i, Item& it) {
   const int pch = (p.a.prefix_len + kN - 1) / kN;
@@ -115,8 +121,8 @@ __device__ __forceinline__ bool item_at(const Params& p, const Cuts& cuts, int i
     it.b = -1;
     it.rows = (int)min((int64_t)kM, (int64_t)p.a.seqs.total_q * p.a.h - it.row0);
     it.ncp = pch;
-    it.c0 = p.nseg ? (int)sg.a : (int)((int64_t)pch * split / p.sp);
-    it.c1 = p.nseg ? (int)sg.b : (int)((int64_t)pch * (split + 1) / p.sp);
+    it.c0 = p.nseg ? (int)sg.a : part(pch, split, p.sp);
+    it.c1 = p.nseg ? (int)sg.b : part(pch, split + 1, p.sp);
     it.k0 = it.pos0 = it.hoff = 0;
     return true;
   }
@@ -125,18 +131,19 @@ __device__ __forceinline__ bool item_at(const Params& p, const Cuts& cuts, int i
   it.split = p.fblk || (p.nseg ? sg.a > 0 || (int)sg.b < p.ns : p.ss > 1);
   SeqInfo s;
   if (!prefix_seq(p.a, it.b, s)) return false;
-  const int64_t r0 = (int64_t)(blk - it.b * p.nblk) * kM, nrow = (int64_t)s.T * p.a.h;
+  // (32 bits: total_q · h is below 2^31)
+  const uint32_t h = p.a.h, r0 = (uint32_t)(blk - it.b * p.nblk) * kM, nrow = s.T * h;
   if (r0 >= nrow) return false;
   it.row0 = (int64_t)s.q0 * p.a.h + r0;
-  it.rows = (int)min((int64_t)kM, nrow - r0);
+  it.rows = (int)min((uint32_t)kM, nrow - r0);
   it.ncp = p.fblk ? 0 : pch;
   it.k0 = s.k0;
-  it.pos0 = s.L - s.T + (int)(r0 / p.a.h);
-  it.hoff = (int)(r0 % p.a.h);
-  const int last = s.L - s.T + (int)((r0 + it.rows - 1) / p.a.h);
+  it.pos0 = s.L - s.T + (int)(r0 / h);
+  it.hoff = (int)(r0 % h);
+  const int last = s.L - s.T + (int)((r0 + it.rows - 1) / h);
   const int n = it.ncp + last / kN + 1;
-  it.c0 = p.nseg ? (int)((int64_t)n * sg.a / p.ns) : (int)((int64_t)n * split / p.ss);
-  it.c1 = p.nseg ? (int)((int64_t)n * sg.b / p.ns) : (int)((int64_t)n * (split + 1) / p.ss);
+  it.c0 = p.nseg ? part(n, sg.a, p.ns) : part(n, split, p.ss);
+  it.c1 = p.nseg ? part(n, sg.b, p.ns) : part(n, split + 1, p.ss);
   return true;
 }
 
