@@ -535,7 +535,7 @@ def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
 
     P describes the sequences behind the prefix.  The prefix is prefix_kv [prefix_len, D], or, in a
     paged cache, the pages prefix_table [>= ceil(prefix_len / page_size)] int32 of kv; without
-    either there is none."""
+    either there is none.  A captured call needs ws."""
     if not kv.is_cuda:
         raise ValueError("kv must be a CUDA tensor")
     index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
@@ -591,7 +591,7 @@ def prefix_mla_attn(P: Problem, q, kv, prefix_kv=None, prefix_table=None,
 def accumulate_attn_weights(P: Problem, q, kv, idx, lse, acc, ws: Optional[Workspace] = None):
     """Add the attention weight every selected position received, summed over heads and queries,
     to acc [B, >= max_k_len] f32 in place (dsa_accumulate_attn_weights); returns acc.  idx and lse
-    are those of sparse_mla_attn or fused_forward on the same q and kv."""
+    are those of sparse_mla_attn or fused_forward on the same q and kv.  A captured call needs ws."""
     if not kv.is_cuda:
         raise ValueError("kv must be a CUDA tensor")
     index, dts = kv.get_device(), _TORCH_DT[P.kv_dtype]
@@ -649,7 +649,7 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
     the result; allocated where None) or, with block_table_out [B, pages] int32, paged with P's
     page size (the *_out tensors are then required; they may be the source's pool, on other pages).
     acc_out [B, >= budget] receives the kept positions' acc and zeros behind them up to column
-    budget."""
+    budget.  A captured call needs ws."""
     if not acc.is_cuda:
         raise ValueError("acc must be a CUDA tensor")
     if acc.get_device() != _current_device():
