@@ -33,7 +33,8 @@ constexpr int kMaxTiles = 9;
 constexpr int kStages = 3;
 constexpr int kProducers = 4;          // warps
 constexpr int kThreads = 32 * (kProducers + 1 + 4);
-constexpr int kMetaBytes = 4096 + 256; // barriers, the warps' sums
+constexpr int kSums = 4;               // chunks whose sums the weights warps hold: buffers, and a barrier each
+constexpr int kMetaBytes = kSums * 4 * kN * 4 + 256; // the warps' sums, barriers
 constexpr int kSCol = 0, kQCol = 128;  // tensor memory: 2 x 64 logit columns, 288 query columns
 
 struct Params {
@@ -148,17 +149,19 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
   uint64_t* drain = bars + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 13);
-  uint64_t* red_full = bars + 14;   // [2] 4 warps have stored a chunk's sums
-  // [4][4][64] the warps' sums, by chunk: a warp may be up to two chunks ahead of the threads that read them
-  float* red = reinterpret_cast<float*>(bars + 16);
+  // [kSums] 4 warps have stored a chunk's sums.  A warp frees a chunk's logits before it stores its sums, so one that reads
+  // none may be two chunks ahead of a reader that has yet to arrive for its own: with two barriers it would arrive in
+  // that reader's place.  With four it comes back to the same one for chunk n + 4, whose logits need chunk
+  // n + 2's freed by every warp, each of which has then passed chunk n.
+  uint64_t* red_full = bars + 14;
+  float* red = reinterpret_cast<float*>(bars + 14 + kSums);  // [kSums][4][64] the warps' sums
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) { mbar_init(&k_full[i], kProducers); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4); }
     mbar_init(q_full, 4);
-    mbar_init(&red_full[0], 4);
-    mbar_init(&red_full[1], 4);
+    for (int i = 0; i < kSums; ++i) mbar_init(&red_full[i], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -352,7 +355,7 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (n >> 1) & 1, abort_flag, a.status,
                                                DSA_FLAG_TIMEOUT))) { stop = true; break; }
         tc_fence_after();
-        float* mine = red + (n & 3) * 256 + quarter * 64;
+        float* mine = red + (n % kSums) * (4 * kN) + quarter * kN;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t s[32];
@@ -372,13 +375,13 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
           mine[half * 32 + lane] = transpose_add(x, lane);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&red_full[n & 1]);
+        if (lane == 0) mbar_arrive(&red_full[n % kSums]);
         if (et >= kN) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(&red_full[n & 1], (n >> 1) & 1, abort_flag, a.status,
+        if (!__all_sync(0xffffffffu, mbar_wait(&red_full[n % kSums], (n / kSums) & 1, abort_flag, a.status,
                                                DSA_FLAG_TIMEOUT))) { stop = true; break; }
         if (pos >= 0) {
-          const float* r = red + (n & 3) * 256 + et;
-          add_weight(a, ri.b, pos, (r[0] + r[64]) + (r[128] + r[192]));
+          const float* r = red + (n % kSums) * (4 * kN) + et;
+          add_weight(a, ri.b, pos, (r[0] + r[kN]) + (r[2 * kN] + r[3 * kN]));
         }
       }
     }
