@@ -332,6 +332,8 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
           tmem_st32(lane_base + kQCol + t * 32, w);
         }
       }
+      int lslot = slot + qchunks - 1, lphase = phase;  // the query block's last chunk
+      if (lslot >= kStages) { lslot -= kStages; lphase ^= 1; }
       slot += qchunks + (ok ? pc.c1 - pc.c0 : 0);  // the piece's place in the ring is passed
       phase ^= (slot / kStages) & 1;
       slot %= kStages;
@@ -339,11 +341,17 @@ attn_weights_tc_kernel(const __grid_constant__ Params p, const __grid_constant__
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
+      if (!ok) {
+        // No logits follow to wait for, and a warp that went on could arrive for the next query before the others
+        // have for this one: the MMA warp releases the block once all four have.
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[lslot], lphase, abort_flag, a.status, DSA_FLAG_TIMEOUT))) break;
+        continue;
+      }
       griddep_wait();  // the sums are zero (and written: the kernels behind this one wait for it alone)
       const float lse = h < a.h ? a.lse[flat] : -INFINITY;
       const bool dead = lse == -INFINITY;  // no such head, or it attended to nothing: it adds nothing
       const float lse2 = dead ? 0.f : lse * kLog2e;
-      for (int c = pc.c0; ok && c < pc.c1; ++c, ++n) {
+      for (int c = pc.c0; c < pc.c1; ++c, ++n) {
         // threads 0..63 add up and store one selected position each
         int pos = -1;
         if (et < kN) {

@@ -80,3 +80,49 @@ def test_two_barriers_for_four_buffers_can_be_overtaken():
 def test_sums_are_read_after_they_are_stored():
     n = constant("kSums")
     assert sums(n, n) is None
+
+
+def queries(good, qchunks, waits, slots, chunks=1):
+    """Queries one after another in a CTA, each a block of qchunks chunks of the ring and, where its sequence is good,
+    `chunks` chunks of rows.  waits: on a refused query, the weights warps wait for the release of its block."""
+    warps = 4
+    counts = {("k_full", i): 1 for i in range(slots)} | {("k_empty", i): 1 for i in range(slots)}
+    counts |= {("s_full", i): 1 for i in (0, 1)} | {("s_empty", i): warps for i in (0, 1)}
+    counts["q_full", 0] = warps
+    producer, mma, weigh = [], [], [[] for _ in range(warps)]
+    use = n = 0  # chunks that went through the ring; chunks of rows
+    for t, ok in enumerate(good):
+        block = [(use + c) % slots for c in range(qchunks)]
+        for c in range(qchunks + (chunks if ok else 0)):
+            slot, turn = (use + c) % slots, (use + c) // slots
+            producer += [("wait", ("k_empty", slot), (turn & 1) ^ 1), ("put", ("ring", slot), (t, c)),
+                         ("arrive", ("k_full", slot), None)]
+        mma.append(("wait", ("q_full", 0), t & 1))
+        mma += [("arrive", ("k_empty", s), None) for s in block]
+        for w, p in enumerate(weigh):
+            c = w // 2  # heads 32 w ..: in the block's first or second chunk, or (few heads) in none
+            if c < qchunks:
+                p += [("wait", ("k_full", block[c]), ((use + c) // slots) & 1), ("read", ("ring", block[c]), (t, c))]
+            p.append(("arrive", ("q_full", 0), None))
+            if not ok and waits:
+                p.append(("wait", ("k_empty", block[-1]), ((use + qchunks - 1) // slots) & 1))
+        use += qchunks
+        for _ in range(chunks if ok else 0):
+            slot, turn = use % slots, use // slots
+            mma += [("wait", ("s_empty", n & 1), ((n >> 1) & 1) ^ 1), ("wait", ("k_full", slot), turn & 1),
+                    ("arrive", ("k_empty", slot), None), ("arrive", ("s_full", n & 1), None)]
+            for p in weigh:
+                p += [("wait", ("s_full", n & 1), (n >> 1) & 1), ("arrive", ("s_empty", n & 1), None)]
+            use, n = use + 1, n + 1
+    return explore([producer, mma] + weigh, counts)
+
+
+@pytest.mark.parametrize("qchunks", [1, 2])
+def test_refused_queries_can_be_overtaken_without_a_wait(qchunks):
+    assert queries([False] * 4 + [True], qchunks, False, 3) is not None
+
+
+@pytest.mark.parametrize("good", ["0000", "00010", "10010", "01011", "1111"])
+@pytest.mark.parametrize("qchunks", [1, 2])
+def test_refused_queries_keep_the_ring_in_order(good, qchunks):
+    assert queries([g == "1" for g in good], qchunks, True, constant("kStages")) is None

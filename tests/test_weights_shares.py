@@ -48,3 +48,31 @@ def test_several_queries_a_cta(q_lens, k, h, d_c, d_rope):
     split, per = shares(sum(q_lens), k)
     assert per > split or per % split  # CTAs with more than one query
     run_twice(Weights(q_lens, [700 + T for T in q_lens], h, d_c, d_rope, k, BF, seed=k + h))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h,d_c,d_rope", [(16, 512, 64), (128, 512, 64), (64, 64, 16), (100, 64, 16)])
+@pytest.mark.parametrize("T,n,k", [(1, 600, 100), (1, 608, 40), (20, 15, 130)])
+def test_refused_queries_between_good_ones(T, n, k, h, d_c, d_rope):
+    """Sequences with more queries than positions: their rows stay as they were, the others' get the same bytes.  (Paged:
+    a longer neighbour keeps its rows.)"""
+    import sparse_attention_lightning_gb300 as dsa
+    from sparse_attention_lightning_gb300 import _abi
+    split, per = shares(T * n, k)
+    assert per > split
+    s = Weights([T] * n, [90] * (n - 1) + [900], h, d_c, d_rope, k, BF, 16, seed=T + h)
+    lse, idx, acc0 = s.attention(), s.idx.cuda(), torch.rand(n, 900).cuda()
+    ref = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, idx, lse, acc0.clone())
+    cu = s.prob.cu_k.cpu()
+    refused = [b for b in range(n - 4) if b % 9 in (2, 3, 4, 5) or (T > 1 and b % 3 == 1)]
+    for b in range(n - 1):  # refused sequences hold T - 1 positions, the next good one what is left over
+        if b in refused:
+            cu[b + 1] = cu[b] + T - 1
+    s.prob.cu_k.copy_(cu)
+    for _ in range(4):
+        ws = dsa.Workspace()
+        got = dsa.accumulate_attn_weights(s.prob, s.q, s.kv, idx, lse, acc0.clone(), ws=ws)
+        assert ws.status() == _abi.DSA_FLAG_BAD_SEQS
+        for b in range(n):
+            want = acc0[b] if b in refused else ref[b]
+            assert torch.equal(got[b], want), b
