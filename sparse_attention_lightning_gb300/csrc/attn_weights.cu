@@ -121,11 +121,12 @@ __global__ void __launch_bounds__(256) attn_weights_finish_kernel(WeightArgs a, 
 
 template <typename TK>
 int launch_typed(const WeightArgs& a, cudaStream_t stream) {
-  const size_t smem = sizeof(float) * ((size_t)(kKeys + kHeads) * (a.d + 4) + kHeads * kKeys);
+  auto bytes = [](int D) constexpr { return (int)sizeof(float) * ((kKeys + kHeads) * (D + 4) + kHeads * kKeys); };
+  const int smem = bytes(a.d);
   auto kern = attn_weights_simt_kernel<TK>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return check_launch("attn_weights_simt: smem attribute");
+  static std::atomic<bool> allowed[64];
+  const int rc = allow_smem<bytes(kMaxWidth)>(kern, allowed, "attn_weights_simt: smem attribute");
+  if (rc != DSA_OK) return rc;
   dim3 grid((unsigned)a.seqs.total_q, (unsigned)((a.top_k + kKeys - 1) / kKeys));
   DSA_LAUNCH("attn_weights_simt", stream, kern<<<grid, kThreads, smem, stream>>>(a));
   return check_launch("attn_weights_simt");

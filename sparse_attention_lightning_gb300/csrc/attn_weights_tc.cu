@@ -37,6 +37,8 @@ constexpr int kSums = 4;               // chunks whose sums the weights warps ho
 constexpr int kMetaBytes = kSums * 4 * kN * 4 + 256; // the warps' sums, barriers
 constexpr int kSCol = 0, kQCol = 128;  // tensor memory: 2 x 64 logit columns, 288 query columns
 
+constexpr int smem_bytes(int ntile) { return kStages * ntile * kTile + kMetaBytes + 1024; }
+
 struct Params {
   WeightArgs a;
   uint32_t chunks; // of a query
@@ -432,7 +434,7 @@ int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   }
   p.chunks = (uint32_t)chunks;
   const int grid = (int)(((int64_t)a.seqs.total_q * p.split + p.per - 1) / p.per);
-  const int smem = kStages * p.ntile * kTile + kMetaBytes + 1024;
+  const int smem = smem_bytes(p.ntile);
   CUtensorMap qmap, kvmap;
   int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, (uint64_t)a.d,
                         (uint64_t)a.seqs.total_q * a.h, (uint64_t)a.d * 2, 64, kN);
@@ -440,8 +442,8 @@ int launch_attn_weights_tc(const WeightArgs& a, cudaStream_t stream) {
   rc = make_tmap_2d(&kvmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, (uint64_t)a.d,
                         (uint64_t)a.seqs.cache_rows(), (uint64_t)a.d * 2, 64, 1);
   if (rc != DSA_OK) return rc;
-  static int allowed[64];
-  rc = allow_smem(attn_weights_tc_kernel, smem, allowed, "attn_weights_tc: smem attribute");
+  static std::atomic<bool> allowed[64];
+  rc = allow_smem<smem_bytes(kMaxTiles)>(attn_weights_tc_kernel, allowed, "attn_weights_tc: smem attribute");
   if (rc != DSA_OK) return rc;
   cudaError_t e = cudaSuccess;
   DSA_LAUNCH("attn_weights_tc", stream,

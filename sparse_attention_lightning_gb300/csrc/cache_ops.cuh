@@ -1,12 +1,15 @@
 // What the operators around the caches share: constants, tensor maps of column tiles, shared-memory limits.
 #pragma once
 
+#include <atomic>
+
 #include "dsa_internal.cuh"
 
 namespace dsa {
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxWidth = 1024 + 256;  // of a latent row (d_c + d_rope)
 
 // Kernels launched with launch_pdl read what the kernels before them wrote by ordinary loads, behind
 // griddep_wait(): the read-only path (__ldg) is for data that nobody changes while the grid runs, and its loads may
@@ -27,17 +30,19 @@ __device__ __forceinline__ int cache_row(const Seqs& s, int b, int k0, int pos) 
 int make_tmap_tiles(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t tiles,
                     uint64_t rows, uint64_t row_bytes, uint32_t box_tiles, uint32_t box_rows);
 
-// Allow `kern` `bytes` of dynamic shared memory; asked of the runtime once for a kernel (its slot:
-// one static array a kernel), device and size.
-template <typename K>
-inline int allow_smem(K kern, int bytes, int (&slot)[64], const char* what) {
+// Allow `kern` BYTES of dynamic shared memory, the most that any of its launches asks for: launches of other host
+// threads, with other sizes, then never find a smaller limit.  Asked of the runtime once for a kernel (its slot:
+// one static array a kernel) and device.
+template <int BYTES, typename K>
+inline int allow_smem(K kern, std::atomic<bool> (&slot)[64], const char* what) {
+  static_assert(BYTES <= 232448, "shared memory");
   int dev = 0;
   cudaGetDevice(&dev);
   const bool keep = dev >= 0 && dev < 64;
-  if (keep && slot[dev] >= bytes) return DSA_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+  if (keep && slot[dev].load(std::memory_order_acquire)) return DSA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess)
     return check_launch(what);
-  if (keep) slot[dev] = bytes;
+  if (keep) slot[dev].store(true, std::memory_order_release);
   return DSA_OK;
 }
 

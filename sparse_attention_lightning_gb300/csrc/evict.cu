@@ -258,9 +258,9 @@ int launch_evict(EvictArgs a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (a.seqs.max_k_len <= kSmemKeys) {
     const int smem = a.seqs.max_k_len * 4;
-    static int allowed[64];
+    static std::atomic<bool> allowed[64];
     const int rc = smem + 16384 <= 49152 ? DSA_OK
-                                         : allow_smem(evict_select_kernel<true>, kSmemKeys * 4, allowed, "evict_select: smem attribute");
+                                         : allow_smem<kSmemKeys * 4>(evict_select_kernel<true>, allowed, "evict_select: smem attribute");
     if (rc != DSA_OK) return rc;
     DSA_LAUNCH("evict_select", stream, e = launch_pdl(evict_select_kernel<true>, dim3(a.seqs.B), dim3(kSel), smem, stream, a));
   } else {
@@ -277,8 +277,8 @@ int launch_evict(EvictArgs a, cudaStream_t stream) {
   while (thr > kMoveLanes && thr * rb > kMoveSmem) thr -= kMoveLanes;
   const int smem = thr * rb, per_sm = rb ? kMoveSmem / smem : 8;
   const int64_t most = (int64_t)num_sms() * (per_sm < 8 ? per_sm : 8), blocks = (total + thr - 1) / thr;
-  static int allowed[64];
-  const int rc2 = smem <= 40960 ? DSA_OK : allow_smem(evict_move_kernel, kMoveSmem, allowed, "evict_move: smem attribute");
+  static std::atomic<bool> allowed[64];
+  const int rc2 = smem <= 40960 ? DSA_OK : allow_smem<kMoveSmem>(evict_move_kernel, allowed, "evict_move: smem attribute");
   if (rc2 != DSA_OK) return rc2;
   DSA_LAUNCH("evict_move", stream,
              e = launch_pdl(evict_move_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(thr / kMoveLanes * 32), smem,

@@ -268,11 +268,11 @@ __global__ void __launch_bounds__(128, 64 / U) prefix_merge_kernel(const __grid_
 
 template <typename TK, typename TO, int KC, int NJ>
 int launch_typed(const PrefixArgs& a, cudaStream_t stream) {
-  const int D = a.d_c + a.d_rope;
-  const int smem = (int)sizeof(float) * (kRows * D + KC * (D + 4) + kRows * KC);
+  auto bytes = [](int D) constexpr { return (int)sizeof(float) * (kRows * D + KC * (D + 4) + kRows * KC); };
+  const int smem = bytes(a.d_c + a.d_rope);
   auto kern = prefix_simt_kernel<TK, TO, KC, NJ>;
-  static int allowed[64];
-  const int rc = smem <= 40960 ? DSA_OK : allow_smem(kern, smem, allowed, "prefix_simt: smem attribute");
+  static std::atomic<bool> allowed[64];
+  const int rc = smem <= 40960 ? DSA_OK : allow_smem<bytes(KC == 16 ? kMaxWidth : 1024)>(kern, allowed, "prefix_simt: smem attribute");
   if (rc != DSA_OK) return rc;
   const int nblk = prefix_simt_blocks(a.max_q_len, a.h);
   dim3 grid((unsigned)(a.seqs.B * nblk), (unsigned)a.splits);

@@ -955,8 +955,8 @@ int launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
   }
   if (rc != DSA_OK) return rc;
   auto kern = nk == 5 ? prefix_tc_kernel<5> : nk == 4 ? prefix_tc_kernel<4> : prefix_tc_kernel<0>;
-  static int allowed[6][64];
-  rc = allow_smem(kern, kSmem, allowed[nk], "prefix_tc: smem attribute");
+  static std::atomic<bool> allowed[6][64];
+  rc = allow_smem<kSmem>(kern, allowed[nk], "prefix_tc: smem attribute");
   if (rc != DSA_OK) return rc;
   cudaError_t e = cudaSuccess;
   DSA_LAUNCH("prefix_tc", stream,
