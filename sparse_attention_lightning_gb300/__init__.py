@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -363,12 +364,14 @@ _TORCH_DT = {_abi.DSA_F32: (torch.float32,), _abi.DSA_BF16: (torch.bfloat16,),
              _abi.DSA_FP8_E4M3: _CODES}
 _F32, _I32, _U8 = (torch.float32,), (torch.int32,), _CODES
 
-_op_ws = {}
+_op_ws = threading.local()  # its attributes' dictionary: a thread's workspaces by (device, stream)
 
 
 def _op_workspace(ws: Optional[Workspace], index: int, stream: int, nbytes: int) -> Workspace:
     """The caller's workspace, grown as needed (its earlier buffers stay alive, a captured graph may
-    refer to them), or this device's and stream's own: calls on two streams do not share scratch.  A
+    refer to them), or this host thread's own of the device and stream: calls on two streams do not share
+    scratch, nor do two threads' calls, whose launches may alternate on one stream.  (A workspace that a
+    caller hands to several threads' calls is theirs to take turns with.)  A
     captured call has to bring its workspace: graphs captured on one stream may be replayed on two, and
     memory allocated while capturing would belong to the graph."""
     if ws is not None:
@@ -382,10 +385,11 @@ def _op_workspace(ws: Optional[Workspace], index: int, stream: int, nbytes: int)
         return ws
     if _capturing():
         raise ValueError(f"a captured call needs a workspace of its own: ws=Workspace(nbytes={nbytes})")
-    held = _op_ws.get((index, stream))
+    mine = _op_ws.__dict__
+    held = mine.get((index, stream))
     if held is None or held.nbytes < nbytes:
         size = max(nbytes, 2 * held.nbytes if held else 0)
-        held = _op_ws[index, stream] = Workspace(torch.device("cuda", index), size)
+        held = mine[index, stream] = Workspace(torch.device("cuda", index), size)
     return held
 
 

@@ -55,3 +55,55 @@ def test_threads_with_different_widths(dtype):
         bodies.append(body)
     in_threads(*bodies)
     assert len(bad) == 9 and not any(bad)
+
+
+def test_default_workspaces_belong_to_a_thread_and_a_stream(monkeypatch):
+    """Threads on one stream, with no GPU: a call's scratch is handed out again to its own thread alone."""
+    import sparse_attention_lightning_gb300 as dsa
+
+    class Fake:
+        def __init__(self, device, nbytes):
+            self.nbytes = nbytes
+
+    monkeypatch.setattr(dsa, "Workspace", Fake)
+    monkeypatch.setattr(dsa, "_capturing", lambda: False)
+    got = [[], []]
+
+    def body(mine):
+        for _ in range(3):
+            mine += [dsa._op_workspace(None, 0, 7, 100), dsa._op_workspace(None, 0, 9, 100)]
+        mine.append(dsa._op_workspace(None, 0, 7, 101))
+
+    in_threads(*[lambda m=m: body(m) for m in got])
+    for mine in got:
+        assert len({id(w) for w in mine[::2][:3]}) == 1 and len({id(w) for w in mine[1::2]}) == 1
+        assert mine[0] is not mine[1] and mine[6] is not mine[0] and mine[6].nbytes == 200
+    assert not {id(w) for w in got[0]} & {id(w) for w in got[1]}
+
+
+@pytest.mark.gpu
+def test_threads_on_one_stream():
+    """An operator is two or three launches that share its scratch; two threads' launches may alternate on the stream."""
+    import sparse_attention_lightning_gb300 as dsa
+    bodies, bad = [], []
+    for seed in (1, 2, 3):
+        w = Weights([9, 30], [600, 800], 16, 64, 16, 200, BF, seed=seed)
+        lse, idx = w.attention(), w.idx.cuda()
+        s = Setup([1, 1], [20, 90], 16, 512, 64, 2000, BF, seed=seed)
+        q = s.q.cuda()
+        w.check(lse=lse)
+        s.check(*s.run())
+        want = (dsa.accumulate_attn_weights(w.prob, w.q, w.kv, idx, lse, torch.zeros(2, 800).cuda()),
+                *dsa.prefix_mla_attn(s.prob, q, s.kv, **s.prefix))
+
+        def body(w=w, lse=lse, idx=idx, s=s, q=q, want=want):
+            for _ in range(100):
+                got = (dsa.accumulate_attn_weights(w.prob, w.q, w.kv, idx, lse,
+                                                   torch.zeros(2, 800, device="cuda")),
+                       *dsa.prefix_mla_attn(s.prob, q, s.kv, **s.prefix))
+                bad.extend(not torch.equal(g, x) for g, x in zip(got, want))
+
+        bodies.append(body)
+    torch.cuda.synchronize()
+    in_threads(*bodies)
+    assert len(bad) == 900 and not any(bad)
