@@ -125,17 +125,25 @@ class Problem:
 
 class Workspace:
     """Caller-owned device scratch; its first 16384 bytes are the status block (the status
-    word and the kernels' synchronisation counters, zero between calls)."""
+    word and the kernels' synchronisation counters, zero between calls).
+
+    A call that needs more than the workspace holds gives it a new buffer, of at least twice the size, with the
+    status block carried over.  Earlier buffers live as long as the workspace (together they are smaller than the
+    current one): captured graphs may refer to them, and calls on other streams may still use them.  A graph's kernels go on
+    reporting into the buffer that the graph was captured with."""
 
     def __init__(self, device=None, nbytes: int = STATUS_BYTES):
         self.device = torch.device(device or "cuda")
         self.buf = torch.zeros(max(STATUS_BYTES, nbytes), dtype=torch.uint8, device=self.device)
+        self._earlier = []
 
     def ensure(self, nbytes: int) -> "Workspace":
-        if self.buf.numel() < nbytes:
-            flags = self.buf[:STATUS_BYTES].clone()
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            self.buf[:STATUS_BYTES].copy_(flags)
+        held = self.buf.numel()
+        if held < nbytes:
+            grown = torch.zeros(max(nbytes, 2 * held), dtype=torch.uint8, device=self.device)
+            grown[:STATUS_BYTES].copy_(self.buf[:STATUS_BYTES])
+            self._earlier.append(self.buf)
+            self.buf = grown
         return self
 
     @property
@@ -368,9 +376,8 @@ _op_ws = threading.local()  # its attributes' dictionary: a thread's workspaces 
 
 
 def _op_workspace(ws: Optional[Workspace], index: int, stream: int, nbytes: int) -> Workspace:
-    """The caller's workspace, grown as needed (its earlier buffers stay alive, a captured graph may
-    refer to them), or this host thread's own of the device and stream: calls on two streams do not share
-    scratch, nor do two threads' calls, whose launches may alternate on one stream.  (A workspace that a
+    """The caller's workspace, grown as needed, or this host thread's own of the device and stream: calls on
+    two streams do not share scratch, nor do two threads' calls, whose launches may alternate on one stream.  (A workspace that a
     caller hands to several threads' calls is theirs to take turns with.)  A
     captured call has to bring its workspace: graphs captured on one stream may be replayed on two, and
     memory allocated while capturing would belong to the graph."""
@@ -380,7 +387,6 @@ def _op_workspace(ws: Optional[Workspace], index: int, stream: int, nbytes: int)
         if ws.nbytes < nbytes:
             if _capturing():
                 raise ValueError(f"a captured call needs a workspace of {nbytes} bytes beforehand")
-            ws.__dict__.setdefault("_earlier", []).append(ws.buf)
             ws.ensure(nbytes)
         return ws
     if _capturing():
