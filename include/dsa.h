@@ -321,8 +321,10 @@ int dsa_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, int32_t quant, float
  * prefix_kv [prefix_len, D] kv_dtype, 16-byte aligned: the prefix's rows; or NULL with
  * prefix_table [ceil(prefix_len / page_size)] device int32 (4-byte aligned): its pages in the
  * paged cache kv.  Exactly one of the two where prefix_len > 0; prefix_table needs a paged p.
- * A page outside the cache sets DSA_FLAG_BAD_INDEX; its keys are skipped.  A row without any key
- * gets out = 0 and lse = -inf.  Rows of a sequence whose cu_q/cu_k are inconsistent are flagged
+ * A key that a row does not see adds nothing to it, whatever it holds.  A visible key with an infinity or a NaN among its
+ * value columns makes those columns of out NaN (0 times it, where its logit is -inf), or all of them.
+ * A page outside the cache sets DSA_FLAG_BAD_INDEX; its keys are skipped.  A row without any key, or
+ * whose logits are all -inf, gets out = 0 and lse = -inf (but for NaN columns as above).  Rows of a sequence whose cu_q/cu_k are inconsistent are flagged
  * (DSA_FLAG_BAD_SEQS) and left as they were.
  * prefix_len + max_k_len < 2^30.
  */

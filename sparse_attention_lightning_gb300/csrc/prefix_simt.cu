@@ -15,6 +15,8 @@
 // than its columns, which spreads it over the banks); max and sum stay within the 16, so a chunk of 32
 // keys needs two block barriers.  One thread a dot, scalar loads and the softmax through shared memory took
 // 45 us for 3 sequences of up to 40 tokens x 8 heads over 256 + 130 keys of 80 columns; this way it is 16.
+#include <float.h>
+
 #include "prefix_attn.cuh"
 
 namespace dsa {
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
     }
   }
   if (place == 0) {
-    if (!last) a.part_ml[(int64_t)split * rows + flat] = make_float2(m, l);
+    if (!last) a.part_ml[(int64_t)split * rows + flat] = make_float2(c0 < c1 ? fmaxf(m, -FLT_MAX) : m, l);
     else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
@@ -186,7 +188,8 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(PrefixArgs a, int
 // ended, each lane takes up to four pieces' (max, sum), and U pieces' outputs are loaded before the first is
 // added: 8 where all blocks run at once, 4 (and twice the blocks on an SM) for more rows: 4096 rows of 2 to 4 pieces
 // take 2 us less that way, 64 rows of 9 pieces 1 us more.  One load after another, those 64 rows took 12 us;
-// so they take 4.  A piece without keys has l = 0 and its O is not read.
+// so they take 4.  A piece without keys has m = -inf and its O is not read; one whose weight is 0 is: 0 times a NaN
+// in it is NaN, as in a row attended whole.
 constexpr int kMaxPieces = 128;
 template <typename TO, int U>
 __global__ void __launch_bounds__(128, 64 / U) prefix_merge_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixMerge mg) {
@@ -219,8 +222,9 @@ __global__ void __launch_bounds__(128, 64 / U) prefix_merge_kernel(const __grid_
   const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
   for (int i = 0; i < kMaxPieces / 32; ++i) {
-    const float f = w[i] == 0.f ? 0.f : exp2f(m[i] - ref);
+    float f = w[i] == 0.f ? 0.f : exp2f(m[i] - ref);
     l = fmaf(f, w[i], l);
+    if (f == 0.f) f = m[i] == -INFINITY ? 0.f : -0.f;  // +0: not read
     w[i] = f;
   }
 #pragma unroll
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(128, 64 / U) prefix_merge_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           f[j] = __shfl_sync(0xffffffffu, w[i], j0 + j);  // 0 past the last piece
-          x[j] = in && f[j] != 0.f
+          x[j] = in && __float_as_uint(f[j]) != 0u
                      ? __ldcg(reinterpret_cast<const float4*>(po + (i * 32 + j0 + j) * stride + c))
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }

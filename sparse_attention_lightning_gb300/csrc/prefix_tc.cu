@@ -29,6 +29,8 @@
 // of the chunk before, the other half: softmax has the first part to finish in, and the last part hides the
 // wait for P·V before the next chunk overwrites its P.
 // Every wait is bounded (DSA_FLAG_TIMEOUT).
+#include <float.h>
+
 #include "prefix_attn.cuh"
 #include "tc_sm100.cuh"
 
@@ -187,6 +189,27 @@ __device__ __forceinline__ bool finite8(uint4& v) {
   }
   v = make_uint4(u[0], u[1], u[2], u[3]);
   return any;
+}
+
+// NaN in those of n output columns from column c in which a key of this item that the row (at position pos) sees and
+// the block's first row does not holds an infinity or a NaN.  (Read from the cache again: the tile's were zeroed.)
+__device__ __noinline__ uint32_t spoilt_columns(const PrefixArgs& a, int b, int k0, int x0, int x1, int c, int n) {
+  uint32_t cols = 0;
+  for (int x = x0; x < x1; ++x) {
+    const int row = cache_row(a.seqs, b, k0, x);
+    if (row < 0) continue;
+    const uint16_t* v = static_cast<const uint16_t*>(a.kv) + (int64_t)row * (a.d_c + a.d_rope) + c;
+    for (int i = 0; i < n; ++i)
+      if ((v[i] & 0x7f80u) == 0x7f80u) cols |= 1u << i;
+  }
+  return cols;
+}
+__device__ __forceinline__ void spoil(const PrefixArgs& a, const Item& it, int pos, int c, int n, uint32_t (&o)[32]) {
+  const int x0 = max(it.pos0 + 1, (it.c0 - it.ncp) * kN), x1 = min(pos + 1, (it.c1 - it.ncp) * kN);
+  const uint32_t cols = spoilt_columns(a, it.b, it.k0, x0, x1, c, n);
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if ((cols >> i) & 1) o[i] = 0x7fffffffu;
 }
 
 // Box of kN (or a page's) rows x 64 columns x 4 column tiles into four consecutive tiles.
@@ -568,6 +591,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
       if (lane == 0) mbar_arrive(qt_full);
     }
     float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum relative to it
+    bool spoilt = false;           // this row sees a key that may have been zeroed for others
     bool stop = false;
     for (int g = 0; g < nch; ++g) {
       const int c = it.c0 + g;
@@ -591,7 +615,9 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
       if (lim0 < kN || bad) {
         // some row does not see some key.  Its p is 0, but 0 times an infinity or a NaN in the
         // key's value columns would not be: those are zeroed in the tile, which the logits have read
-        // already (a row that does see such a key has a NaN logit)
+        // already.  A row that does see such a key has a logit that is not finite (the value columns are columns of
+        // the key): NaN or +inf, and its whole output is NaN; or -inf, and where the zeroed ones would have
+        // made its output NaN (0 times them) NaN is written in the end
         if (!a.seqs.paged() &&
             !__all_sync(0xffffffffu, mbar_wait(&v_full[g % kVSlots], (g / kVSlots) & 1, abort_flag,
                                                a.status, DSA_FLAG_TIMEOUT))) { stop = true; break; }
@@ -615,8 +641,10 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         if ((bad & in) && it.half == 0) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
         const uint64_t see = in & ~bad;
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
+        for (int i = 0; i < kN; ++i) {
           if (!((see >> i) & 1)) s[i] = -INFINITY;
+          else if (s[i] == -INFINITY && i >= lim0) spoilt = true;
+        }
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -679,6 +707,7 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         __syncwarp();  // the load is the whole warp's
         tmem_ld32(lane_base + kOCol + 32 * b, o);
         const int n = min(32, ncol - 32 * b);  // 16 or 32 columns
+        if (spoilt) spoil(a, it, pos, vcol0 + 32 * b, n, o);
         if (f32) {
           float4* dst = reinterpret_cast<float4*>(mine) + 8 * b;
 #pragma unroll
@@ -711,7 +740,8 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
                      : "memory");
       }
       if (live && it.half == 0) {
-        if (split) a.part_ml[(int64_t)it.piece * rows_all + flat] = make_float2(m, l);
+        // (m = -inf is a piece without keys, whose output the merge does not read)
+        if (split) a.part_ml[(int64_t)it.piece * rows_all + flat] = make_float2(fmaxf(m, -FLT_MAX), l);
         else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
