@@ -353,7 +353,7 @@ int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void*
  * Eviction from the caches by accumulated attention weight.  Sequence b (L_b positions) keeps
  * n_b = min(L_b, budget): all where L_b <= budget; otherwise its first `sink` positions, its last
  * `recent` ones, and the budget - sink - recent with the largest acc between them (among equal
- * ones the smaller positions; NaN counts as largest where its sign is positive).  Kept
+ * ones the smaller positions; every NaN counts as larger than any number).  Kept
  * positions keep their order and move to the caches' *_out tensors:
  *   kept[b, 0..n_b-1] = the kept positions, ascending; kept[b, n_b..budget-1] = -1
  *   cu_k_out[b] = Σ_{b' < b} n_b'                           (num_seqs + 1 entries)

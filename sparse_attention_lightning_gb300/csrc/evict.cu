@@ -36,6 +36,9 @@ __device__ __forceinline__ int seq_keep(const EvictArgs& a, int b, int& L) {
   return min(L, a.budget);
 }
 
+// order_key with every NaN, whatever its sign and payload, above all numbers.
+__device__ __forceinline__ uint32_t weight_key(float f) { return f != f ? 0xffffffffu : order_key(f); }
+
 __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kSel) evict_select_kernel(EvictArgs a) {
   }
   const float* acc = a.acc + (int64_t)b * a.ld_acc;
   const int lo = a.sink, hi = L - a.recent;
-  auto key = [&](int i) { return SMEM ? keys[i] : order_key(acc[i]); };
+  auto key = [&](int i) { return SMEM ? keys[i] : weight_key(acc[i]); };
   int need = a.budget - a.sink - a.recent;
   const bool any = need > 0;
   uint32_t prefix = 0;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kSel) evict_select_kernel(EvictArgs a) {
 #pragma unroll
         for (int j = 0; j < kFly; ++j)
           if (i + j * kSel < hi) {
-            const uint32_t k = order_key(f[j]);
+            const uint32_t k = weight_key(f[j]);
             keys[i + j * kSel] = k;
             atomicAdd(&hist[k >> 21], 1);
           }
