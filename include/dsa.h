@@ -371,8 +371,8 @@ int dsa_accumulate_attn_weights(const dsa_problem* p, const void* q, const void*
  * MXFP8) comes with its *_out, or both are NULL (not moved).  Destination rows must not be rows
  * the call reads: a packed *_out that overlaps its source is refused; with pages, source and
  * destination may be one pool, in which the destination's pages must not be the sources'.
- * acc [num_seqs, ld_acc >= max_k_len] f32; acc_out [num_seqs, ld_acc_out >= budget] f32 or NULL,
- * not overlapping acc; cu_k_out not overlapping p's cu_k; 1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
+ * acc [num_seqs, ld_acc >= max_k_len] f32; acc_out [num_seqs, ld_acc_out >= budget] f32 or NULL, whose bytes from first to
+ * last element and acc's do not overlap; cu_k_out not overlapping p's cu_k; 1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
  */
 int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t budget, int32_t sink,
               int32_t recent, int32_t* kept, int32_t* cu_k_out, float* acc_out, int64_t ld_acc_out,

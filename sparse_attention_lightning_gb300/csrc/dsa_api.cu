@@ -714,7 +714,9 @@ int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t bu
   if (acc_out) {
     if (((uintptr_t)acc_out & 3u) != 0 || ld_acc_out < budget)
       return set_error(DSA_ERR_INVALID_ARG, "acc_out is not 4-byte aligned or ld_acc_out < budget");
-    if (overlap(acc, ld_acc * p->num_seqs * 4, acc_out, ld_acc_out * p->num_seqs * 4))
+    // from the first element to the last: what lies behind it may be another tensor's
+    const int64_t rows = p->num_seqs - 1;
+    if (overlap(acc, (rows * ld_acc + p->max_k_len) * 4, acc_out, (rows * ld_acc_out + budget) * 4))
       return set_error(DSA_ERR_INVALID_ARG, "acc_out overlaps acc");
   }
   EvictArgs a{};

@@ -1,10 +1,13 @@
-"""Eviction by weights that are not numbers."""
+"""Eviction by weights that are not numbers, and from slices of wider rows."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import cache_ops as C
-from test_evict import _caches
+from sparse_attention_lightning_gb300 import _abi
+from test_evict import _caches, _problem
 
 
 @pytest.mark.gpu
@@ -29,3 +32,18 @@ def test_every_nan_counts_as_largest(L, budget, bits):
     assert r.kept[0].tolist() == want.tolist()
     assert torch.equal(r.acc[0].cpu().view(torch.int32), acc[0][want].view(torch.int32))
     assert torch.equal(r.kv[:budget].cpu(), keys["kv"][want])
+
+
+def test_acc_out_may_follow_a_strided_acc():
+    """A slice of wider rows ends with its last element, not with its last row's stride."""
+    L, A = _abi.lib(), 1 << 24
+    p = _problem()  # 2 sequences, up to 40 positions
+
+    def call(acc, ld, out, ld_out, budget=16):  # no workspace: the check behind this one refuses the call
+        return L.dsa_evict(ctypes.byref(p), acc, ld, budget, 2, 4, 2 * A, 3 * A, out, ld_out, None, None, None, None, None,
+                           None, None, 0, 0, 0, None, 1 << 30, None)
+
+    bad, passed = _abi.DSA_ERR_INVALID_ARG, _abi.DSA_ERR_WORKSPACE
+    assert call(A, 100, A + 4 * 140, 16) == passed and call(A, 100, A + 4 * 139, 16) == bad
+    assert call(A + 4 * 66, 50, A, 50) == passed and call(A + 4 * 65, 50, A, 50) == bad
+    assert call(A, 40, A + 4 * 80, 16) == passed and call(A, 40, A + 4 * 79, 16) == bad
