@@ -81,6 +81,8 @@ class Problem:
         tq = self.c.total_q
         self._shapes = ((tq, h, self.d), (self.cache_rows, self.d), (tq, h, d_c), (tq, h), (tq, top_k))
         self._device = self.cu_q.get_device()
+        if any(t.get_device() != self._device for t in (self.cu_k, self.block_table) if t is not None):
+            raise ValueError("cu_q, cu_k and block_table must be on one device")
 
     @classmethod
     def from_config(cls, cfg, cu_q: torch.Tensor, cu_k: torch.Tensor, sm_scale: float = 0.0,
