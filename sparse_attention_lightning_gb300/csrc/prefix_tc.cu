@@ -191,25 +191,19 @@ __device__ __forceinline__ bool finite8(uint4& v) {
   return any;
 }
 
-// NaN in those of n output columns from column c in which a key of this item that the row (at position pos) sees and
-// the block's first row does not holds an infinity or a NaN.  (Read from the cache again: the tile's were zeroed.)
-__device__ __noinline__ uint32_t spoilt_columns(const PrefixArgs& a, int b, int k0, int x0, int x1, int c, int n) {
-  uint32_t cols = 0;
+// NaN in those of a row's n output columns from column c (at `out`, f32 or bf16) in which one of the keys at positions
+// [x0, x1) of its sequence holds an infinity or a NaN.  (Read from the cache: the tile's were zeroed.)
+__device__ __noinline__ void spoil(const PrefixArgs& a, int b, int k0, int x0, int x1, int c, int n, bool f32, uint8_t* out) {
   for (int x = x0; x < x1; ++x) {
     const int row = cache_row(a.seqs, b, k0, x);
     if (row < 0) continue;
     const uint16_t* v = static_cast<const uint16_t*>(a.kv) + (int64_t)row * (a.d_c + a.d_rope) + c;
-    for (int i = 0; i < n; ++i)
-      if ((v[i] & 0x7f80u) == 0x7f80u) cols |= 1u << i;
+    for (int i = 0; i < n; ++i) {
+      if ((v[i] & 0x7f80u) != 0x7f80u) continue;
+      if (f32) reinterpret_cast<uint32_t*>(out)[i] = 0x7fffffffu;
+      else reinterpret_cast<uint16_t*>(out)[i] = 0x7fffu;
+    }
   }
-  return cols;
-}
-__device__ __forceinline__ void spoil(const PrefixArgs& a, const Item& it, int pos, int c, int n, uint32_t (&o)[32]) {
-  const int x0 = max(it.pos0 + 1, (it.c0 - it.ncp) * kN), x1 = min(pos + 1, (it.c1 - it.ncp) * kN);
-  const uint32_t cols = spoilt_columns(a, it.b, it.k0, x0, x1, c, n);
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if ((cols >> i) & 1) o[i] = 0x7fffffffu;
 }
 
 // Box of kN (or a page's) rows x 64 columns x 4 column tiles into four consecutive tiles.
@@ -641,9 +635,13 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         if ((bad & in) && it.half == 0) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
         const uint64_t see = in & ~bad;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
+        for (int i = 0; i < kN; ++i)
           if (!((see >> i) & 1)) s[i] = -INFINITY;
-          else if (s[i] == -INFINITY && i >= lim0) spoilt = true;
+        if (lim > lim0) {  // it sees keys that the first row does not
+          uint32_t none[2] = {0u, 0u};
+#pragma unroll
+          for (int i = 0; i < kN; ++i) none[i >> 5] |= s[i] == -INFINITY ? 1u << (i & 31) : 0u;
+          spoilt |= (see & ((uint64_t)none[1] << 32 | none[0])) != 0;
         }
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -707,7 +705,6 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
         __syncwarp();  // the load is the whole warp's
         tmem_ld32(lane_base + kOCol + 32 * b, o);
         const int n = min(32, ncol - 32 * b);  // 16 or 32 columns
-        if (spoilt) spoil(a, it, pos, vcol0 + 32 * b, n, o);
         if (f32) {
           float4* dst = reinterpret_cast<float4*>(mine) + 8 * b;
 #pragma unroll
@@ -729,6 +726,10 @@ prefix_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps 
             }
         }
       }
+      // the keys that the row sees and the block's first row does not, in this item's chunks
+      if (spoilt)
+        spoil(a, it.b, it.k0, max(it.pos0 + 1, (it.c0 - it.ncp) * kN), min(pos + 1, (it.c1 - it.ncp) * kN), vcol0, ncol,
+              f32, mine);
       fence_proxy_async_smem();  // our writes, seen by the bulk copy
       if (live) {
         const int64_t at = flat * a.d_c + vcol0;
