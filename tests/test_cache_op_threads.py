@@ -107,3 +107,44 @@ def test_threads_on_one_stream():
     torch.cuda.synchronize()
     in_threads(*bodies)
     assert len(bad) == 900 and not any(bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_lens", [[1, 1], [70, 5]])
+def test_weights_on_two_streams(q_lens):
+    """Calls on two streams at once, with default scratch and as graphs with a workspace each, behind a wait that lets
+    both start together."""
+    import sparse_attention_lightning_gb300 as dsa
+    from sparse_attention_lightning_gb300 import _abi
+    sets = []
+    for seed in (1, 2):
+        w = Weights(q_lens, [3000, 900], 128, 512, 64, 700, BF, seed=seed)
+        lse, idx = w.attention(), w.idx.cuda()
+        want = dsa.accumulate_attn_weights(w.prob, w.q, w.kv, idx, lse, torch.zeros(2, 3000).cuda())
+        sets.append((w, lse, idx, want, torch.cuda.Stream(), torch.zeros(2, 3000).cuda()))
+    for _ in range(10):
+        torch.cuda.synchronize()
+        for w, lse, idx, want, st, acc in sets:
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(200_000)
+                acc.zero_()
+                dsa.accumulate_attn_weights(w.prob, w.q, w.kv, idx, lse, acc)
+        torch.cuda.synchronize()
+        assert all(torch.equal(acc, want) for _, _, _, want, _, acc in sets)
+    graphs = []
+    for w, lse, idx, want, st, acc in sets:
+        ws = dsa.Workspace(nbytes=w.prob.workspace_size(_abi.OP_ATTN_WEIGHTS))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            acc.zero_()
+            dsa.accumulate_attn_weights(w.prob, w.q, w.kv, idx, lse, acc, ws=ws)
+        graphs.append((graph, ws))
+    for _ in range(10):
+        torch.cuda.synchronize()
+        for (graph, _ws), s in zip(graphs, sets):
+            with torch.cuda.stream(s[4]):
+                torch.cuda._sleep(200_000)
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(acc, want) for _, _, _, want, _, acc in sets)

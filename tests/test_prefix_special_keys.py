@@ -57,3 +57,13 @@ class OneInfinity(Setup):
 def test_infinity_in_a_value_column(q_lens, k_lens, P, x, h, dtype, d_c, d_rope, c, page):
     s = OneInfinity(x, c, q_lens, k_lens, h, d_c, d_rope, P, dtype, page=page, seed=h + x)
     s.check_all(*s.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d_c,d_rope", [(BF, 512, 64), (BF, 64, 16), (F32, 64, 16)])
+def test_infinity_in_a_piece_without_weight(dtype, d_c, d_rope):
+    """One prefix key takes all weight: the piece with the infinity is merged with weight 0, and 0 times its NaN is NaN."""
+    s = OneInfinity(40, 9, [1], [41], 1, d_c, d_rope, 6000, dtype, seed=4)
+    s.pre[17] = (s.q[0, 0] * (300 * (d_c + d_rope) ** 0.5 / s.q[0, 0].double().square().sum())).to(dtype)
+    s.prefix = dict(prefix_kv=s.pre.cuda())
+    s.check_all(*s.run())
