@@ -285,14 +285,16 @@ int dsa_indexer_prolog(int32_t total_q, int32_t h_idx, int32_t d_idx, int32_t d_
  * elements, in fp32:
  *   h = x + residual  (h = x without a residual; h_out is h rounded to dtype)
  *   y = h · rsqrt(Σ h² / d + eps) · weight  (from the unrounded h)
- *   quant = DSA_FP8_E4M3: scale[r] = max|y| / 448 (f32; 1 where that is below the smallest
- *     normal number), codes = E4M3(y / scale) (nearest even, saturated to ±448): on rows of
- *     d_idx elements these are k_idx and k_scale of the FP8 indexer;
+ *   quant = DSA_FP8_E4M3: scale[r] = max|y| / 448 (f32, formed as max|h · weight| · rsqrt(...) / 448; 1 where
+ *     that is below the smallest normal number), codes = E4M3(y · r) (nearest even, saturated to ±448) with r the
+ *     fp32 reciprocal of scale (E4M3(y / scale) differs, by one code, only where y / scale lies within a few fp32
+ *     roundings of the middle between two codes): on rows of d_idx elements these are k_idx and k_scale of the FP8 indexer;
  *   quant = DSA_MXFP8_E4M3: scale[r, g] the E8M0 byte e + 127 of the smallest power of two with
  *     max|y| <= 448·2^e over the 32 elements of group g (127 for an all-zero group; byte 255
  *     is never written), codes = E4M3(y / 2^e): k_idx and k_scale of the MXFP8 indexer;
  *   quant = 0: no codes (codes and scale are ignored).
- * A row with a NaN or an infinity comes out as NaN where 0 · infinity or a NaN arises, like the formula.
+ * A row with a NaN or an infinity comes out as NaN where 0 · infinity or a NaN arises, like the formula; so does
+ * Σ h² that overflows fp32 (|h| from about 2^64 / √d on) count as infinite: y is 0 there.
  * x [rows, d] and residual [rows, d] dtype (F32 or BF16), row strides ld_x, ld_res >= d elements;
  * weight [d] dtype; h_out [rows, d] dtype, required with residual (NULL without); y [rows, d]
  * dtype, required without quant (may be NULL with); codes [rows, d] bytes; scale [rows] f32 or
@@ -341,7 +343,11 @@ int dsa_prefix_mla_attn(const dsa_problem* p, int32_t prefix_len, const void* pr
  * queries, set DSA_FLAG_BAD_SEQS; an entry outside [0, pos(t)] or on a page outside the cache sets
  * DSA_FLAG_BAD_INDEX); neither do heads whose lse is -inf; a repeated entry adds as often
  * as it appears.  The result does not depend on the order of the additions: the same call gives the
- * same bytes.
+ * same bytes.  Where max_q_len > 1 the weights are added in 64-bit fixed point, each rounded to half a unit of
+ * 2^-(62 - c), 2^c the first power of two from 2 · h · max_q_len on (128 heads x 4096 queries: 2^-42), and then once to acc.
+ * That holds a position's sum as long as lse belongs to this idx (a query's weights then add up to
+ * h over its entries).  With a smaller lse the sums mean nothing, may wrap around where an entry is repeated, and
+ * weights above 2 · h are added in no fixed order.
  * q, kv, idx, lse as in dsa_sparse_mla_attn (lse required); acc [num_seqs, ld_acc] f32, ld_acc >=
  * max_k_len, added to in place (columns at or past a sequence's length stay as they are).
  */

@@ -28,7 +28,8 @@ __device__ __forceinline__ void add_weight(const WeightArgs& a, int b, int pos, 
     atomicAdd(acc, w);
   } else if (w <= 2.f * a.h) {
     // w is at most h (probabilities; the factor 2 covers their rounding), and fx_scale leaves
-    // room for max_q_len such sums; rounded to half a unit
+    // room for max_q_len such sums (a query's repeated entries share its h); rounded to half a unit, which a weight of
+    // 2^-20 of a head still has 22 bits above at 128 heads x 4096 queries
     atomicAdd(reinterpret_cast<unsigned long long*>(a.fx + (int64_t)b * a.seqs.max_k_len + pos),
               (unsigned long long)__double2ll_rn((double)w * a.fx_scale));
   } else {
