@@ -6,7 +6,8 @@
 // query's heads are the MMA's M = 128 and live in tensor memory (288 columns), and three chunks of 64
 // gathered rows (216 KB) are in flight on an SM.  (With the keys as M and the query in shared memory, 64 KB
 // were: 34 us for the decode step below.)  The sum over heads is then one
-// over lanes: a thread takes one head's 64 exponentials, 62 shuffles a warp transpose and add them, and
+// over lanes: a thread takes one head's 64 exponentials (of fp32 logits · scale − lse in one rounding, by the
+// hardware's 2^x: some 2^-20 of a weight in all, for logits in the tens), 62 shuffles a warp transpose and add them, and
 // the four warps' sums meet in shared memory.
 //
 // Per chunk of 64 selected rows: four producer warps gather them by TMA, four rows x 128 bytes a copy, into the
@@ -47,16 +48,6 @@ struct Params {
   uint32_t per;    // consecutive units of a CTA
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // Rows r0..r3, 64 columns from column c, to four consecutive 128-byte rows of shared memory.
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int c, int r0, int r1,
                                             int r2, int r3) {

@@ -17,6 +17,20 @@ constexpr int kMaxWidth = 1024 + 256;  // of a latent row (d_c + d_rope)
 // then passes beside the kernel before: a call of 20 to 140 us is 2 to 3 us shorter in a row of calls), and let only
 // their own operator's next kernel start early, as a caller's next one may read its inputs ahead of its wait.
 
+// 2^x by the special-function unit (relative error about 2^-22; results below the normal numbers are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // key_row by ordinary loads.
 __device__ __forceinline__ int cache_row(const Seqs& s, int b, int k0, int pos) {
   if (!s.paged()) return k0 + pos;

@@ -24,7 +24,9 @@
 // Per chunk of 64 keys: the producer thread loads tiles by TMA; the MMA thread issues
 // S(g) = Q·Kᵀ (M=128, N=64, K=D) and O += P(g-1)·V (M=128, N=256, K=64; P from tensor memory);
 // four softmax warps, a thread a row, take the running max (it moves only when a row's max grows
-// by more than 2^8; O is then rescaled), the sum in fp32 of the unrounded p, and write P.
+// by more than 2^8; O is then rescaled), the sum in fp32 of the unrounded p, and write P.  P is rounded to bf16 there, the
+// type that the MMA wants beside bf16 values: each p is off by 2^-8 of it at most, in either direction, and the output by
+// less than its own rounding to bf16 (against 64 bits: 1.0 to 1.3 times the error of fp32 p and a rounded output).
 // Order of the MMAs: S over the K tiles (their buffers are refilled meanwhile), over half the V tiles, P·V
 // of the chunk before, the other half: softmax has the first part to finish in, and the last part hides the
 // wait for P·V before the next chunk overwrites its P.
@@ -149,12 +151,6 @@ __device__ __forceinline__ bool item_at(const Params& p, const Cuts& cuts, int i
   return true;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 64 consecutive tensor-memory columns of this warp's 32 lanes (two loads, one wait each).
 __device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
   uint32_t r[32];
@@ -169,13 +165,6 @@ __device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
 }
 
 // Zero the infinities and NaNs among 8 bf16 values; whether there were any.
