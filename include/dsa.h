@@ -85,6 +85,7 @@ enum dsa_dtype {
                                   * internal invariant failed (a gather row outside the cache, a
                                   * tile coordinate or query row out of range, an output slot at
                                   * or past top_k); the access was clamped or skipped */
+#define DSA_FLAG_NO_PAGES  0x10u /* dsa_reserve_pages: too few free pages; some rows got none */
 
 /* Operations, for dsa_workspace_size(). */
 enum dsa_op {
@@ -95,7 +96,9 @@ enum dsa_op {
   DSA_OP_FUSED_FORWARD = 5,
   DSA_OP_PREFIX_MLA_ATTN = 6,
   DSA_OP_ATTN_WEIGHTS = 7,
-  DSA_OP_EVICT = 8
+  DSA_OP_EVICT = 8,
+  DSA_OP_KV4_ROWS = 9,         /* dsa_write_kv4, dsa_read_kv4 */
+  DSA_OP_SPARSE_MLA_ATTN4 = 10
 };
 
 /* Shape, types and sequence layout of one DSA problem. */
@@ -386,6 +389,131 @@ int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t bu
               const void* k_scale, void* k_scale_out, const int32_t* table_out,
               int32_t max_pages_out, int32_t num_pages_out, int64_t rows_out, void* ws,
               size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, ...), on the rope columns of queries or
+ * of keys ahead of their cache.  For token t, head h and pair i of d / 2, (u, v) the pair's columns:
+ *   phi = positions[axis[i], t] * turn[i] * 2 pi / 2^64
+ *   (u, v) -> (u cos phi - v sin phi, u sin phi + v cos phi);  inverse: with -phi
+ * turn[i] is the turns of one position as a fixed-point fraction of 2^64 (a frequency of f radians a position:
+ * f / (2 pi) * 2^64, modulo 2^64), so that angles of positions up to +-2^31 are exact modulo one turn
+ * but for turn's own rounding; sine, cosine and products are fp32, rounded once to dtype.
+ * interleaved: pair i is columns 2i and 2i + 1; otherwise i and i + d/2.
+ * x, out: element (t, h, c) at t * x_token + h * x_head + c (strides in elements, >= 0), F32 or BF16,
+ * aligned to their element (rows on 16-byte boundaries are faster); out may be x with the same strides,
+ * and otherwise must not overlap it (tensors with the same strides that interleave without
+ * sharing an element, as two column ranges of one tensor, may) nor the positions.
+ * positions [axes][ld_pos] device int32, ld_pos >= tokens; turn [d/2] and axis [d/2] HOST memory, read before
+ * the call returns; axis[i] < axes <= 255.  d even, 2 .. 256.  One launch, no workspace; tokens = 0 launches nothing.
+ */
+int dsa_rotate_axes(int64_t tokens, int32_t heads, int32_t d, int32_t dtype, int32_t interleaved,
+                    int32_t inverse, int32_t axes, const uint64_t* turn, const uint8_t* axis,
+                    const int32_t* positions, int64_t ld_pos, const void* x, int64_t x_token,
+                    int64_t x_head, void* out, int64_t out_token, int64_t out_head, void* stream);
+
+/*
+ * The latent cache in 4 bits.  A cache row of D = d_c + d_rope columns takes
+ * dsa_kv4_row_bytes(d_c, d_rope) bytes (512 + 64: 416 instead of 1152), in this order:
+ *   d_c / 2     codes: E2M1 (a sign; magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6), eight columns a
+ *               little-endian 32-bit word: of eight, column 2k at bit 4k, column 2k + 1 at bit 16 + 4k
+ *   2 * d_rope  the rope columns in bf16
+ *   d_c / 16    scales, a byte for 16 columns: an fp16 number without its sign and its seven
+ *               lowest bits (byte << 7; 0 .. 61440 in steps of at most 1/8, 0xf8 and above: NaN)
+ *   zeros up to a multiple of 16 bytes
+ * Column c < d_c is code[c] * scale[c / 16], which is a bf16 number exactly.  The cache is packed or
+ * paged like kv: [cache rows][row bytes] uint8.
+ */
+int dsa_kv4_row_bytes(int32_t d_c, int32_t d_rope, int32_t* bytes);
+
+/*
+ * Write the new tokens' rows: query row t of p (the last T_b positions of its sequence b) goes to the
+ * cache row of its position.  Over every 16 latent columns
+ *   scale = max|x| / 6 to the nearest scale (ties to even, at most 61440),
+ *   code  = x / scale to the nearest code (ties to even, at most 6 in magnitude; 0 where the scale is 0);
+ * 16 columns with an infinity or a NaN among them become NaN (scale byte 0xff).  Rope columns are rounded to bf16.
+ * latent [total_q, d_c] and k_rope [total_q, d_rope] kv_dtype, rows ld_latent >= d_c and ld_rope >= d_rope
+ * elements apart, aligned to their element (16-byte aligned rows are faster); k_rope may be NULL
+ * where d_rope = 0.  kv4 must not overlap them.  Rows of a sequence whose cu_q/cu_k are inconsistent, and rows on
+ * a page outside the cache, set DSA_FLAG_BAD_SEQS and are not written.  Other rows stay as they were.
+ */
+int dsa_write_kv4(const dsa_problem* p, const void* latent, int64_t ld_latent, const void* k_rope,
+                  int64_t ld_rope, void* kv4, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Read every position's row back, packed: out [total_k, D] kv_dtype, row cu_k[b] + s = position s of
+ * sequence b (what dense attention over the sequence, or over it as a shared prefix, takes).  Rows of a sequence
+ * whose cu_k is inconsistent (DSA_FLAG_BAD_SEQS) or on a page outside the cache (DSA_FLAG_BAD_INDEX) are left as
+ * they were.  out must not overlap kv4.
+ */
+int dsa_read_kv4(const dsa_problem* p, const void* kv4, void* out, void* ws, size_t ws_bytes,
+                 void* stream);
+
+/*
+ * dsa_sparse_mla_attn over a 4-bit latent cache: the same sums with kv's rows decoded from kv4
+ * [cache rows][row bytes].  q, idx, out and lse, skipped and repeated entries as there; a row without a valid entry,
+ * or whose logits are all -inf, gets out = 0 and lse = -inf.  An entry that is skipped adds nothing, whatever its row holds.
+ * Rows of a sequence whose cu_q/cu_k are inconsistent, or that has more than max_q_len queries, set DSA_FLAG_BAD_SEQS
+ * and are left as they were.
+ */
+int dsa_sparse_mla_attn4(const dsa_problem* p, const void* q, const void* kv4, const int32_t* idx,
+                         void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Pages shared by rows of a block table.  table [rows, width] int32 (rows ld_table >= width apart) holds the pages of a
+ * row in order, -1 behind them; refs [num_pages] int32 counts the table entries that hold a page.  A page
+ * with refs <= 0 is free.  All results depend on the arguments alone: the lowest free pages are given out first.
+ * page_size: a power of two >= 16; num_pages * page_size < 2^31, rows * width < 2^31.  All int32 arrays are device
+ * memory, 4-byte aligned, and must not overlap.  caches: `num_caches` <= 8 device addresses (16-byte aligned) of
+ * caches with num_pages * page_size rows of row_bytes[c] bytes each (both arrays HOST memory, read before the call returns).
+ * An entry that names a row outside the table, positions beyond it or a page outside the pool is left out and sets
+ * DSA_FLAG_BAD_INDEX.
+ */
+
+/* Bytes of workspace that the calls below need: with n entries at most, whatever their order (n = 0:
+ * dsa_fork_pages and dsa_free_pages need 16384). */
+int dsa_pages_workspace_size(int32_t rows, int32_t n, int32_t num_pages, size_t* bytes);
+
+/*
+ * Fork: for each entry i, row dst[i] gets the pages of row src[i]'s first lens[i] positions, shared
+ * (refs + 1 each), and -1 behind them.  What row dst[i] held before is not given back (dsa_free_pages does that).  Where a row
+ * is named by several dst the first entry counts; an entry whose src is some entry's dst is left out.
+ * Neither row's cache rows are touched: dsa_reserve_pages makes a page of its own for the tokens that follow.
+ */
+int dsa_fork_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                   int32_t num_pages, int32_t page_size, int32_t n, const int32_t* src,
+                   const int32_t* dst, const int32_t* lens, void* ws, size_t ws_bytes, void* stream);
+
+/* Free: every page of the rows named has a holder less, and their entries become -1.  A row may be named twice. */
+int dsa_free_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                   int32_t num_pages, int32_t n, const int32_t* row, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/*
+ * Reserve: row[i], which holds lens[i] positions, gets pages of its own for positions lens[i] ..
+ * new_lens[i] - 1.  New pages where it has none (or shares one there); and where its last held page is not
+ * full, will be written to and has other holders, a new page with the held positions' rows copied in all
+ * caches (their other rows stay as they were) - but if all the page's holders are entries of this call that
+ * would copy it, the first of them keeps it.  Pages are given out entry by entry; an entry gets
+ * all it needs or nothing (then DSA_FLAG_NO_PAGES is set, also for every later entry that needs pages).
+ * held[i] = new_lens[i], or lens[i] where the entry got nothing.  Of several entries of one row the first counts.  Which pages are free and
+ * shared is as at the call's start.
+ */
+int dsa_reserve_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                      int32_t num_pages, int32_t page_size, int32_t n, const int32_t* row,
+                      const int32_t* lens, const int32_t* new_lens, int32_t* held,
+                      int32_t num_caches, void* const* caches, const int64_t* row_bytes, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * Compact: the pages in use become pages 0 .. live - 1.  The k-th page in use at or behind `live` moves, in all
+ * caches, to the k-th free page before it; table and refs follow.  moved[p] (num_pages) is where page p went (p itself
+ * where it stayed, -1 for a free page), live[0] the number of pages in use.  Rows of pages at or behind live
+ * keep their bytes.  Every holder has to be in the table: an entry of a free page becomes -1 (DSA_FLAG_BAD_INDEX).
+ */
+int dsa_compact_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                      int32_t num_pages, int32_t page_size, int32_t* moved, int32_t* live,
+                      int32_t num_caches, void* const* caches, const int64_t* row_bytes, void* ws,
+                      size_t ws_bytes, void* stream);
 
 /* Zero the workspace status block (the status word and the kernels' counters; enqueued on
  * `stream`). */

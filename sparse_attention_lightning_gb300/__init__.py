@@ -7,7 +7,8 @@ kernels.  There is no CPU or framework fallback: if the library is missing,
 calls raise.
 
 Names follow the C ABI: indexer_scores, topk, fused_indexer, sparse_mla_attn,
-fused_forward, indexer_prolog, add_rmsnorm, prefix_mla_attn, accumulate_attn_weights, evict.
+fused_forward, indexer_prolog, add_rmsnorm, prefix_mla_attn, accumulate_attn_weights, evict,
+rotate_axes, write_kv4, read_kv4, sparse_mla_attn4, fork_pages, free_pages, reserve_pages, compact_pages.
 """
 from __future__ import annotations
 
@@ -23,7 +24,9 @@ from ._abi import STATUS_BYTES, DsaError, lib  # noqa: F401
 
 __all__ = ["Problem", "Workspace", "indexer_scores", "topk", "fused_indexer", "sparse_mla_attn",
            "fused_forward", "indexer_prolog", "add_rmsnorm", "prefix_mla_attn",
-           "accumulate_attn_weights", "evict", "Eviction", "DsaError", "lib", "trace"]
+           "accumulate_attn_weights", "evict", "Eviction", "Rotary", "rotate_axes", "kv4_row_bytes",
+           "write_kv4", "read_kv4", "sparse_mla_attn4", "fork_pages", "free_pages", "reserve_pages",
+           "compact_pages", "DsaError", "lib", "trace"]
 
 _DT = {torch.float32: _abi.DSA_F32, torch.bfloat16: _abi.DSA_BF16,
        torch.uint8: _abi.DSA_FP8_E4M3, torch.float8_e4m3fn: _abi.DSA_FP8_E4M3}
@@ -741,6 +744,357 @@ def evict(P: Problem, acc, budget: int, sink: int = 0, recent: int = 0, kv=None,
     if rc:
         _abi.check(rc)
     return Eviction(kept, cu_k_out, k_lens, acc_out, *moved)
+
+
+# ---------------------------------------------------------------------------
+# The latent cache in 4 bits, rotary positions and pages.
+
+class Rotary:
+    """Frequencies and axes of a rotation of d_rope columns: pair i turns by inv_freq[i] radians a position of its axis.
+
+    sections: pairs of each axis in order, d_rope / 2 together (default: one axis); or axes: the axis of
+    every pair.  inv_freq: d_rope / 2 frequencies (default theta ** (-2 i / d_rope)).  interleaved: pair i is columns 2i and
+    2i + 1, otherwise i and i + d_rope / 2.  Host data only: one object serves every device and stream."""
+
+    def __init__(self, d_rope: int, sections: Optional[Sequence[int]] = None, theta: float = 10000.0,
+                 inv_freq: Optional[Sequence[float]] = None, axes: Optional[Sequence[int]] = None,
+                 interleaved: bool = True):
+        if d_rope < 2 or d_rope % 2 or d_rope > 256:
+            raise ValueError(f"d_rope is {d_rope}: an even number from 2 to 256 is needed")
+        n = d_rope // 2
+        if inv_freq is None:
+            inv_freq = [float(theta) ** (-i / n) for i in range(n)]
+        inv_freq = [float(f) for f in inv_freq]
+        if sections is not None:
+            if axes is not None:
+                raise ValueError("sections and axes exclude each other")
+            if any(k < 0 for k in sections):
+                raise ValueError("sections must not be negative")
+            axes, num = [a for a, k in enumerate(sections) for _ in range(k)], len(sections)
+        else:
+            axes = [0] * n if axes is None else [int(a) for a in axes]
+            num = max(axes, default=0) + 1
+        if len(inv_freq) != n or len(axes) != n:
+            raise ValueError(f"{n} pairs need {n} frequencies and axes, not {len(inv_freq)} and {len(axes)}")
+        if not all(math.isfinite(f) for f in inv_freq) or min(axes) < 0 or not 1 <= num <= 255:
+            raise ValueError("frequencies must be finite, axes from 0 to 254")
+        self.d_rope, self.num_axes, self.interleaved = d_rope, num, bool(interleaved)
+        # turns a position as a fraction of 2^64 (of the 64-bit quotient, exactly)
+        self.turn = (ctypes.c_uint64 * n)(*(_turn(f) for f in inv_freq))
+        self.axis = (ctypes.c_uint8 * n)(*axes)
+
+
+def _turn(f: float) -> int:
+    num, den = (f / (2.0 * math.pi)).as_integer_ratio()
+    return ((num << 65) // den + 1 >> 1) % (1 << 64)
+
+
+def _head_strides(t: torch.Tensor, name: str, d: int):
+    """(tokens, heads, token stride, head stride) of a tensor [T, H, d] or [T, d] with contiguous columns."""
+    if t.dim() == 2:
+        (T, c), (st, sc) = t.shape, t.stride()
+        H, sh = 1, d
+    elif t.dim() == 3:
+        (T, H, c), (st, sh, sc) = t.shape, t.stride()
+    else:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, H, {d}] or [T, {d}]")
+    if c != d:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {d} columns")
+    if sc != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return T, H, st, sh
+
+
+def rotate_axes(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out=None, inverse: bool = False):
+    """Rotate rope columns x [T, H, d_rope] or [T, d_rope] (f32 or bf16, any strides of tokens and heads, e.g. the
+    last columns of the queries) by positions [axes, T] or, with one axis, [T] int32 (dsa_rotate_axes).
+
+    out: like x, its own strides; out=x rotates in place; a new contiguous tensor by default.  inverse turns
+    back.  Returns out."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dtype, index, d = x.dtype, x.get_device(), rotary.d_rope
+    if dtype is torch.bfloat16:
+        dt = _abi.DSA_BF16
+    elif dtype is torch.float32:
+        dt = _abi.DSA_F32
+    else:
+        raise ValueError(f"x has dtype {dtype}")
+    if index != _current_device():
+        return _elsewhere(index, rotate_axes, x, positions, rotary, out, inverse)
+    T, H, st, sh = _head_strides(x, "x", d)
+    if positions.dtype is not torch.int32 or positions.get_device() != index:
+        raise ValueError(f"positions must be an int32 tensor on cuda:{index}")
+    shape, n = positions.shape, rotary.num_axes
+    if shape != (n, T) and not (n == 1 and shape == (T,)):
+        raise ValueError(f"positions has shape {tuple(shape)}, expected {(n, T)}")
+    if T > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions' last dimension must be contiguous")
+    ld = positions.stride(0) if n > 1 else T
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    elif out.dtype is not dtype or out.shape != x.shape or out.get_device() != index:
+        raise ValueError("out must have x's shape, dtype and device")
+    if H == 0:
+        return out
+    _, _, ot, oh = _head_strides(out, "out", d)
+    rc = lib().dsa_rotate_axes(T, H, d, dt, rotary.interleaved, bool(inverse), n, rotary.turn, rotary.axis,
+                               positions.data_ptr(), ld, x.data_ptr(), st, sh, out.data_ptr(), ot, oh,
+                               _raw_stream(index))
+    if rc:
+        _abi.check(rc)
+    return out
+
+
+def kv4_row_bytes(d_c: int, d_rope: int) -> int:
+    """Bytes of a row of the 4-bit latent cache (512 + 64 columns: 416)."""
+    n = ctypes.c_int32(0)
+    _abi.check(lib().dsa_kv4_row_bytes(d_c, d_rope, ctypes.byref(n)))
+    return n.value
+
+
+def _kv4_shape(P: Problem):
+    shape = P.__dict__.get("_kv4")
+    if shape is None:
+        shape = P._kv4 = (P.cache_rows, kv4_row_bytes(P.d_c, P.d_rope))
+    return shape
+
+
+def _row_tensor(t, name: str, dts, rows: int, width: int, index: int) -> int:
+    """Row stride of a tensor [rows, width] with contiguous rows."""
+    if t is None or t.dtype not in dts or t.get_device() != index or t.shape != (rows, width):
+        raise ValueError(f"{name} must be a {dts[0]} tensor {[rows, width]} on cuda:{index}")
+    return width if t.is_contiguous() else _row_stride(t, name)
+
+
+def write_kv4(P: Problem, latent, k_rope, kv4, ws: Optional[Workspace] = None):
+    """Write the rows of P's new tokens (the last of each sequence) to the 4-bit latent cache (dsa_write_kv4).
+
+    latent [total_q, d_c] and k_rope [total_q, d_rope] (None without rope columns) of P's kv_dtype, e.g. slices of a
+    projection's output; kv4 [cache rows, kv4_row_bytes(d_c, d_rope)] uint8.  Returns kv4.  A captured call needs ws."""
+    if not kv4.is_cuda:
+        raise ValueError("kv4 must be a CUDA tensor")
+    index, dts = kv4.get_device(), _TORCH_DT[P.kv_dtype]
+    if index != _current_device():
+        return _elsewhere(index, write_kv4, P, latent, k_rope, kv4, ws)
+    _want(kv4, "kv4", (torch.uint8,), _kv4_shape(P), index)
+    _there(P, index)
+    ld = _row_tensor(latent, "latent", dts, P.c.total_q, P.d_c, index)
+    rope = ld_rope = 0
+    if P.d_rope:
+        ld_rope = _row_tensor(k_rope, "k_rope", dts, P.c.total_q, P.d_rope, index)
+        rope = k_rope.data_ptr()
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, STATUS_BYTES)
+    rc = lib().dsa_write_kv4(P._ref, latent.data_ptr(), ld, rope, ld_rope, kv4.data_ptr(), ws.buf.data_ptr(), ws.nbytes,
+                             stream)
+    if rc:
+        _abi.check(rc)
+    return kv4
+
+
+def read_kv4(P: Problem, kv4, out=None, ws: Optional[Workspace] = None):
+    """Every position's row of the 4-bit latent cache, decoded and packed: out [total_k, D] of P's kv_dtype
+    (dsa_read_kv4).  A captured call needs ws."""
+    if not kv4.is_cuda:
+        raise ValueError("kv4 must be a CUDA tensor")
+    index = kv4.get_device()
+    if index != _current_device():
+        return _elsewhere(index, read_kv4, P, kv4, out, ws)
+    _want(kv4, "kv4", (torch.uint8,), _kv4_shape(P), index)
+    _there(P, index)
+    if out is None:
+        out = torch.empty((P.c.total_k, P.d), dtype=_TORCH_OUT[P.kv_dtype], device=kv4.device)
+    else:
+        _want(out, "out", _TORCH_DT[P.kv_dtype], (P.c.total_k, P.d), index)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, STATUS_BYTES)
+    rc = lib().dsa_read_kv4(P._ref, kv4.data_ptr(), out.data_ptr(), ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return out
+
+
+def sparse_mla_attn4(P: Problem, q, kv4, idx, out=None, lse=None, want_lse: bool = True,
+                     ws: Optional[Workspace] = None):
+    """sparse_mla_attn over the 4-bit latent cache kv4 [cache rows, kv4_row_bytes(d_c, d_rope)] uint8
+    (dsa_sparse_mla_attn4): (out[ΣT, H, d_c], lse or None).  A captured call needs ws."""
+    if not kv4.is_cuda:
+        raise ValueError("kv4 must be a CUDA tensor")
+    index = kv4.get_device()
+    if index != _current_device():
+        return _elsewhere(index, sparse_mla_attn4, P, q, kv4, idx, out, lse, want_lse, ws)
+    q_shape, _, out_shape, lse_shape, idx_shape = P._shapes
+    _want(q, "q", _TORCH_DT[P.kv_dtype], q_shape, index)
+    _want(kv4, "kv4", (torch.uint8,), _kv4_shape(P), index)
+    _want(idx, "idx", _I32, idx_shape, index)
+    _there(P, index)
+    if out is None:
+        out = torch.empty(out_shape, dtype=_TORCH_OUT[P.out_dtype], device=kv4.device)
+    else:
+        _want(out, "out", _TORCH_DT[P.out_dtype], out_shape, index)
+    if lse is not None:
+        _want(lse, "lse", _F32, lse_shape, index)
+    elif want_lse:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=kv4.device)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, _ws_bytes(P, _abi.OP_SPARSE_MLA_ATTN4))
+    rc = lib().dsa_sparse_mla_attn4(P._ref, q.data_ptr(), kv4.data_ptr(), idx.data_ptr(), out.data_ptr(),
+                                    0 if lse is None else lse.data_ptr(), ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return out, lse
+
+
+def _pages_of(table, refs, index: int):
+    """(address, rows, width, row stride) of a block table [rows, width] int32; refs [pages] int32."""
+    if table.dtype is not torch.int32 or table.dim() != 2 or 0 in table.shape \
+            or not (table.is_contiguous() or ((table.shape[1] == 1 or table.stride(1) == 1)
+                                              and (table.shape[0] == 1 or table.stride(0) >= table.shape[1]))):
+        raise ValueError("table must be an int32 tensor [rows, pages] with contiguous rows")
+    if refs.dtype is not torch.int32 or refs.dim() != 1 or refs.get_device() != index or not refs.is_contiguous() \
+            or not refs.numel():
+        raise ValueError(f"refs must be a contiguous int32 tensor [num_pages] on cuda:{index}")
+    rows, width = table.shape
+    return table.data_ptr(), rows, width, table.stride(0) if rows > 1 else width
+
+
+def _entries(named, index: int) -> int:
+    """Number of entries of index tensors [n] int32."""
+    n = None
+    for name, t in named:
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous() \
+                or (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{'n' if n is None else n}] on cuda:{index}")
+        n = t.shape[0]
+    return n
+
+
+def _cache_list(caches, rows: int, index: int):
+    """Addresses and row bytes of caches with `rows` rows."""
+    n = len(caches)
+    at, size = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+    for i, t in enumerate(caches):
+        if t.dim() < 1 or t.shape[0] != rows or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"caches[{i}] must be a contiguous tensor of {rows} rows on cuda:{index}")
+        at[i] = t.data_ptr()
+        size[i] = t.numel() // rows * t.element_size()
+    return n, at, size
+
+
+_page_ws = {}  # workspace bytes by (rows, entries, pages)
+
+
+def _pages_ws(ws, index: int, stream: int, rows: int, n: int, pages: int) -> Workspace:
+    key = (rows, n, pages)
+    size = _page_ws.get(key)
+    if size is None:
+        b = ctypes.c_size_t(0)
+        _abi.check(lib().dsa_pages_workspace_size(rows, n, pages, ctypes.byref(b)))
+        if len(_page_ws) > 4096:
+            _page_ws.clear()
+        size = _page_ws[key] = b.value
+    return _op_workspace(ws, index, stream, size)
+
+
+def fork_pages(table, refs, src, dst, lens, page_size: int, ws: Optional[Workspace] = None):
+    """Row dst[i] of the block table gets the pages of row src[i]'s first lens[i] positions, shared (dsa_fork_pages).
+
+    table [rows, pages] int32 (-1 behind a row's pages), refs [num_pages] int32: table entries that hold a page; src, dst,
+    lens [n] int32, all on one device.  What dst held is not given back: free_pages first.  reserve_pages then
+    makes room for the tokens that follow.  Returns table.  A captured call needs ws."""
+    if not table.is_cuda:
+        raise ValueError("table must be a CUDA tensor")
+    index = table.get_device()
+    if index != _current_device():
+        return _elsewhere(index, fork_pages, table, refs, src, dst, lens, page_size, ws)
+    at, rows, width, ld = _pages_of(table, refs, index)
+    n = _entries((("src", src), ("dst", dst), ("lens", lens)), index)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, STATUS_BYTES)
+    rc = lib().dsa_fork_pages(at, rows, width, ld, refs.data_ptr(), refs.shape[0], page_size, n, src.data_ptr(),
+                              dst.data_ptr(), lens.data_ptr(), ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return table
+
+
+def free_pages(table, refs, rows, ws: Optional[Workspace] = None):
+    """Give back the pages of the block table's rows named in rows [n] int32 (dsa_free_pages); their entries become
+    -1.  Returns table.  A captured call needs ws."""
+    if not table.is_cuda:
+        raise ValueError("table must be a CUDA tensor")
+    index = table.get_device()
+    if index != _current_device():
+        return _elsewhere(index, free_pages, table, refs, rows, ws)
+    at, num, width, ld = _pages_of(table, refs, index)
+    n = _entries((("rows", rows),), index)
+    stream = _raw_stream(index)
+    ws = _op_workspace(ws, index, stream, STATUS_BYTES)
+    rc = lib().dsa_free_pages(at, num, width, ld, refs.data_ptr(), refs.shape[0], n, rows.data_ptr(), ws.buf.data_ptr(),
+                              ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return table
+
+
+def reserve_pages(table, refs, rows, lens, new_lens, page_size: int, caches=(), held=None,
+                  ws: Optional[Workspace] = None):
+    """Give row rows[i] of the block table, which holds lens[i] positions, pages of its own to write positions lens[i] ..
+    new_lens[i] - 1 to (dsa_reserve_pages): new ones, and a copy, in all caches, of a last page that others hold too.
+
+    caches: up to 8 contiguous tensors of num_pages * page_size rows.  Returns held [n] int32: new_lens[i], or lens[i] where
+    the free pages did not suffice (ws.status() then has DSA_FLAG_NO_PAGES).  A captured call needs ws."""
+    if not table.is_cuda:
+        raise ValueError("table must be a CUDA tensor")
+    index = table.get_device()
+    if index != _current_device():
+        return _elsewhere(index, reserve_pages, table, refs, rows, lens, new_lens, page_size, caches, held, ws)
+    at, num, width, ld = _pages_of(table, refs, index)
+    n = _entries((("rows", rows), ("lens", lens), ("new_lens", new_lens)), index)
+    count, addresses, sizes = _cache_list(caches, refs.shape[0] * page_size, index)
+    if held is None:
+        held = torch.empty((n,), dtype=torch.int32, device=table.device)
+    else:
+        _want(held, "held", _I32, (n,), index)
+    stream = _raw_stream(index)
+    ws = _pages_ws(ws, index, stream, num, n, refs.shape[0])
+    rc = lib().dsa_reserve_pages(at, num, width, ld, refs.data_ptr(), refs.shape[0], page_size, n, rows.data_ptr(),
+                                 lens.data_ptr(), new_lens.data_ptr(), held.data_ptr(), count, addresses, sizes,
+                                 ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return held
+
+
+def compact_pages(table, refs, page_size: int, caches=(), moved=None, live=None, ws: Optional[Workspace] = None):
+    """Move the pages in use to the front of the pool, in all caches; table and refs follow (dsa_compact_pages).
+
+    Every holder of a page has to be in the table.  Returns (moved [num_pages] int32: where each page went, -1 for a free one;
+    live [1] int32: the pages in use).  A captured call needs ws."""
+    if not table.is_cuda:
+        raise ValueError("table must be a CUDA tensor")
+    index = table.get_device()
+    if index != _current_device():
+        return _elsewhere(index, compact_pages, table, refs, page_size, caches, moved, live, ws)
+    at, num, width, ld = _pages_of(table, refs, index)
+    pages = refs.shape[0]
+    count, addresses, sizes = _cache_list(caches, pages * page_size, index)
+    if moved is None:
+        moved = torch.empty((pages,), dtype=torch.int32, device=table.device)
+    else:
+        _want(moved, "moved", _I32, (pages,), index)
+    if live is None:
+        live = torch.empty((1,), dtype=torch.int32, device=table.device)
+    else:
+        _want(live, "live", _I32, (1,), index)
+    stream = _raw_stream(index)
+    ws = _pages_ws(ws, index, stream, num, 0, pages)
+    rc = lib().dsa_compact_pages(at, num, width, ld, refs.data_ptr(), pages, page_size, moved.data_ptr(), live.data_ptr(),
+                                 count, addresses, sizes, ws.buf.data_ptr(), ws.nbytes, stream)
+    if rc:
+        _abi.check(rc)
+    return moved, live
 
 
 class trace:

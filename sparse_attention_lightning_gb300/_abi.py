@@ -13,8 +13,9 @@ DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_WORKSPAC
     DSA_ERR_TIMEOUT = range(6)
 DSA_F32, DSA_BF16, DSA_FP8_E4M3, DSA_MXFP8_E4M3 = 0, 1, 2, 3
 DSA_FLAG_BAD_INDEX, DSA_FLAG_BAD_SEQS, DSA_FLAG_TIMEOUT, DSA_FLAG_CHECK = 0x1, 0x2, 0x4, 0x8
+DSA_FLAG_NO_PAGES = 0x10
 OP_INDEXER_SCORES, OP_TOPK, OP_FUSED_INDEXER, OP_SPARSE_MLA_ATTN, OP_FUSED_FORWARD = 1, 2, 3, 4, 5
-OP_PREFIX_MLA_ATTN, OP_ATTN_WEIGHTS, OP_EVICT = 6, 7, 8
+OP_PREFIX_MLA_ATTN, OP_ATTN_WEIGHTS, OP_EVICT, OP_KV4_ROWS, OP_SPARSE_MLA_ATTN4 = 6, 7, 8, 9, 10
 
 # Every symbol include/dsa.h declares.
 EXPORTS = ("dsa_workspace_size", "dsa_indexer_scores", "dsa_topk", "dsa_fused_indexer",
@@ -22,7 +23,10 @@ EXPORTS = ("dsa_workspace_size", "dsa_indexer_scores", "dsa_topk", "dsa_fused_in
            "dsa_status_str", "dsa_last_error", "dsa_abi_version", "dsa_trace_begin",
            "dsa_trace_end", "dsa_trace_count", "dsa_trace_get", "dsa_fused_indexer_static",
            "dsa_selftest_wait_timeout", "dsa_indexer_prolog", "dsa_add_rmsnorm",
-           "dsa_prefix_mla_attn", "dsa_accumulate_attn_weights", "dsa_evict")
+           "dsa_prefix_mla_attn", "dsa_accumulate_attn_weights", "dsa_evict", "dsa_rotate_axes",
+           "dsa_kv4_row_bytes", "dsa_write_kv4", "dsa_read_kv4", "dsa_sparse_mla_attn4",
+           "dsa_pages_workspace_size", "dsa_fork_pages", "dsa_free_pages", "dsa_reserve_pages",
+           "dsa_compact_pages")
 
 
 class DsaProblem(ctypes.Structure):
@@ -75,7 +79,7 @@ def lib() -> ctypes.CDLL:
                           "`python -m sparse_attention_lightning_gb300.build`")
     L = ctypes.CDLL(_path)
     P = ctypes.POINTER(DsaProblem)
-    vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "dsa_workspace_size": [P, ctypes.c_int, ctypes.POINTER(sz)],
         "dsa_indexer_scores": [P, vp, vp, vp, vp, vp, vp, i64, vp, sz, vp],
@@ -93,6 +97,16 @@ def lib() -> ctypes.CDLL:
         "dsa_accumulate_attn_weights": [P, vp, vp, vp, vp, vp, i64, vp, sz, vp],
         "dsa_evict": [P, vp, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, i64,
                       vp, vp, vp, vp, vp, vp, vp, ctypes.c_int32, ctypes.c_int32, i64, vp, sz, vp],
+        "dsa_rotate_axes": [i64] + [i32] * 6 + [vp, vp, vp, i64, vp, i64, i64, vp, i64, i64, vp],
+        "dsa_kv4_row_bytes": [i32, i32, ctypes.POINTER(i32)],
+        "dsa_write_kv4": [P, vp, i64, vp, i64, vp, vp, sz, vp],
+        "dsa_read_kv4": [P, vp, vp, vp, sz, vp],
+        "dsa_sparse_mla_attn4": [P, vp, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_pages_workspace_size": [i32, i32, i32, ctypes.POINTER(sz)],
+        "dsa_fork_pages": [vp, i32, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp],
+        "dsa_free_pages": [vp, i32, i32, i64, vp, i32, i32, vp, vp, sz, vp],
+        "dsa_reserve_pages": [vp, i32, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp],
+        "dsa_compact_pages": [vp, i32, i32, i64, vp, i32, i32, vp, vp, i32, vp, vp, vp, sz, vp],
         "dsa_read_status": [vp, vp, ctypes.POINTER(ctypes.c_uint32)],
         "dsa_abi_version": [],
         "dsa_trace_begin": [ctypes.c_int],

@@ -12,7 +12,10 @@
 #include "attn_weights.cuh"
 #include "dsa_internal.cuh"
 #include "evict.cuh"
+#include "kv4.cuh"
+#include "pages.cuh"
 #include "prefix_attn.cuh"
+#include "rotary.cuh"
 #include "tc_sm100.cuh"
 
 namespace dsa {
@@ -472,6 +475,120 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// ----------------------------------------------------------------------------
+// The 4-bit latent cache.
+
+Kv4Rows kv4_rows(const dsa_problem* p, void* ws) {
+  Kv4Rows a{};
+  a.seqs = seqs_of(p);
+  a.max_q_len = p->max_q_len;
+  a.d_c = p->d_c;
+  a.d_rope = p->d_rope;
+  a.dtype = p->kv_dtype;
+  a.status = static_cast<uint32_t*>(ws);
+  return a;
+}
+int64_t kv4_bytes(const dsa_problem* p) { return seqs_of(p).cache_rows() * kv4_row_bytes(p->d_c, p->d_rope); }
+
+Attn4Args attn4_args(const dsa_problem* p) {
+  Attn4Args a{};
+  a.seqs = seqs_of(p);
+  a.max_q_len = p->max_q_len;
+  a.h = p->h;
+  a.d_c = p->d_c;
+  a.d_rope = p->d_rope;
+  a.top_k = p->top_k;
+  a.kv_dtype = p->kv_dtype;
+  a.out_dtype = p->out_dtype;
+  a.scale_log2 = scale_of(p) * kLog2e;
+  a.splits = attn4_simt_splits(a);
+  return a;
+}
+// Partial outputs and their (max, sum) for every piece of every row.
+size_t carve_attn4(Attn4Args& a, void* ws) {
+  Carve c;
+  const size_t rows = (size_t)a.seqs.total_q * a.h, n = a.splits > 1 ? a.splits : 0;
+  const size_t o = c.take(n * rows * a.d_c * 4), m = c.take(n * rows * 8);
+  if (ws) {
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + m);
+    a.status = static_cast<uint32_t*>(ws);
+  }
+  return c.off;
+}
+
+// ----------------------------------------------------------------------------
+// Pages.
+
+int check_i32(const void* p, const char* name) {
+  if (!p || ((uintptr_t)p & 3u) != 0) return set_error(DSA_ERR_INVALID_ARG, "%s is NULL or not 4-byte aligned", name);
+  return DSA_OK;
+}
+
+// The table, the counts and n entries; fills `a`.
+int check_pages(PagesArgs& a, int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                int32_t num_pages, int32_t page_size, int32_t n) {
+  if (rows < 1 || width < 1 || num_pages < 1 || n < 0 || ld_table < width)
+    return set_error(DSA_ERR_INVALID_ARG, "rows = %d, width = %d, ld_table = %lld, num_pages = %d, n = %d", rows, width,
+                     (long long)ld_table, num_pages, n);
+  if (page_size < 16 || (page_size & (page_size - 1)) != 0)
+    return set_error(DSA_ERR_UNSUPPORTED, "page_size = %d (a power of two >= 16)", page_size);
+  if ((int64_t)num_pages * page_size >= (int64_t(1) << 31) || (int64_t)rows * width >= (int64_t(1) << 31))
+    return set_error(DSA_ERR_UNSUPPORTED, "num_pages * page_size or rows * width >= 2^31");
+  DSA_TRY(check_i32(table, "table"));
+  DSA_TRY(check_i32(refs, "refs"));
+  a.table = table;
+  a.rows = rows;
+  a.width = width;
+  a.ld_table = ld_table;
+  a.refs = refs;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.n = n;
+  return DSA_OK;
+}
+
+struct Span {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+// No two of the spans overlap.
+int check_apart(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(s[i].p, s[i].bytes, s[j].p, s[j].bytes))
+        return set_error(DSA_ERR_INVALID_ARG, "%s overlaps %s", s[i].name, s[j].name);
+  return DSA_OK;
+}
+Span table_span(const PagesArgs& a) { return {a.table, ((a.rows - 1) * a.ld_table + a.width) * 4, "table"}; }
+Span refs_span(const PagesArgs& a) { return {a.refs, (int64_t)a.num_pages * 4, "refs"}; }
+
+int check_caches(PagesArgs& a, int32_t num, void* const* caches, const int64_t* row_bytes, Span* spans) {
+  if (num < 0 || num > kMaxCaches) return set_error(DSA_ERR_UNSUPPORTED, "num_caches = %d (0..%d)", num, kMaxCaches);
+  if (num > 0 && (!caches || !row_bytes)) return set_error(DSA_ERR_INVALID_ARG, "caches or row_bytes is NULL");
+  a.caches.n = num;
+  for (int c = 0; c < num; ++c) {
+    DSA_TRY(check_ptr(caches[c], "a cache"));
+    if (row_bytes[c] < 1 || row_bytes[c] > (int64_t(1) << 20))
+      return set_error(DSA_ERR_UNSUPPORTED, "row_bytes = %lld (1..2^20)", (long long)row_bytes[c]);
+    if (row_bytes[c] * a.page_size > (int64_t(1) << 40))
+      return set_error(DSA_ERR_UNSUPPORTED, "a page of more than 2^40 bytes");
+    a.caches.base[c] = static_cast<char*>(caches[c]);
+    a.caches.row_bytes[c] = row_bytes[c];
+    spans[c] = {caches[c], (int64_t)a.num_pages * a.page_size * row_bytes[c], "a cache"};
+  }
+  return DSA_OK;
+}
+
+size_t pages_ws(int32_t rows, int32_t n, int32_t num_pages) {
+  Carve c;
+  const size_t r = n > 0 ? reserve_scratch_bytes(rows, n, num_pages) : 0, m = compact_scratch_bytes(num_pages);
+  c.take(r > m ? r : m);
+  return c.off;
+}
+int32_t* pages_scratch(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kStatusBytes); }
+
 }  // namespace
 }  // namespace dsa
 
@@ -524,6 +641,13 @@ int dsa_workspace_size(const dsa_problem* p, int op, size_t* bytes) {
       *bytes = carve_weights(p, nullptr, nullptr);
       break;
     case DSA_OP_EVICT: DSA_TRY(check_problem(p, false, false)); *bytes = kStatusBytes; break;
+    case DSA_OP_KV4_ROWS: DSA_TRY(check_problem(p, false, true)); *bytes = kStatusBytes; break;
+    case DSA_OP_SPARSE_MLA_ATTN4: {
+      DSA_TRY(check_problem(p, false, true));
+      Attn4Args a = attn4_args(p);
+      *bytes = carve_attn4(a, nullptr);
+      break;
+    }
     default: return set_error(DSA_ERR_INVALID_ARG, "unknown op %d", op);
   }
   return DSA_OK;
@@ -771,6 +895,239 @@ int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t bu
   a.rows_out = rows_out;
   a.status = static_cast<uint32_t*>(ws);
   return launch_evict(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_rotate_axes(int64_t tokens, int32_t heads, int32_t d, int32_t dtype, int32_t interleaved,
+                    int32_t inverse, int32_t axes, const uint64_t* turn, const uint8_t* axis,
+                    const int32_t* positions, int64_t ld_pos, const void* x, int64_t x_token,
+                    int64_t x_head, void* out, int64_t out_token, int64_t out_head, void* stream) {
+  if (dtype != DSA_F32 && dtype != DSA_BF16) return set_error(DSA_ERR_INVALID_ARG, "dtype = %d (F32 or BF16)", dtype);
+  if (tokens < 0 || heads < 1 || axes < 1 || axes > 255 || ld_pos < tokens)
+    return set_error(DSA_ERR_INVALID_ARG, "tokens = %lld, heads = %d, axes = %d, ld_pos = %lld", (long long)tokens, heads,
+                     axes, (long long)ld_pos);
+  if (d < 2 || d > 2 * kMaxPairs || d % 2) return set_error(DSA_ERR_UNSUPPORTED, "d = %d (2..256, even)", d);
+  if (!turn || !axis) return set_error(DSA_ERR_INVALID_ARG, "turn or axis is NULL");
+  if (x_token < 0 || x_head < 0 || out_token < 0 || out_head < 0)
+    return set_error(DSA_ERR_INVALID_ARG, "negative strides");
+  if (tokens >= (int64_t(1) << 31) || (int64_t)tokens * heads >= (int64_t(1) << 40))
+    return set_error(DSA_ERR_UNSUPPORTED, "tokens = %lld", (long long)tokens);
+  for (int i = 0; i < d / 2; ++i)
+    if (axis[i] >= axes) return set_error(DSA_ERR_INVALID_ARG, "axis[%d] = %d of %d axes", i, axis[i], axes);
+  if (tokens == 0) return DSA_OK;
+  const int64_t size = dtype == DSA_F32 ? 4 : 2;
+  auto bad = [&](const void* p) { return !p || (uintptr_t)p % size != 0; };
+  if (bad(x) || bad(out)) return set_error(DSA_ERR_INVALID_ARG, "x or out is NULL or not aligned to its element");
+  DSA_TRY(check_i32(positions, "positions"));
+  // the rows of out are apart from each other
+  if ((heads > 1 && out_head < d) || (tokens > 1 && out_token < d) ||
+      (heads > 1 && tokens > 1 && out_token < out_head * (heads - 1) + d && out_head < out_token * (tokens - 1) + d))
+    return set_error(DSA_ERR_INVALID_ARG, "rows of out overlap (strides %lld, %lld)", (long long)out_token, (long long)out_head);
+  const int64_t nx = ((tokens - 1) * x_token + (heads - 1) * x_head + d) * size;
+  const int64_t no = ((tokens - 1) * out_token + (heads - 1) * out_head + d) * size;
+  const bool same = (tokens == 1 || x_token == out_token) && (heads == 1 || x_head == out_head);
+  if (!(same && x == out) && overlap(x, nx, out, no)) {
+    // same strides: the rows interleave if their starts, modulo the strides, are d columns apart either way
+    const int64_t step = heads > 1 ? out_head : out_token;
+    const int64_t off = (int64_t)((uintptr_t)out - (uintptr_t)x);
+    const int64_t r = step > 0 ? ((off % (step * size)) + step * size) % (step * size) : 0;
+    const bool comb = heads == 1 || tokens == 1 || out_token % out_head == 0;
+    if (!(same && step > 0 && comb && r >= d * size && r <= (step - d) * size))
+      return set_error(DSA_ERR_INVALID_ARG, "out overlaps x");
+  }
+  if (overlap(positions, ((axes - 1) * ld_pos + tokens) * 4, out, no))
+    return set_error(DSA_ERR_INVALID_ARG, "out overlaps positions");
+  RotaryArgs a{};
+  a.tokens = tokens;
+  a.heads = heads;
+  a.d = d;
+  a.dtype = dtype;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  a.pos = positions;
+  a.ld_pos = ld_pos;
+  a.x = x;
+  a.xt = tokens > 1 ? x_token : 0;  // (a stride that no row needs says nothing about alignment)
+  a.xh = heads > 1 ? x_head : 0;
+  a.out = out;
+  a.ot = tokens > 1 ? out_token : 0;
+  a.oh = heads > 1 ? out_head : 0;
+  memcpy(a.turn, turn, (size_t)d / 2 * sizeof(uint64_t));
+  memcpy(a.axis, axis, (size_t)d / 2);
+  return launch_rotary(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_kv4_row_bytes(int32_t d_c, int32_t d_rope, int32_t* bytes) {
+  if (!bytes) return set_error(DSA_ERR_INVALID_ARG, "bytes is NULL");
+  if (d_c < 16 || d_c > 1024 || d_c % 16 || d_rope < 0 || d_rope > 256 || d_rope % 16)
+    return set_error(DSA_ERR_UNSUPPORTED, "d_c = %d, d_rope = %d", d_c, d_rope);
+  *bytes = kv4_row_bytes(d_c, d_rope);
+  return DSA_OK;
+}
+
+int dsa_write_kv4(const dsa_problem* p, const void* latent, int64_t ld_latent, const void* k_rope,
+                  int64_t ld_rope, void* kv4, void* ws, size_t ws_bytes, void* stream) {
+  DSA_TRY(check_problem(p, false, true));
+  DSA_TRY(check_ptr(kv4, "kv4"));
+  DSA_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  if (p->total_q == 0) return DSA_OK;
+  const int64_t size = p->kv_dtype == DSA_F32 ? 4 : 2;
+  const bool rope = p->d_rope > 0;
+  if (!latent || (uintptr_t)latent % size || ld_latent < p->d_c)
+    return set_error(DSA_ERR_INVALID_ARG, "latent is NULL or not aligned to its element, or ld_latent = %lld", (long long)ld_latent);
+  if (rope && (!k_rope || (uintptr_t)k_rope % size || ld_rope < p->d_rope))
+    return set_error(DSA_ERR_INVALID_ARG, "k_rope is NULL or not aligned to its element, or ld_rope = %lld", (long long)ld_rope);
+  const int64_t last = p->total_q - 1;
+  if (overlap(kv4, kv4_bytes(p), latent, (last * ld_latent + p->d_c) * size) ||
+      (rope && overlap(kv4, kv4_bytes(p), k_rope, (last * ld_rope + p->d_rope) * size)))
+    return set_error(DSA_ERR_INVALID_ARG, "kv4 overlaps latent or k_rope");
+  Kv4Rows a = kv4_rows(p, ws);
+  a.latent = latent;
+  a.ld_latent = ld_latent;
+  a.k_rope = k_rope;
+  a.ld_rope = ld_rope;
+  a.kv4 = static_cast<uint8_t*>(kv4);
+  return launch_write_kv4(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_read_kv4(const dsa_problem* p, const void* kv4, void* out, void* ws, size_t ws_bytes, void* stream) {
+  DSA_TRY(check_problem(p, false, true));
+  DSA_TRY(check_ptr(kv4, "kv4"));
+  DSA_TRY(check_ptr(out, "out"));
+  DSA_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  if (overlap(kv4, kv4_bytes(p), out, (int64_t)p->total_k * (p->d_c + p->d_rope) * (p->kv_dtype == DSA_F32 ? 4 : 2)))
+    return set_error(DSA_ERR_INVALID_ARG, "out overlaps kv4");
+  Kv4Rows a = kv4_rows(p, ws);
+  a.kv4 = const_cast<uint8_t*>(static_cast<const uint8_t*>(kv4));
+  a.out = out;
+  return launch_read_kv4(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_sparse_mla_attn4(const dsa_problem* p, const void* q, const void* kv4, const int32_t* idx,
+                         void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  DSA_TRY(check_problem(p, false, true));
+  const bool none = p->total_q == 0;
+  if (!none && p->max_q_len < 1)
+    return set_error(DSA_ERR_INVALID_ARG, "max_q_len = %d with total_q = %d", p->max_q_len, p->total_q);
+  DSA_TRY(check_ptr(q, "q", none));
+  DSA_TRY(check_ptr(kv4, "kv4"));
+  DSA_TRY(check_ptr(idx, "idx", none));
+  DSA_TRY(check_ptr(out, "out", none));
+  DSA_TRY(check_ptr(lse, "lse", true));
+  if ((int64_t)p->total_q * p->h >= (int64_t(1) << 31))
+    return set_error(DSA_ERR_UNSUPPORTED, "too many (query, head) rows");
+  Attn4Args a = attn4_args(p);
+  DSA_TRY(check_ws(ws, ws_bytes, carve_attn4(a, nullptr)));
+  if (none) return DSA_OK;
+  carve_attn4(a, ws);
+  a.q = q;
+  a.kv4 = static_cast<const uint8_t*>(kv4);
+  a.idx = idx;
+  a.out = out;
+  a.lse = lse;
+  return launch_attn4_simt(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_pages_workspace_size(int32_t rows, int32_t n, int32_t num_pages, size_t* bytes) {
+  if (!bytes) return set_error(DSA_ERR_INVALID_ARG, "bytes is NULL");
+  if (rows < 1 || n < 0 || num_pages < 1)
+    return set_error(DSA_ERR_INVALID_ARG, "rows = %d, n = %d, num_pages = %d", rows, n, num_pages);
+  *bytes = pages_ws(rows, n, num_pages);
+  return DSA_OK;
+}
+
+int dsa_fork_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                   int32_t num_pages, int32_t page_size, int32_t n, const int32_t* src,
+                   const int32_t* dst, const int32_t* lens, void* ws, size_t ws_bytes, void* stream) {
+  PagesArgs a{};
+  DSA_TRY(check_pages(a, table, rows, width, ld_table, refs, num_pages, page_size, n));
+  DSA_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  if (n == 0) return DSA_OK;
+  DSA_TRY(check_i32(src, "src"));
+  DSA_TRY(check_i32(dst, "dst"));
+  DSA_TRY(check_i32(lens, "lens"));
+  const int64_t nb = (int64_t)n * 4;
+  const Span in[3] = {{src, nb, "src"}, {dst, nb, "dst"}, {lens, nb, "lens"}};
+  const Span out[2] = {table_span(a), refs_span(a)};
+  DSA_TRY(check_apart(out, 2));
+  for (const Span& i : in) {
+    const Span s[3] = {i, out[0], out[1]};
+    DSA_TRY(check_apart(s, 3));
+  }
+  a.src = src;
+  a.dst = dst;
+  a.lens = lens;
+  a.status = static_cast<uint32_t*>(ws);
+  return launch_fork_pages(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_free_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                   int32_t num_pages, int32_t n, const int32_t* row, void* ws, size_t ws_bytes, void* stream) {
+  PagesArgs a{};
+  DSA_TRY(check_pages(a, table, rows, width, ld_table, refs, num_pages, 16, n));
+  DSA_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  if (n == 0) return DSA_OK;
+  DSA_TRY(check_i32(row, "row"));
+  const Span s[3] = {{row, (int64_t)n * 4, "row"}, table_span(a), refs_span(a)};
+  DSA_TRY(check_apart(s, 3));
+  a.dst = row;
+  a.status = static_cast<uint32_t*>(ws);
+  return launch_free_pages(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_reserve_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                      int32_t num_pages, int32_t page_size, int32_t n, const int32_t* row,
+                      const int32_t* lens, const int32_t* new_lens, int32_t* held, int32_t num_caches,
+                      void* const* caches, const int64_t* row_bytes, void* ws, size_t ws_bytes, void* stream) {
+  PagesArgs a{};
+  DSA_TRY(check_pages(a, table, rows, width, ld_table, refs, num_pages, page_size, n));
+  Span out[3 + kMaxCaches];
+  DSA_TRY(check_caches(a, num_caches, caches, row_bytes, out + 3));
+  DSA_TRY(check_ws(ws, ws_bytes, n > 0 ? pages_ws(rows, n, num_pages) : kStatusBytes));
+  if (n == 0) return DSA_OK;
+  DSA_TRY(check_i32(row, "row"));
+  DSA_TRY(check_i32(lens, "lens"));
+  DSA_TRY(check_i32(new_lens, "new_lens"));
+  DSA_TRY(check_i32(held, "held"));
+  const int64_t nb = (int64_t)n * 4;
+  out[0] = table_span(a);
+  out[1] = refs_span(a);
+  out[2] = {held, nb, "held"};
+  DSA_TRY(check_apart(out, 3 + num_caches));
+  const Span in[3] = {{row, nb, "row"}, {lens, nb, "lens"}, {new_lens, nb, "new_lens"}};
+  for (const Span& i : in)
+    for (int k = 0; k < 3 + num_caches; ++k) {
+      const Span s[2] = {i, out[k]};
+      DSA_TRY(check_apart(s, 2));
+    }
+  a.dst = row;
+  a.lens = lens;
+  a.new_lens = new_lens;
+  a.held = held;
+  a.status = static_cast<uint32_t*>(ws);
+  a.scratch = pages_scratch(ws);
+  return launch_reserve_pages(a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_compact_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table, int32_t* refs,
+                      int32_t num_pages, int32_t page_size, int32_t* moved, int32_t* live, int32_t num_caches,
+                      void* const* caches, const int64_t* row_bytes, void* ws, size_t ws_bytes, void* stream) {
+  PagesArgs a{};
+  DSA_TRY(check_pages(a, table, rows, width, ld_table, refs, num_pages, page_size, 0));
+  Span out[4 + kMaxCaches];
+  DSA_TRY(check_caches(a, num_caches, caches, row_bytes, out + 4));
+  DSA_TRY(check_ws(ws, ws_bytes, pages_ws(rows, 0, num_pages)));
+  DSA_TRY(check_i32(moved, "moved"));
+  DSA_TRY(check_i32(live, "live"));
+  out[0] = table_span(a);
+  out[1] = refs_span(a);
+  out[2] = {moved, (int64_t)num_pages * 4, "moved"};
+  out[3] = {live, 4, "live"};
+  DSA_TRY(check_apart(out, 4 + num_caches));
+  a.moved = moved;
+  a.live = live;
+  a.status = static_cast<uint32_t*>(ws);
+  a.scratch = pages_scratch(ws);
+  return launch_compact_pages(a, static_cast<cudaStream_t>(stream));
 }
 
 int dsa_clear_status(void* ws, void* stream) {
