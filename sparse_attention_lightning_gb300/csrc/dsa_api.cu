@@ -501,7 +501,7 @@ Attn4Args attn4_args(const dsa_problem* p) {
   a.kv_dtype = p->kv_dtype;
   a.out_dtype = p->out_dtype;
   a.scale_log2 = scale_of(p) * kLog2e;
-  a.splits = attn4_simt_splits(a);
+  a.splits = attn4_tc_eligible(a) ? attn4_tc_splits(a) : attn4_simt_splits(a);
   return a;
 }
 // Partial outputs and their (max, sum) for every piece of every row.
@@ -1024,7 +1024,8 @@ int dsa_sparse_mla_attn4(const dsa_problem* p, const void* q, const void* kv4, c
   a.idx = idx;
   a.out = out;
   a.lse = lse;
-  return launch_attn4_simt(a, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return attn4_tc_eligible(a) ? launch_attn4_tc(a, s) : launch_attn4_simt(a, s);
 }
 
 int dsa_pages_workspace_size(int32_t rows, int32_t n, int32_t num_pages, size_t* bytes) {
