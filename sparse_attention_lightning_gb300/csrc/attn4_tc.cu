@@ -2,28 +2,32 @@
 //
 //   S_i = scale · q[t,h,:]·kv[row_i, :],  out = Σ softmax(S)_i · kv[row_i, :512],  lse = log Σ exp S_i
 //
-// A query's heads are the MMA's M = 128 rows.  A 128 x 512 fp32 accumulator is all of the tensor memory, so a CTA accumulates
-// 256 output columns, two CTAs a query, each with the whole logits: 576 + 256 columns of MMA a CTA where 544 would do, without
-// an exchange between SMs.  The twin finds the rows in L2.  Few queries are cut into pieces of their entries, merged
-// afterwards.
+// A query's heads are the MMA's M = 128 rows, a CTA takes a query (or a piece of its entries, merged afterwards), and
+// goes over its entries twice, 64 at a time:
+//   phase 1, logits:  S = Q·Kᵀ (M=128, N=64, K=576), p = 2^(S − m) to a scratch of the CTA (16 KB a chunk, in L2)
+//   phase 2, values:  O += P·V (M=128, N=2·256, K=64)
+// Why twice.  A 128 x 512 fp32 accumulator is all of the tensor memory, so logits and values do not fit it together.
+// In one pass two CTAs a query, each with half the values, had to compute the logits twice, from a query of which most was
+// in shared memory (6 KB of operands an MMA, 128 B a clock): operands and decoded rows of a chunk took 285 KB of
+// shared-memory traffic in each of them, 2,230 clocks, where its MMAs needed 2,020, and the two together 7,000 clocks a chunk.
+// Apart, the query's 288 columns and three logit buffers fill the tensor memory in phase 1 and the accumulator does in
+// phase 2, nothing is computed twice (2,212 clocks of MMAs), and a chunk's traffic is 173 and 202 KB.  The price is that rows are decoded
+// twice (416 bytes of a row come from L2 the second time) and P goes through L2.
 //
-// Eight warps gather and decode.  A row is 416 bytes, so the gather is a third of what bf16 rows take and goes through
-// registers, kAhead chunks of 64 entries ahead: a lane takes one row (eight rows a warp) and, of it, 16-byte pieces 64 bytes apart,
+// The running maximum m of a head only decides the scale of p: it is a whole number (of log2), moves when a chunk's maximum is more than
+// 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which is exact, instead of rescaling O.
+// The sum is in fp32 of the unrounded p.  P is rounded to bf16, which the MMA wants beside bf16 values: 2^-8 of each p at
+// most, in either direction.
+//
+// Eight warps gather and decode.  A row is 416 bytes, so the gather goes through registers, a chunk ahead: a lane takes one
+// row (eight rows a warp) and, of it, 32 bytes of codes (64 columns) twice and 32 of rope columns,
 // and stores what they decode to in the MMA's operand layout.  A quarter warp's eight lanes hold eight different rows, whose 16-byte
 // stores the 128-byte swizzle spreads over all banks.  Decoding is two shifts, two logical operations and a product for
 // a pair of columns (kv4.cuh): the operand is the value times 2^-16, exactly, which the logits' scale and the output make good;
-// rope columns get the same factor.  Some 400 instructions a lane and chunk, 800 of a scheduler's ~2,100 clocks.
+// rope columns get the same factor.
 //
-// Shared memory: five query tiles (80 KB) and two chunks of nine tiles of [64 keys x 64 columns] (144 KB).  A chunk's
-// five "K tiles" (the other half's columns and the rope) are free again once its logits are done, its four "V tiles" (the CTA's own
-// columns) after P·V, half a chunk later.  Tensor memory: O (256 columns), two logit buffers (64; P, as bf16 pairs, overwrites
-// the first half of its own logits), the query columns that match the V tiles (128).
-//
-// One thread issues S(g) over the K tiles and half the V tiles, P(g-1)·V, and the other half of S(g): softmax has the
-// first part to finish in, and the last hides the wait for P·V before the next chunk overwrites its P.  Four softmax warps, a
-// thread a head: the running max moves only when a row's grows by more than 2^8 (O is then rescaled), the sum is in fp32 of
-// the unrounded p.  P is rounded to bf16, which the MMA wants beside bf16 values: 2^-8 of each p at most, in either
-// direction.  Every wait is bounded (DSA_FLAG_TIMEOUT).
+// Shared memory: three chunks of nine tiles of [64 keys x 64 columns] in phase 1, two of eight and four P tiles in phase 2.
+// Every wait is bounded (DSA_FLAG_TIMEOUT).
 #include <float.h>
 
 #include "kv4.cuh"
@@ -37,28 +41,39 @@ using namespace tc;
 constexpr int kM = 128;                    // heads
 constexpr int kN = 64;                     // entries of a chunk
 constexpr int kTile = kN * 128;            // 8 KB: 64 keys x 64 columns
-constexpr int kQTile = kM * 128;           // 16 KB
-constexpr int kVT = 4, kKT = 5;            // V and K tiles of a chunk
-constexpr int kSlot = (kVT + kKT) * kTile; // 72 KB
-constexpr int kDecoders = 8;               // warps
-constexpr int kSoftWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kDecoders + 1);
-constexpr int kMmaWarp = kSoftWarps + kDecoders;
-constexpr int kAhead = 1;                  // chunks whose rows are in flight ahead of the one being decoded
-constexpr int kBarBytes = 512;
-constexpr int kSmem = kKT * kQTile + 2 * kSlot + kBarBytes + 1024;
-constexpr int kOCol = 0, kSCol = 256, kQCol = 384;
+constexpr int kQTile = kM * 128;           // 16 KB: 128 heads x 64 columns, or a chunk's P
 constexpr int kDc = 512, kDr = 64, kD = kDc + kDr;
-constexpr int kRow = kv4_row_bytes(kDc, kDr);
+constexpr int kTiles = kD / 64, kVTiles = kDc / 64;
+constexpr int kRow = kv4_row_bytes(kDc, kDr), kRaw = kN * kRow;  // a gathered chunk: 26 KB
+constexpr int kStages = 3;                                       // of them in flight
+constexpr int kKSlots = 2, kKSlot = kTiles * kTile;              // phase 1: 2 x 72 KB
+constexpr int kVSlots = 3, kVSlot = kVTiles / 2 * kTile;         // phase 2: 3 x 32 KB (half the columns of a chunk)
+constexpr int kPSlots = 3;                                       //   and 3 x 16 KB
+constexpr int kSBufs = 3;                  // logit buffers
+constexpr int kMasks = 8;                  // chunks whose skipped entries are known (see the gathering warp)
+constexpr int kSoftWarps = 4;
+constexpr int kDecoders = 8;               // warps
+constexpr int kMmaWarp = kSoftWarps + kDecoders, kGatherWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kGatherWarp + 1);
+constexpr int kRing = kKSlots * kKSlot;
+constexpr int kBarBytes = 512;
+constexpr int kSmem = kRing + kStages * kRaw + kBarBytes + 1024;
+constexpr int kQCol = 0, kSCol = kD / 2;   // tensor memory of phase 1: 288 query columns, the logits; of phase 2: O
 constexpr int kRopeAt = kv4_rope_at(kDc), kScaleAt = kv4_scale_at(kDc, kDr);
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kGrowLog2 = 8.0f;
+constexpr int64_t kPBytes = kM * kN * 2, kRefBytes = kM * 4;  // scratch of a chunk
 static_assert(kSmem <= 232448, "shared memory");
-static_assert(kVT * kQTile <= kSlot, "the query passes through the second chunk's tiles");
-static_assert(kM * (256 * 4 + 16) <= 2 * kSlot, "the output leaves through the key tiles");
+static_assert(kSCol + kSBufs * kN <= 512, "tensor memory");
+static_assert(kVSlots * kVSlot + kPSlots * kQTile <= kRing, "phase 2's ring");
+static_assert(kTiles * kQTile <= kRing, "the query passes through the ring");
+static_assert(kRaw % 1024 == 0 && 4 * kRow % 128 == 0, "four gathered rows start where a copy may");
+static_assert(kM * (256 * 4 + 16) <= kRing && kM * (512 * 2 + 16) <= kRing, "the output leaves through the ring");
 
 struct Params {
   Attn4Args a;
-  int chunks;  // of a query
+  int chunks;     // of a query
+  int items;      // pieces of all queries
+  int most;       // chunks of the longest piece
 };
 
 // kv4_query_row by a whole warp: a 32-way search over cu_q, whose last round loads all that is needed of the
@@ -94,15 +109,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// A lane's share of one row: of the K and the V columns two pieces of 32 columns with their scales each, and two pieces of 8 rope
-// columns.
-struct Share {
-  uint4 k[2], v[2], rope[2];
-  uint16_t ks[2], vs[2];
-  bool ok;
-};
+// Rows r0..r3, whole, to consecutive rows of shared memory.
+__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int r0, int r1, int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
+      : "memory");
+}
 
-// 32 columns into four 16-byte pieces of a tile row, from logical piece c on.
+// 32 columns (a gathered row's 16-byte piece and their two scales) into the four 16-byte pieces of an operand row from logical piece c
+// on, XOR-ed with x.
 __device__ __forceinline__ void decode32(uint8_t* row, int c, int x, const uint4& w, uint32_t scales) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   const uint32_t s[2] = {kv4_scale_pair(scales & 0xffu), kv4_scale_pair(scales >> 8)};
@@ -127,407 +144,474 @@ __device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
+attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ CUtensorMap kvmap) {
   griddep_wait();
   const Attn4Args& a = p.a;
   if (a.splits > 1) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int half = blockIdx.x & 1, piece = (int)((blockIdx.x >> 1) % (uint32_t)a.splits);
-  const int t = (int)((blockIdx.x >> 1) / (uint32_t)a.splits);
-  const int64_t rows_all = (int64_t)a.seqs.total_q * a.h, row0 = (int64_t)t * a.h;
+  const int64_t rows_all = (int64_t)a.seqs.total_q * a.h;
   const bool split = a.splits > 1;
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* qs = smem;                           // [5][128][128 B]
-  uint8_t* slots = qs + kKT * kQTile;           // [2][4 V tiles, 5 K tiles]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(slots + 2 * kSlot);
-  uint64_t* k_full = bars;         // [2] 8 warps have stored the K tiles
-  uint64_t* k_empty = bars + 2;    // [2] multiplied
-  uint64_t* v_full = bars + 4;     // [2]
-  uint64_t* v_empty = bars + 6;    // [2]
-  uint64_t* s_full = bars + 8;     // [2] logits of the buffer's chunk complete
-  uint64_t* p_full = bars + 10;    // [2] the softmax warps have written P
-  uint64_t* pv_done = bars + 12;   // [2]
-  uint64_t* q_full = bars + 14;    // the query tiles in shared memory
-  uint64_t* q_staged = bars + 15;  // those on their way to tensor memory
-  uint64_t* qt_full = bars + 16;   // the query columns in tensor memory
-  uint64_t* drain = bars + 17;
-  uint8_t* valid = reinterpret_cast<uint8_t*>(bars + 18);  // [2][8] a bit an entry that is not skipped
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
-  int* last_chunk = reinterpret_cast<int*>(bars + 21);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
+  uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* ptiles = ring + kVSlots * kVSlot;
+  uint8_t* raw = ring + kRing;     // [3][64][416]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + kStages * kRaw);
+  uint64_t* r_full = bars;         // [3] a chunk's rows gathered
+  uint64_t* r_empty = bars + 3;    // [3] decoded (8 warps)
+  uint64_t* k_full = bars + 6;     // [2] 8 warps have stored a chunk's tiles
+  uint64_t* k_empty = bars + 8;    // [2] multiplied
+  uint64_t* s_full = bars + 10;    // [3] logits complete
+  uint64_t* s_empty = bars + 13;   // [3] read
+  uint64_t* v_full = bars + 16;    // [3]
+  uint64_t* v_empty = bars + 19;   // [3]
+  uint64_t* p_full = bars + 22;    // [3]
+  uint64_t* p_empty = bars + 25;   // [3]
+  uint64_t* m_full = bars + 28;    // [8] a chunk's mask
+  uint64_t* q_staged = bars + 36;  // the query on its way to tensor memory
+  uint64_t* qt_full = bars + 37;   // there
+  uint64_t* o_full = bars + 38;    // O complete
+  constexpr int kBars = 39;
+  volatile uint64_t* valid = bars + kBars;  // [8] a bit an entry that is not skipped
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars + 8);
+  int* last_chunk = reinterpret_cast<int*>(bars + kBars + 9);
+  volatile uint64_t* holes = bars + kBars + 11;  // [3] a bit a row of a gathered chunk that is there
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kBars + 10);
+  static_assert((kBars + 14) * 8 <= kBarBytes, "barriers");
 
   const int live_warps = (a.h + 31) / 32;  // of the softmax: the others' rows are no head's
+  if (warp == kMmaWarp) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], kDecoders);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], kDecoders);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], live_warps);
-      mbar_init(&pv_done[i], 1);
-    }
-    mbar_init(q_full, 1);
+    for (int i = 0; i < kStages; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], kDecoders); }
+    for (int i = 0; i < kKSlots; ++i) { mbar_init(&k_full[i], kDecoders); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < kSBufs; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], live_warps); }
+    for (int i = 0; i < kVSlots; ++i) { mbar_init(&v_full[i], kDecoders); mbar_init(&v_empty[i], 1); }
+    for (int i = 0; i < kPSlots; ++i) { mbar_init(&p_full[i], live_warps); mbar_init(&p_empty[i], 1); }
+    for (int i = 0; i < kMasks; ++i) mbar_init(&m_full[i], 1);
     mbar_init(q_staged, 1);
     mbar_init(qt_full, live_warps);
-    mbar_init(drain, 1);
-    *last_chunk = -1;
+    mbar_init(o_full, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
-  RowInfo ri;
-  const bool good = warp_query_row(a, t, lane, ri);
-  tc_fence_before();
-  cta_sync();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int c0 = (int)((int64_t)p.chunks * piece / a.splits), c1 = (int)((int64_t)p.chunks * (piece + 1) / a.splits);
-  const int32_t* idx = a.idx + (int64_t)t * a.top_k;
-  const int end = min(a.top_k, c1 * kN);
-  if (good) {
-    // the piece ends with its last chunk that is not all padding (a short history's row is mostly -1)
-    int last = -1;
-    for (int i = c0 * kN + (int)threadIdx.x; i < end; i += kThreads)
-      if (idx[i] != -1) last = i / kN;
-    last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0 && last >= 0) atomicMax(last_chunk, last);
-  }
-  cta_sync();
-  const int nch = good ? max(0, *last_chunk + 1 - c0) : 0;
+  uint8_t* const scratch = a.scratch + (int64_t)blockIdx.x * p.most * (kPBytes + kRefBytes);
+  float* const refs = reinterpret_cast<float*>(scratch + (int64_t)p.most * kPBytes);  // [chunk][128]
 
-  // half h: its V tiles are column tiles 4h .. 4h + 3; the K tiles the other four and the rope's
-  const int vt0 = half * kVT;
-  auto ktile = [&](int j) { return j < vt0 ? j : j + kVT; };
-  if (nch == 0) {
-    // no entries: nothing, or zeros
-    for (int i = threadIdx.x; good && i < a.h; i += kThreads) {
-      if (half) continue;
-      if (split) a.part_ml[(int64_t)piece * rows_all + row0 + i] = make_float2(-INFINITY, 0.f);
-      else if (a.lse) a.lse[row0 + i] = -INFINITY;
+  // The barriers' phases go on from item to item: chunks so far, the parity of the items that had any.
+  uint32_t done = 0, turn = 0;
+  for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    const int t = item / a.splits, piece = item - t * a.splits;
+    const int64_t row0 = (int64_t)t * a.h;
+    if (threadIdx.x == 0) *last_chunk = -1;
+    RowInfo ri;
+    const bool good = warp_query_row(a, t, lane, ri);
+    const int c0 = (int)((int64_t)p.chunks * piece / a.splits), c1 = (int)((int64_t)p.chunks * (piece + 1) / a.splits);
+    const int32_t* idx = a.idx + (int64_t)t * a.top_k;
+    const int end = min(a.top_k, c1 * kN);
+    tc_fence_before();
+    cta_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (good) {
+      // the piece ends with its last chunk that is not all padding (a short history's row is mostly -1)
+      int last = -1;
+      for (int i = c0 * kN + (int)threadIdx.x; i < end; i += kThreads)
+        if (idx[i] != -1) last = i / kN;
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0 && last >= 0) atomicMax(last_chunk, last);
     }
-    const int per = a.out_dtype == DSA_F32 ? 64 : 32;  // 16-byte pieces of the row's half
-    for (int i = threadIdx.x; good && !split && i < a.h * per; i += kThreads)
-      reinterpret_cast<uint4*>(a.out)[(row0 + i / per) * (2 * per) + half * per + i % per] = make_uint4(0u, 0u, 0u, 0u);
-  } else if (warp == kMmaWarp) {
-    // ---------------- query loads, MMA issue ----------------
-    if (elect_one()) {
-      mbar_arrive_expect_tx(q_staged, kVT * kQTile);
-      for (int j = 0; j < kVT; ++j) tma_load_2d(slots + kSlot + j * kQTile, &qmap, q_staged, (vt0 + j) * 64, (int)row0);
-      mbar_arrive_expect_tx(q_full, kKT * kQTile);
-      for (int j = 0; j < kKT; ++j) tma_load_2d(qs + j * kQTile, &qmap, q_full, ktile(j) * 64, (int)row0);
-      const uint32_t idesc_s = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
-      const uint64_t qd = sdesc_sw128(smem_u32(qs), 16, 1024);
-      const uint64_t vd0 = sdesc_sw128(smem_u32(slots), 16, 1024);
-      const uint64_t kd0 = sdesc_sw128(smem_u32(slots) + kVT * kTile, 16, 1024);
-      const uint64_t pd0 = sdesc_sw128(smem_u32(slots), kTile, 1024);  // V tiles as P·V reads them
-      bool stop = !mbar_wait(qt_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
-                  !mbar_wait(q_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-      tc_fence_after();
-      // a barrier is tested ahead of the MMAs that come before its use, and waited for only where it was not complete
-      auto test = [&](uint64_t* bar, uint32_t parity) { return mbar_test(smem_u32(bar), parity); };
-      auto sure = [&](bool ready, uint64_t* bar, uint32_t parity) {
-        return ready || mbar_wait(bar, parity, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-      };
-      auto pv = [&](int g, bool ready) -> bool {
-        const int s = g & 1;
-        if (!sure(ready, &p_full[s], (g >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t pa = tmem + kSCol + s * kN;
-        const uint64_t b0 = pd0 + (uint64_t)(s * (kSlot >> 4));
-        const uint32_t acc = g > 0;
-#pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk)
-          mma_bf16_ts(tmem + kOCol, pa + kk * 8, b0 + (uint64_t)(kk * 128), idesc_pv, kk ? 1u : acc);
-        mma_commit(&v_empty[s]);
-        mma_commit(&pv_done[s]);
-        return true;
-      };
-      for (int g = 0; g < nch && !stop; ++g) {
-        const int s = g & 1;
-        const uint32_t par = (g >> 1) & 1;
-        bool ready = test(&k_full[s], par);
-        // the buffer's last P (chunk g - 2) has been read
-        if (g >= 2 && !mbar_wait(&pv_done[s], par ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) break;
-        if (!sure(ready, &k_full[s], par)) break;
-        tc_fence_after();
-        ready = test(&v_full[s], par);
-        const uint32_t d = tmem + kSCol + s * kN;
-        const uint64_t kd = kd0 + (uint64_t)(s * (kSlot >> 4)), vd = vd0 + (uint64_t)(s * (kSlot >> 4));
-#pragma unroll
-        for (int j = 0; j < kKT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_bf16(d, qd + (uint64_t)(j * (kQTile >> 4) + i * 2), kd + (uint64_t)(j * (kTile >> 4) + i * 2), idesc_s,
-                     j || i ? 1u : 0u);
-        mma_commit(&k_empty[s]);
-        if (!sure(ready, &v_full[s], par)) break;
-        tc_fence_after();
-        ready = g > 0 && test(&p_full[s ^ 1], ((g - 1) >> 1) & 1);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, vd + (uint64_t)(j * (kTile >> 4) + i * 2), idesc_s, 1u);
-        if (g > 0 && !pv(g - 1, ready)) break;
-#pragma unroll
-        for (int j = 2; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, vd + (uint64_t)(j * (kTile >> 4) + i * 2), idesc_s, 1u);
-        mma_commit(&s_full[s]);
-        if (g == nch - 1) pv(g, false);
+    cta_sync();
+    const int nch = good ? max(0, *last_chunk + 1 - c0) : 0;
+
+    if (nch == 0) {
+      // no entries: nothing, or zeros
+      for (int i = threadIdx.x; good && i < a.h; i += kThreads) {
+        if (split) a.part_ml[(int64_t)piece * rows_all + row0 + i] = make_float2(-INFINITY, 0.f);
+        else if (a.lse) a.lse[row0 + i] = -INFINITY;
       }
-      mma_commit(drain);
-      mbar_wait_drain(drain, 0);
-      // every copy issued has landed before the CTA may exit
-      mbar_wait_drain(q_staged, 0);
-      mbar_wait_drain(q_full, 0);
-    }
-  } else if (warp >= kSoftWarps) {
-    // ---------------- gather and decode ----------------
-    const int w = warp - kSoftWarps, x = lane & 7, sub = lane >> 3;  // row of the chunk w · 8 + x
-    const int r = w * 8 + x;
-    const bool paged = a.seqs.paged();
-    const int sh = paged ? __ffs(a.seqs.page_size) - 1 : 0;
-    const int32_t* table = a.seqs.block_table + (int64_t)ri.b * a.seqs.max_pages;
-    auto load_idx = [&](int g) {
-      const int i = (c0 + g) * kN + r;
-      return i < end ? idx[i] : -1;
-    };
-    auto load_page = [&](int v) { return paged && v >= 0 && v <= ri.pos ? table[v >> sh] : 0; };
-    // the row of chunk g's entry v with its page pg, and its loads
-    auto fetch = [&](int v, int pg, Share& f) {
-      int row = -1;
-      if (v >= 0 && v <= ri.pos) {
-        if (!paged) row = ri.k0 + v;
-        else if ((unsigned)pg < (unsigned)a.seqs.num_pages) row = (pg << sh) | (v & (a.seqs.page_size - 1));
-      }
-      if (row < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
-      if (!dsa_check(row < a.seqs.cache_rows(), a.status)) row = -1;
-      f.ok = row >= 0;
-      if (!f.ok) {  // zeros: its P is 0, and its columns have to be finite
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f.k[i] = f.v[i] = f.rope[i] = make_uint4(0u, 0u, 0u, 0u);
-          f.ks[i] = f.vs[i] = 0;
-        }
-        return;
-      }
-      const uint8_t* src = a.kv4 + (int64_t)row * kRow;
-      const int kp = (1 - half) * 8 + sub, vp = half * 8 + sub;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f.k[i] = *reinterpret_cast<const uint4*>(src + (kp + 4 * i) * 16);
-        f.ks[i] = *reinterpret_cast<const uint16_t*>(src + kScaleAt + (kp + 4 * i) * 2);
-        f.rope[i] = *reinterpret_cast<const uint4*>(src + kRopeAt + (sub + 4 * i) * 16);
-        f.v[i] = *reinterpret_cast<const uint4*>(src + (vp + 4 * i) * 16);
-        f.vs[i] = *reinterpret_cast<const uint16_t*>(src + kScaleAt + (vp + 4 * i) * 2);
-      }
-    };
-    Share f[kAhead + 1];
-    int v1 = load_idx(0), v2 = load_idx(1);  // (past the piece: -1)
-    int pg1 = load_page(v1);
-    static_assert(kAhead == 1, "");
-    fetch(v1, pg1, f[0]);
-    v1 = v2;
-    pg1 = load_page(v1);
-    v2 = load_idx(2);
-    bool stop = false;
-    for (int g0 = 0; g0 < nch && !stop; g0 += kAhead + 1) {
-#pragma unroll
-      for (int u = 0; u <= kAhead; ++u) {
-        const int g = g0 + u;
-        if (g >= nch) break;
-        const Share& now = f[u];
-        // the next chunk's rows, the pages of the one after it, the entries of the one after that
-        if (g + kAhead < nch) fetch(v1, pg1, f[(u + kAhead) % (kAhead + 1)]);
-        v1 = v2;
-        pg1 = load_page(v1);
-        v2 = load_idx(g + kAhead + 2);
-        const int s = g & 1;
-        const uint32_t par = (g >> 1) & 1;
-        uint8_t* tiles = slots + s * kSlot;
-        // (the second chunk's tiles bring the query first)
-        if (!__all_sync(0xffffffffu, (g != 1 || mbar_wait(qt_full, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT)) &&
-                                         mbar_wait(&k_empty[s], par ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
-          stop = true;
-          break;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          decode32(tiles + (kVT + 2 * i + (sub >> 1)) * kTile + r * 128, (sub & 1) * 4, x, now.k[i], now.ks[i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          constexpr uint32_t kShrink = 0x37803780u;  // 2^-16 twice
-          *reinterpret_cast<uint4*>(tiles + (kVT + kKT - 1) * kTile + r * 128 + (((sub + 4 * i) ^ x) * 16)) =
-              make_uint4(mul_bf16x2(now.rope[i].x, kShrink), mul_bf16x2(now.rope[i].y, kShrink),
-                         mul_bf16x2(now.rope[i].z, kShrink), mul_bf16x2(now.rope[i].w, kShrink));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[s]);
-        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[s], par ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
-          stop = true;
-          break;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          decode32(tiles + (2 * i + (sub >> 1)) * kTile + r * 128, (sub & 1) * 4, x, now.v[i], now.vs[i]);
-        const uint32_t m = __ballot_sync(0xffffffffu, now.ok);
-        if (lane == 0) valid[s * 8 + w] = (uint8_t)m;  // (softmax has read the chunk before's: its P has been multiplied)
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[s]);
-      }
-    }
-  } else if (warp < live_warps) {
-    // ---------------- softmax: thread = head ----------------
-    const int r = warp * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    bool stop = !__all_sync(0xffffffffu, mbar_wait(q_staged, 0, abort_flag, a.status, DSA_FLAG_TIMEOUT));
-    if (!stop) {
-#pragma unroll
-      for (int j = 0; j < kVT; ++j) {
-        const uint8_t* from = slots + kSlot + j * kQTile + r * 128;
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(from + ((i ^ (r & 7)) * 16));
-          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-        }
-        tmem_st32(lane_base + kQCol + j * 32, w);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qt_full);
-    }
-    const float scale = a.scale_log2 * (1.f / kKv4Shrink);
-    float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum relative to it
-    for (int g = 0; g < nch && !stop; ++g) {
-      const int s = g & 1;
-      const uint32_t par = (g >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[s], par, abort_flag, a.status, DSA_FLAG_TIMEOUT) &&
-                                       mbar_wait(&v_full[s], par, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
-        stop = true;
-        break;
-      }
-      tc_fence_after();
-      const uint64_t see = *reinterpret_cast<volatile uint64_t*>(valid + s * 8);
-      const uint32_t sbuf = lane_base + kSCol + s * kN;
-      float z[kN];
-      load_row(sbuf, z);
-      if (see != ~0ull) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (!((see >> i) & 1)) z[i] = -INFINITY;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
-      const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      const bool grow = mc > m + kRescaleLog2;  // the first entries always (m = -inf)
-      if (__any_sync(0xffffffffu, grow)) {
-        const float m_new = grow ? mc : m;
-        const float factor = grow ? ex2(m - m_new) : 1.f;
-        l *= factor;
-        if (g > 0) {
-          // O holds the chunks before g at the old reference: rescale it once P·V(g - 1) is in
-          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[s ^ 1], ((g - 1) >> 1) & 1, abort_flag, a.status,
-                                                 DSA_FLAG_TIMEOUT))) { stop = true; break; }
-          tc_fence_after();
-          __syncwarp();
-          for (int b = 0; b < 8; ++b) {
-            uint32_t o[32];
-            tmem_ld32(lane_base + kOCol + 32 * b, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-            tmem_st32(lane_base + kOCol + 32 * b, o);
+      const int per = a.out_dtype == DSA_F32 ? 128 : 64;  // 16-byte pieces of a row
+      for (int i = threadIdx.x; good && !split && i < a.h * per; i += kThreads)
+        reinterpret_cast<uint4*>(a.out)[row0 * per + i] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (warp == kMmaWarp) {
+      // ---------------- query loads, MMA issue ----------------
+      if (elect_one()) {
+        mbar_arrive_expect_tx(q_staged, kTiles * kQTile);
+        for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)row0);
+        const uint32_t idesc_s = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
+        const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t vd0 = sdesc_sw128(smem_u32(ring), kTile, 1024);  // V tiles as P·V reads them
+        const uint64_t pd0 = sdesc_sw128(smem_u32(ptiles), 16, 1024);
+        bool stop = !mbar_wait(qt_full, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+        for (int g = 0; g < nch && !stop; ++g) {
+          const uint32_t n = done + g, ks = n % kKSlots, sb = n % kSBufs;
+          if (!mbar_wait(&s_empty[sb], ((n / kSBufs) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
+              !mbar_wait(&k_full[ks], (n / kKSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+            stop = true;
+            break;
           }
+          tc_fence_after();
+          const uint32_t d = tmem + kSCol + sb * kN;
+          const uint64_t kd = kd0 + (uint64_t)(ks * (kKSlot >> 4));
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, kd + (uint64_t)(j * (kTile >> 4) + i * 2), idesc_s,
+                          j || i ? 1u : 0u);
+          mma_commit(&k_empty[ks]);
+          mma_commit(&s_full[sb]);
         }
-        m = m_new;
-      }
-      const float ref = m == -INFINITY ? 0.f : m;  // nothing visible so far
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t pk[32];
+        for (int g = 0; g < 2 * nch && !stop; ++g) {  // half g & 1 of the columns
+          const uint32_t n = done + (g >> 1), vn = 2 * done + g, vs = vn % kVSlots, ps = n % kPSlots;
+          if (!mbar_wait(&v_full[vs], (vn / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
+              ((g & 1) == 0 && !mbar_wait(&p_full[ps], (n / kPSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
+            break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + (uint64_t)(vs * (kVSlot >> 4)), pd = pd0 + (uint64_t)(ps * (kQTile >> 4));
+          const uint32_t acc = g > 1;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float p0 = ex2(fmaf(z[2 * i], scale, -ref));
-        const float p1 = ex2(fmaf(z[2 * i + 1], scale, -ref));
-        sum[(2 * i) & 3] += p0;
-        sum[(2 * i + 1) & 3] += p1;
-        pk[i] = bf16x2(p0, p1);
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_bf16(tmem + (g & 1) * 256, pd + (uint64_t)(kk * 2), vd + (uint64_t)(kk * 128), idesc_pv, kk ? 1u : acc);
+          mma_commit(&v_empty[vs]);
+          if (g & 1) mma_commit(&p_empty[ps]);
+        }
+        mma_commit(o_full);
+        mbar_wait_drain(o_full, turn);
+        mbar_wait_drain(q_staged, turn);  // every copy issued has landed before the CTA goes on
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      __syncwarp();
-      tmem_st32(sbuf, pk);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
-    }
-    if (!stop)
-      stop = !__all_sync(0xffffffffu, mbar_wait(&pv_done[(nch - 1) & 1], ((nch - 1) >> 1) & 1, abort_flag, a.status,
-                                                DSA_FLAG_TIMEOUT));
-    if (!stop) {
-      tc_fence_after();
-      // O goes out through the key tiles (all of them have been multiplied): a thread writes its row there, 16 bytes more
-      // than its length apart from the next, and sends it with one bulk copy
-      const bool live = r < a.h;
-      const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kKv4Shrink);
-      const bool f32 = split || a.out_dtype == DSA_F32;
-      const int row_bytes = 256 * (f32 ? 4 : 2);
-      uint8_t* mine = slots + r * (row_bytes + 16);
-      for (int b = 0; b < 8; ++b) {
-        uint32_t o[32];
-        __syncwarp();  // the load is the whole warp's
-        tmem_ld32(lane_base + kOCol + 32 * b, o);
-        if (f32) {
-          float4* dst = reinterpret_cast<float4*>(mine) + 8 * b;
+    } else if (warp == kGatherWarp) {
+      // ---------------- gather: the chunks of phase 1, then the same again for phase 2 ----------------
+      // Lanes 0..31 take entries lane and lane + 32, read three steps ahead; their pages are read two steps ahead.
+      const bool paged = a.seqs.paged();
+      const int sh = paged ? __ffs(a.seqs.page_size) - 1 : 0;
+      const int32_t* table = a.seqs.block_table + (int64_t)ri.b * a.seqs.max_pages;
+      const int steps = 2 * nch;
+      auto load_idx = [&](int n, int h) {  // of step n
+        const int i = (c0 + (n < nch ? n : n - nch)) * kN + 32 * h + lane;
+        return n < steps && i < end ? idx[i] : -1;
+      };
+      auto load_page = [&](int v) { return paged && v >= 0 && v <= ri.pos ? table[v >> sh] : 0; };
+      auto row_of = [&](int v, int pg) {
+        int row = -1;
+        if (v >= 0 && v <= ri.pos) {
+          if (!paged) row = ri.k0 + v;
+          else if ((unsigned)pg < (unsigned)a.seqs.num_pages) row = (pg << sh) | (v & (a.seqs.page_size - 1));
+        }
+        if (row < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+        return dsa_check(row < a.seqs.cache_rows(), a.status) ? row : -1;
+      };
+      int v[3][2], pg[2][2];  // entries of steps n, n + 1, n + 2; pages of n, n + 1
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(mine) + 4 * b;
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) v[j][h] = load_idx(j, h);
+        pg[0][h] = load_page(v[0][h]);
+        pg[1][h] = load_page(v[1][h]);
+      }
+      uint32_t last = 0;  // steps whose copies were issued
+      for (int n = 0; n < steps; ++n) {
+        const uint32_t x = 2 * done + n, st = x % kStages;
+        int row[2];
+        uint32_t ok[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          row[h] = row_of(v[0][h], pg[0][h]);
+          ok[h] = __ballot_sync(0xffffffffu, row[h] >= 0);
+          // A skipped entry repeats another of its four (its P is 0, and the other's columns count anyway); four skipped
+          // ones copy nothing, and are decoded as zeros.
+          const uint32_t four = (ok[h] >> (lane & 28)) & 15u;
+          const int other = __shfl_sync(0xffffffffu, row[h], (lane & 28) + (four ? __ffs(four) - 1 : 0));
+          if (row[h] < 0) row[h] = other;
+          v[0][h] = v[1][h];
+          v[1][h] = v[2][h];
+          v[2][h] = load_idx(n + 3, h);
+          pg[0][h] = pg[1][h];
+          pg[1][h] = load_page(v[1][h]);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&r_empty[st], ((x / kStages) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
+          break;
+        const uint64_t mask = (uint64_t)ok[1] << 32 | ok[0];
+        const uint32_t any[2] = {(ok[0] | ok[0] >> 1 | ok[0] >> 2 | ok[0] >> 3) & 0x11111111u,
+                                 (ok[1] | ok[1] >> 1 | ok[1] >> 2 | ok[1] >> 3) & 0x11111111u};
+        if (lane == 0) {
+          if (n < nch) {
+            // (softmax has read the mask of eight chunks ago: these rows' stage was last decoded for the chunk five after
+            // it, into tiles freed by the logits of the chunk three after it, whose buffer softmax had left)
+            const uint32_t ms = (done + n) % kMasks;
+            valid[ms] = mask;
+            mbar_arrive(&m_full[ms]);
+          }
+          holes[st] = ((uint64_t)any[1] << 32 | any[0]) * 15;
+          mbar_arrive_expect_tx(&r_full[st], (uint32_t)((__popc(any[0]) + __popc(any[1])) * 4 * kRow));
+        }
+        __syncwarp();
+        // a lane issues the copy of four entries: lanes 0, 4, .. those of its first, lanes 1, 5, .. of its second
+        const int first = lane & 28;
+        int r4[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r4[h][j] = __shfl_sync(0xffffffffu, row[h], first + j);
+        if ((lane & 3) < 2) {
+          const int h = lane & 1;
+          if (((h ? any[1] : any[0]) >> first) & 1u)
+            gather4(raw + st * kRaw + (32 * h + first) * kRow, &kvmap, &r_full[st], h ? r4[1][0] : r4[0][0], h ? r4[1][1] : r4[0][1],
+                    h ? r4[1][2] : r4[0][2], h ? r4[1][3] : r4[0][3]);
+        }
+        __syncwarp();
+        last = x + 1;
+      }
+      // every copy issued has landed before the CTA goes on
+      for (uint32_t x = last > kStages ? last - kStages : 0; x < last; ++x) mbar_wait_drain(&r_full[x % kStages], (x / kStages) & 1);
+    } else if (warp >= kSoftWarps) {
+      // ---------------- decode: the chunks of phase 1, then those of phase 2 ----------------
+      // Eight neighbouring lanes read 16-byte pieces of four rows (8 banks apart) and two pieces each, and store theirs at eight
+      // different places of the swizzle: no bank is asked for twice.
+      const int w = warp - kSoftWarps, pair = (lane >> 2) & 1, grp = lane >> 4;
+      const int r = w * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), x = r & 7;  // row of the chunk
+      const int steps = 2 * nch;
+      for (int n = 0; n < steps; ++n) {
+        const uint32_t rn = 2 * done + n, st = rn % kStages;
+        bool ok = mbar_wait(&r_full[st], (rn / kStages) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+        const uint8_t* src = raw + st * kRaw + r * kRow;
+        const bool there = (holes[st] >> r) & 1;
+        // piece i: columns 32 (2 (2 i + grp) + pair) ..
+        auto piece = [&](int i, uint4& v, uint32_t& s) {
+          const int k = 2 * (2 * i + grp) + pair;
+          v = there ? *reinterpret_cast<const uint4*>(src + 16 * k) : make_uint4(0u, 0u, 0u, 0u);
+          s = there ? *reinterpret_cast<const uint16_t*>(src + kScaleAt + 2 * k) : 0u;
+        };
+        if (n < nch) {
+          const uint32_t kn = done + n, ks = kn % kKSlots;
+          // (the query passes through the tiles first)
+          ok = ok && (n >= kKSlots || mbar_wait(qt_full, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT)) &&
+               mbar_wait(&k_empty[ks], ((kn / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          uint8_t* tiles = ring + ks * kKSlot;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            uint4 v;
+            uint32_t s;
+            piece(i, v, s);
+            decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v, s);
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            constexpr uint32_t kShrink = 0x37803780u;  // 2^-16 twice
+            const int c = 2 * i + grp + 4 * pair;
+            const uint4 v = there ? *reinterpret_cast<const uint4*>(src + kRopeAt + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + ((c ^ x) * 16)) =
+                make_uint4(mul_bf16x2(v.x, kShrink), mul_bf16x2(v.y, kShrink), mul_bf16x2(v.z, kShrink), mul_bf16x2(v.w, kShrink));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&r_empty[st]);
+            mbar_arrive(&k_full[ks]);
+          }
+        } else {
+          const int g = n - nch;
+          // (the first tiles are some of phase 1's: its last MMAs are done)
+          const uint32_t lg = done + nch - 1;
+          ok = ok && (g > 0 || mbar_wait(&s_full[lg % kSBufs], (lg / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t vn = 2 * (done + g) + h, vs = vn % kVSlots;
+            ok = ok && mbar_wait(&v_empty[vs], ((vn / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint8_t* tiles = ring + vs * kVSlot;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint4 v;
+              uint32_t s;
+              piece(2 * h + i, v, s);
+              decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v, s);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (h == 1) mbar_arrive(&r_empty[st]);
+              mbar_arrive(&v_full[vs]);
+            }
+          }
+          if (!__all_sync(0xffffffffu, ok)) break;
         }
       }
-      fence_proxy_async_smem();  // our writes, seen by the bulk copy
-      if (live) {
-        const int64_t at = (row0 + r) * kDc + half * 256;
-        void* dst = split ? static_cast<void*>(a.part_o + (int64_t)piece * rows_all * kDc + at)
-                    : f32 ? static_cast<void*>(static_cast<float*>(a.out) + at)
-                          : static_cast<void*>(static_cast<__nv_bfloat16*>(a.out) + at);
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                         reinterpret_cast<uint64_t>(dst)), "r"(smem_u32(mine)), "r"(row_bytes)
-                     : "memory");
-        if (half == 0) {
+    } else if (warp < live_warps) {
+      // ---------------- softmax: thread = head ----------------
+      const int r = warp * 32 + lane;
+      const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+      bool stop = !__all_sync(0xffffffffu, mbar_wait(q_staged, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT));
+      if (!stop) {
+#pragma unroll 3
+        for (int j = 0; j < kTiles; ++j) {
+          const uint8_t* from = ring + j * kQTile + r * 128;
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + ((i ^ (r & 7)) * 16));
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+          }
+          tmem_st32(lane_base + kQCol + j * 32, w);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qt_full);
+      }
+      const float scale = a.scale_log2 * (1.f / kKv4Shrink);
+      float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
+      uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
+      for (int g = 0; g < nch && !stop; ++g) {
+        const uint32_t n = done + g, ms = n % kMasks, sb = n % kSBufs;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&s_full[sb], (n / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) &&
+                            mbar_wait(&m_full[ms], (n / kMasks) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t see = valid[ms];
+        float z[kN];
+        load_row(lane_base + kSCol + sb * kN, z);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
+        if (see != ~0ull) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (!((see >> i) & 1)) z[i] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
+        const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        if (mc > m + kGrowLog2) {  // the first entries always (m = -inf)
+          const float m_new = ceilf(mc);
+          l *= ex2(m - m_new);
+          m = m_new;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;  // nothing visible so far
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p0 = ex2(fmaf(z[8 * i + 2 * e], scale, -ref));
+            const float p1 = ex2(fmaf(z[8 * i + 2 * e + 1], scale, -ref));
+            sum[(2 * e) & 3] += p0;
+            sum[(2 * e + 1) & 3] += p1;
+            pk[e] = bf16x2(p0, p1);
+          }
+          __stcg(pbuf + (8 * g + i) * kM, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        __stcg(refs + g * kM + r, m);
+      }
+      // phase 2: this thread's row of P, relative to the last m (a power of two: exact)
+      uint4 pk[8];
+      float ref = 0.f;
+      auto load_p = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pk[i] = __ldcg(pbuf + (8 * g + i) * kM);
+        ref = __ldcg(refs + g * kM + r);
+      };
+      if (!stop) load_p(0);
+      for (int g = 0; g < nch && !stop; ++g) {
+        const uint32_t n = done + g, ps = n % kPSlots;
+        // (phase 1's MMAs are done with the tiles: softmax has read their last logits)
+        if (!__all_sync(0xffffffffu, mbar_wait(&p_empty[ps], ((n / kPSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+          stop = true;
+          break;
+        }
+        if (__any_sync(0xffffffffu, ref != m)) {
+          const float f = ref == m ? 1.f : ex2(ref - m);
+          const uint32_t ff = bf16x2(f, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            pk[i] = make_uint4(mul_bf16x2(pk[i].x, ff), mul_bf16x2(pk[i].y, ff), mul_bf16x2(pk[i].z, ff),
+                               mul_bf16x2(pk[i].w, ff));
+        }
+        uint8_t* to = ptiles + ps * kQTile + r * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(to + ((i ^ (r & 7)) * 16)) = pk[i];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[ps]);
+        if (g + 1 < nch) load_p(g + 1);
+      }
+      if (!stop)
+        stop = !__all_sync(0xffffffffu, mbar_wait(o_full, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT) && *abort_flag == 0);
+      if (!stop) {
+        tc_fence_after();
+        // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
+        // there, 16 bytes more than its length apart from the next, and sends it with one bulk copy
+        const bool live = r < a.h;
+        const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kKv4Shrink);
+        const bool f32 = split || a.out_dtype == DSA_F32;
+        constexpr int kRowBytes = 1024;
+        uint8_t* mine = ring + r * (kRowBytes + 16);
+        char* out = split ? reinterpret_cast<char*>(a.part_o + ((int64_t)piece * rows_all + row0 + r) * kDc)
+                          : static_cast<char*>(a.out) + (row0 + r) * kDc * (f32 ? 4 : 2);
+        for (int c = 0; c < 16; ++c) {
+          uint32_t o[32];
+          __syncwarp();  // the load is the whole warp's
+          tmem_ld32(lane_base + 32 * c, o);
+          if (f32) {
+            float4* dst = reinterpret_cast<float4*>(mine) + 8 * (c & 7);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                   __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(mine) + 4 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (c == 15 || (f32 && c == 7)) {
+            fence_proxy_async_smem();  // our writes, seen by the bulk copy
+            if (live)
+              asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                               reinterpret_cast<uint64_t>(out + (f32 && c == 15 ? kRowBytes : 0))),
+                           "r"(smem_u32(mine)), "r"(kRowBytes)
+                           : "memory");
+            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+        }
+        if (live) {
           if (split) a.part_ml[(int64_t)piece * rows_all + row0 + r] = make_float2(fmaxf(m, -FLT_MAX), l);
           else if (a.lse) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       }
-      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if (nch) turn ^= 1;
+    done += nch;
+    tc_fence_before();
+    cta_sync();
+    if (*abort_flag) break;  // (no wait is under way that could set it now)
   }
-  tc_fence_before();
-  cta_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*tmem_slot, 512);
   }
 }
 
-constexpr double kStart = 4;  // a CTA's start and end, in chunks
+constexpr double kStart = 3;  // an item's start and end, in chunks (of both phases)
 constexpr size_t kMostPartial = size_t(1) << 30;
+
+int chunks_of(const Attn4Args& a) { return (a.top_k + kN - 1) / kN; }
+int64_t ctas_of(const Attn4Args& a) {
+  const int64_t items = (int64_t)a.seqs.total_q * a.splits;
+  return items < num_sms() ? items : num_sms();
+}
 
 }  // namespace
 
@@ -535,18 +619,19 @@ bool attn4_tc_eligible(const Attn4Args& a) {
   return a.kv_dtype == DSA_BF16 && a.d_c == kDc && a.d_rope == kDr && a.h <= kM;
 }
 
-// Pieces a query's entries are cut into: a wave ends with its longest CTA, and merging costs a launch (about
-// three chunks) and the partial outputs' traffic (at 4 TB/s, a chunk being about a microsecond).
+// Pieces a query's entries are cut into: a round of items ends with its longest, and merging costs a launch (about
+// two chunks) and the partial outputs' traffic (at 4 TB/s, a chunk being about two microseconds).
 int attn4_tc_splits(const Attn4Args& a) {
-  const int64_t items = 2 * (int64_t)a.seqs.total_q, chunks = (a.top_k + kN - 1) / kN;
+  const int64_t items = a.seqs.total_q;
+  const int chunks = chunks_of(a);
   if (items == 0) return 1;
-  const double row_cost = (double)a.seqs.total_q * a.h * a.d_c * 8 / 4e6;
+  const double row_cost = (double)a.seqs.total_q * a.h * a.d_c * 8 / 8e6;
   int best = 1;
   double cost = 1e30;
-  for (int s = 1; s <= chunks; ++s) {
+  for (int s = 1; s <= chunks && s <= 64; ++s) {
     if (s > 1 && (size_t)s * a.seqs.total_q * a.h * (a.d_c * 4 + 8) > kMostPartial) break;
-    const int64_t waves = (items * s + num_sms() - 1) / num_sms();
-    const double c = waves * ((double)((chunks + s - 1) / s) + kStart) + (s > 1 ? 3 + s * row_cost : 0);
+    const int64_t rounds = (items * s + num_sms() - 1) / num_sms();
+    const double c = rounds * ((double)((chunks + s - 1) / s) + kStart) + (s > 1 ? 2 + s * row_cost : 0);
     if (c < cost) {
       cost = c;
       best = s;
@@ -555,21 +640,30 @@ int attn4_tc_splits(const Attn4Args& a) {
   return best;
 }
 
+size_t attn4_tc_scratch(const Attn4Args& a) {
+  return (size_t)ctas_of(a) * ((chunks_of(a) + a.splits - 1) / a.splits) * (kPBytes + kRefBytes);
+}
+
 int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
-  p.chunks = (a.top_k + kN - 1) / kN;
-  const int64_t items = 2 * (int64_t)a.seqs.total_q * a.splits;
-  if (items > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "attn4: grid too large");
+  p.chunks = chunks_of(a);
+  p.most = (p.chunks + a.splits - 1) / a.splits;
+  const int64_t items = (int64_t)a.seqs.total_q * a.splits;
+  if (items > 0x3fffffff) return set_error(DSA_ERR_UNSUPPORTED, "attn4: too many queries");
+  p.items = (int)items;
   CUtensorMap qmap;
   int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kD, (uint64_t)a.seqs.total_q * a.h, kD * 2, 64, kM);
+  if (rc != DSA_OK) return rc;
+  CUtensorMap kvmap;  // whole rows
+  rc = make_tmap_2d(&kvmap, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.kv4, kRow / 4, (uint64_t)a.seqs.cache_rows(), kRow, kRow / 4, 1, false);
   if (rc != DSA_OK) return rc;
   static std::atomic<bool> allowed[64];
   rc = allow_smem<kSmem>(attn4_tc_kernel, allowed, "attn4_tc: smem attribute");
   if (rc != DSA_OK) return rc;
   cudaError_t e = cudaSuccess;
   DSA_LAUNCH("attn4_tc", stream,
-             e = launch_pdl(attn4_tc_kernel, dim3((unsigned)items), dim3(kThreads), kSmem, stream, p, qmap));
+             e = launch_pdl(attn4_tc_kernel, dim3((unsigned)ctas_of(a)), dim3(kThreads), kSmem, stream, p, qmap, kvmap));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
   rc = check_launch("attn4_tc");
   if (rc != DSA_OK || a.splits == 1) return rc;

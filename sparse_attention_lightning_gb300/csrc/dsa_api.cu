@@ -504,12 +504,14 @@ Attn4Args attn4_args(const dsa_problem* p) {
   a.splits = attn4_tc_eligible(a) ? attn4_tc_splits(a) : attn4_simt_splits(a);
   return a;
 }
-// Partial outputs and their (max, sum) for every piece of every row.
+// Partial outputs and their (max, sum) for every piece of every row, and the kernel's own scratch.
 size_t carve_attn4(Attn4Args& a, void* ws) {
   Carve c;
   const size_t rows = (size_t)a.seqs.total_q * a.h, n = a.splits > 1 ? a.splits : 0;
   const size_t o = c.take(n * rows * a.d_c * 4), m = c.take(n * rows * 8);
+  const size_t s = c.take(attn4_tc_eligible(a) ? attn4_tc_scratch(a) : 0);
   if (ws) {
+    a.scratch = static_cast<uint8_t*>(ws) + s;
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + m);
     a.status = static_cast<uint32_t*>(ws);
