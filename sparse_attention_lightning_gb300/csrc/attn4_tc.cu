@@ -50,23 +50,22 @@ constexpr int kKSlots = 2, kKSlot = kTiles * kTile;              // phase 1: 2 x
 constexpr int kVSlots = 3, kVSlot = kVTiles / 2 * kTile;         // phase 2: 3 x 32 KB (half the columns of a chunk)
 constexpr int kPSlots = 3;                                       //   and 3 x 16 KB
 constexpr int kSBufs = 3;                  // logit buffers
-constexpr int kMasks = 8;                  // chunks whose skipped entries are known (see the gathering warp)
 constexpr int kSoftWarps = 4;
 constexpr int kDecoders = 8;               // warps
-constexpr int kMmaWarp = kSoftWarps + kDecoders, kGatherWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kGatherWarp + 1);
+constexpr int kMmaWarp = kSoftWarps + kDecoders;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kRing = kKSlots * kKSlot;
 constexpr int kBarBytes = 512;
 constexpr int kSmem = kRing + kStages * kRaw + kBarBytes + 1024;
 constexpr int kQCol = 0, kSCol = kD / 2;   // tensor memory of phase 1: 288 query columns, the logits; of phase 2: O
 constexpr int kRopeAt = kv4_rope_at(kDc), kScaleAt = kv4_scale_at(kDc, kDr);
 constexpr float kGrowLog2 = 8.0f;
-constexpr int64_t kPBytes = kM * kN * 2, kRefBytes = kM * 4;  // scratch of a chunk
+constexpr int kMostRows = 2048;            // entries of a query
+constexpr int64_t kPBytes = kM * kN * 2, kRefBytes = kM * 4, kListBytes = kN * 4;  // scratch of a chunk
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(kSCol + kSBufs * kN <= 512, "tensor memory");
 static_assert(kVSlots * kVSlot + kPSlots * kQTile <= kRing, "phase 2's ring");
 static_assert(kTiles * kQTile <= kRing, "the query passes through the ring");
-static_assert(kRaw % 1024 == 0 && 4 * kRow % 128 == 0, "four gathered rows start where a copy may");
 static_assert(kM * (256 * 4 + 16) <= kRing && kM * (512 * 2 + 16) <= kRing, "the output leaves through the ring");
 
 struct Params {
@@ -109,13 +108,9 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Rows r0..r3, whole, to consecutive rows of shared memory.
-__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int r0, int r1, int r2, int r3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-      : "memory");
+// 16 bytes to shared memory, asynchronously; zeros where !there (nothing is read then).
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // 32 columns (a gathered row's 16-byte piece and their two scales) into the four 16-byte pieces of an operand row from logical piece c
@@ -144,8 +139,7 @@ __device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
-                const __grid_constant__ CUtensorMap kvmap) {
+attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
   griddep_wait();
   const Attn4Args& a = p.a;
   if (a.splits > 1) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
@@ -158,71 +152,96 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   uint8_t* ptiles = ring + kVSlots * kVSlot;
   uint8_t* raw = ring + kRing;     // [3][64][416]
   uint64_t* bars = reinterpret_cast<uint64_t*>(raw + kStages * kRaw);
-  uint64_t* r_full = bars;         // [3] a chunk's rows gathered
-  uint64_t* r_empty = bars + 3;    // [3] decoded (8 warps)
-  uint64_t* k_full = bars + 6;     // [2] 8 warps have stored a chunk's tiles
-  uint64_t* k_empty = bars + 8;    // [2] multiplied
-  uint64_t* s_full = bars + 10;    // [3] logits complete
-  uint64_t* s_empty = bars + 13;   // [3] read
-  uint64_t* v_full = bars + 16;    // [3]
-  uint64_t* v_empty = bars + 19;   // [3]
-  uint64_t* p_full = bars + 22;    // [3]
-  uint64_t* p_empty = bars + 25;   // [3]
-  uint64_t* m_full = bars + 28;    // [8] a chunk's mask
-  uint64_t* q_staged = bars + 36;  // the query on its way to tensor memory
-  uint64_t* qt_full = bars + 37;   // there
-  uint64_t* o_full = bars + 38;    // O complete
-  constexpr int kBars = 39;
-  volatile uint64_t* valid = bars + kBars;  // [8] a bit an entry that is not skipped
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars + 8);
-  int* last_chunk = reinterpret_cast<int*>(bars + kBars + 9);
-  volatile uint64_t* holes = bars + kBars + 11;  // [3] a bit a row of a gathered chunk that is there
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kBars + 10);
-  static_assert((kBars + 14) * 8 <= kBarBytes, "barriers");
+  uint64_t* k_full = bars;         // [2] 8 warps have stored a chunk's tiles
+  uint64_t* k_empty = bars + 2;    // [2] multiplied
+  uint64_t* s_full = bars + 4;     // [3] logits complete
+  uint64_t* s_empty = bars + 7;    // [3] read
+  uint64_t* v_full = bars + 10;    // [3]
+  uint64_t* v_empty = bars + 13;   // [3]
+  uint64_t* p_full = bars + 16;    // [3]
+  uint64_t* p_empty = bars + 19;   // [3]
+  uint64_t* q_staged = bars + 22;  // the query on its way to tensor memory
+  uint64_t* qt_full = bars + 23;   // there
+  uint64_t* o_full = bars + 24;    // O complete
+  constexpr int kBars = 25;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kBars + 1);
+  int* counts = reinterpret_cast<int*>(bars + kBars + 2);  // [warps] entries of a warp's share
+  static_assert((kBars + 2) * 8 + kThreads / 32 * 4 <= kBarBytes, "barriers");
 
   const int live_warps = (a.h + 31) / 32;  // of the softmax: the others' rows are no head's
   if (warp == kMmaWarp) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], kDecoders); }
     for (int i = 0; i < kKSlots; ++i) { mbar_init(&k_full[i], kDecoders); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < kSBufs; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], live_warps); }
     for (int i = 0; i < kVSlots; ++i) { mbar_init(&v_full[i], kDecoders); mbar_init(&v_empty[i], 1); }
     for (int i = 0; i < kPSlots; ++i) { mbar_init(&p_full[i], live_warps); mbar_init(&p_empty[i], 1); }
-    for (int i = 0; i < kMasks; ++i) mbar_init(&m_full[i], 1);
     mbar_init(q_staged, 1);
     mbar_init(qt_full, live_warps);
     mbar_init(o_full, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  uint8_t* const scratch = a.scratch + (int64_t)blockIdx.x * p.most * (kPBytes + kRefBytes);
+  uint8_t* const scratch = a.scratch + (int64_t)blockIdx.x * p.most * (kPBytes + kRefBytes + kListBytes);
   float* const refs = reinterpret_cast<float*>(scratch + (int64_t)p.most * kPBytes);  // [chunk][128]
 
-  // The barriers' phases go on from item to item: chunks so far, the parity of the items that had any.
-  uint32_t done = 0, turn = 0;
+  int32_t* const list = reinterpret_cast<int32_t*>(refs + (int64_t)p.most * kM);  // cache rows of the entries, without those skipped
+  // The barriers' phases go on from item to item: chunks so far, the parity of the items and of those that had any.
+  uint32_t done = 0, turn = 0, full_turn = 0;
   for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
     const int t = item / a.splits, piece = item - t * a.splits;
     const int64_t row0 = (int64_t)t * a.h;
-    if (threadIdx.x == 0) *last_chunk = -1;
+    // The query comes while the entries are looked up (the ring is free: all roles have left the item before).
+    if (warp == kMmaWarp && elect_one()) {
+      mbar_arrive_expect_tx(q_staged, kTiles * kQTile);
+      for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)row0);
+    }
+    __syncwarp();
     RowInfo ri;
     const bool good = warp_query_row(a, t, lane, ri);
     const int c0 = (int)((int64_t)p.chunks * piece / a.splits), c1 = (int)((int64_t)p.chunks * (piece + 1) / a.splits);
     const int32_t* idx = a.idx + (int64_t)t * a.top_k;
     const int end = min(a.top_k, c1 * kN);
+    // The piece's entries as cache rows, without the skipped ones (a short history's row is mostly -1): a warp takes
+    // consecutive ones, all its loads at once.
+    constexpr int kWarps = kThreads / 32, kMine = (kMostRows + 32 * kWarps - 1) / (32 * kWarps);
+    int row[kMine], mine = 0;
+    if (good) {
+      const int per = (end - c0 * kN + 32 * kWarps - 1) / (32 * kWarps);  // at most kMine
+      const int e0 = c0 * kN + warp * per * 32;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int e = e0 + j * 32 + lane;
+        row[j] = j < per && e < end ? idx[e] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int v = row[j];
+        row[j] = v >= 0 && v <= ri.pos ? cache_row(a.seqs, ri.b, ri.k0, v) : -1;
+        if (row[j] < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
+        if (!dsa_check(row[j] < a.seqs.cache_rows(), a.status)) row[j] = -1;
+        mine += __popc(__ballot_sync(0xffffffffu, row[j] >= 0));
+      }
+      if (lane == 0) counts[warp] = mine;
+    }
     tc_fence_before();
     cta_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    int total = 0;
     if (good) {
-      // the piece ends with its last chunk that is not all padding (a short history's row is mostly -1)
-      int last = -1;
-      for (int i = c0 * kN + (int)threadIdx.x; i < end; i += kThreads)
-        if (idx[i] != -1) last = i / kN;
-      last = __reduce_max_sync(0xffffffffu, last);
-      if (lane == 0 && last >= 0) atomicMax(last_chunk, last);
+      const int c = lane < kWarps ? counts[lane] : 0;
+      int at = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+      total = __reduce_add_sync(0xffffffffu, c);
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const uint32_t m = __ballot_sync(0xffffffffu, row[j] >= 0);
+        if (row[j] >= 0) list[at + __popc(m & ((1u << lane) - 1u))] = row[j];
+        at += __popc(m);
+      }
     }
     cta_sync();
-    const int nch = good ? max(0, *last_chunk + 1 - c0) : 0;
+    const int nch = (total + kN - 1) / kN;
 
     if (nch == 0) {
       // no entries: nothing, or zeros
@@ -236,13 +255,11 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     } else if (warp == kMmaWarp) {
       // ---------------- query loads, MMA issue ----------------
       if (elect_one()) {
-        mbar_arrive_expect_tx(q_staged, kTiles * kQTile);
-        for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)row0);
         const uint32_t idesc_s = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
         const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
         const uint64_t vd0 = sdesc_sw128(smem_u32(ring), kTile, 1024);  // V tiles as P·V reads them
         const uint64_t pd0 = sdesc_sw128(smem_u32(ptiles), 16, 1024);
-        bool stop = !mbar_wait(qt_full, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+        bool stop = !mbar_wait(qt_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT);
         for (int g = 0; g < nch && !stop; ++g) {
           const uint32_t n = done + g, ks = n % kKSlots, sb = n % kSBufs;
           if (!mbar_wait(&s_empty[sb], ((n / kSBufs) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
@@ -277,167 +294,102 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           if (g & 1) mma_commit(&p_empty[ps]);
         }
         mma_commit(o_full);
-        mbar_wait_drain(o_full, turn);
-        mbar_wait_drain(q_staged, turn);  // every copy issued has landed before the CTA goes on
+        mbar_wait_drain(o_full, full_turn);
       }
-    } else if (warp == kGatherWarp) {
-      // ---------------- gather: the chunks of phase 1, then the same again for phase 2 ----------------
-      // Lanes 0..31 take entries lane and lane + 32, read three steps ahead; their pages are read two steps ahead.
-      const bool paged = a.seqs.paged();
-      const int sh = paged ? __ffs(a.seqs.page_size) - 1 : 0;
-      const int32_t* table = a.seqs.block_table + (int64_t)ri.b * a.seqs.max_pages;
-      const int steps = 2 * nch;
-      auto load_idx = [&](int n, int h) {  // of step n
-        const int i = (c0 + (n < nch ? n : n - nch)) * kN + 32 * h + lane;
-        return n < steps && i < end ? idx[i] : -1;
-      };
-      auto load_page = [&](int v) { return paged && v >= 0 && v <= ri.pos ? table[v >> sh] : 0; };
-      auto row_of = [&](int v, int pg) {
-        int row = -1;
-        if (v >= 0 && v <= ri.pos) {
-          if (!paged) row = ri.k0 + v;
-          else if ((unsigned)pg < (unsigned)a.seqs.num_pages) row = (pg << sh) | (v & (a.seqs.page_size - 1));
-        }
-        if (row < 0 && v != -1) atomicOr(a.status, DSA_FLAG_BAD_INDEX);
-        return dsa_check(row < a.seqs.cache_rows(), a.status) ? row : -1;
-      };
-      int v[3][2], pg[2][2];  // entries of steps n, n + 1, n + 2; pages of n, n + 1
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int j = 0; j < 3; ++j) v[j][h] = load_idx(j, h);
-        pg[0][h] = load_page(v[0][h]);
-        pg[1][h] = load_page(v[1][h]);
-      }
-      uint32_t last = 0;  // steps whose copies were issued
-      for (int n = 0; n < steps; ++n) {
-        const uint32_t x = 2 * done + n, st = x % kStages;
-        int row[2];
-        uint32_t ok[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          row[h] = row_of(v[0][h], pg[0][h]);
-          ok[h] = __ballot_sync(0xffffffffu, row[h] >= 0);
-          // A skipped entry repeats another of its four (its P is 0, and the other's columns count anyway); four skipped
-          // ones copy nothing, and are decoded as zeros.
-          const uint32_t four = (ok[h] >> (lane & 28)) & 15u;
-          const int other = __shfl_sync(0xffffffffu, row[h], (lane & 28) + (four ? __ffs(four) - 1 : 0));
-          if (row[h] < 0) row[h] = other;
-          v[0][h] = v[1][h];
-          v[1][h] = v[2][h];
-          v[2][h] = load_idx(n + 3, h);
-          pg[0][h] = pg[1][h];
-          pg[1][h] = load_page(v[1][h]);
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&r_empty[st], ((x / kStages) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
-          break;
-        const uint64_t mask = (uint64_t)ok[1] << 32 | ok[0];
-        const uint32_t any[2] = {(ok[0] | ok[0] >> 1 | ok[0] >> 2 | ok[0] >> 3) & 0x11111111u,
-                                 (ok[1] | ok[1] >> 1 | ok[1] >> 2 | ok[1] >> 3) & 0x11111111u};
-        if (lane == 0) {
-          if (n < nch) {
-            // (softmax has read the mask of eight chunks ago: these rows' stage was last decoded for the chunk five after
-            // it, into tiles freed by the logits of the chunk three after it, whose buffer softmax had left)
-            const uint32_t ms = (done + n) % kMasks;
-            valid[ms] = mask;
-            mbar_arrive(&m_full[ms]);
-          }
-          holes[st] = ((uint64_t)any[1] << 32 | any[0]) * 15;
-          mbar_arrive_expect_tx(&r_full[st], (uint32_t)((__popc(any[0]) + __popc(any[1])) * 4 * kRow));
-        }
-        __syncwarp();
-        // a lane issues the copy of four entries: lanes 0, 4, .. those of its first, lanes 1, 5, .. of its second
-        const int first = lane & 28;
-        int r4[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) r4[h][j] = __shfl_sync(0xffffffffu, row[h], first + j);
-        if ((lane & 3) < 2) {
-          const int h = lane & 1;
-          if (((h ? any[1] : any[0]) >> first) & 1u)
-            gather4(raw + st * kRaw + (32 * h + first) * kRow, &kvmap, &r_full[st], h ? r4[1][0] : r4[0][0], h ? r4[1][1] : r4[0][1],
-                    h ? r4[1][2] : r4[0][2], h ? r4[1][3] : r4[0][3]);
-        }
-        __syncwarp();
-        last = x + 1;
-      }
-      // every copy issued has landed before the CTA goes on
-      for (uint32_t x = last > kStages ? last - kStages : 0; x < last; ++x) mbar_wait_drain(&r_full[x % kStages], (x / kStages) & 1);
     } else if (warp >= kSoftWarps) {
-      // ---------------- decode: the chunks of phase 1, then those of phase 2 ----------------
-      // Eight neighbouring lanes read 16-byte pieces of four rows (8 banks apart) and two pieces each, and store theirs at eight
-      // different places of the swizzle: no bank is asked for twice.
+      // ---------------- gather and decode: the chunks of phase 1, then the same again for phase 2 ----------------
+      // A warp takes eight rows of every chunk: their 16-byte pieces are copied to its part of a stage, two steps ahead, and come to
+      // registers from there.  Eight neighbouring lanes read pieces of four rows (8 banks apart) and two pieces each, and
+      // store what they decode to at eight different places of the swizzle: no bank is asked for twice.
       const int w = warp - kSoftWarps, pair = (lane >> 2) & 1, grp = lane >> 4;
       const int r = w * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), x = r & 7;  // row of the chunk
       const int steps = 2 * nch;
+      // lane l holds the cache row of the warp's row l & 7, read a step ahead of its copy; -1 behind the last entry: zeros (its P is
+      // 0, and its columns have to be finite)
+      auto load_row_of = [&](int n) {
+        const int e = (n < nch ? n : n - nch) * kN + w * 8 + (lane & 7);
+        return n < steps && e < total ? __ldcg(list + e) : -1;
+      };
+      constexpr int kPieces = kRow / 16, kCopies = (8 * kPieces + 31) / 32;
+      uint8_t* const mine_raw = raw + w * 8 * kRow;
+      int next_row = load_row_of(0);
+      auto gather = [&](int n) {
+        const int row_of = next_row;
+        next_row = load_row_of(n + 1);
+        if (n < steps) {
+          const uint32_t dst = smem_u32(mine_raw + (uint32_t)n % kStages * kRaw) + lane * 16;
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i) {
+            const int f = i * 32 + lane, j = f / kPieces;  // piece f of the warp's rows, in row j
+            const int from = __shfl_sync(0xffffffffu, row_of, j & 7);
+            if (f < 8 * kPieces) copy16_async(dst + i * 512, a.kv4 + (int64_t)max(from, 0) * kRow + (f - j * kPieces) * 16, from >= 0);
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int n = 0; n < kStages - 1; ++n) gather(n);
       for (int n = 0; n < steps; ++n) {
-        const uint32_t rn = 2 * done + n, st = rn % kStages;
-        bool ok = mbar_wait(&r_full[st], (rn / kStages) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-        const uint8_t* src = raw + st * kRaw + r * kRow;
-        const bool there = (holes[st] >> r) & 1;
-        // piece i: columns 32 (2 (2 i + grp) + pair) ..
-        auto piece = [&](int i, uint4& v, uint32_t& s) {
+        __syncwarp();  // the stage has been read
+        gather(n + kStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        const uint8_t* src = raw + (uint32_t)n % kStages * kRaw + r * kRow;
+        uint4 v[4], rope[2];  // piece i: columns 32 (2 (2 i + grp) + pair) ..
+        uint32_t sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const int k = 2 * (2 * i + grp) + pair;
-          v = there ? *reinterpret_cast<const uint4*>(src + 16 * k) : make_uint4(0u, 0u, 0u, 0u);
-          s = there ? *reinterpret_cast<const uint16_t*>(src + kScaleAt + 2 * k) : 0u;
-        };
+          v[i] = *reinterpret_cast<const uint4*>(src + 16 * k);
+          sc[i] = *reinterpret_cast<const uint16_t*>(src + kScaleAt + 2 * k);
+        }
+        if (n < nch) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) rope[i] = *reinterpret_cast<const uint4*>(src + kRopeAt + 16 * (2 * i + grp + 4 * pair));
+        }
         if (n < nch) {
           const uint32_t kn = done + n, ks = kn % kKSlots;
           // (the query passes through the tiles first)
-          ok = ok && (n >= kKSlots || mbar_wait(qt_full, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT)) &&
-               mbar_wait(&k_empty[ks], ((kn / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          if (!__all_sync(0xffffffffu,
+                          (n >= kKSlots || mbar_wait(qt_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT)) &&
+                              mbar_wait(&k_empty[ks], ((kn / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
+            break;
           uint8_t* tiles = ring + ks * kKSlot;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 v;
-            uint32_t s;
-            piece(i, v, s);
-            decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v, s);
-          }
+          for (int i = 0; i < 4; ++i) decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[i], sc[i]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             constexpr uint32_t kShrink = 0x37803780u;  // 2^-16 twice
-            const int c = 2 * i + grp + 4 * pair;
-            const uint4 v = there ? *reinterpret_cast<const uint4*>(src + kRopeAt + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + ((c ^ x) * 16)) =
-                make_uint4(mul_bf16x2(v.x, kShrink), mul_bf16x2(v.y, kShrink), mul_bf16x2(v.z, kShrink), mul_bf16x2(v.w, kShrink));
+            *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + (((2 * i + grp + 4 * pair) ^ x) * 16)) =
+                make_uint4(mul_bf16x2(rope[i].x, kShrink), mul_bf16x2(rope[i].y, kShrink), mul_bf16x2(rope[i].z, kShrink),
+                           mul_bf16x2(rope[i].w, kShrink));
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&r_empty[st]);
-            mbar_arrive(&k_full[ks]);
-          }
+          if (lane == 0) mbar_arrive(&k_full[ks]);
         } else {
           const int g = n - nch;
           // (the first tiles are some of phase 1's: its last MMAs are done)
           const uint32_t lg = done + nch - 1;
-          ok = ok && (g > 0 || mbar_wait(&s_full[lg % kSBufs], (lg / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT));
+          bool ok = g > 0 || mbar_wait(&s_full[lg % kSBufs], (lg / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t vn = 2 * (done + g) + h, vs = vn % kVSlots;
             ok = ok && mbar_wait(&v_empty[vs], ((vn / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             uint8_t* tiles = ring + vs * kVSlot;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint4 v;
-              uint32_t s;
-              piece(2 * h + i, v, s);
-              decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v, s);
-            }
+            for (int i = 0; i < 2; ++i)
+              decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[2 * h + i], sc[2 * h + i]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              if (h == 1) mbar_arrive(&r_empty[st]);
-              mbar_arrive(&v_full[vs]);
-            }
+            if (lane == 0) mbar_arrive(&v_full[vs]);
           }
-          if (!__all_sync(0xffffffffu, ok)) break;
+          if (!ok) break;
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // every copy has landed before the CTA goes on
     } else if (warp < live_warps) {
       // ---------------- softmax: thread = head ----------------
       const int r = warp * 32 + lane;
@@ -463,24 +415,22 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
       uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
       for (int g = 0; g < nch && !stop; ++g) {
-        const uint32_t n = done + g, ms = n % kMasks, sb = n % kSBufs;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&s_full[sb], (n / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) &&
-                            mbar_wait(&m_full[ms], (n / kMasks) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+        const uint32_t n = done + g, sb = n % kSBufs;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], (n / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const uint64_t see = valid[ms];
         float z[kN];
         load_row(lane_base + kSCol + sb * kN, z);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[sb]);
-        if (see != ~0ull) {
+        if (g == nch - 1) {  // behind the last entry
+          const int n_in = total - g * kN;
 #pragma unroll
           for (int i = 0; i < kN; ++i)
-            if (!((see >> i) & 1)) z[i] = -INFINITY;
+            if (i >= n_in) z[i] = -INFINITY;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -542,7 +492,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         if (g + 1 < nch) load_p(g + 1);
       }
       if (!stop)
-        stop = !__all_sync(0xffffffffu, mbar_wait(o_full, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT) && *abort_flag == 0);
+        stop = !__all_sync(0xffffffffu, mbar_wait(o_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT) && *abort_flag == 0);
       if (!stop) {
         tc_fence_after();
         // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
@@ -589,15 +539,17 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           if (split) a.part_ml[(int64_t)piece * rows_all + row0 + r] = make_float2(fmaxf(m, -FLT_MAX), l);
           else if (a.lse) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       }
     }
-    if (nch) turn ^= 1;
+    if (nch == 0 && warp == kMmaWarp) mbar_wait_drain(q_staged, turn);  // (nobody else waited for the query)
+    turn ^= 1;
+    if (nch) full_turn ^= 1;
     done += nch;
     tc_fence_before();
     cta_sync();
     if (*abort_flag) break;  // (no wait is under way that could set it now)
   }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(*tmem_slot, 512);
@@ -641,7 +593,7 @@ int attn4_tc_splits(const Attn4Args& a) {
 }
 
 size_t attn4_tc_scratch(const Attn4Args& a) {
-  return (size_t)ctas_of(a) * ((chunks_of(a) + a.splits - 1) / a.splits) * (kPBytes + kRefBytes);
+  return (size_t)ctas_of(a) * ((chunks_of(a) + a.splits - 1) / a.splits) * (kPBytes + kRefBytes + kListBytes);
 }
 
 int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
@@ -655,15 +607,12 @@ int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
   CUtensorMap qmap;
   int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kD, (uint64_t)a.seqs.total_q * a.h, kD * 2, 64, kM);
   if (rc != DSA_OK) return rc;
-  CUtensorMap kvmap;  // whole rows
-  rc = make_tmap_2d(&kvmap, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.kv4, kRow / 4, (uint64_t)a.seqs.cache_rows(), kRow, kRow / 4, 1, false);
-  if (rc != DSA_OK) return rc;
   static std::atomic<bool> allowed[64];
   rc = allow_smem<kSmem>(attn4_tc_kernel, allowed, "attn4_tc: smem attribute");
   if (rc != DSA_OK) return rc;
   cudaError_t e = cudaSuccess;
   DSA_LAUNCH("attn4_tc", stream,
-             e = launch_pdl(attn4_tc_kernel, dim3((unsigned)ctas_of(a)), dim3(kThreads), kSmem, stream, p, qmap, kvmap));
+             e = launch_pdl(attn4_tc_kernel, dim3((unsigned)ctas_of(a)), dim3(kThreads), kSmem, stream, p, qmap));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
   rc = check_launch("attn4_tc");
   if (rc != DSA_OK || a.splits == 1) return rc;
@@ -671,3 +620,4 @@ int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
 }
 
 }  // namespace dsa
+
