@@ -113,11 +113,20 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
+// What the operands hold is the value times 2^-14: kv4_pair() times the scale times 2^112, which is within bf16's range for every
+// scale and brings the first one that is none (0xf8) to infinity.
+constexpr float kShrink = 0x1p-14f;
+constexpr uint32_t kShrinkPair = 0x38803880u, kUp112 = 0x77807780u;  // 2^-14, 2^112, twice in bf16
+
 // 32 columns (a gathered row's 16-byte piece and their two scales) into the four 16-byte pieces of an operand row from logical piece c
 // on, XOR-ed with x.
 __device__ __forceinline__ void decode32(uint8_t* row, int c, int x, const uint4& w, uint32_t scales) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  const uint32_t s[2] = {kv4_scale_pair(scales & 0xffu), kv4_scale_pair(scales >> 8)};
+  // Both scales at once: byte << 4 is its exponent and mantissa in bf16's places, 2^-112 times the scale, so twice 2^112; infinity times
+  // 0, added, makes what is not a number one.
+  uint32_t two = mul_bf16x2(mul_bf16x2(__byte_perm(scales, 0u, 0x4140) << 4, kUp112), kUp112);
+  asm("fma.rn.bf16x2 %0, %0, %1, %0;" : "+r"(two) : "r"(0u));
+  const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t f = s[i >> 1];
@@ -359,10 +368,9 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           for (int i = 0; i < 4; ++i) decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[i], sc[i]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            constexpr uint32_t kShrink = 0x37803780u;  // 2^-16 twice
             *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + (((2 * i + grp + 4 * pair) ^ x) * 16)) =
-                make_uint4(mul_bf16x2(rope[i].x, kShrink), mul_bf16x2(rope[i].y, kShrink), mul_bf16x2(rope[i].z, kShrink),
-                           mul_bf16x2(rope[i].w, kShrink));
+                make_uint4(mul_bf16x2(rope[i].x, kShrinkPair), mul_bf16x2(rope[i].y, kShrinkPair), mul_bf16x2(rope[i].z, kShrinkPair),
+                           mul_bf16x2(rope[i].w, kShrinkPair));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -411,7 +419,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         __syncwarp();
         if (lane == 0) mbar_arrive(qt_full);
       }
-      const float scale = a.scale_log2 * (1.f / kKv4Shrink);
+      const float scale = a.scale_log2 * (1.f / kShrink);
       float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
       uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
       for (int g = 0; g < nch && !stop; ++g) {
@@ -498,7 +506,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
         // there, 16 bytes more than its length apart from the next, and sends it with one bulk copy
         const bool live = r < a.h;
-        const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kKv4Shrink);
+        const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kShrink);
         const bool f32 = split || a.out_dtype == DSA_F32;
         constexpr int kRowBytes = 1024;
         uint8_t* mine = ring + r * (kRowBytes + 16);

@@ -48,15 +48,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// A scale times 2^110, twice in a pair of bf16: times kv4_pair() it gives a column's value times 2^-16, in one
-// multiplication and within bf16's range for every scale.
-constexpr float kKv4Shrink = 0x1p-16f;
-__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t byte) {
-  const float s = kv4_scale(byte) * 0x1p110f;  // exact: four bits
-  const uint32_t h = __float_as_uint(s) >> 16;
-  return h | h << 16;
-}
-
 // Eight columns of a word in fp32, from their scale.
 __device__ __forceinline__ void kv4_widen8(uint32_t w, float scale, float (&f)[8]) {
   const uint32_t p[4] = {kv4_pair<0>(w), kv4_pair<1>(w), kv4_pair<2>(w), kv4_pair<3>(w)};
