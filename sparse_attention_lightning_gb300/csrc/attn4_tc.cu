@@ -108,9 +108,9 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// 16 bytes to shared memory, asynchronously; zeros where !there (nothing is read then).
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+// 16 bytes to shared memory, asynchronously.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // What the operands hold is the value times 2^-14: kv4_pair() times the scale times 2^112, which is within bf16's range for every
@@ -313,12 +313,9 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       const int w = warp - kSoftWarps, pair = (lane >> 2) & 1, grp = lane >> 4;
       const int r = w * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), x = r & 7;  // row of the chunk
       const int steps = 2 * nch;
-      // lane l holds the cache row of the warp's row l & 7, read a step ahead of its copy; -1 behind the last entry: zeros (its P is
-      // 0, and its columns have to be finite)
-      auto load_row_of = [&](int n) {
-        const int e = (n < nch ? n : n - nch) * kN + w * 8 + (lane & 7);
-        return n < steps && e < total ? __ldcg(list + e) : -1;
-      };
+      // Lane l holds the cache row of the warp's row l & 7, read a step ahead of its copy.  Behind the last entry the last
+      // one is repeated: its P is 0 there, and what its columns hold the query attends to anyway.
+      auto load_row_of = [&](int n) { return __ldcg(list + min((n < nch ? n : n - nch) * kN + w * 8 + (lane & 7), total - 1)); };
       constexpr int kPieces = kRow / 16, kCopies = (8 * kPieces + 31) / 32;
       uint8_t* const mine_raw = raw + w * 8 * kRow;
       int next_row = load_row_of(0);
@@ -331,7 +328,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           for (int i = 0; i < kCopies; ++i) {
             const int f = i * 32 + lane, j = f / kPieces;  // piece f of the warp's rows, in row j
             const int from = __shfl_sync(0xffffffffu, row_of, j & 7);
-            if (f < 8 * kPieces) copy16_async(dst + i * 512, a.kv4 + (int64_t)max(from, 0) * kRow + (f - j * kPieces) * 16, from >= 0);
+            if (f < 8 * kPieces) copy16_async(dst + i * 512, a.kv4 + (int64_t)from * kRow + (f - j * kPieces) * 16);
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
