@@ -17,37 +17,51 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Eight columns as they are in memory: a 16-byte vector of bf16, two of fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+struct Eight {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(u[j] << 16);
-      f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    uint32_t w[4];
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
   }
-}
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t u[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(u[j] << 16);
+        f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x); f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z); f[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    }
+  }
+  __device__ __forceinline__ void narrow(const float (&f)[8]) {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                          __float_as_uint(f[4 * i + 3]));
+    }
+  }
+};
 
 __device__ __forceinline__ void sine(const RotaryArgs& a, int pair, int64_t t, float& s, float& c) {
   const int64_t p = a.pos[a.axis[pair] * a.ld_pos + t];
@@ -56,46 +70,55 @@ __device__ __forceinline__ void sine(const RotaryArgs& a, int pair, int64_t t, f
   if (a.inverse) s = -s;
 }
 
-// NH heads a thread: heads h, h + step, ...
+// NH heads a thread: heads h, h + step, ...; `tokens` tokens a block, or `parts` blocks a token.
+struct Cut {
+  int step, slots, tokens, parts;
+};
 template <typename T, bool INTERLEAVED, int NH>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, int step) {
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, const Cut k) {
   griddep_wait();
-  const int slots = a.d / (INTERLEAVED ? 8 : 16);
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t rest = i / slots;
-  const int s = (int)(i - rest * slots);
-  const int64_t t = rest / step;
-  const int h0 = (int)(rest - t * step);
-  if (t >= a.tokens) return;
-  constexpr int NP = INTERLEAVED ? 4 : 8;
+  const uint32_t group = blockIdx.x / (uint32_t)k.parts, part = blockIdx.x - group * k.parts;
+  const uint32_t per = (uint32_t)(k.step * k.slots);  // threads a token
+  const uint32_t i = k.tokens > 1 ? threadIdx.x : part * kThreads + threadIdx.x;
+  const uint32_t tt = k.tokens > 1 ? i / per : 0u, rest = i - tt * per;
+  const int h0 = (int)(rest / (uint32_t)k.slots), s = (int)(rest - h0 * k.slots);
+  const int64_t t = (int64_t)group * k.tokens + tt;
+  if (rest >= per || (int)tt >= k.tokens || t >= a.tokens) return;
+  constexpr int NP = INTERLEAVED ? 4 : 8, NV = INTERLEAVED ? 1 : 2;
   const int c0 = s * 8, p0 = s * NP, half = a.d / 2;
   const T* x = static_cast<const T*>(a.x) + t * a.xt + c0;
   T* o = static_cast<T*>(a.out) + t * a.ot + c0;
-  float f[NH][INTERLEAVED ? 1 : 2][8];
+  Eight<T> e[NH][NV];
 #pragma unroll
   for (int j = 0; j < NH; ++j) {
-    const int h = h0 + j * step;
+    const int h = h0 + j * k.step;
     if (h >= a.heads) break;
-    load8(x + h * a.xh, f[j][0]);
-    if constexpr (!INTERLEAVED) load8(x + h * a.xh + half, f[j][1]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) e[j][v].load(x + h * a.xh + v * half);
   }
   float sn[NP], cs[NP];
 #pragma unroll
-  for (int k = 0; k < NP; ++k) sine(a, p0 + k, t, sn[k], cs[k]);
+  for (int q = 0; q < NP; ++q) sine(a, p0 + q, t, sn[q], cs[q]);
 #pragma unroll
   for (int j = 0; j < NH; ++j) {
-    const int h = h0 + j * step;
+    const int h = h0 + j * k.step;
     if (h >= a.heads) break;
+    float f[NV][8];
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      float& u = INTERLEAVED ? f[j][0][2 * k] : f[j][0][k];
-      float& v = INTERLEAVED ? f[j][0][2 * k + 1] : f[j][INTERLEAVED ? 0 : 1][k];
-      const float p = u * cs[k] - v * sn[k], q = u * sn[k] + v * cs[k];
-      u = p;
-      v = q;
+    for (int v = 0; v < NV; ++v) e[j][v].widen(f[v]);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      float& u = INTERLEAVED ? f[0][2 * q] : f[0][q];
+      float& w = INTERLEAVED ? f[0][2 * q + 1] : f[NV - 1][q];
+      const float y = u * cs[q] - w * sn[q], z = u * sn[q] + w * cs[q];
+      u = y;
+      w = z;
     }
-    store8(o + h * a.oh, f[j][0]);
-    if constexpr (!INTERLEAVED) store8(o + h * a.oh + half, f[j][1]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      e[j][v].narrow(f[v]);
+      e[j][v].store(o + h * a.oh + v * half);
+    }
   }
 }
 
@@ -121,8 +144,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const __grid_con
 }
 
 template <typename K, typename... A>
-int launch_blocks(K kern, int64_t threads, cudaStream_t stream, const A&... args) {
-  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+int launch_blocks(K kern, int64_t blocks, cudaStream_t stream, const A&... args) {
   if (blocks > 0x7fffffff) return set_error(DSA_ERR_UNSUPPORTED, "rotary: too many rows");
   cudaError_t e = cudaSuccess;
   DSA_LAUNCH("rotary", stream, e = launch_pdl(kern, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args...));
@@ -130,21 +152,25 @@ int launch_blocks(K kern, int64_t threads, cudaStream_t stream, const A&... args
   return check_launch("rotary");
 }
 
+template <typename T, bool INTERLEAVED, int NH>
+int launch_heads(const RotaryArgs& a, cudaStream_t stream) {
+  Cut k;
+  k.slots = a.d / (INTERLEAVED ? 8 : 16);
+  k.step = (a.heads + NH - 1) / NH;
+  const int64_t per = (int64_t)k.step * k.slots;
+  if (per > 0x7fffffff / 2) return set_error(DSA_ERR_UNSUPPORTED, "rotary: too many heads");
+  k.tokens = per < kThreads ? (int)(kThreads / per) : 1;
+  k.parts = (int)((per + kThreads - 1) / kThreads);
+  return launch_blocks(rotary_kernel<T, INTERLEAVED, NH>, (a.tokens + k.tokens - 1) / k.tokens * k.parts, stream, a, k);
+}
+
 template <typename T, bool INTERLEAVED>
 int launch_wide(const RotaryArgs& a, cudaStream_t stream) {
-  const int64_t slots = a.d / (INTERLEAVED ? 8 : 16);
   // Heads a thread: 8 where that leaves every SM 1024 threads, fewer otherwise.
-  const int64_t rows = a.tokens * slots;
-  const int64_t fill = 1024 * (int64_t)num_sms();
-  if (a.heads >= 8 && rows * a.heads / 8 >= fill) {
-    const int step = (a.heads + 7) / 8;
-    return launch_blocks(rotary_kernel<T, INTERLEAVED, 8>, rows * step, stream, a, step);
-  }
-  if (a.heads >= 2 && rows * a.heads / 2 >= fill) {
-    const int step = (a.heads + 1) / 2;
-    return launch_blocks(rotary_kernel<T, INTERLEAVED, 2>, rows * step, stream, a, step);
-  }
-  return launch_blocks(rotary_kernel<T, INTERLEAVED, 1>, rows * a.heads, stream, a, a.heads);
+  const int64_t rows = a.tokens * a.heads * (a.d / (INTERLEAVED ? 8 : 16)), fill = 1024 * (int64_t)num_sms();
+  if (a.heads >= 8 && rows / 8 >= fill) return launch_heads<T, INTERLEAVED, 8>(a, stream);
+  if (a.heads >= 2 && rows / 2 >= fill) return launch_heads<T, INTERLEAVED, 2>(a, stream);
+  return launch_heads<T, INTERLEAVED, 1>(a, stream);
 }
 
 }  // namespace
@@ -154,11 +180,12 @@ int launch_rotary(const RotaryArgs& a, cudaStream_t stream) {
   const uintptr_t at = (uintptr_t)a.x | (uintptr_t)a.out | (uintptr_t)(a.xt * size) | (uintptr_t)(a.xh * size) |
                        (uintptr_t)(a.ot * size) | (uintptr_t)(a.oh * size);
   const bool wide = at % 16 == 0 && a.d % (a.interleaved ? 8 : 16) == 0;
+  const int64_t pairs = (a.tokens * a.heads * (a.d / 2) + kThreads - 1) / kThreads;  // blocks of them
   if (a.dtype == DSA_F32) {
-    if (!wide) return launch_blocks(rotary_pairs_kernel<float>, a.tokens * a.heads * (a.d / 2), stream, a);
+    if (!wide) return launch_blocks(rotary_pairs_kernel<float>, pairs, stream, a);
     return a.interleaved ? launch_wide<float, true>(a, stream) : launch_wide<float, false>(a, stream);
   }
-  if (!wide) return launch_blocks(rotary_pairs_kernel<__nv_bfloat16>, a.tokens * a.heads * (a.d / 2), stream, a);
+  if (!wide) return launch_blocks(rotary_pairs_kernel<__nv_bfloat16>, pairs, stream, a);
   return a.interleaved ? launch_wide<__nv_bfloat16, true>(a, stream) : launch_wide<__nv_bfloat16, false>(a, stream);
 }
 
