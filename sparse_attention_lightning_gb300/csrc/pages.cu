@@ -6,7 +6,7 @@
 //
 // The counting is a few tens of thousands of words: one CTA does it (a grid's worth of blocks would wait for each
 // other at every step), 16 loads a thread in flight, one block-wide sum for 16384 pages.  The bytes are moved by a
-// kernel of the whole GPU behind it, 16 KB a block at a time, four 16-byte loads a thread.
+// kernel of the whole GPU behind it, 32 KB a block at a time, eight 16-byte loads a thread.
 #include <limits.h>
 
 #include "pages.cuh"
@@ -17,8 +17,9 @@ namespace {
 constexpr int kOne = 1024;         // threads of the counting CTA
 constexpr int kSpan = 16;          // pages a lane looks at in a round
 constexpr int kRound = kOne * kSpan;
+constexpr int kItems = 4;         // table entries a thread looks at in a round
 constexpr int kMove = 256;         // threads of a moving block
-constexpr int kSeg = kMove * 64;   // bytes it moves at a time
+constexpr int kSeg = kMove * 128;  // bytes it moves at a time
 
 __device__ __forceinline__ bool page_ok(const PagesArgs& a, int p) { return (unsigned)p < (unsigned)a.num_pages; }
 __device__ __forceinline__ int64_t entry(const PagesArgs& a, int row, int j) { return row * a.ld_table + j; }
@@ -113,6 +114,7 @@ struct Reserve {
   int* mark;   // [rows] the first entry of a row
   int* cnt;    // [num_pages] entries of the call that would copy a page
   int* first;  // [num_pages] the first of them
+  int* item;   // [n + 1] the table entries looked at before entry i's: its copy, if any, and those behind its held pages
   int* off;    // [n + 1] new pages before entry i's
   int* old;    // [num_pages] by new page in order: the page it replaces, -1: none, -2: not given out
   int* list;   // [num_pages] the free pages in order
@@ -120,9 +122,9 @@ struct Reserve {
   int* cdst;   //     left out, -2 where nothing is copied
   int* crows;
   __host__ __device__ Reserve(int32_t* p, int rows, int n, int num_pages)
-      : mark(p), cnt(mark + rows), first(cnt + num_pages), off(first + num_pages), old(off + n + 1),
+      : mark(p), cnt(mark + rows), first(cnt + num_pages), item(first + num_pages), off(item + n + 1), old(off + n + 1),
         list(old + num_pages), csrc(list + num_pages), cdst(csrc + n), crows(cdst + n) {}
-  static int64_t words(int64_t rows, int64_t n, int64_t num_pages) { return rows + 4 * num_pages + 4 * n + 1; }
+  static int64_t words(int64_t rows, int64_t n, int64_t num_pages) { return rows + 4 * num_pages + 5 * n + 2; }
 };
 
 // A page behind the held positions that the row can keep: it is its only holder.
@@ -174,34 +176,77 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
     }
   }
   __syncthreads();
-  // new pages of each entry (a page all of whose holders are in the call stays with the first)
-  for (int i = warp; i < a.n; i += 32) {
-    const int p = R.csrc[i];
-    int n = 0;
-    if (p != -1) {
-      bool copy = p >= 0;
-      if (copy && R.cnt[p] == a.refs[p] && R.first[p] == i) copy = false;
-      __syncwarp();
-      if (lane == 0 && p >= 0 && !copy) R.csrc[i] = -2;
-      const int r = a.dst[i], j1 = pages_of(a.new_lens[i], ps);
-      for (int j0 = pages_of(a.lens[i], ps); j0 < j1; j0 += 32) {
-        const int j = j0 + lane;
-        n += __popc(__ballot_sync(0xffffffffu, j < j1 && !own_page(a, a.table[entry(a, r, j)])));
-      }
-      n += copy;
-    }
-    if (lane == 0) R.off[i] = n;
-  }
-  __syncthreads();
-  uint32_t total = 0;
+  // (a page all of whose holders are in the call stays with the first)
+  uint32_t items = 0;
   for (int i0 = 0; i0 < a.n; i0 += kOne) {
     const int i = i0 + tid;
+    int n = 0;
+    if (i < a.n && R.csrc[i] != -1) {
+      const int p = R.csrc[i];
+      n = pages_of(a.new_lens[i], ps) - pages_of(a.lens[i], ps) + (p >= 0);
+      if (p >= 0 && R.cnt[p] == a.refs[p] && R.first[p] == i) {
+        R.csrc[i] = -2;
+        --n;
+      }
+    }
     uint32_t sum;
-    const uint32_t before = block_sum(i < a.n ? (uint32_t)R.off[i] : 0u, part, sum);
-    if (i < a.n) R.off[i] = (int)(total + before);
-    total += sum;  // (a table has fewer than 2^31 entries)
+    const uint32_t before = block_sum((uint32_t)n, part, sum);
+    if (i < a.n) R.item[i] = (int)(items + before);
+    items += sum;  // (a table has fewer than 2^31 entries)
   }
-  if (tid == 0) R.off[a.n] = (int)total;
+  if (tid == 0) R.item[a.n] = (int)items;
+  __syncthreads();
+  // The items in the entries' order, kItems a thread side by side: which want a page, and how many did before.  visit(entry,
+  // table entry's column, its page, whether it wants one, wanted before) for each; the total.
+  auto walk = [&](auto visit) -> uint32_t {
+    uint32_t total = 0;
+    for (uint32_t x0 = 0; x0 < items; x0 += kOne * kItems) {
+      const uint32_t x = x0 + tid * kItems;
+      int i = 0;
+      if (x < items) {
+        int hi = a.n - 1;  // the last entry whose items begin at or before x
+        while (i < hi) {
+          const int mid = (i + hi + 1) >> 1;
+          if ((uint32_t)R.item[mid] <= x) i = mid; else hi = mid - 1;
+        }
+      }
+      int ent[kItems], col[kItems], was[kItems];
+      bool need[kItems];
+      uint32_t n = 0;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        need[k] = false;
+        if (x + k < items) {
+          while ((uint32_t)R.item[i + 1] <= x + k) ++i;
+          const bool copy = R.csrc[i] >= 0;
+          const int j = (int)(x + k) - R.item[i];
+          ent[k] = i;
+          col[k] = copy && j == 0 ? a.lens[i] / ps : pages_of(a.lens[i], ps) + j - copy;
+          was[k] = a.table[entry(a, a.dst[i], col[k])];
+          need[k] = (copy && j == 0) || !own_page(a, was[k]);
+          n += need[k];
+        }
+      }
+      uint32_t sum;
+      uint32_t at = total + block_sum(n, part, sum);
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        if (x + k < items) visit(ent[k], col[k], was[k], need[k], at);
+        at += need[k];
+      }
+      total += sum;
+    }
+    return total;
+  };
+  // the new pages before each entry's (an entry without items has those of the next one with any)
+  const uint32_t total = walk([&](int i, int col, int, bool, uint32_t at) {
+    const int begin = R.csrc[i] >= 0 ? a.lens[i] / ps : pages_of(a.lens[i], ps);
+    if (col == begin)
+      for (int e = i; e >= 0 && R.item[e] == R.item[i]; --e) R.off[e] = (int)at;
+  });
+  __syncthreads();
+  for (int i = tid; i <= a.n; i += kOne)
+    if ((uint32_t)R.item[i] == items) R.off[i] = (int)total;
   // as many free pages as are wanted
   uint32_t found = 0;
   for (int64_t base = 0; base < a.num_pages && found < total; base += kRound) {
@@ -230,44 +275,29 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
   __syncthreads();
   const int nfree = (int)found;
   // given out in the entries' order: all that an entry needs, or nothing
-  for (int i = warp; i < a.n; i += 32) {
-    const int p = R.csrc[i];
+  for (int i = tid; i < a.n; i += kOne) {
+    const int p = R.csrc[i], k0 = R.off[i], k1 = R.off[i + 1], L = a.lens[i];
     if (p == -1) continue;
-    const int r = a.dst[i], L = a.lens[i], N = a.new_lens[i], k1 = R.off[i + 1];
-    int k = R.off[i];
-    if (k < k1 && k1 > nfree) {
-      for (int x = k + lane; x < nfree; x += 32) R.old[x] = -2;
-      if (lane == 0) {
-        a.held[i] = L;
-        atomicOr(a.status, DSA_FLAG_NO_PAGES);
-      }
+    if (k0 < k1 && k1 > nfree) {
+      a.held[i] = L;
+      atomicOr(a.status, DSA_FLAG_NO_PAGES);
       continue;
     }
+    a.held[i] = a.new_lens[i];
     if (p >= 0) {
-      if (lane == 0) {
-        const int to = R.list[k];
-        R.old[k] = p;
-        a.table[entry(a, r, L / ps)] = to;
-        R.cdst[i] = to;
-        R.crows[i] = L % ps;
-      }
-      ++k;
+      R.cdst[i] = R.list[k0];
+      R.crows[i] = L % ps;
     }
-    const int j1 = pages_of(N, ps);
-    for (int j0 = pages_of(L, ps); j0 < j1; j0 += 32) {
-      const int j = j0 + lane;
-      const int was = j < j1 ? a.table[entry(a, r, j)] : -1;
-      const bool need = j < j1 && !own_page(a, was);
-      const uint32_t m = __ballot_sync(0xffffffffu, need);
-      const int x = k + __popc(m & ((1u << lane) - 1u));
-      if (need && x < k1) {
-        R.old[x] = page_ok(a, was) && a.refs[was] > 1 ? was : -1;
-        a.table[entry(a, r, j)] = R.list[x];
-      }
-      k += __popc(m);
-    }
-    if (lane == 0) a.held[i] = N;
   }
+  walk([&](int i, int col, int was, bool need, uint32_t at) {
+    if (!need || (int)at >= nfree) return;
+    if (R.off[i + 1] > nfree) {
+      R.old[at] = -2;
+      return;
+    }
+    R.old[at] = page_ok(a, was) && a.refs[was] > 1 ? was : -1;
+    a.table[entry(a, a.dst[i], col)] = R.list[at];
+  });
   __syncthreads();
   // the counts, which the steps above went by
   for (int k = tid; k < (int)total && k < nfree; k += kOne) {
@@ -340,11 +370,24 @@ __global__ void __launch_bounds__(kOne) compact_kernel(const __grid_constant__ P
     holes += sum >> 16;
   }
   __syncthreads();
-  for (int k = tid; k < (int)moves; k += kOne) {  // (as many holes as moves: both are live minus those that stay)
-    const int s = C.src[k], d = C.dst[k];
-    a.moved[s] = d;
-    a.refs[d] = a.refs[s];
-    a.refs[s] = 0;
+  // (as many holes as moves: both are live minus those that stay)
+  for (int k0 = tid; k0 < (int)moves; k0 += 8 * kOne) {
+    int s[8], d[8], n[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = min(k0 + j * kOne, (int)moves - 1);
+      s[j] = C.src[k];
+      d[j] = C.dst[k];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) n[j] = a.refs[s[j]];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (k0 + j * kOne >= (int)moves) break;
+      a.moved[s[j]] = d[j];
+      a.refs[d[j]] = n[j];
+      a.refs[s[j]] = 0;
+    }
   }
   if (tid == 0) {
     C.count[0] = (int)moves;
@@ -363,17 +406,18 @@ struct Moves {
   bool remap;        // the table's entries go by a.moved first
 };
 
-__device__ __forceinline__ void move_piece(char* dst, const char* src, int64_t bytes) {
+__device__ __forceinline__ void move_piece(char* dst, const char* src, int bytes) {
   // pages start on 16-byte boundaries; what is left of 16 bytes at the end goes byte by byte
-  const int whole = (int)(bytes >> 4), rest = (int)(bytes & 15);
+  constexpr int kLoads = kSeg / 16 / kMove;
+  const int whole = bytes >> 4, rest = bytes & 15;
   const uint4* s = reinterpret_cast<const uint4*>(src);
   uint4* d = reinterpret_cast<uint4*>(dst);
-  uint4 v[4];
+  uint4 v[kLoads];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < kLoads; ++j)
     if ((int)threadIdx.x + j * kMove < whole) v[j] = __ldcs(s + threadIdx.x + j * kMove);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < kLoads; ++j)
     if ((int)threadIdx.x + j * kMove < whole) __stcs(d + threadIdx.x + j * kMove, v[j]);
   if ((int)threadIdx.x < rest) dst[whole * 16 + threadIdx.x] = src[whole * 16 + threadIdx.x];
 }
@@ -394,18 +438,28 @@ __global__ void __launch_bounds__(kMove) move_kernel(const __grid_constant__ Pag
   }
   const int segs = a.caches.seg0[a.caches.n];
   const int64_t items = (int64_t)(m.count ? *m.count : m.n) * segs;
+  // (an item's pages are looked up while the one before it moves)
+  struct Next {
+    int g, rows, src, dst;
+  };
+  auto look = [&](int64_t x) -> Next {
+    if (x >= items) return Next{0, 0, 0, 0};
+    const int k = (int)(x / segs);
+    return Next{(int)(x - (int64_t)k * segs), m.rows ? m.rows[k] : a.page_size, m.src[k], m.dst[k]};
+  };
+  Next next = look(blockIdx.x);
   for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
-    const int k = (int)(x / segs), g = (int)(x - (int64_t)k * segs);
-    const int rows = m.rows ? m.rows[k] : a.page_size;
-    if (rows <= 0) continue;
+    const Next now = next;
+    next = look(x + gridDim.x);
+    if (now.rows <= 0) continue;
     int c = 0;
-    while (g >= a.caches.seg0[c + 1]) ++c;
+    while (now.g >= a.caches.seg0[c + 1]) ++c;
     const int64_t rb = a.caches.row_bytes[c], page = rb * a.page_size;
-    const int64_t at = (int64_t)(g - a.caches.seg0[c]) * kSeg;
-    const int64_t left = rb * rows - at;
+    const int64_t at = (int64_t)(now.g - a.caches.seg0[c]) * kSeg;
+    const int64_t left = rb * now.rows - at;
     if (left <= 0) continue;
     char* base = a.caches.base[c];
-    move_piece(base + m.dst[k] * page + at, base + m.src[k] * page + at, left < kSeg ? left : kSeg);
+    move_piece(base + now.dst * page + at, base + now.src * page + at, (int)(left < kSeg ? left : kSeg));
   }
 }
 
