@@ -103,6 +103,12 @@ __device__ __forceinline__ bool warp_query_row(const Attn4Args& a, int t, int la
   return true;
 }
 
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -113,17 +119,46 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// What the operands hold is the value times 2^-14: kv4_pair() times the scale times 2^112, which is within bf16's range for every
-// scale and brings the first one that is none (0xf8) to infinity.
-constexpr float kShrink = 0x1p-14f;
-constexpr uint32_t kShrinkPair = 0x38803880u, kUp112 = 0x77807780u;  // 2^-14, 2^112, twice in bf16
+// Phase 1's operand: fp16, 2^-3 times the value.  A code's two bits and a scale's four, from 2^-17 · 0.5 to 61440 · 6, are fp16
+// numbers exactly that way, subnormal ones among them, and the conversion is the hardware's: two instructions a pair instead of
+// five.  It takes a byte, two neighbouring nibbles: pairs of columns (0, 2), (4, 6), (1, 3), (5, 7) of eight, so the
+// query's columns stand in that order too.
+constexpr float kShrinkK = 0x1p-3f;
+constexpr uint32_t kShrinkKf16 = 0x30003000u, kShrinkKbf16 = 0x3e003e00u;  // 2^-3 twice
+// Phase 2's: bf16 beside P's (an fp16 P would lose what is 2^-39 of a row's largest), 2^-14 times the value: kv4_pair() times the scale
+// times 2^112, which is within bf16's range for every scale and brings the first one that is none (0xf8) to infinity.
+constexpr float kShrinkV = 0x1p-14f;
+constexpr uint32_t kUp112 = 0x77807780u;  // 2^112 twice in bf16
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // 32 columns (a gathered row's 16-byte piece and their two scales) into the four 16-byte pieces of an operand row from logical piece c
-// on, XOR-ed with x.
-__device__ __forceinline__ void decode32(uint8_t* row, int c, int x, const uint4& w, uint32_t scales) {
+// on, XOR-ed with x.  Both scales are decoded at once (their exponent and mantissa go to fp16's or bf16's places); infinity times 0,
+// added, makes a scale that is not a number one.
+__device__ __forceinline__ void decode32_k(uint8_t* row, int c, int x, const uint4& w, uint32_t scales) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  // Both scales at once: byte << 4 is its exponent and mantissa in bf16's places, 2^-112 times the scale, so twice 2^112; infinity times
-  // 0, added, makes what is not a number one.
+  uint32_t two = mul_f16x2(__byte_perm(scales, 0u, 0x4140) << 7, kShrinkKf16);
+  asm("fma.rn.f16x2 %0, %0, %1, %0;" : "+r"(two) : "r"(0u));
+  const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t o[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(u[i]));
+    const uint32_t f = s[i >> 1];
+    *reinterpret_cast<uint4*>(row + (((c + i) ^ x) * 16)) =
+        make_uint4(mul_f16x2(o[0], f), mul_f16x2(o[1], f), mul_f16x2(o[2], f), mul_f16x2(o[3], f));
+  }
+}
+__device__ __forceinline__ void decode32_v(uint8_t* row, int c, int x, const uint4& w, uint32_t scales) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t two = mul_bf16x2(mul_bf16x2(__byte_perm(scales, 0u, 0x4140) << 4, kUp112), kUp112);
   asm("fma.rn.bf16x2 %0, %0, %1, %0;" : "+r"(two) : "r"(0u));
   const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
@@ -134,6 +169,23 @@ __device__ __forceinline__ void decode32(uint8_t* row, int c, int x, const uint4
         make_uint4(mul_bf16x2(kv4_pair<0>(u[i]), f), mul_bf16x2(kv4_pair<1>(u[i]), f),
                    mul_bf16x2(kv4_pair<2>(u[i]), f), mul_bf16x2(kv4_pair<3>(u[i]), f));
   }
+}
+
+// kind::f16 with both operands fp16 (format 0), fp32 accumulate, K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The largest finite magnitude among pairs of bf16 whose signs are cleared (an infinity or a NaN counts as 0).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
 }
 
 // 64 consecutive tensor-memory columns of this warp's 32 lanes.
@@ -264,7 +316,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     } else if (warp == kMmaWarp) {
       // ---------------- query loads, MMA issue ----------------
       if (elect_one()) {
-        const uint32_t idesc_s = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
+        const uint32_t idesc_s = idesc_f16(kM, kN), idesc_r = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
         const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
         const uint64_t vd0 = sdesc_sw128(smem_u32(ring), kTile, 1024);  // V tiles as P·V reads them
         const uint64_t pd0 = sdesc_sw128(smem_u32(ptiles), 16, 1024);
@@ -283,7 +335,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           for (int j = 0; j < kTiles; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, kd + (uint64_t)(j * (kTile >> 4) + i * 2), idesc_s,
+              mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, kd + (uint64_t)(j * (kTile >> 4) + i * 2), j < kVTiles ? idesc_s : idesc_r,
                           j || i ? 1u : 0u);
           mma_commit(&k_empty[ks]);
           mma_commit(&s_full[sb]);
@@ -362,12 +414,12 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             break;
           uint8_t* tiles = ring + ks * kKSlot;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[i], sc[i]);
+          for (int i = 0; i < 4; ++i) decode32_k(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[i], sc[i]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + (((2 * i + grp + 4 * pair) ^ x) * 16)) =
-                make_uint4(mul_bf16x2(rope[i].x, kShrinkPair), mul_bf16x2(rope[i].y, kShrinkPair), mul_bf16x2(rope[i].z, kShrinkPair),
-                           mul_bf16x2(rope[i].w, kShrinkPair));
+                make_uint4(mul_bf16x2(rope[i].x, kShrinkKbf16), mul_bf16x2(rope[i].y, kShrinkKbf16), mul_bf16x2(rope[i].z, kShrinkKbf16),
+                           mul_bf16x2(rope[i].w, kShrinkKbf16));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -386,7 +438,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
             uint8_t* tiles = ring + vs * kVSlot;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              decode32(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[2 * h + i], sc[2 * h + i]);
+              decode32_v(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[2 * h + i], sc[2 * h + i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&v_full[vs]);
@@ -399,24 +451,72 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       // ---------------- softmax: thread = head ----------------
       const int r = warp * 32 + lane;
       const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+      int shift = 0;  // the row's logits are 2^shift times what its operands say
       bool stop = !__all_sync(0xffffffffu, mbar_wait(q_staged, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT));
       if (!stop) {
-#pragma unroll 3
+        // The latent columns go to fp16, times the power of two that brings the row's largest finite one into [2^14, 2^15) (what is
+        // 2^-29 of it begins to lose bits, far below the logits' own rounding); the rope columns get the same factor, which is held where
+        // they stay within bf16's range.
+        const uint8_t* const row = ring + r * 128;
+        auto piece = [&](int j, int i) { return *reinterpret_cast<const uint4*>(row + j * kQTile + ((i ^ (r & 7)) * 16)); };
+        uint32_t top[2] = {0u, 0u}, odd = 0u;
+#pragma unroll 1
         for (int j = 0; j < kTiles; ++j) {
-          const uint8_t* from = ring + j * kQTile + r * 128;
+          uint32_t t = 0u;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = piece(j, i);
+            t = max_bf16x2(max_bf16x2(t, v.x & 0x7fff7fffu), max_bf16x2(v.y & 0x7fff7fffu, max_bf16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+          }
+          if (finite_pair(t) != t) odd = 1u;  // (the maximum passes NaNs over)
+          top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
+        }
+        if (__any_sync(0xffffffffu, odd)) {  // infinities: once more without them
+          top[0] = top[1] = 0u;
+          for (int j = 0; j < kTiles; ++j)
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = piece(j, i);
+              const uint32_t t = max_bf16x2(max_bf16x2(finite_pair(v.x & 0x7fff7fffu), finite_pair(v.y & 0x7fff7fffu)),
+                                            max_bf16x2(finite_pair(v.z & 0x7fff7fffu), finite_pair(v.w & 0x7fff7fffu)));
+              top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
+            }
+        }
+        auto exponent = [](uint32_t t) { return (int)(max(t & 0x7fffu, t >> 16 & 0x7fffu) >> 7) - 127; };  // (0 and subnormal: -127)
+        const int e0 = exponent(top[0]), e1 = exponent(top[1]);
+        shift = min(max(e0 == -127 ? 0 : e0 - 14, max(e1 - 100, -100)), 113);
+        const float down = __uint_as_float((uint32_t)(127 - shift) << 23);
+        const uint32_t down_bf16 = (uint32_t)(127 - shift) << 7;
+#pragma unroll 1
+        for (int j = 0; j < kVTiles; ++j) {
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(from + ((i ^ (r & 7)) * 16));
-            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            const uint4 v = piece(j, i);
+            auto lo = [&](uint32_t u) { return __uint_as_float(u << 16) * down; };
+            auto hi = [&](uint32_t u) { return __uint_as_float(u & 0xffff0000u) * down; };
+            w[4 * i] = f16x2(lo(v.x), lo(v.y));
+            w[4 * i + 1] = f16x2(lo(v.z), lo(v.w));
+            w[4 * i + 2] = f16x2(hi(v.x), hi(v.y));
+            w[4 * i + 3] = f16x2(hi(v.z), hi(v.w));
           }
           tmem_st32(lane_base + kQCol + j * 32, w);
+        }
+        {
+          const uint32_t two = down_bf16 | down_bf16 << 16;
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = piece(kVTiles, i);
+            w[4 * i] = mul_bf16x2(v.x, two); w[4 * i + 1] = mul_bf16x2(v.y, two);
+            w[4 * i + 2] = mul_bf16x2(v.z, two); w[4 * i + 3] = mul_bf16x2(v.w, two);
+          }
+          tmem_st32(lane_base + kQCol + kVTiles * 32, w);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(qt_full);
       }
-      const float scale = a.scale_log2 * (1.f / kShrink);
+      const float scale = a.scale_log2 * (1.f / kShrinkK) * __uint_as_float((uint32_t)(127 + shift) << 23);
       float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
       uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
       for (int g = 0; g < nch && !stop; ++g) {
@@ -503,7 +603,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
         // there, 16 bytes more than its length apart from the next, and sends it with one bulk copy
         const bool live = r < a.h;
-        const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kShrink);
+        const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kShrinkV);
         const bool f32 = split || a.out_dtype == DSA_F32;
         constexpr int kRowBytes = 1024;
         uint8_t* mine = ring + r * (kRowBytes + 16);
