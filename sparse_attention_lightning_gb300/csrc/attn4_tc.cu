@@ -45,18 +45,20 @@ constexpr int kQTile = kM * 128;           // 16 KB: 128 heads x 64 columns, or 
 constexpr int kDc = 512, kDr = 64, kD = kDc + kDr;
 constexpr int kTiles = kD / 64, kVTiles = kDc / 64;
 constexpr int kRow = kv4_row_bytes(kDc, kDr), kRaw = kN * kRow;  // a gathered chunk: 26 KB
-constexpr int kStages = 3;                                       // of them in flight
 constexpr int kKSlots = 2, kKSlot = kTiles * kTile;              // phase 1: 2 x 72 KB
-constexpr int kVSlots = 3, kVSlot = kVTiles / 2 * kTile;         // phase 2: 3 x 32 KB (half the columns of a chunk)
-constexpr int kPSlots = 3;                                       //   and 3 x 16 KB
+constexpr int kVSlots = 4, kVSlot = kVTiles / 2 * kTile;         // phase 2: 4 x 32 KB (half the columns of a chunk)
+constexpr int kPSlots = 2;                                       //   and 2 x 16 KB
 constexpr int kSBufs = 3;                  // logit buffers
 constexpr int kSoftWarps = 4;
-constexpr int kDecoders = 8;               // warps
-constexpr int kMmaWarp = kSoftWarps + kDecoders;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kRing = kKSlots * kKSlot;
+constexpr int kGroups = 2, kDecoders = 8;  // groups of decoding warps, which take the chunks in turn
+constexpr int kMmaWarp = kSoftWarps + kGroups * kDecoders;
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole groups of four warps: their registers are set together)
+// Registers a thread of softmax, of the decoders, of the MMA's four warps; together at most what the block is launched with.
+constexpr int kLaunchRegs = 80, kSoftRegs = 136, kDecodeRegs = 72, kMmaRegs = 56;
+static_assert(128 * kSoftRegs + 32 * kGroups * kDecoders * kDecodeRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "registers");
+constexpr int kRing = kVSlots * kVSlot + kPSlots * kQTile;
 constexpr int kBarBytes = 512;
-constexpr int kSmem = kRing + kStages * kRaw + kBarBytes + 1024;
+constexpr int kSmem = kRing + kGroups * kRaw + kBarBytes + 1024;
 constexpr int kQCol = 0, kSCol = kD / 2;   // tensor memory of phase 1: 288 query columns, the logits; of phase 2: O
 constexpr int kRopeAt = kv4_rope_at(kDc), kScaleAt = kv4_scale_at(kDc, kDr);
 constexpr float kGrowLog2 = 8.0f;
@@ -64,7 +66,7 @@ constexpr int kMostRows = 2048;            // entries of a query
 constexpr int64_t kPBytes = kM * kN * 2, kRefBytes = kM * 4, kListBytes = kN * 4;  // scratch of a chunk
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(kSCol + kSBufs * kN <= 512, "tensor memory");
-static_assert(kVSlots * kVSlot + kPSlots * kQTile <= kRing, "phase 2's ring");
+static_assert(kKSlots * kKSlot <= kRing, "phase 1's ring");
 static_assert(kTiles * kQTile <= kRing, "the query passes through the ring");
 static_assert(kM * (256 * 4 + 16) <= kRing && kM * (512 * 2 + 16) <= kRing, "the output leaves through the ring");
 
@@ -199,6 +201,17 @@ __device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
   for (int i = 0; i < 32; ++i) s[32 + i] = __uint_as_float(r[i]);
 }
 
+// The block's barrier, which each role meets in its own code.
+__device__ __forceinline__ void block_sync() {
+  __syncwarp();
+  asm volatile("barrier.cta.sync.aligned 0;" ::: "memory");
+}
+
+struct Item {
+  int t, piece, nch, total;
+  int64_t row0;
+};
+
 __global__ void __launch_bounds__(kThreads, 1)
 attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
   griddep_wait();
@@ -211,16 +224,16 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ptiles = ring + kVSlots * kVSlot;
-  uint8_t* raw = ring + kRing;     // [3][64][416]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + kStages * kRaw);
+  uint8_t* raw = ring + kRing;     // [2][64][416]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + kGroups * kRaw);
   uint64_t* k_full = bars;         // [2] 8 warps have stored a chunk's tiles
   uint64_t* k_empty = bars + 2;    // [2] multiplied
   uint64_t* s_full = bars + 4;     // [3] logits complete
   uint64_t* s_empty = bars + 7;    // [3] read
-  uint64_t* v_full = bars + 10;    // [3]
-  uint64_t* v_empty = bars + 13;   // [3]
-  uint64_t* p_full = bars + 16;    // [3]
-  uint64_t* p_empty = bars + 19;   // [3]
+  uint64_t* v_full = bars + 10;    // [4]
+  uint64_t* v_empty = bars + 14;   // [4]
+  uint64_t* p_full = bars + 18;    // [2]
+  uint64_t* p_empty = bars + 20;   // [2]
   uint64_t* q_staged = bars + 22;  // the query on its way to tensor memory
   uint64_t* qt_full = bars + 23;   // there
   uint64_t* o_full = bars + 24;    // O complete
@@ -249,19 +262,21 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   int32_t* const list = reinterpret_cast<int32_t*>(refs + (int64_t)p.most * kM);  // cache rows of the entries, without those skipped
   // The barriers' phases go on from item to item: chunks so far, the parity of the items and of those that had any.
   uint32_t done = 0, turn = 0, full_turn = 0;
-  for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
-    const int t = item / a.splits, piece = item - t * a.splits;
-    const int64_t row0 = (int64_t)t * a.h;
+  // An item's row, its entries' chunks; one without entries is written here.
+  auto begin = [&](int item, Item& it) {
+    it.t = item / a.splits;
+    it.piece = item - it.t * a.splits;
+    it.row0 = (int64_t)it.t * a.h;
     // The query comes while the entries are looked up (the ring is free: all roles have left the item before).
     if (warp == kMmaWarp && elect_one()) {
       mbar_arrive_expect_tx(q_staged, kTiles * kQTile);
-      for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)row0);
+      for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)it.row0);
     }
     __syncwarp();
     RowInfo ri;
-    const bool good = warp_query_row(a, t, lane, ri);
-    const int c0 = (int)((int64_t)p.chunks * piece / a.splits), c1 = (int)((int64_t)p.chunks * (piece + 1) / a.splits);
-    const int32_t* idx = a.idx + (int64_t)t * a.top_k;
+    const bool good = warp_query_row(a, it.t, lane, ri);
+    const int c0 = (int)((int64_t)p.chunks * it.piece / a.splits), c1 = (int)((int64_t)p.chunks * (it.piece + 1) / a.splits);
+    const int32_t* idx = a.idx + (int64_t)it.t * a.top_k;
     const int end = min(a.top_k, c1 * kN);
     // The piece's entries as cache rows, without the skipped ones (a short history's row is mostly -1): a warp takes
     // consecutive ones, all its loads at once.
@@ -286,9 +301,8 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       if (lane == 0) counts[warp] = mine;
     }
     tc_fence_before();
-    cta_sync();
+    block_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     int total = 0;
     if (good) {
       const int c = lane < kWarps ? counts[lane] : 0;
@@ -301,358 +315,396 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         at += __popc(m);
       }
     }
-    cta_sync();
-    const int nch = (total + kN - 1) / kN;
-
-    if (nch == 0) {
-      // no entries: nothing, or zeros
-      for (int i = threadIdx.x; good && i < a.h; i += kThreads) {
-        if (split) a.part_ml[(int64_t)piece * rows_all + row0 + i] = make_float2(-INFINITY, 0.f);
-        else if (a.lse) a.lse[row0 + i] = -INFINITY;
+    block_sync();
+    it.total = total;
+    it.nch = (total + kN - 1) / kN;
+    if (total || !good) return;
+    for (int i = threadIdx.x; i < a.h; i += kThreads) {
+      if (split) a.part_ml[(int64_t)it.piece * rows_all + it.row0 + i] = make_float2(-INFINITY, 0.f);
+      else if (a.lse) a.lse[it.row0 + i] = -INFINITY;
+    }
+    const int per = a.out_dtype == DSA_F32 ? 128 : 64;  // 16-byte pieces of a row
+    for (int i = threadIdx.x; !split && i < a.h * per; i += kThreads)
+      reinterpret_cast<uint4*>(a.out)[it.row0 * per + i] = make_uint4(0u, 0u, 0u, 0u);
+  };
+  // False: a wait was given up.  (None is under way that could be now.)
+  auto finish = [&](const Item& it) -> bool {
+    if (it.nch == 0 && warp == kMmaWarp) mbar_wait_drain(q_staged, turn);  // (nobody else waited for the query)
+    turn ^= 1;
+    if (it.nch) full_turn ^= 1;
+    done += it.nch;
+    tc_fence_before();
+    block_sync();
+    return *abort_flag == 0;
+  };
+  tc_fence_before();
+  block_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+      Item it;
+      begin(item, it);
+      const int nch = it.nch;
+      if (nch && warp == kMmaWarp) {
+        // ---------------- query loads, MMA issue ----------------
+        if (elect_one()) {
+          const uint32_t idesc_s = idesc_f16(kM, kN), idesc_r = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
+          const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+          const uint64_t vd0 = sdesc_sw128(smem_u32(ring), kTile, 1024);  // V tiles as P·V reads them
+          const uint64_t pd0 = sdesc_sw128(smem_u32(ptiles), 16, 1024);
+          bool stop = !mbar_wait(qt_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+          for (int g = 0; g < nch && !stop; ++g) {
+            const uint32_t n = done + g, ks = n % kKSlots, sb = n % kSBufs;
+            if (!mbar_wait(&s_empty[sb], ((n / kSBufs) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
+                !mbar_wait(&k_full[ks], (n / kKSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + kSCol + sb * kN;
+            const uint64_t kd = kd0 + (uint64_t)(ks * (kKSlot >> 4));
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, kd + (uint64_t)(j * (kTile >> 4) + i * 2), j < kVTiles ? idesc_s : idesc_r,
+                            j || i ? 1u : 0u);
+            mma_commit(&k_empty[ks]);
+            mma_commit(&s_full[sb]);
+          }
+          for (int g = 0; g < 2 * nch && !stop; ++g) {  // half g & 1 of the columns
+            const uint32_t n = done + (g >> 1), vn = 2 * done + g, vs = vn % kVSlots, ps = n % kPSlots;
+            if (!mbar_wait(&v_full[vs], (vn / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
+                ((g & 1) == 0 && !mbar_wait(&p_full[ps], (n / kPSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
+              break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)(vs * (kVSlot >> 4)), pd = pd0 + (uint64_t)(ps * (kQTile >> 4));
+            const uint32_t acc = g > 1;
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk)
+              mma_bf16(tmem + (g & 1) * 256, pd + (uint64_t)(kk * 2), vd + (uint64_t)(kk * 128), idesc_pv, kk ? 1u : acc);
+            mma_commit(&v_empty[vs]);
+            if (g & 1) mma_commit(&p_empty[ps]);
+          }
+          mma_commit(o_full);
+          mbar_wait_drain(o_full, full_turn);
+        }
       }
-      const int per = a.out_dtype == DSA_F32 ? 128 : 64;  // 16-byte pieces of a row
-      for (int i = threadIdx.x; good && !split && i < a.h * per; i += kThreads)
-        reinterpret_cast<uint4*>(a.out)[row0 * per + i] = make_uint4(0u, 0u, 0u, 0u);
-    } else if (warp == kMmaWarp) {
-      // ---------------- query loads, MMA issue ----------------
-      if (elect_one()) {
-        const uint32_t idesc_s = idesc_f16(kM, kN), idesc_r = idesc_bf16(kM, kN), idesc_pv = idesc_bf16(kM, 256, false, true);
-        const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
-        const uint64_t vd0 = sdesc_sw128(smem_u32(ring), kTile, 1024);  // V tiles as P·V reads them
-        const uint64_t pd0 = sdesc_sw128(smem_u32(ptiles), 16, 1024);
-        bool stop = !mbar_wait(qt_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+      if (!finish(it)) break;
+    }
+  } else if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
+    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+      Item it;
+      begin(item, it);
+      const int nch = it.nch, total = it.total;
+      if (nch) {
+        // ---------------- gather and decode: the chunks of phase 1, then the same again for phase 2 ----------------
+        // The two groups take the chunks in turn: a chunk is a chain of waits and latencies as long as its work, which the other
+        // group's work fills.  A warp takes eight rows: their 16-byte pieces are copied to its part of the group's stage and
+        // come to registers from there, when the copies of the group's next chunk begin.  Eight neighbouring lanes read pieces of four rows (8 banks
+        // apart) and two pieces each, and store what they decode to at eight different places of the swizzle: no bank is
+        // asked for twice.
+        const int w = (warp - kSoftWarps) % kDecoders, group = (warp - kSoftWarps) / kDecoders;
+        const int pair = (lane >> 2) & 1, grp = lane >> 4;
+        const int r = w * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), x = r & 7;  // row of the chunk
+        // the group's chunks, and its steps: its chunks of phase 1, then the same again
+        const int count = (nch - group + kGroups - 1) / kGroups, steps = 2 * count;
+        auto chunk_of = [&](int i) { return group + kGroups * (i < count ? i : i - count); };
+        // Lane l holds the cache row of the warp's row l & 7, read a step ahead of its copy.  Behind the last entry the last
+        // one is repeated: its P is 0 there, and what its columns hold the query attends to anyway.
+        auto load_row_of = [&](int i) { return __ldcg(list + min(chunk_of(i) * kN + w * 8 + (lane & 7), total - 1)); };
+        constexpr int kPieces = kRow / 16, kCopies = (8 * kPieces + 31) / 32;
+        uint8_t* const mine_raw = raw + group * kRaw + w * 8 * kRow;
+        int next_row = load_row_of(0);
+        auto gather = [&](int i) {
+          const int row_of = next_row;
+          next_row = load_row_of(i + 1);
+          const uint32_t dst = smem_u32(mine_raw) + lane * 16;
+#pragma unroll
+          for (int c = 0; c < kCopies; ++c) {
+            const int f = c * 32 + lane, j = f / kPieces;  // piece f of the warp's rows, in row j
+            const int from = __shfl_sync(0xffffffffu, row_of, j & 7);
+            if (f < 8 * kPieces) copy16_async(dst + c * 512, a.kv4 + (int64_t)from * kRow + (f - j * kPieces) * 16);
+          }
+        };
+        if (steps) gather(0);
+        for (int i = 0; i < steps; ++i) {
+          const int n = i < count ? chunk_of(i) : nch + chunk_of(i);  // phase 1: [0, nch), phase 2: [nch, 2 nch)
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+          const uint8_t* src = raw + group * kRaw + r * kRow;
+          uint4 v[4], rope[2];  // piece j: columns 32 (2 (2 j + grp) + pair) ..
+          uint32_t sc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = 2 * (2 * j + grp) + pair;
+            v[j] = *reinterpret_cast<const uint4*>(src + 16 * k);
+            sc[j] = *reinterpret_cast<const uint16_t*>(src + kScaleAt + 2 * k);
+          }
+          if (n < nch) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rope[j] = *reinterpret_cast<const uint4*>(src + kRopeAt + 16 * (2 * j + grp + 4 * pair));
+          }
+          asm volatile("" : "+r"(v[0].x), "+r"(v[1].x), "+r"(v[2].x), "+r"(v[3].x), "+r"(sc[0]), "+r"(sc[1]), "+r"(sc[2]), "+r"(sc[3]) :: "memory");
+          __syncwarp();  // the stage has been read
+          if (i + 1 < steps) gather(i + 1);
+          if (n < nch) {
+            const uint32_t kn = done + n, ks = kn % kKSlots;
+            // (the query passes through the tiles first)
+            if (!__all_sync(0xffffffffu,
+                            (n >= kKSlots || mbar_wait(qt_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT)) &&
+                                mbar_wait(&k_empty[ks], ((kn / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
+              break;
+            uint8_t* tiles = ring + ks * kKSlot;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) decode32_k(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[i], sc[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + (((2 * i + grp + 4 * pair) ^ x) * 16)) =
+                  make_uint4(mul_bf16x2(rope[i].x, kShrinkKbf16), mul_bf16x2(rope[i].y, kShrinkKbf16), mul_bf16x2(rope[i].z, kShrinkKbf16),
+                             mul_bf16x2(rope[i].w, kShrinkKbf16));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[ks]);
+          } else {
+            const int g = n - nch;
+            // (the first tiles are some of phase 1's: its last MMAs are done)
+            const uint32_t lg = done + nch - 1;
+            bool ok = g >= kGroups || mbar_wait(&s_full[lg % kSBufs], (lg / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t vn = 2 * (done + g) + h, vs = vn % kVSlots;
+              ok = ok && mbar_wait(&v_empty[vs], ((vn / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              uint8_t* tiles = ring + vs * kVSlot;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                decode32_v(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[2 * h + i], sc[2 * h + i]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&v_full[vs]);
+            }
+            if (!ok) break;
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // every copy has landed before the CTA goes on
+      }
+      if (!finish(it)) break;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+      Item it;
+      begin(item, it);
+      const int nch = it.nch, total = it.total;
+      const int piece = it.piece;
+      const int64_t row0 = it.row0;
+      if (nch && warp < live_warps) {
+        // ---------------- softmax: thread = head ----------------
+        const int r = warp * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        int shift = 0;  // the row's logits are 2^shift times what its operands say
+        bool stop = !__all_sync(0xffffffffu, mbar_wait(q_staged, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT));
+        if (!stop) {
+          // The latent columns go to fp16, times the power of two that brings the row's largest finite one into [2^14, 2^15) (what is
+          // 2^-29 of it begins to lose bits, far below the logits' own rounding); the rope columns get the same factor, which is held where
+          // they stay within bf16's range.
+          const uint8_t* const row = ring + r * 128;
+          auto piece = [&](int j, int i) { return *reinterpret_cast<const uint4*>(row + j * kQTile + ((i ^ (r & 7)) * 16)); };
+          uint32_t top[2] = {0u, 0u}, odd = 0u;
+#pragma unroll 1
+          for (int j = 0; j < kTiles; ++j) {
+            uint32_t t = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = piece(j, i);
+              t = max_bf16x2(max_bf16x2(t, v.x & 0x7fff7fffu), max_bf16x2(v.y & 0x7fff7fffu, max_bf16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+            }
+            if (finite_pair(t) != t) odd = 1u;  // (the maximum passes NaNs over)
+            top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
+          }
+          if (__any_sync(0xffffffffu, odd)) {  // infinities: once more without them
+            top[0] = top[1] = 0u;
+            for (int j = 0; j < kTiles; ++j)
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = piece(j, i);
+                const uint32_t t = max_bf16x2(max_bf16x2(finite_pair(v.x & 0x7fff7fffu), finite_pair(v.y & 0x7fff7fffu)),
+                                              max_bf16x2(finite_pair(v.z & 0x7fff7fffu), finite_pair(v.w & 0x7fff7fffu)));
+                top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
+              }
+          }
+          auto exponent = [](uint32_t t) { return (int)(max(t & 0x7fffu, t >> 16 & 0x7fffu) >> 7) - 127; };  // (0 and subnormal: -127)
+          const int e0 = exponent(top[0]), e1 = exponent(top[1]);
+          shift = min(max(e0 == -127 ? 0 : e0 - 14, max(e1 - 100, -100)), 113);
+          const float down = __uint_as_float((uint32_t)(127 - shift) << 23);
+          const uint32_t down_bf16 = (uint32_t)(127 - shift) << 7;
+#pragma unroll 1
+          for (int j = 0; j < kVTiles; ++j) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = piece(j, i);
+              auto lo = [&](uint32_t u) { return __uint_as_float(u << 16) * down; };
+              auto hi = [&](uint32_t u) { return __uint_as_float(u & 0xffff0000u) * down; };
+              w[4 * i] = f16x2(lo(v.x), lo(v.y));
+              w[4 * i + 1] = f16x2(lo(v.z), lo(v.w));
+              w[4 * i + 2] = f16x2(hi(v.x), hi(v.y));
+              w[4 * i + 3] = f16x2(hi(v.z), hi(v.w));
+            }
+            tmem_st32(lane_base + kQCol + j * 32, w);
+          }
+          {
+            const uint32_t two = down_bf16 | down_bf16 << 16;
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = piece(kVTiles, i);
+              w[4 * i] = mul_bf16x2(v.x, two); w[4 * i + 1] = mul_bf16x2(v.y, two);
+              w[4 * i + 2] = mul_bf16x2(v.z, two); w[4 * i + 3] = mul_bf16x2(v.w, two);
+            }
+            tmem_st32(lane_base + kQCol + kVTiles * 32, w);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(qt_full);
+        }
+        const float scale = a.scale_log2 * (1.f / kShrinkK) * __uint_as_float((uint32_t)(127 + shift) << 23);
+        float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
+        uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
         for (int g = 0; g < nch && !stop; ++g) {
-          const uint32_t n = done + g, ks = n % kKSlots, sb = n % kSBufs;
-          if (!mbar_wait(&s_empty[sb], ((n / kSBufs) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
-              !mbar_wait(&k_full[ks], (n / kKSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)) {
+          const uint32_t n = done + g, sb = n % kSBufs;
+          if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], (n / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + kSCol + sb * kN;
-          const uint64_t kd = kd0 + (uint64_t)(ks * (kKSlot >> 4));
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16_ts(d, tmem + kQCol + j * 32 + i * 8, kd + (uint64_t)(j * (kTile >> 4) + i * 2), j < kVTiles ? idesc_s : idesc_r,
-                          j || i ? 1u : 0u);
-          mma_commit(&k_empty[ks]);
-          mma_commit(&s_full[sb]);
-        }
-        for (int g = 0; g < 2 * nch && !stop; ++g) {  // half g & 1 of the columns
-          const uint32_t n = done + (g >> 1), vn = 2 * done + g, vs = vn % kVSlots, ps = n % kPSlots;
-          if (!mbar_wait(&v_full[vs], (vn / kVSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT) ||
-              ((g & 1) == 0 && !mbar_wait(&p_full[ps], (n / kPSlots) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
-            break;
-          tc_fence_after();
-          const uint64_t vd = vd0 + (uint64_t)(vs * (kVSlot >> 4)), pd = pd0 + (uint64_t)(ps * (kQTile >> 4));
-          const uint32_t acc = g > 1;
-#pragma unroll
-          for (int kk = 0; kk < kN / 16; ++kk)
-            mma_bf16(tmem + (g & 1) * 256, pd + (uint64_t)(kk * 2), vd + (uint64_t)(kk * 128), idesc_pv, kk ? 1u : acc);
-          mma_commit(&v_empty[vs]);
-          if (g & 1) mma_commit(&p_empty[ps]);
-        }
-        mma_commit(o_full);
-        mbar_wait_drain(o_full, full_turn);
-      }
-    } else if (warp >= kSoftWarps) {
-      // ---------------- gather and decode: the chunks of phase 1, then the same again for phase 2 ----------------
-      // A warp takes eight rows of every chunk: their 16-byte pieces are copied to its part of a stage, two steps ahead, and come to
-      // registers from there.  Eight neighbouring lanes read pieces of four rows (8 banks apart) and two pieces each, and
-      // store what they decode to at eight different places of the swizzle: no bank is asked for twice.
-      const int w = warp - kSoftWarps, pair = (lane >> 2) & 1, grp = lane >> 4;
-      const int r = w * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), x = r & 7;  // row of the chunk
-      const int steps = 2 * nch;
-      // Lane l holds the cache row of the warp's row l & 7, read a step ahead of its copy.  Behind the last entry the last
-      // one is repeated: its P is 0 there, and what its columns hold the query attends to anyway.
-      auto load_row_of = [&](int n) { return __ldcg(list + min((n < nch ? n : n - nch) * kN + w * 8 + (lane & 7), total - 1)); };
-      constexpr int kPieces = kRow / 16, kCopies = (8 * kPieces + 31) / 32;
-      uint8_t* const mine_raw = raw + w * 8 * kRow;
-      int next_row = load_row_of(0);
-      auto gather = [&](int n) {
-        const int row_of = next_row;
-        next_row = load_row_of(n + 1);
-        if (n < steps) {
-          const uint32_t dst = smem_u32(mine_raw + (uint32_t)n % kStages * kRaw) + lane * 16;
-#pragma unroll
-          for (int i = 0; i < kCopies; ++i) {
-            const int f = i * 32 + lane, j = f / kPieces;  // piece f of the warp's rows, in row j
-            const int from = __shfl_sync(0xffffffffu, row_of, j & 7);
-            if (f < 8 * kPieces) copy16_async(dst + i * 512, a.kv4 + (int64_t)from * kRow + (f - j * kPieces) * 16);
-          }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-#pragma unroll
-      for (int n = 0; n < kStages - 1; ++n) gather(n);
-      for (int n = 0; n < steps; ++n) {
-        __syncwarp();  // the stage has been read
-        gather(n + kStages - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        __syncwarp();
-        const uint8_t* src = raw + (uint32_t)n % kStages * kRaw + r * kRow;
-        uint4 v[4], rope[2];  // piece i: columns 32 (2 (2 i + grp) + pair) ..
-        uint32_t sc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 2 * (2 * i + grp) + pair;
-          v[i] = *reinterpret_cast<const uint4*>(src + 16 * k);
-          sc[i] = *reinterpret_cast<const uint16_t*>(src + kScaleAt + 2 * k);
-        }
-        if (n < nch) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) rope[i] = *reinterpret_cast<const uint4*>(src + kRopeAt + 16 * (2 * i + grp + 4 * pair));
-        }
-        if (n < nch) {
-          const uint32_t kn = done + n, ks = kn % kKSlots;
-          // (the query passes through the tiles first)
-          if (!__all_sync(0xffffffffu,
-                          (n >= kKSlots || mbar_wait(qt_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT)) &&
-                              mbar_wait(&k_empty[ks], ((kn / kKSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT)))
-            break;
-          uint8_t* tiles = ring + ks * kKSlot;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) decode32_k(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[i], sc[i]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            *reinterpret_cast<uint4*>(tiles + kVTiles * kTile + r * 128 + (((2 * i + grp + 4 * pair) ^ x) * 16)) =
-                make_uint4(mul_bf16x2(rope[i].x, kShrinkKbf16), mul_bf16x2(rope[i].y, kShrinkKbf16), mul_bf16x2(rope[i].z, kShrinkKbf16),
-                           mul_bf16x2(rope[i].w, kShrinkKbf16));
-          }
-          fence_proxy_async_smem();
+          float z[kN];
+          load_row(lane_base + kSCol + sb * kN, z);
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[ks]);
-        } else {
-          const int g = n - nch;
-          // (the first tiles are some of phase 1's: its last MMAs are done)
-          const uint32_t lg = done + nch - 1;
-          bool ok = g > 0 || mbar_wait(&s_full[lg % kSBufs], (lg / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+          if (lane == 0) mbar_arrive(&s_empty[sb]);
+          if (g == nch - 1) {  // behind the last entry
+            const int n_in = total - g * kN;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t vn = 2 * (done + g) + h, vs = vn % kVSlots;
-            ok = ok && mbar_wait(&v_empty[vs], ((vn / kVSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            uint8_t* tiles = ring + vs * kVSlot;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              decode32_v(tiles + (2 * i + grp) * kTile + r * 128, 4 * pair, x, v[2 * h + i], sc[2 * h + i]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_full[vs]);
+            for (int i = 0; i < kN; ++i)
+              if (i >= n_in) z[i] = -INFINITY;
           }
-          if (!ok) break;
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");  // every copy has landed before the CTA goes on
-    } else if (warp < live_warps) {
-      // ---------------- softmax: thread = head ----------------
-      const int r = warp * 32 + lane;
-      const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-      int shift = 0;  // the row's logits are 2^shift times what its operands say
-      bool stop = !__all_sync(0xffffffffu, mbar_wait(q_staged, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT));
-      if (!stop) {
-        // The latent columns go to fp16, times the power of two that brings the row's largest finite one into [2^14, 2^15) (what is
-        // 2^-29 of it begins to lose bits, far below the logits' own rounding); the rope columns get the same factor, which is held where
-        // they stay within bf16's range.
-        const uint8_t* const row = ring + r * 128;
-        auto piece = [&](int j, int i) { return *reinterpret_cast<const uint4*>(row + j * kQTile + ((i ^ (r & 7)) * 16)); };
-        uint32_t top[2] = {0u, 0u}, odd = 0u;
-#pragma unroll 1
-        for (int j = 0; j < kTiles; ++j) {
-          uint32_t t = 0u;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
+          const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          if (mc > m + kGrowLog2) {  // the first entries always (m = -inf)
+            const float m_new = ceilf(mc);
+            l *= ex2(m - m_new);
+            m = m_new;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;  // nothing visible so far
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 v = piece(j, i);
-            t = max_bf16x2(max_bf16x2(t, v.x & 0x7fff7fffu), max_bf16x2(v.y & 0x7fff7fffu, max_bf16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-          }
-          if (finite_pair(t) != t) odd = 1u;  // (the maximum passes NaNs over)
-          top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
-        }
-        if (__any_sync(0xffffffffu, odd)) {  // infinities: once more without them
-          top[0] = top[1] = 0u;
-          for (int j = 0; j < kTiles; ++j)
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = piece(j, i);
-              const uint32_t t = max_bf16x2(max_bf16x2(finite_pair(v.x & 0x7fff7fffu), finite_pair(v.y & 0x7fff7fffu)),
-                                            max_bf16x2(finite_pair(v.z & 0x7fff7fffu), finite_pair(v.w & 0x7fff7fffu)));
-              top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p0 = ex2(fmaf(z[8 * i + 2 * e], scale, -ref));
+              const float p1 = ex2(fmaf(z[8 * i + 2 * e + 1], scale, -ref));
+              sum[(2 * e) & 3] += p0;
+              sum[(2 * e + 1) & 3] += p1;
+              pk[e] = bf16x2(p0, p1);
             }
-        }
-        auto exponent = [](uint32_t t) { return (int)(max(t & 0x7fffu, t >> 16 & 0x7fffu) >> 7) - 127; };  // (0 and subnormal: -127)
-        const int e0 = exponent(top[0]), e1 = exponent(top[1]);
-        shift = min(max(e0 == -127 ? 0 : e0 - 14, max(e1 - 100, -100)), 113);
-        const float down = __uint_as_float((uint32_t)(127 - shift) << 23);
-        const uint32_t down_bf16 = (uint32_t)(127 - shift) << 7;
-#pragma unroll 1
-        for (int j = 0; j < kVTiles; ++j) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = piece(j, i);
-            auto lo = [&](uint32_t u) { return __uint_as_float(u << 16) * down; };
-            auto hi = [&](uint32_t u) { return __uint_as_float(u & 0xffff0000u) * down; };
-            w[4 * i] = f16x2(lo(v.x), lo(v.y));
-            w[4 * i + 1] = f16x2(lo(v.z), lo(v.w));
-            w[4 * i + 2] = f16x2(hi(v.x), hi(v.y));
-            w[4 * i + 3] = f16x2(hi(v.z), hi(v.w));
+            __stcg(pbuf + (8 * g + i) * kM, make_uint4(pk[0], pk[1], pk[2], pk[3]));
           }
-          tmem_st32(lane_base + kQCol + j * 32, w);
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          __stcg(refs + g * kM + r, m);
         }
-        {
-          const uint32_t two = down_bf16 | down_bf16 << 16;
-          uint32_t w[32];
+        // phase 2: this thread's row of P, relative to the last m (a power of two: exact)
+        uint4 pk[8];
+        float ref = 0.f;
+        auto load_p = [&](int g) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = piece(kVTiles, i);
-            w[4 * i] = mul_bf16x2(v.x, two); w[4 * i + 1] = mul_bf16x2(v.y, two);
-            w[4 * i + 2] = mul_bf16x2(v.z, two); w[4 * i + 3] = mul_bf16x2(v.w, two);
+          for (int i = 0; i < 8; ++i) pk[i] = __ldcg(pbuf + (8 * g + i) * kM);
+          ref = __ldcg(refs + g * kM + r);
+        };
+        if (!stop) load_p(0);
+        for (int g = 0; g < nch && !stop; ++g) {
+          const uint32_t n = done + g, ps = n % kPSlots;
+          // (phase 1's MMAs are done with the tiles: softmax has read their last logits)
+          if (!__all_sync(0xffffffffu, mbar_wait(&p_empty[ps], ((n / kPSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
+            stop = true;
+            break;
           }
-          tmem_st32(lane_base + kQCol + kVTiles * 32, w);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qt_full);
-      }
-      const float scale = a.scale_log2 * (1.f / kShrinkK) * __uint_as_float((uint32_t)(127 + shift) << 23);
-      float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
-      uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
-      for (int g = 0; g < nch && !stop; ++g) {
-        const uint32_t n = done + g, sb = n % kSBufs;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], (n / kSBufs) & 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
-          stop = true;
-          break;
-        }
-        tc_fence_after();
-        float z[kN];
-        load_row(lane_base + kSCol + sb * kN, z);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[sb]);
-        if (g == nch - 1) {  // behind the last entry
-          const int n_in = total - g * kN;
-#pragma unroll
-          for (int i = 0; i < kN; ++i)
-            if (i >= n_in) z[i] = -INFINITY;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
-        const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        if (mc > m + kGrowLog2) {  // the first entries always (m = -inf)
-          const float m_new = ceilf(mc);
-          l *= ex2(m - m_new);
-          m = m_new;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;  // nothing visible so far
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p0 = ex2(fmaf(z[8 * i + 2 * e], scale, -ref));
-            const float p1 = ex2(fmaf(z[8 * i + 2 * e + 1], scale, -ref));
-            sum[(2 * e) & 3] += p0;
-            sum[(2 * e + 1) & 3] += p1;
-            pk[e] = bf16x2(p0, p1);
-          }
-          __stcg(pbuf + (8 * g + i) * kM, make_uint4(pk[0], pk[1], pk[2], pk[3]));
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        __stcg(refs + g * kM + r, m);
-      }
-      // phase 2: this thread's row of P, relative to the last m (a power of two: exact)
-      uint4 pk[8];
-      float ref = 0.f;
-      auto load_p = [&](int g) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pk[i] = __ldcg(pbuf + (8 * g + i) * kM);
-        ref = __ldcg(refs + g * kM + r);
-      };
-      if (!stop) load_p(0);
-      for (int g = 0; g < nch && !stop; ++g) {
-        const uint32_t n = done + g, ps = n % kPSlots;
-        // (phase 1's MMAs are done with the tiles: softmax has read their last logits)
-        if (!__all_sync(0xffffffffu, mbar_wait(&p_empty[ps], ((n / kPSlots) & 1) ^ 1, abort_flag, a.status, DSA_FLAG_TIMEOUT))) {
-          stop = true;
-          break;
-        }
-        if (__any_sync(0xffffffffu, ref != m)) {
-          const float f = ref == m ? 1.f : ex2(ref - m);
-          const uint32_t ff = bf16x2(f, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            pk[i] = make_uint4(mul_bf16x2(pk[i].x, ff), mul_bf16x2(pk[i].y, ff), mul_bf16x2(pk[i].z, ff),
-                               mul_bf16x2(pk[i].w, ff));
-        }
-        uint8_t* to = ptiles + ps * kQTile + r * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(to + ((i ^ (r & 7)) * 16)) = pk[i];
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[ps]);
-        if (g + 1 < nch) load_p(g + 1);
-      }
-      if (!stop)
-        stop = !__all_sync(0xffffffffu, mbar_wait(o_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT) && *abort_flag == 0);
-      if (!stop) {
-        tc_fence_after();
-        // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
-        // there, 16 bytes more than its length apart from the next, and sends it with one bulk copy
-        const bool live = r < a.h;
-        const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kShrinkV);
-        const bool f32 = split || a.out_dtype == DSA_F32;
-        constexpr int kRowBytes = 1024;
-        uint8_t* mine = ring + r * (kRowBytes + 16);
-        char* out = split ? reinterpret_cast<char*>(a.part_o + ((int64_t)piece * rows_all + row0 + r) * kDc)
-                          : static_cast<char*>(a.out) + (row0 + r) * kDc * (f32 ? 4 : 2);
-        for (int c = 0; c < 16; ++c) {
-          uint32_t o[32];
-          __syncwarp();  // the load is the whole warp's
-          tmem_ld32(lane_base + 32 * c, o);
-          if (f32) {
-            float4* dst = reinterpret_cast<float4*>(mine) + 8 * (c & 7);
+          if (__any_sync(0xffffffffu, ref != m)) {
+            const float f = ref == m ? 1.f : ex2(ref - m);
+            const uint32_t ff = bf16x2(f, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                   __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(mine) + 4 * c;
+              pk[i] = make_uint4(mul_bf16x2(pk[i].x, ff), mul_bf16x2(pk[i].y, ff), mul_bf16x2(pk[i].z, ff),
+                                 mul_bf16x2(pk[i].w, ff));
+          }
+          uint8_t* to = ptiles + ps * kQTile + r * 128;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(to + ((i ^ (r & 7)) * 16)) = pk[i];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[ps]);
+          if (g + 1 < nch) load_p(g + 1);
+        }
+        if (!stop)
+          stop = !__all_sync(0xffffffffu, mbar_wait(o_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT) && *abort_flag == 0);
+        if (!stop) {
+          tc_fence_after();
+          // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
+          // there, 16 bytes more than its length apart from the next, and sends it with one bulk copy
+          const bool live = r < a.h;
+          const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kShrinkV);
+          const bool f32 = split || a.out_dtype == DSA_F32;
+          constexpr int kRowBytes = 1024;
+          uint8_t* mine = ring + r * (kRowBytes + 16);
+          char* out = split ? reinterpret_cast<char*>(a.part_o + ((int64_t)piece * rows_all + row0 + r) * kDc)
+                            : static_cast<char*>(a.out) + (row0 + r) * kDc * (f32 ? 4 : 2);
+          for (int c = 0; c < 16; ++c) {
+            uint32_t o[32];
+            __syncwarp();  // the load is the whole warp's
+            tmem_ld32(lane_base + 32 * c, o);
+            if (f32) {
+              float4* dst = reinterpret_cast<float4*>(mine) + 8 * (c & 7);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                     __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(mine) + 4 * c;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            if (c == 15 || (f32 && c == 7)) {
+              fence_proxy_async_smem();  // our writes, seen by the bulk copy
+              if (live)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 reinterpret_cast<uint64_t>(out + (f32 && c == 15 ? kRowBytes : 0))),
+                             "r"(smem_u32(mine)), "r"(kRowBytes)
+                             : "memory");
+              asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
             }
           }
-          if (c == 15 || (f32 && c == 7)) {
-            fence_proxy_async_smem();  // our writes, seen by the bulk copy
-            if (live)
-              asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                               reinterpret_cast<uint64_t>(out + (f32 && c == 15 ? kRowBytes : 0))),
-                           "r"(smem_u32(mine)), "r"(kRowBytes)
-                           : "memory");
-            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+          if (live) {
+            if (split) a.part_ml[(int64_t)piece * rows_all + row0 + r] = make_float2(fmaxf(m, -FLT_MAX), l);
+            else if (a.lse) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           }
         }
-        if (live) {
-          if (split) a.part_ml[(int64_t)piece * rows_all + row0 + r] = make_float2(fmaxf(m, -FLT_MAX), l);
-          else if (a.lse) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        }
       }
+      if (!finish(it)) break;
     }
-    if (nch == 0 && warp == kMmaWarp) mbar_wait_drain(q_staged, turn);  // (nobody else waited for the query)
-    turn ^= 1;
-    if (nch) full_turn ^= 1;
-    done += nch;
-    tc_fence_before();
-    cta_sync();
-    if (*abort_flag) break;  // (no wait is under way that could set it now)
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   if (warp == kMmaWarp) {
@@ -715,7 +767,17 @@ int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
   static std::atomic<bool> allowed[64];
   rc = allow_smem<kSmem>(attn4_tc_kernel, allowed, "attn4_tc: smem attribute");
   if (rc != DSA_OK) return rc;
+  // (a kernel built with other registers would wait forever for those it sets)
+  static std::atomic<int> regs{0};
   cudaError_t e = cudaSuccess;
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, attn4_tc_kernel);
+    if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
+    regs.store(attr.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs)
+    return set_error(DSA_ERR_UNSUPPORTED, "attn4_tc: built with %d registers, not %d", regs.load(), kLaunchRegs);
   DSA_LAUNCH("attn4_tc", stream,
              e = launch_pdl(attn4_tc_kernel, dim3((unsigned)ctas_of(a)), dim3(kThreads), kSmem, stream, p, qmap));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
