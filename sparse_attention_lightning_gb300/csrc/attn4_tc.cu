@@ -54,14 +54,16 @@ constexpr int kGroups = 2, kDecoders = 8;  // groups of decoding warps, which ta
 constexpr int kMmaWarp = kSoftWarps + kGroups * kDecoders;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole groups of four warps: their registers are set together)
 // Registers a thread of softmax, of the decoders, of the MMA's four warps; together at most what the block is launched with.
+constexpr int kParts = (kSoftWarps + kGroups * kDecoders) / 4;  // warps that take a quarter of the heads to tensor memory
 constexpr int kLaunchRegs = 80, kSoftRegs = 136, kDecodeRegs = 72, kMmaRegs = 56;
 static_assert(128 * kSoftRegs + 32 * kGroups * kDecoders * kDecodeRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "registers");
 constexpr int kRing = kVSlots * kVSlot + kPSlots * kQTile;
-constexpr int kBarBytes = 512;
-constexpr int kSmem = kRing + kGroups * kRaw + kBarBytes + 1024;
+constexpr int kBarBytes = 512, kTopBytes = 2 * kM * 4;
+constexpr int kSmem = kRing + kGroups * kRaw + kBarBytes + kTopBytes + 1024;
 constexpr int kQCol = 0, kSCol = kD / 2;   // tensor memory of phase 1: 288 query columns, the logits; of phase 2: O
 constexpr int kRopeAt = kv4_rope_at(kDc), kScaleAt = kv4_scale_at(kDc, kDr);
 constexpr float kGrowLog2 = 8.0f;
+constexpr int kNoQuery = 1 << 20;
 constexpr int kMostRows = 2048;            // entries of a query
 constexpr int64_t kPBytes = kM * kN * 2, kRefBytes = kM * 4, kListBytes = kN * 4;  // scratch of a chunk
 static_assert(kSmem <= 232448, "shared memory");
@@ -241,6 +243,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kBars + 1);
   int* counts = reinterpret_cast<int*>(bars + kBars + 2);  // [warps] entries of a warp's share
+  uint32_t* tops = reinterpret_cast<uint32_t*>(bars + kBarBytes / 8);  // [2][128] largest magnitude of a head's latent, rope columns
   static_assert((kBars + 2) * 8 + kThreads / 32 * 4 <= kBarBytes, "barriers");
 
   const int live_warps = (a.h + 31) / 32;  // of the softmax: the others' rows are no head's
@@ -251,7 +254,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     for (int i = 0; i < kVSlots; ++i) { mbar_init(&v_full[i], kDecoders); mbar_init(&v_empty[i], 1); }
     for (int i = 0; i < kPSlots; ++i) { mbar_init(&p_full[i], live_warps); mbar_init(&p_empty[i], 1); }
     mbar_init(q_staged, 1);
-    mbar_init(qt_full, live_warps);
+    mbar_init(qt_full, live_warps * kParts);
     mbar_init(o_full, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -260,6 +263,10 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   float* const refs = reinterpret_cast<float*>(scratch + (int64_t)p.most * kPBytes);  // [chunk][128]
 
   int32_t* const list = reinterpret_cast<int32_t*>(refs + (int64_t)p.most * kM);  // cache rows of the entries, without those skipped
+  tc_fence_before();
+  block_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   // The barriers' phases go on from item to item: chunks so far, the parity of the items and of those that had any.
   uint32_t done = 0, turn = 0, full_turn = 0;
   // An item's row, its entries' chunks; one without entries is written here.
@@ -273,23 +280,23 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)it.row0);
     }
     __syncwarp();
-    RowInfo ri;
-    const bool good = warp_query_row(a, it.t, lane, ri);
     const int c0 = (int)((int64_t)p.chunks * it.piece / a.splits), c1 = (int)((int64_t)p.chunks * (it.piece + 1) / a.splits);
     const int32_t* idx = a.idx + (int64_t)it.t * a.top_k;
     const int end = min(a.top_k, c1 * kN);
     // The piece's entries as cache rows, without the skipped ones (a short history's row is mostly -1): a warp takes
-    // consecutive ones, all its loads at once.
+    // consecutive ones, all its loads at once, ahead of the row's lookup.
     constexpr int kWarps = kThreads / 32, kMine = (kMostRows + 32 * kWarps - 1) / (32 * kWarps);
+    const int per_warp = (end - c0 * kN + 32 * kWarps - 1) / (32 * kWarps);  // at most kMine
     int row[kMine], mine = 0;
-    if (good) {
-      const int per = (end - c0 * kN + 32 * kWarps - 1) / (32 * kWarps);  // at most kMine
-      const int e0 = c0 * kN + warp * per * 32;
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        const int e = e0 + j * 32 + lane;
-        row[j] = j < per && e < end ? idx[e] : -1;
-      }
+    for (int j = 0; j < kMine; ++j) {
+      const int e = c0 * kN + (warp * per_warp + j) * 32 + lane;
+      row[j] = j < per_warp && e < end ? idx[e] : -1;
+    }
+    if (threadIdx.x < 2 * kM) tops[threadIdx.x] = 0u;
+    RowInfo ri;
+    const bool good = warp_query_row(a, it.t, lane, ri);
+    if (good) {
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         const int v = row[j];
@@ -327,6 +334,70 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     for (int i = threadIdx.x; !split && i < a.h * per; i += kThreads)
       reinterpret_cast<uint4*>(a.out)[it.row0 * per + i] = make_uint4(0u, 0u, 0u, 0u);
   };
+  // The query to tensor memory, by all warps but the MMA's: those of a quarter of the heads (each warp can write to one) take a few
+  // of the column tiles each.  The latent columns go to fp16, times the power of two that brings the head's largest finite one into
+  // [2^14, 2^15) (what is 2^-29 of it begins to lose bits, far below the logits' own rounding); the rope columns get the same
+  // factor, which is held where they stay within bf16's range.  The factor's exponent, or kNoQuery (a wait was given up).
+  auto stage_query = [&](int quarter, int part) -> int {
+    const int r = quarter * 32 + lane;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(q_staged, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT));
+    const bool mine = ok && quarter < live_warps;
+    const uint8_t* const row = ring + r * 128;
+    auto piece = [&](int j, int i) { return *reinterpret_cast<const uint4*>(row + j * kQTile + ((i ^ (r & 7)) * 16)); };
+    for (int j = part; mine && j < kTiles; j += kParts) {
+      uint32_t t = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 v = piece(j, i);
+        t = max_bf16x2(max_bf16x2(t, v.x & 0x7fff7fffu),
+                       max_bf16x2(v.y & 0x7fff7fffu, max_bf16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+      if (__any_sync(0xffffffffu, finite_pair(t) != t)) {  // infinities: once more without them (the maximum passes NaNs over)
+        t = 0u;
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = piece(j, i);
+          t = max_bf16x2(t, max_bf16x2(max_bf16x2(finite_pair(v.x & 0x7fff7fffu), finite_pair(v.y & 0x7fff7fffu)),
+                                       max_bf16x2(finite_pair(v.z & 0x7fff7fffu), finite_pair(v.w & 0x7fff7fffu))));
+        }
+      }
+      atomicMax(&tops[(j == kVTiles ? kM : 0) + r], max(t & 0x7fffu, t >> 16 & 0x7fffu));
+    }
+    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kMmaWarp) : "memory");
+    if (!ok) return kNoQuery;
+    const int e0 = (int)(tops[r] >> 7) - 127, e1 = (int)(tops[kM + r] >> 7) - 127;  // (0 and subnormal: -127)
+    const int shift = min(max(e0 == -127 ? 0 : e0 - 14, max(e1 - 100, -100)), 113);
+    const float down = __uint_as_float((uint32_t)(127 - shift) << 23);
+    const uint32_t two = (uint32_t)(127 - shift) * 0x00800080u;  // the same twice in bf16
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    for (int j = part; mine && j < kTiles; j += kParts) {
+      uint32_t w[32];
+      if (j < kVTiles) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = piece(j, i);
+          auto lo = [&](uint32_t u) { return __uint_as_float(u << 16) * down; };
+          auto hi = [&](uint32_t u) { return __uint_as_float(u & 0xffff0000u) * down; };
+          w[4 * i] = f16x2(lo(v.x), lo(v.y));
+          w[4 * i + 1] = f16x2(lo(v.z), lo(v.w));
+          w[4 * i + 2] = f16x2(hi(v.x), hi(v.y));
+          w[4 * i + 3] = f16x2(hi(v.z), hi(v.w));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = piece(j, i);
+          w[4 * i] = mul_bf16x2(v.x, two); w[4 * i + 1] = mul_bf16x2(v.y, two);
+          w[4 * i + 2] = mul_bf16x2(v.z, two); w[4 * i + 3] = mul_bf16x2(v.w, two);
+        }
+      }
+      __syncwarp();
+      tmem_st32(lane_base + kQCol + j * 32, w);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (mine && lane == 0) mbar_arrive(qt_full);
+    return shift;
+  };
   // False: a wait was given up.  (None is under way that could be now.)
   auto finish = [&](const Item& it) -> bool {
     if (it.nch == 0 && warp == kMmaWarp) mbar_wait_drain(q_staged, turn);  // (nobody else waited for the query)
@@ -337,10 +408,6 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     block_sync();
     return *abort_flag == 0;
   };
-  tc_fence_before();
-  block_sync();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
@@ -431,7 +498,8 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           }
         };
         if (steps) gather(0);
-        for (int i = 0; i < steps; ++i) {
+        bool stop = stage_query(warp & 3, 1 + (warp - kSoftWarps) / 4) == kNoQuery;
+        for (int i = 0; !stop && i < steps; ++i) {
           const int n = i < count ? chunk_of(i) : nch + chunk_of(i);  // phase 1: [0, nch), phase 2: [nch, 2 nch)
           asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
@@ -504,75 +572,12 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       const int nch = it.nch, total = it.total;
       const int piece = it.piece;
       const int64_t row0 = it.row0;
-      if (nch && warp < live_warps) {
+      if (nch) {
         // ---------------- softmax: thread = head ----------------
         const int r = warp * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        int shift = 0;  // the row's logits are 2^shift times what its operands say
-        bool stop = !__all_sync(0xffffffffu, mbar_wait(q_staged, turn, abort_flag, a.status, DSA_FLAG_TIMEOUT));
-        if (!stop) {
-          // The latent columns go to fp16, times the power of two that brings the row's largest finite one into [2^14, 2^15) (what is
-          // 2^-29 of it begins to lose bits, far below the logits' own rounding); the rope columns get the same factor, which is held where
-          // they stay within bf16's range.
-          const uint8_t* const row = ring + r * 128;
-          auto piece = [&](int j, int i) { return *reinterpret_cast<const uint4*>(row + j * kQTile + ((i ^ (r & 7)) * 16)); };
-          uint32_t top[2] = {0u, 0u}, odd = 0u;
-#pragma unroll 1
-          for (int j = 0; j < kTiles; ++j) {
-            uint32_t t = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = piece(j, i);
-              t = max_bf16x2(max_bf16x2(t, v.x & 0x7fff7fffu), max_bf16x2(v.y & 0x7fff7fffu, max_bf16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-            }
-            if (finite_pair(t) != t) odd = 1u;  // (the maximum passes NaNs over)
-            top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
-          }
-          if (__any_sync(0xffffffffu, odd)) {  // infinities: once more without them
-            top[0] = top[1] = 0u;
-            for (int j = 0; j < kTiles; ++j)
-              for (int i = 0; i < 8; ++i) {
-                const uint4 v = piece(j, i);
-                const uint32_t t = max_bf16x2(max_bf16x2(finite_pair(v.x & 0x7fff7fffu), finite_pair(v.y & 0x7fff7fffu)),
-                                              max_bf16x2(finite_pair(v.z & 0x7fff7fffu), finite_pair(v.w & 0x7fff7fffu)));
-                top[j == kTiles - 1] = max_bf16x2(top[j == kTiles - 1], t);
-              }
-          }
-          auto exponent = [](uint32_t t) { return (int)(max(t & 0x7fffu, t >> 16 & 0x7fffu) >> 7) - 127; };  // (0 and subnormal: -127)
-          const int e0 = exponent(top[0]), e1 = exponent(top[1]);
-          shift = min(max(e0 == -127 ? 0 : e0 - 14, max(e1 - 100, -100)), 113);
-          const float down = __uint_as_float((uint32_t)(127 - shift) << 23);
-          const uint32_t down_bf16 = (uint32_t)(127 - shift) << 7;
-#pragma unroll 1
-          for (int j = 0; j < kVTiles; ++j) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = piece(j, i);
-              auto lo = [&](uint32_t u) { return __uint_as_float(u << 16) * down; };
-              auto hi = [&](uint32_t u) { return __uint_as_float(u & 0xffff0000u) * down; };
-              w[4 * i] = f16x2(lo(v.x), lo(v.y));
-              w[4 * i + 1] = f16x2(lo(v.z), lo(v.w));
-              w[4 * i + 2] = f16x2(hi(v.x), hi(v.y));
-              w[4 * i + 3] = f16x2(hi(v.z), hi(v.w));
-            }
-            tmem_st32(lane_base + kQCol + j * 32, w);
-          }
-          {
-            const uint32_t two = down_bf16 | down_bf16 << 16;
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = piece(kVTiles, i);
-              w[4 * i] = mul_bf16x2(v.x, two); w[4 * i + 1] = mul_bf16x2(v.y, two);
-              w[4 * i + 2] = mul_bf16x2(v.z, two); w[4 * i + 3] = mul_bf16x2(v.w, two);
-            }
-            tmem_st32(lane_base + kQCol + kVTiles * 32, w);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(qt_full);
-        }
+        const int shift = stage_query(warp & 3, 0);  // the row's logits are 2^shift times what its operands say
+        bool stop = shift == kNoQuery || warp >= live_warps;  // (the others' rows are no head's)
         const float scale = a.scale_log2 * (1.f / kShrinkK) * __uint_as_float((uint32_t)(127 + shift) << 23);
         float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
         uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
