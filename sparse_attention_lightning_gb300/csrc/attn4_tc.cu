@@ -6,28 +6,30 @@
 // goes over its entries twice, 64 at a time:
 //   phase 1, logits:  S = Q·Kᵀ (M=128, N=64, K=576), p = 2^(S − m) to a scratch of the CTA (16 KB a chunk, in L2)
 //   phase 2, values:  O += P·V (M=128, N=2·256, K=64)
-// Why twice.  A 128 x 512 fp32 accumulator is all of the tensor memory, so logits and values do not fit it together.
-// In one pass two CTAs a query, each with half the values, had to compute the logits twice, from a query of which most was
-// in shared memory (6 KB of operands an MMA, 128 B a clock): operands and decoded rows of a chunk took 285 KB of
-// shared-memory traffic in each of them, 2,230 clocks, where its MMAs needed 2,020, and the two together 7,000 clocks a chunk.
-// Apart, the query's 288 columns and three logit buffers fill the tensor memory in phase 1 and the accumulator does in
-// phase 2, nothing is computed twice (2,212 clocks of MMAs), and a chunk's traffic is 173 and 202 KB.  The price is that rows are decoded
-// twice (416 bytes of a row come from L2 the second time) and P goes through L2.
+// Why twice.  A 128 x 512 fp32 accumulator is all of the tensor memory, so logits and values do not fit it together.  (The first
+// form was one pass by two CTAs a query, each with half the values, both with the whole logits from a query of which five
+// ninths were in shared memory: 3,500 clocks a chunk in each of the two.)  Apart, the query's 288 columns and three logit buffers fill the
+// tensor memory in phase 1, the accumulator does in phase 2, and nothing is multiplied twice: 2,212 clocks of MMAs a chunk.  The
+// price is that rows are copied and decoded twice and P goes through L2.
+//
+// What bounds it: not the MMAs (taking all but one of a chunk's out changes nothing), but the way of a chunk through
+// gather, decoding, softmax and their hand-overs, some 4,200 clocks for both phases: instructions (54 % of the issue slots), 1,152
+// clocks of operand stores, and the chains of waits between the roles.  1,024 queries of 2,048 entries, 128 heads: 534 us
+// (0.58 of the MMAs' floor), with one pass 890.  Steps on the way there: rows gathered by TMA, four 416-byte rows a copy (87
+// clocks each: 730), by 16-byte asynchronous copies of the decoding warps (662), scales two at a time (618), fp16 logits (591), decoding in two groups
+// (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.
 //
 // The running maximum m of a head only decides the scale of p: it is a whole number (of log2), moves when a chunk's maximum is more than
 // 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which is exact, instead of rescaling O.
 // The sum is in fp32 of the unrounded p.  P is rounded to bf16, which the MMA wants beside bf16 values: 2^-8 of each p at
 // most, in either direction.
 //
-// Eight warps gather and decode.  A row is 416 bytes, so the gather goes through registers, a chunk ahead: a lane takes one
-// row (eight rows a warp) and, of it, 32 bytes of codes (64 columns) twice and 32 of rope columns,
-// and stores what they decode to in the MMA's operand layout.  A quarter warp's eight lanes hold eight different rows, whose 16-byte
-// stores the 128-byte swizzle spreads over all banks.  Decoding is two shifts, two logical operations and a product for
-// a pair of columns (kv4.cuh): the operand is the value times 2^-16, exactly, which the logits' scale and the output make good;
-// rope columns get the same factor.
+// Roles of a CTA's 24 warps: four take the softmax, a thread a head; sixteen gather and decode, in two groups that take
+// the chunks in turn; one issues the MMAs (its warp group's other three only look up entries).  The CTAs are persistent, one an SM.  An item begins
+// with its entries looked up by all warps (cache rows, without skipped entries, to a list in L2) while its query is loaded.
 //
-// Shared memory: three chunks of nine tiles of [64 keys x 64 columns] in phase 1, two of eight and four P tiles in phase 2.
-// Every wait is bounded (DSA_FLAG_TIMEOUT).
+// Shared memory: two chunks of nine tiles of [64 keys x 64 columns] in phase 1, four halves of a chunk and two P tiles in
+// phase 2; a stage of gathered rows a group.  Every wait is bounded (DSA_FLAG_TIMEOUT).
 #include <float.h>
 
 #include "kv4.cuh"
@@ -53,8 +55,8 @@ constexpr int kSoftWarps = 4;
 constexpr int kGroups = 2, kDecoders = 8;  // groups of decoding warps, which take the chunks in turn
 constexpr int kMmaWarp = kSoftWarps + kGroups * kDecoders;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole groups of four warps: their registers are set together)
-// Registers a thread of softmax, of the decoders, of the MMA's four warps; together at most what the block is launched with.
 constexpr int kParts = (kSoftWarps + kGroups * kDecoders) / 4;  // warps that take a quarter of the heads to tensor memory
+// Registers a thread of softmax, of the decoders, of the MMA's four warps; together at most what the block is launched with.
 constexpr int kLaunchRegs = 80, kSoftRegs = 136, kDecodeRegs = 72, kMmaRegs = 56;
 static_assert(128 * kSoftRegs + 32 * kGroups * kDecoders * kDecodeRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "registers");
 constexpr int kRing = kVSlots * kVSlot + kPSlots * kQTile;
@@ -180,12 +182,13 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// The largest finite magnitude among pairs of bf16 whose signs are cleared (an infinity or a NaN counts as 0).
+// The larger of pairs of bf16 (a NaN is passed over).
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// A pair of bf16 magnitudes with 0 for an infinity or a NaN.
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
   if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;

@@ -387,6 +387,86 @@ def test_extreme_scales_and_logits(h):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("h,top_k", [(128, 70), (40, 200), (16, 513)])
+def test_more_queries_than_sms(h, top_k):
+    """Several queries a CTA one after another: full rows, short ones, rows without an entry, in every order."""
+    s = Setup([300, 1, 90], [300, 40, 700], h, dtype=BF, top_k=top_k, page=64, seed=h, spread=2.0, **FULL)
+    idx = s.draw_idx()
+    g = torch.Generator().manual_seed(1)
+    idx[torch.rand(idx.shape[0], generator=g) < 0.3] = -1
+    idx[5:340:7, 3:] = -1
+    out, lse = s.attend(idx)
+    s.check(out, lse, idx, rows=set(range(0, 391, 3)) | {390})
+    for _ in range(3):
+        again, lse2 = s.attend(idx)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h", [128, 16])
+def test_queries_of_any_magnitude(h):
+    """Heads of zeros, of subnormal and of huge numbers, of widely spread ones, latent and rope columns apart; infinities and NaNs
+    stay in their head."""
+    s = Setup([1], [150], h, dtype=BF, top_k=130, seed=12, **FULL)
+    q = s.q.float()[0]
+    wide = torch.exp2(torch.rand(h, 576, generator=s.g) * 60 - 50)
+    q[1] = 0
+    q[2] *= 2.0 ** -130
+    q[3] *= 2.0 ** 14
+    q[4] *= wide[4]
+    q[5, :512], q[5, 512:] = q[5, :512] * 2.0 ** -60, q[5, 512:]
+    q[6, :512], q[6, 512:] = q[6, :512], q[6, 512:] * 2.0 ** -60
+    q[7, :512], q[7, 512:] = 0, q[7, 512:] * 2.0
+    q[8, 7:] = 0
+    odd = {9: ("nan", 3), 10: ("inf", 100), 11: ("-inf", 511), 12: ("nan", 540), 13: ("inf", 575)}
+    for head, (v, c) in odd.items():
+        q[head, c] = float(v)
+    s.q = q.bfloat16()[None]
+    idx = s.draw_idx()
+    out, lse = s.attend(idx)
+    keys = K.decode(s.host[s.at[0]], 512, 64)[idx[0].numpy()]
+    for head, (v, c) in odd.items():
+        nan = v == "nan" or (keys[:, c] * (1 if v == "inf" else -1) > 0).any() or (keys[:, c] == 0).any()
+        assert bool(torch.isnan(out[0, head]).all()) == bool(nan), head
+    rest = [i for i in range(h) if i not in odd]
+    q64 = s.q[0].double().numpy()[rest]
+    ro, rl, mag, top = C.attend(q64, keys, 512, s.scale)
+    delta = 578 * 2.0 ** -24 * top
+    rel = 2 * delta + 130 * 2.0 ** -24 + 2.0 ** -20
+    err = np.abs(out[0].float().cpu().double().numpy()[rest] - ro)
+    assert np.all(err <= (rel[:, None] + 2.0 ** -8) * mag * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ro) + 1e-38)
+    assert np.all(np.abs(lse[0].cpu().double().numpy()[rest] - rl) <= delta + 138 * 2.0 ** -24 + 2.0 ** -20 * (1 + np.abs(rl)))
+
+
+@pytest.mark.gpu
+def test_no_queries():
+    import sparse_attention_lightning_gb300 as dsa
+    s = Setup([0, 0], [30, 5], 128, dtype=BF, top_k=16, seed=3, **FULL)
+    out, lse = s.attend(torch.empty(0, 16, dtype=torch.int32))
+    assert out.shape == (0, 128, 512) and lse.shape == (0, 128)
+    before = s.kv4.clone()
+    none = torch.empty(0, 576).bfloat16().cuda()
+    dsa.write_kv4(s.prob, none[:, :512], none[:, 512:], s.kv4)
+    assert torch.equal(s.kv4, before) and dsa.read_kv4(s.prob, s.kv4).shape == (35, 576)
+
+
+@pytest.mark.gpu
+def test_checked_build_raises_no_flag_and_matches():
+    import sparse_attention_lightning_gb300 as dsa
+    from sparse_attention_lightning_gb300 import build
+    build.build(checked=True)
+    for h, dims, dtype in ((128, FULL, BF), (16, FULL, BF), (4, dict(d_c=64, d_rope=16), F32)):
+        s = Setup([3, 1, 30], [700, 2500, 90], h, dtype=dtype, top_k=333, page=64, seed=h, **dims)
+        idx = s.draw_idx(holes=0.2)
+        want = s.attend(idx)
+        with _abi.using(_abi.CHECKED_LIB_PATH):
+            ws = dsa.Workspace()
+            got = s.attend(idx, ws=ws)
+            assert ws.status() == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
 def test_bad_sequences_are_reported():
     import sparse_attention_lightning_gb300 as dsa
     for h, dtype, dims in ((128, BF, FULL), (4, F32, dict(d_c=64, d_rope=16))):
