@@ -12,6 +12,7 @@ rotate_axes, write_kv4, read_kv4, sparse_mla_attn4, fork_pages, free_pages, rese
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import threading
@@ -971,15 +972,16 @@ def _entries(named, index: int) -> int:
 
 
 def _cache_list(caches, rows: int, index: int):
-    """Addresses and row bytes of caches with `rows` rows."""
-    n = len(caches)
-    at, size = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
-    for i, t in enumerate(caches):
-        if t.dim() < 1 or t.shape[0] != rows or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"caches[{i}] must be a contiguous tensor of {rows} rows on cuda:{index}")
-        at[i] = t.data_ptr()
-        size[i] = t.numel() // rows * t.element_size()
-    return n, at, size
+    """(number, their addresses, their row bytes) of caches with `rows` rows: one array, kept by the caller while its
+    address is in use."""
+    at, size = [], []
+    for t in caches:
+        shape = t.shape
+        if not shape or shape[0] != rows or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"caches[{len(at)}] must be a contiguous tensor of {rows} rows on cuda:{index}")
+        at.append(t.data_ptr())
+        size.append(t.nbytes // rows)
+    return len(at), array.array("q", at + size)
 
 
 _page_ws = {}  # workspace bytes by (rows, entries, pages)
@@ -1052,15 +1054,16 @@ def reserve_pages(table, refs, rows, lens, new_lens, page_size: int, caches=(), 
         return _elsewhere(index, reserve_pages, table, refs, rows, lens, new_lens, page_size, caches, held, ws)
     at, num, width, ld = _pages_of(table, refs, index)
     n = _entries((("rows", rows), ("lens", lens), ("new_lens", new_lens)), index)
-    count, addresses, sizes = _cache_list(caches, refs.shape[0] * page_size, index)
+    count, listed = _cache_list(caches, refs.shape[0] * page_size, index)
     if held is None:
         held = torch.empty((n,), dtype=torch.int32, device=table.device)
     else:
         _want(held, "held", _I32, (n,), index)
+    listed_at = listed.buffer_info()[0]
     stream = _raw_stream(index)
     ws = _pages_ws(ws, index, stream, num, n, refs.shape[0])
     rc = lib().dsa_reserve_pages(at, num, width, ld, refs.data_ptr(), refs.shape[0], page_size, n, rows.data_ptr(),
-                                 lens.data_ptr(), new_lens.data_ptr(), held.data_ptr(), count, addresses, sizes,
+                                 lens.data_ptr(), new_lens.data_ptr(), held.data_ptr(), count, listed_at, listed_at + 8 * count,
                                  ws.buf.data_ptr(), ws.nbytes, stream)
     if rc:
         _abi.check(rc)
@@ -1079,7 +1082,7 @@ def compact_pages(table, refs, page_size: int, caches=(), moved=None, live=None,
         return _elsewhere(index, compact_pages, table, refs, page_size, caches, moved, live, ws)
     at, num, width, ld = _pages_of(table, refs, index)
     pages = refs.shape[0]
-    count, addresses, sizes = _cache_list(caches, pages * page_size, index)
+    count, listed = _cache_list(caches, pages * page_size, index)
     if moved is None:
         moved = torch.empty((pages,), dtype=torch.int32, device=table.device)
     else:
@@ -1088,10 +1091,11 @@ def compact_pages(table, refs, page_size: int, caches=(), moved=None, live=None,
         live = torch.empty((1,), dtype=torch.int32, device=table.device)
     else:
         _want(live, "live", _I32, (1,), index)
+    listed_at = listed.buffer_info()[0]
     stream = _raw_stream(index)
     ws = _pages_ws(ws, index, stream, num, 0, pages)
     rc = lib().dsa_compact_pages(at, num, width, ld, refs.data_ptr(), pages, page_size, moved.data_ptr(), live.data_ptr(),
-                                 count, addresses, sizes, ws.buf.data_ptr(), ws.nbytes, stream)
+                                 count, listed_at, listed_at + 8 * count, ws.buf.data_ptr(), ws.nbytes, stream)
     if rc:
         _abi.check(rc)
     return moved, live

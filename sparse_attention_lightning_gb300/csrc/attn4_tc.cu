@@ -19,8 +19,9 @@
 // clocks each: 730), by 16-byte asynchronous copies of the decoding warps (662), scales two at a time (618), fp16 logits (591), decoding in two groups
 // (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.
 //
-// The running maximum m of a head only decides the scale of p: it is a whole number (of log2), moves when a chunk's maximum is more than
-// 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which is exact, instead of rescaling O.
+// The running maximum m of a head only decides the scale of p: it starts as the first chunk's, moves by whole numbers (of log2) when a
+// chunk's maximum is more than 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which is exact,
+// instead of rescaling O.
 // The sum is in fp32 of the unrounded p.  P is rounded to bf16, which the MMA wants beside bf16 values: 2^-8 of each p at
 // most, in either direction.
 //
@@ -582,7 +583,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
         const int shift = stage_query(warp & 3, 0);  // the row's logits are 2^shift times what its operands say
         bool stop = shift == kNoQuery || warp >= live_warps;  // (the others' rows are no head's)
         const float scale = a.scale_log2 * (1.f / kShrinkK) * __uint_as_float((uint32_t)(127 + shift) << 23);
-        float m = -INFINITY, l = 0.f;  // the reference (log2 units, whole) and the sum relative to it
+        float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum relative to it
         uint4* const pbuf = reinterpret_cast<uint4*>(scratch) + r;  // piece i of chunk g at [(8 g + i) · 128]
         for (int g = 0; g < nch && !stop; ++g) {
           const uint32_t n = done + g, sb = n % kSBufs;
@@ -607,7 +608,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
           const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           if (mc > m + kGrowLog2) {  // the first entries always (m = -inf)
-            const float m_new = ceilf(mc);
+            const float m_new = m == -INFINITY ? mc : m + ceilf(mc - m);
             l *= ex2(m - m_new);
             m = m_new;
           }
