@@ -265,7 +265,6 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   }
   uint8_t* const scratch = a.scratch + (int64_t)blockIdx.x * p.most * (kPBytes + kRefBytes + kListBytes);
   float* const refs = reinterpret_cast<float*>(scratch + (int64_t)p.most * kPBytes);  // [chunk][128]
-
   int32_t* const list = reinterpret_cast<int32_t*>(refs + (int64_t)p.most * kM);  // cache rows of the entries, without those skipped
   tc_fence_before();
   block_sync();
@@ -520,8 +519,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
 #pragma unroll
             for (int j = 0; j < 2; ++j) rope[j] = *reinterpret_cast<const uint4*>(src + kRopeAt + 16 * (2 * j + grp + 4 * pair));
           }
-          asm volatile("" : "+r"(v[0].x), "+r"(v[1].x), "+r"(v[2].x), "+r"(v[3].x), "+r"(sc[0]), "+r"(sc[1]), "+r"(sc[2]), "+r"(sc[3]) :: "memory");
-          __syncwarp();  // the stage has been read
+          __syncwarp();  // the stage has been read (a warp's loads of shared memory are served in order, ahead of the copies)
           if (i + 1 < steps) gather(i + 1);
           if (n < nch) {
             const uint32_t kn = done + n, ks = kn % kKSlots;

@@ -904,7 +904,7 @@ int dsa_rotate_axes(int64_t tokens, int32_t heads, int32_t d, int32_t dtype, int
                     const int32_t* positions, int64_t ld_pos, const void* x, int64_t x_token,
                     int64_t x_head, void* out, int64_t out_token, int64_t out_head, void* stream) {
   if (dtype != DSA_F32 && dtype != DSA_BF16) return set_error(DSA_ERR_INVALID_ARG, "dtype = %d (F32 or BF16)", dtype);
-  if (tokens < 0 || heads < 1 || axes < 1 || axes > 255 || ld_pos < tokens)
+  if (tokens < 0 || heads < 1 || axes < 1 || axes > 255 || (ld_pos != 0 && ld_pos < tokens))
     return set_error(DSA_ERR_INVALID_ARG, "tokens = %lld, heads = %d, axes = %d, ld_pos = %lld", (long long)tokens, heads,
                      axes, (long long)ld_pos);
   if (d < 2 || d > 2 * kMaxPairs || d % 2) return set_error(DSA_ERR_UNSUPPORTED, "d = %d (2..256, even)", d);

@@ -47,7 +47,7 @@ def test_argument_checks():
 
     assert call(T=-1) == bad and call(H=0) == bad and call(dt=2) == bad and call(axes=0) == bad and call(axes=256) == bad
     assert call(d=63) == unsup and call(d=0) == unsup and call(d=258) == unsup
-    assert call(ld=3) == bad and call(turn=None) == bad and call(axis=None) == bad
+    assert call(ld=3) == bad and call(ld=-1) == bad and call(turn=None) == bad and call(axis=None) == bad
     assert call(axis=(ctypes.c_uint8 * 128)(0, 1)) == bad          # an axis without positions
     assert call(x=None) == bad and call(out=None) == bad and call(x=A + 1) == bad and call(pos=None) == bad
     assert call(pos=(1 << 30) + 2) == bad and call(xt=-1) == bad and call(oh=-64) == bad
@@ -150,6 +150,9 @@ def test_layouts(dtype):
     x = torch.randn(37, 1, 16, generator=g).to(dtype)
     y = dsa.rotate_axes(x.cuda().expand(37, 5, 16), strided, rot)
     check(y, x.expand(37, 5, 16), pos, *args)
+    same = pos[:1].expand(2, 37)  # text: every axis has the token's position
+    y = dsa.rotate_axes(x.cuda(), pos[:1].cuda().expand(2, 37), rot)
+    check(y, x, same, *args)
 
 
 @pytest.mark.gpu
