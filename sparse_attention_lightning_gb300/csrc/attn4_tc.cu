@@ -2,7 +2,7 @@
 //
 //   S_i = scale · q[t,h,:]·kv[row_i, :],  out = Σ softmax(S)_i · kv[row_i, :512],  lse = log Σ exp S_i
 //
-// A query's heads are the MMA's M = 128 rows, a CTA takes a query (or a piece of its entries, merged afterwards), and
+// A query's heads are the MMA's M = 128 rows, a CTA takes a query (or a piece of its entries, joined afterwards), and
 // goes over its entries twice, 64 at a time:
 //   phase 1, logits:  S = Q·Kᵀ (M=128, N=64, K=576), p = 2^(S − m) to a scratch of the CTA (16 KB a chunk, in L2)
 //   phase 2, values:  O += P·V (M=128, N=2·256, K=64)
@@ -17,7 +17,8 @@
 // clocks of operand stores, and the chains of waits between the roles.  1,024 queries of 2,048 entries, 128 heads: 534 us
 // (0.58 of the MMAs' floor), with one pass 890.  Steps on the way there: rows gathered by TMA, four 416-byte rows a copy (87
 // clocks each: 730), by 16-byte asynchronous copies of the decoding warps (662), scales two at a time (618), fp16 logits (591), decoding in two groups
-// (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.
+// (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.  32 queries of 2,048 entries: 36.4 us
+// of four CTAs each, of which the first MMA comes after 13,000 clocks, eight chunks take 31,000 and O's way out 22,000.
 //
 // The running maximum m of a head only decides the scale of p: it starts as the first chunk's, moves by whole numbers (of log2) when a
 // chunk's maximum is more than 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which is exact,
@@ -31,7 +32,15 @@
 //
 // Shared memory: two chunks of nine tiles of [64 keys x 64 columns] in phase 1, four halves of a chunk and two P tiles in
 // phase 2; a stage of gathered rows a group.  Every wait is bounded (DSA_FLAG_TIMEOUT).
+//
+// Pieces of a query in a cluster: each CTA tells the others its heads' (m, l) after phase 1, brings its O to the common m and sum on
+// its way from tensor to shared memory, and sums up its share of the columns of all pieces from there, in their order, at 16
+// bytes a clock and CTA (192 KB: 12,000 clocks; half as fast in shares of 128 bytes; loads for several rows at once, shares kept together and a
+// share's sums while the next columns are put there were no faster).  Partial outputs through L2 and a merge in their place took 42 us
+// (the merge 13), but suit pieces shorter than an eighth.
 #include <float.h>
+
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "tc_sm100.cuh"
@@ -62,7 +71,9 @@ constexpr int kLaunchRegs = 80, kSoftRegs = 136, kDecodeRegs = 72, kMmaRegs = 56
 static_assert(128 * kSoftRegs + 32 * kGroups * kDecoders * kDecodeRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "registers");
 constexpr int kRing = kVSlots * kVSlot + kPSlots * kQTile;
 constexpr int kBarBytes = 512, kTopBytes = 2 * kM * 4;
-constexpr int kSmem = kRing + kGroups * kRaw + kBarBytes + kTopBytes + 1024;
+constexpr int kMostPieces = 8;             // of a query: CTAs of a cluster
+constexpr int kSumBytes = kMostPieces * kM * 8;
+constexpr int kSmem = kRing + kGroups * kRaw + kBarBytes + kTopBytes + kSumBytes + 1024;
 constexpr int kQCol = 0, kSCol = kD / 2;   // tensor memory of phase 1: 288 query columns, the logits; of phase 2: O
 constexpr int kRopeAt = kv4_rope_at(kDc), kScaleAt = kv4_scale_at(kDc, kDr);
 constexpr float kGrowLog2 = 8.0f;
@@ -73,12 +84,13 @@ static_assert(kSmem <= 232448, "shared memory");
 static_assert(kSCol + kSBufs * kN <= 512, "tensor memory");
 static_assert(kKSlots * kKSlot <= kRing, "phase 1's ring");
 static_assert(kTiles * kQTile <= kRing, "the query passes through the ring");
-static_assert(kM * (256 * 4 + 16) <= kRing && kM * (512 * 2 + 16) <= kRing, "the output leaves through the ring");
+constexpr int kOutRow = 1024;              // the output leaves through the ring, 256 fp32 columns of 128 heads at a time
+static_assert(kM * kOutRow <= kVSlots * kVSlot, "the output's way through the ring");
 
 struct Params {
   Attn4Args a;
   int chunks;     // of a query
-  int items;      // pieces of all queries
+  int items;      // queries, or pieces of all of them that leave partial outputs
   int most;       // chunks of the longest piece
 };
 
@@ -213,19 +225,45 @@ __device__ __forceinline__ void block_sync() {
   asm volatile("barrier.cta.sync.aligned 0;" ::: "memory");
 }
 
+// The cluster's barrier in two halves, and its shared memory (addresses of mapa()).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 struct Item {
-  int t, piece, nch, total;
+  bool good;  // the query belongs to a sequence
+  int piece, nch, total;
   int64_t row0;
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int S>
+__global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kThreads, 1)
 attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
   griddep_wait();
   const Attn4Args& a = p.a;
-  if (a.splits > 1) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = S > 1 ? (int)cluster_ctarank() : 0;
   const int64_t rows_all = (int64_t)a.seqs.total_q * a.h;
-  const bool split = a.splits > 1;
+  const bool partial = S == 1 && a.splits > 1;
+  if (partial) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -248,7 +286,9 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kBars + 1);
   int* counts = reinterpret_cast<int*>(bars + kBars + 2);  // [warps] entries of a warp's share
   uint32_t* tops = reinterpret_cast<uint32_t*>(bars + kBarBytes / 8);  // [2][128] largest magnitude of a head's latent, rope columns
-  static_assert((kBars + 2) * 8 + kThreads / 32 * 4 <= kBarBytes, "barriers");
+  int* holds = counts + kThreads / 32;                     // [pieces] entries of a piece
+  float2* sums = reinterpret_cast<float2*>(tops + 2 * kM);  // [pieces][128] a piece's (m, l)
+  static_assert((kBars + 2) * 8 + (kThreads / 32 + kMostPieces) * 4 <= kBarBytes, "barriers");
 
   const int live_warps = (a.h + 31) / 32;  // of the softmax: the others' rows are no head's
   if (warp == kMmaWarp) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
@@ -267,24 +307,25 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   float* const refs = reinterpret_cast<float*>(scratch + (int64_t)p.most * kPBytes);  // [chunk][128]
   int32_t* const list = reinterpret_cast<int32_t*>(refs + (int64_t)p.most * kM);  // cache rows of the entries, without those skipped
   tc_fence_before();
-  block_sync();
+  if (S > 1) cluster_sync();  // (the others' shared memory is written from the first item on)
+  else block_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // The barriers' phases go on from item to item: chunks so far, the parity of the items and of those that had any.
   uint32_t done = 0, turn = 0, full_turn = 0;
-  // An item's row, its entries' chunks; one without entries is written here.
+  // An item's query, its entries' chunks.
   auto begin = [&](int item, Item& it) {
-    it.t = item / a.splits;
-    it.piece = item - it.t * a.splits;
-    it.row0 = (int64_t)it.t * a.h;
+    const int t = S > 1 ? item : item / a.splits, pieces = S > 1 ? S : a.splits;
+    it.piece = S > 1 ? rank : item - t * a.splits;
+    it.row0 = (int64_t)t * a.h;
     // The query comes while the entries are looked up (the ring is free: all roles have left the item before).
     if (warp == kMmaWarp && elect_one()) {
       mbar_arrive_expect_tx(q_staged, kTiles * kQTile);
       for (int j = 0; j < kTiles; ++j) tma_load_2d(ring + j * kQTile, &qmap, q_staged, j * 64, (int)it.row0);
     }
     __syncwarp();
-    const int c0 = (int)((int64_t)p.chunks * it.piece / a.splits), c1 = (int)((int64_t)p.chunks * (it.piece + 1) / a.splits);
-    const int32_t* idx = a.idx + (int64_t)it.t * a.top_k;
+    const int c0 = p.chunks * it.piece / pieces, c1 = p.chunks * (it.piece + 1) / pieces;
+    const int32_t* idx = a.idx + (int64_t)t * a.top_k;
     const int end = min(a.top_k, c1 * kN);
     // The piece's entries as cache rows, without the skipped ones (a short history's row is mostly -1): a warp takes
     // consecutive ones, all its loads at once, ahead of the row's lookup.
@@ -298,7 +339,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     }
     if (threadIdx.x < 2 * kM) tops[threadIdx.x] = 0u;
     RowInfo ri;
-    const bool good = warp_query_row(a, it.t, lane, ri);
+    const bool good = warp_query_row(a, t, lane, ri);
     if (good) {
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
@@ -326,16 +367,9 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       }
     }
     block_sync();
+    it.good = good;
     it.total = total;
     it.nch = (total + kN - 1) / kN;
-    if (total || !good) return;
-    for (int i = threadIdx.x; i < a.h; i += kThreads) {
-      if (split) a.part_ml[(int64_t)it.piece * rows_all + it.row0 + i] = make_float2(-INFINITY, 0.f);
-      else if (a.lse) a.lse[it.row0 + i] = -INFINITY;
-    }
-    const int per = a.out_dtype == DSA_F32 ? 128 : 64;  // 16-byte pieces of a row
-    for (int i = threadIdx.x; !split && i < a.h * per; i += kThreads)
-      reinterpret_cast<uint4*>(a.out)[it.row0 * per + i] = make_uint4(0u, 0u, 0u, 0u);
   };
   // The query to tensor memory, by all warps but the MMA's: those of a quarter of the heads (each warp can write to one) take a few
   // of the column tiles each.  The latent columns go to fp16, times the power of two that brings the head's largest finite one into
@@ -401,22 +435,107 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     if (mine && lane == 0) mbar_arrive(qt_full);
     return shift;
   };
-  // False: a wait was given up.  (None is under way that could be now.)
+  auto sync = [&] {
+    if (S > 1) cluster_sync();
+    else block_sync();
+  };
+  // The item's end, of all roles: O, scaled, to shared memory and from there, summed over the query's pieces, to the output: 256
+  // columns at a time (pieces of up to 64 heads: all), of which each CTA of the cluster takes its share of all heads.  False: a wait was given up.
   auto finish = [&](const Item& it) -> bool {
     if (it.nch == 0 && warp == kMmaWarp) mbar_wait_drain(q_staged, turn);  // (nobody else waited for the query)
+    if (S > 1) cluster_wait();  // the pieces' sums are there
+    else block_sync();
+    bool stopped = false;
+    if (it.good) {
+      const bool stages = warp >= kSoftWarps && warp < kMmaWarp && (warp & 3) < live_warps && it.nch;
+      const int r = (warp & 3) * 32 + lane;
+      float factor = 0.f;
+      if (warp < kMmaWarp) {
+        float top = -FLT_MAX, sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < S; ++c) top = fmaxf(top, sums[c * kM + r].x);
+#pragma unroll
+        for (int c = 0; c < S; ++c) sum += sums[c * kM + r].y * ex2(sums[c * kM + r].x - top);
+        factor = sum == 0.f ? 0.f : ex2(sums[rank * kM + r].x - top) / sum * (1.f / kShrinkV);
+        if (partial) {
+          factor = 1.f / kShrinkV;
+          if (warp < kSoftWarps && r < a.h) a.part_ml[it.piece * rows_all + it.row0 + r] = sums[r];
+        } else if (a.lse && warp < kSoftWarps && rank == 0 && r < a.h) {
+          a.lse[it.row0 + r] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        }
+      }
+      if (stages) {
+        mbar_wait(o_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT);
+        tc_fence_after();
+      }
+      auto put_out = [&](auto columns) {
+        constexpr int kCols = decltype(columns)::value;
+#pragma unroll
+        for (int half = 0; half < kDc / kCols; ++half) {
+          if (stages) {
+#pragma unroll 1
+            for (int c = (warp - kSoftWarps) / 4; c < kCols / 32; c += kGroups * kDecoders / 4) {
+              uint32_t o[32];
+              __syncwarp();  // the load is the whole warp's
+              tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kCols + c * 32, o);
+              uint8_t* const to = ring + r * (kCols * 4) + c * 128;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(to + ((i ^ (r & 7)) * 16)) =
+                    make_float4(__uint_as_float(o[4 * i]) * factor, __uint_as_float(o[4 * i + 1]) * factor,
+                                __uint_as_float(o[4 * i + 2]) * factor, __uint_as_float(o[4 * i + 3]) * factor);
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();  // the next query comes to the same place
+          }
+          sync();
+          constexpr int kPer = kCols / 4 / S;  // 16-byte pieces of a row that are this CTA's
+          for (int i = threadIdx.x; i < a.h * kPer; i += kThreads) {
+            const int row = i / kPer, k = rank * kPer + i % kPer;
+            const uint32_t at = smem_u32(ring) + row * (kCols * 4) + ((k ^ (row & 7)) * 16);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kAtOnce = S < 4 ? S : 4;
+#pragma unroll
+            for (int c0 = 0; c0 < S; c0 += kAtOnce) {
+              float4 v[kAtOnce];
+#pragma unroll
+              for (int c = 0; c < kAtOnce; ++c)
+                v[c] = holds[c0 + c] == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : ld_cluster4(S > 1 ? mapa(at, c0 + c) : at);
+#pragma unroll
+              for (int c = 0; c < kAtOnce; ++c) o = make_float4(o.x + v[c].x, o.y + v[c].y, o.z + v[c].z, o.w + v[c].w);
+            }
+            const int64_t to = (it.row0 + row) * kDc + half * kCols + k * 4;
+            if (partial) *reinterpret_cast<float4*>(a.part_o + it.piece * rows_all * kDc + to) = o;
+            else if (a.out_dtype == DSA_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = o;
+            else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+          }
+          // (all pieces stop together: none writes to what another has left)
+          if (S > 1 && half == kDc / kCols - 1)
+            stopped = __any_sync(0xffffffffu, ld_cluster(mapa(smem_u32(const_cast<int*>(abort_flag)), lane % S)) != 0);
+          sync();
+        }
+      };
+      if (S > 1 && a.h <= 64) put_out(std::integral_constant<int, 512>());
+      else put_out(std::integral_constant<int, 256>());
+    }
     turn ^= 1;
     if (it.nch) full_turn ^= 1;
     done += it.nch;
-    tc_fence_before();
-    block_sync();
-    return *abort_flag == 0;
+    if (S == 1) {
+      if (!it.good) block_sync();
+      stopped = *abort_flag != 0;
+    } else if (!it.good) {
+      cluster_sync();
+    }
+    return !stopped;
   };
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    for (int item = blockIdx.x / S; item < p.items; item += gridDim.x / S) {
       Item it;
       begin(item, it);
       const int nch = it.nch;
+      if (S > 1) cluster_arrive();
       if (nch && warp == kMmaWarp) {
         // ---------------- query loads, MMA issue ----------------
         if (elect_one()) {
@@ -466,10 +585,11 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     }
   } else if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
-    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    for (int item = blockIdx.x / S; item < p.items; item += gridDim.x / S) {
       Item it;
       begin(item, it);
       const int nch = it.nch, total = it.total;
+      if (S > 1) cluster_arrive();
       if (nch) {
         // ---------------- gather and decode: the chunks of phase 1, then the same again for phase 2 ----------------
         // The two groups take the chunks in turn: a chunk is a chain of waits and latencies as long as its work, which the other
@@ -568,15 +688,28 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    for (int item = blockIdx.x / S; item < p.items; item += gridDim.x / S) {
       Item it;
       begin(item, it);
       const int nch = it.nch, total = it.total;
-      const int piece = it.piece;
-      const int64_t row0 = it.row0;
+      const int r = warp * 32 + lane;
+      // The head's sum goes to all pieces' CTAs, which take O together.
+      auto give = [&](float m, float l) {
+        if (S == 1) {
+          sums[r] = make_float2(fmaxf(m, -FLT_MAX), l);
+          if (r == 0) holds[0] = total;
+        } else {
+#pragma unroll
+          for (int c = 0; c < S; ++c) {
+            st_cluster(mapa(smem_u32(&sums[rank * kM + r]), c), fmaxf(m, -FLT_MAX), l);
+            if (r == 0) st_cluster(mapa(smem_u32(&holds[rank]), c), total);
+          }
+          cluster_arrive();
+        }
+      };
+      if (nch == 0) give(-INFINITY, 0.f);
       if (nch) {
         // ---------------- softmax: thread = head ----------------
-        const int r = warp * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
         const int shift = stage_query(warp & 3, 0);  // the row's logits are 2^shift times what its operands say
         bool stop = shift == kNoQuery || warp >= live_warps;  // (the others' rows are no head's)
@@ -628,6 +761,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           __stcg(refs + g * kM + r, m);
         }
+        give(m, l);
         // phase 2: this thread's row of P, relative to the last m (a power of two: exact)
         uint4 pk[8];
         float ref = 0.f;
@@ -660,73 +794,50 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           if (lane == 0) mbar_arrive(&p_full[ps]);
           if (g + 1 < nch) load_p(g + 1);
         }
-        if (!stop)
-          stop = !__all_sync(0xffffffffu, mbar_wait(o_full, full_turn, abort_flag, a.status, DSA_FLAG_TIMEOUT) && *abort_flag == 0);
-        if (!stop) {
-          tc_fence_after();
-          // O goes out through the ring (all tiles have been multiplied), 256 fp32 or 512 bf16 columns at a time: a thread writes its row
-          // there, 16 bytes more than its length apart from the next, and sends it with one bulk copy
-          const bool live = r < a.h;
-          const float inv = (split ? 1.f : (l == 0.f ? 0.f : 1.f / l)) * (1.f / kShrinkV);
-          const bool f32 = split || a.out_dtype == DSA_F32;
-          constexpr int kRowBytes = 1024;
-          uint8_t* mine = ring + r * (kRowBytes + 16);
-          char* out = split ? reinterpret_cast<char*>(a.part_o + ((int64_t)piece * rows_all + row0 + r) * kDc)
-                            : static_cast<char*>(a.out) + (row0 + r) * kDc * (f32 ? 4 : 2);
-          for (int c = 0; c < 16; ++c) {
-            uint32_t o[32];
-            __syncwarp();  // the load is the whole warp's
-            tmem_ld32(lane_base + 32 * c, o);
-            if (f32) {
-              float4* dst = reinterpret_cast<float4*>(mine) + 8 * (c & 7);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                     __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(mine) + 4 * c;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-            if (c == 15 || (f32 && c == 7)) {
-              fence_proxy_async_smem();  // our writes, seen by the bulk copy
-              if (live)
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                 reinterpret_cast<uint64_t>(out + (f32 && c == 15 ? kRowBytes : 0))),
-                             "r"(smem_u32(mine)), "r"(kRowBytes)
-                             : "memory");
-              asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
-            }
-          }
-          if (live) {
-            if (split) a.part_ml[(int64_t)piece * rows_all + row0 + r] = make_float2(fmaxf(m, -FLT_MAX), l);
-            else if (a.lse) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-          }
-        }
       }
       if (!finish(it)) break;
     }
   }
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(*tmem_slot, 512);
   }
 }
 
-constexpr double kStart = 3;  // an item's start and end, in chunks (of both phases)
+// In times of a chunk (both phases; two microseconds): an item's start and end, the merge's launch, a partial output's way through L2
+// and what a cluster's CTA reads of the others, of 128 heads.
+constexpr double kStart = 5.5, kMerge = 2, kPartial = 0.04;
+double joining(int cluster) { return cluster > 1 ? 1 + cluster / 2 : 0; }
 constexpr size_t kMostPartial = size_t(1) << 30;
 
 int chunks_of(const Attn4Args& a) { return (a.top_k + kN - 1) / kN; }
+// Clusters that are at work at once (a processing cluster's SMs are cut into them).
+int clusters_of(int pieces) { return pieces == 1 ? num_sms() : pieces == 2 ? num_sms() / 2 : pieces == 4 ? num_sms() * 9 / 38 : num_sms() / 10; }
 int64_t ctas_of(const Attn4Args& a) {
-  const int64_t items = (int64_t)a.seqs.total_q * a.splits;
-  return items < num_sms() ? items : num_sms();
+  const int64_t items = (int64_t)a.seqs.total_q * a.splits, most = clusters_of(a.cluster);
+  return (items < most ? items : most) * a.cluster;
+}
+
+template <int S>
+int launch_pieces(const Params& p, const CUtensorMap& qmap, cudaStream_t stream) {
+  static std::atomic<bool> allowed[64];
+  int rc = allow_smem<kSmem>(attn4_tc_kernel<S>, allowed, "attn4_tc: smem attribute");
+  if (rc != DSA_OK) return rc;
+  // (a kernel built with other registers would wait forever for those it sets)
+  static std::atomic<int> regs{0};
+  cudaError_t e = cudaSuccess;
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, attn4_tc_kernel<S>);
+    if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
+    regs.store(attr.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs)
+    return set_error(DSA_ERR_UNSUPPORTED, "attn4_tc: built with %d registers, not %d", regs.load(), kLaunchRegs);
+  DSA_LAUNCH("attn4_tc", stream,
+             e = launch_pdl(attn4_tc_kernel<S>, dim3((unsigned)ctas_of(p.a)), dim3(kThreads), kSmem, stream, p, qmap));
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
+  return check_launch("attn4_tc");
 }
 
 }  // namespace
@@ -735,62 +846,53 @@ bool attn4_tc_eligible(const Attn4Args& a) {
   return a.kv_dtype == DSA_BF16 && a.d_c == kDc && a.d_rope == kDr && a.h <= kM;
 }
 
-// Pieces a query's entries are cut into: a round of items ends with its longest, and merging costs a launch (about
-// two chunks) and the partial outputs' traffic (at 4 TB/s, a chunk being about two microseconds).
-int attn4_tc_splits(const Attn4Args& a) {
-  const int64_t items = a.seqs.total_q;
+// Few queries are cut into pieces to fill the SMs: a round of items ends with its longest.  Either a cluster of 2, 4 or 8 CTAs takes a
+// query and joins its pieces in shared memory, or any number of CTAs leave partial outputs for a merge: a launch and their way
+// through L2 more, but pieces of any length.  2,048 entries, 128 heads, clusters | partial outputs: 1 query 30.8 us (8 pieces) | 23.9 (32), 12 queries
+// 32.6 | 30.6, 32 queries 36.4 (4) | 41.8 (4), 64 queries 52.0 (2) | 69.6; 16 heads: 4 queries 20.6 | 24.2, 18 queries 26.5 (4) | 24.3 (8), 48
+// queries 40.2 (2) | 35.8 (3).
+void attn4_tc_plan(Attn4Args& a) {
   const int chunks = chunks_of(a);
-  if (items == 0) return 1;
-  const double row_cost = (double)a.seqs.total_q * a.h * a.d_c * 8 / 8e6;
-  int best = 1;
-  double cost = 1e30;
-  for (int s = 1; s <= chunks && s <= 64; ++s) {
-    if (s > 1 && (size_t)s * a.seqs.total_q * a.h * (a.d_c * 4 + 8) > kMostPartial) break;
-    const int64_t rounds = (items * s + num_sms() - 1) / num_sms();
-    const double c = rounds * ((double)((chunks + s - 1) / s) + kStart) + (s > 1 ? 2 + s * row_cost : 0);
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
-  }
-  return best;
+  const int64_t queries = a.seqs.total_q;
+  const double heads = a.h / 128.0;
+  double best = 1e30;
+  auto consider = [&](int cluster, int splits) {
+    const int64_t rounds = (queries * splits + clusters_of(cluster) - 1) / clusters_of(cluster);
+    const int pieces = cluster * splits, longest = (chunks + pieces - 1) / pieces;
+    // (a piece is three chunks long at least: a single one waits for itself)
+    const double cost = rounds * ((longest < 3 ? 3 : longest) + kStart + heads * joining(cluster)) +
+                        (splits > 1 ? kMerge + kPartial * heads * queries * splits : 0);
+    if (cost >= best) return;
+    best = cost;
+    a.cluster = cluster;
+    a.splits = splits;
+  };
+  for (int c = 1; c <= kMostPieces && c <= chunks; c *= 2) consider(c, 1);
+  for (int n = 2; n <= chunks && n * queries * a.h * (a.d_c * 4 + 8) <= (int64_t)kMostPartial; ++n) consider(1, n);
 }
 
 size_t attn4_tc_scratch(const Attn4Args& a) {
-  return (size_t)ctas_of(a) * ((chunks_of(a) + a.splits - 1) / a.splits) * (kPBytes + kRefBytes + kListBytes);
+  return (size_t)ctas_of(a) * ((chunks_of(a) + a.cluster * a.splits - 1) / (a.cluster * a.splits)) * (kPBytes + kRefBytes + kListBytes);
 }
 
 int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.chunks = chunks_of(a);
-  p.most = (p.chunks + a.splits - 1) / a.splits;
+  p.most = (p.chunks + a.cluster * a.splits - 1) / (a.cluster * a.splits);
   const int64_t items = (int64_t)a.seqs.total_q * a.splits;
   if (items > 0x3fffffff) return set_error(DSA_ERR_UNSUPPORTED, "attn4: too many queries");
   p.items = (int)items;
   CUtensorMap qmap;
   int rc = make_tmap_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kD, (uint64_t)a.seqs.total_q * a.h, kD * 2, 64, kM);
   if (rc != DSA_OK) return rc;
-  static std::atomic<bool> allowed[64];
-  rc = allow_smem<kSmem>(attn4_tc_kernel, allowed, "attn4_tc: smem attribute");
-  if (rc != DSA_OK) return rc;
-  // (a kernel built with other registers would wait forever for those it sets)
-  static std::atomic<int> regs{0};
-  cudaError_t e = cudaSuccess;
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, attn4_tc_kernel);
-    if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
-    regs.store(attr.numRegs, std::memory_order_relaxed);
+  switch (a.cluster) {
+    case 1: rc = launch_pieces<1>(p, qmap, stream); break;
+    case 2: return launch_pieces<2>(p, qmap, stream);
+    case 4: return launch_pieces<4>(p, qmap, stream);
+    default: return launch_pieces<8>(p, qmap, stream);
   }
-  if (regs.load(std::memory_order_relaxed) != kLaunchRegs)
-    return set_error(DSA_ERR_UNSUPPORTED, "attn4_tc: built with %d registers, not %d", regs.load(), kLaunchRegs);
-  DSA_LAUNCH("attn4_tc", stream,
-             e = launch_pdl(attn4_tc_kernel, dim3((unsigned)ctas_of(a)), dim3(kThreads), kSmem, stream, p, qmap));
-  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
-  rc = check_launch("attn4_tc");
-  if (rc != DSA_OK || a.splits == 1) return rc;
-  return launch_attn4_merge(a, stream);
+  return rc != DSA_OK || a.splits == 1 ? rc : launch_attn4_merge(a, stream);
 }
 
 }  // namespace dsa

@@ -501,7 +501,9 @@ Attn4Args attn4_args(const dsa_problem* p) {
   a.kv_dtype = p->kv_dtype;
   a.out_dtype = p->out_dtype;
   a.scale_log2 = scale_of(p) * kLog2e;
-  a.splits = attn4_tc_eligible(a) ? attn4_tc_splits(a) : attn4_simt_splits(a);
+  a.splits = a.cluster = 1;
+  if (attn4_tc_eligible(a)) attn4_tc_plan(a);
+  else a.splits = attn4_simt_splits(a);
   return a;
 }
 // Partial outputs and their (max, sum) for every piece of every row, and the kernel's own scratch.

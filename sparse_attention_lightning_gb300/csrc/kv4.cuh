@@ -101,14 +101,15 @@ struct Attn4Args {
   void* out;
   float* lse;
   uint32_t* status;
-  int splits;          // pieces a row's entries are cut into
+  int splits;          // pieces a row's entries are cut into that leave partial outputs
+  int cluster;         // tcgen05 path: or CTAs of a cluster that share a row's entries
   float* part_o;       // [pieces][total_q · h][d_c] unnormalised partial outputs
   float2* part_ml;     // [pieces][total_q · h] (max in log2 units, sum)
   uint8_t* scratch;    // tcgen05 path: attn4_tc_scratch() bytes
 };
 // tcgen05 path (bf16, 512 + 64 columns).
 bool attn4_tc_eligible(const Attn4Args& a);
-int attn4_tc_splits(const Attn4Args& a);
+void attn4_tc_plan(Attn4Args& a);  // sets splits, cluster
 size_t attn4_tc_scratch(const Attn4Args& a);
 int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream);
 int attn4_simt_splits(const Attn4Args& a);

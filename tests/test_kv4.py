@@ -403,6 +403,37 @@ def test_more_queries_than_sms(h, top_k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("queries,h,top_k,out_dtype", [
+    (1, 128, 2048, BF), (2, 40, 2000, F32), (5, 16, 2048, BF), (9, 64, 1999, F32), (14, 128, 2048, F32), (30, 128, 2048, BF),
+    (30, 65, 777, F32), (33, 20, 2048, BF), (60, 128, 2048, BF), (61, 96, 1030, F32), (76, 33, 130, BF), (170, 128, 2048, BF),
+    (180, 16, 2048, F32)])
+def test_pieces_of_a_query(queries, h, top_k, out_dtype):
+    """Queries cut into pieces, joined by the CTAs of a cluster or by a merge, in one round and in several: pieces without an
+    entry, queries without any, one entry behind nothing; the same again from a captured graph."""
+    import sparse_attention_lightning_gb300 as dsa
+    s = Setup([queries], [2100 + queries], h, dtype=BF, top_k=top_k, page=64, seed=queries, spread=2.0, out_dtype=out_dtype, **FULL)
+    idx = s.draw_idx()
+    if queries > 4:
+        idx[1, :top_k * 3 // 4] = -1
+        idx[2, top_k // 5:] = -1
+        idx[3] = -1
+        idx[4, :-1] = -1
+        idx[queries - 1, top_k // 3:top_k * 2 // 3] = -1
+    ws = dsa.Workspace()
+    out, lse = s.attend(idx, ws=ws)
+    assert ws.status() == 0
+    s.check(out, lse, idx, rows=set(range(0, queries, 1 + queries // 12)) | {0, 1, 2, 3, 4, queries - 1})
+    q, dev, out2, lse2 = s.q.cuda(), idx.cuda(), torch.zeros_like(out), torch.zeros_like(lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dsa.sparse_mla_attn4(s.prob, q, s.kv4, dev, out=out2, lse=lse2, ws=ws)
+    for _ in range(3):
+        out2.fill_(3), lse2.fill_(3)
+        g.replay()
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("h", [128, 16])
 def test_queries_of_any_magnitude(h):
     """Heads of zeros, of subnormal and of huge numbers, of widely spread ones, latent and rope columns apart; infinities and NaNs
