@@ -9,7 +9,8 @@
 //
 // One CTA = one query × 16 heads × one share of the entries; 16 threads a head: two entries each for the logits,
 // four columns in 64 each for the values, by 16-byte loads of shared memory (a decoded row is four floats longer than its columns,
-// which spreads it over the banks).  Bound by latency for few queries and by shared-memory loads for many.
+// which spreads it over the banks).  Bound by latency for few queries and by shared-memory loads for many: 32 queries of 2,048
+// entries and 128 heads, 512 + 64 columns in fp32 1,386 us (13 TFLOP/s), 256 + 64 in bf16 824.
 #include <float.h>
 
 #include "kv4.cuh"

@@ -7,6 +7,10 @@
 // The counting is a few tens of thousands of words: one CTA does it (a grid's worth of blocks would wait for each
 // other at every step), 16 loads a thread in flight, one block-wide sum for 16384 pages.  The bytes are moved by a
 // kernel of the whole GPU behind it, 32 KB a block at a time, eight 16-byte loads a thread.
+//
+// 32 sequences of up to 32,768 positions and 16 samples of each: free 7.7 us, fork 8.1, reserve 24.4 (a chain of ten
+// steps of one CTA, one to two us each) and its copies 8.1.  A million rows in three caches, half of them gone: counted in 16.4 us and
+// moved in 57 (177 MB in, 177 out: 6.2 TB/s).
 #include <limits.h>
 
 #include "pages.cuh"

@@ -10,6 +10,8 @@
 // Bound by HBM for many rows: 2 · 16 bytes of every 8 bf16 columns.  A thread takes 8 columns (4 pairs side by side,
 // or, where a pair's two columns are half a row apart, 16: 8 of each half) of up to 8 heads of a token, so that
 // the sines (30 to 40 instructions a pair) are shared by the heads and the heads' loads are in flight together.
+// 8,192 tokens of 128 heads, 64 of 576 columns in place: 46.5 us, 5.8 TB/s (0.85 of a copy's rate: 128 bytes of every 1,152).
+// One token of 128 heads: 2.1 us.
 #include "rotary.cuh"
 
 namespace dsa {
