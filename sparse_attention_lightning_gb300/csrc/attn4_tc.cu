@@ -867,7 +867,7 @@ void attn4_tc_plan(Attn4Args& a) {
     a.cluster = cluster;
     a.splits = splits;
   };
-  for (int c = 1; c <= kMostPieces && c <= chunks; c *= 2) consider(c, 1);
+  for (int c = 1; c <= kMostPieces && c <= chunks && clusters_of(c) > 0; c *= 2) consider(c, 1);
   for (int n = 2; n <= chunks && n * queries * a.h * (a.d_c * 4 + 8) <= (int64_t)kMostPartial; ++n) consider(1, n);
 }
 

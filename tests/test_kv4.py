@@ -70,6 +70,17 @@ def test_argument_checks():
     assert attn(problem(max_q_len=0)) == bad
 
 
+@pytest.mark.parametrize("total_q", [0, 1, 5, 40, 170, 5000])
+@pytest.mark.parametrize("h,top_k", [(128, 2048), (16, 999), (1, 1), (64, 130)])
+def test_workspace_of_any_device(total_q, h, top_k):
+    """Sized without a device too, where a cluster of CTAs has no place."""
+    p = _abi.DsaProblem(num_seqs=1, total_q=total_q, total_k=8192, max_q_len=total_q, max_k_len=8192, h_idx=4, d_idx=32, h=h, d_c=512,
+                        d_rope=64, top_k=top_k, idx_dtype=0, kv_dtype=_abi.DSA_BF16, out_dtype=_abi.DSA_BF16, sm_scale=0.0,
+                        cu_q=4096, cu_k=8192)
+    n = ctypes.c_size_t(0)
+    assert _abi.lib().dsa_workspace_size(ctypes.byref(p), _abi.OP_SPARSE_MLA_ATTN4, ctypes.byref(n)) == 0 and n.value > 0
+
+
 class Setup:
     """Sequences with a 4-bit cache, packed or paged; unused bytes of the cache are 0xff (NaN scales, NaN rope columns)."""
 
