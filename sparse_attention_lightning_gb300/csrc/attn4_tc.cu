@@ -257,13 +257,12 @@ struct Item {
 template <int S>
 __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kThreads, 1)
 attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
-  griddep_wait();
+  griddep_launch();  // what comes next may be set up meanwhile; it waits for this grid to end
   const Attn4Args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = S > 1 ? (int)cluster_ctarank() : 0;
   const int64_t rows_all = (int64_t)a.seqs.total_q * a.h;
   const bool partial = S == 1 && a.splits > 1;
-  if (partial) griddep_launch();  // the merge may be set up meanwhile; it waits for this grid to end
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -311,6 +310,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   else block_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_wait();
   // The barriers' phases go on from item to item: chunks so far, the parity of the items and of those that had any.
   uint32_t done = 0, turn = 0, full_turn = 0;
   // An item's query, its entries' chunks.
