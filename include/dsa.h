@@ -494,7 +494,9 @@ int dsa_free_pages(int32_t* table, int32_t rows, int32_t width, int64_t ld_table
  * full, will be written to and has other holders, a new page with the held positions' rows copied in all
  * caches (their other rows stay as they were) - but if all the page's holders are entries of this call that
  * would copy it, the first of them keeps it.  Pages are given out entry by entry; an entry gets
- * all it needs or nothing (then DSA_FLAG_NO_PAGES is set, also for every later entry that needs pages).
+ * all it needs or nothing (then DSA_FLAG_NO_PAGES is set, also for every later entry that needs pages).  An entry that was to
+ * keep a page gets nothing where one of those that were to copy it gets nothing, as that one goes on holding the page: no page of
+ * positions lens[i] .. held[i] - 1 has another holder after the call.
  * held[i] = new_lens[i], or lens[i] where the entry got nothing.  Of several entries of one row the first counts.  Which pages are free and
  * shared is as at the call's start.
  */

@@ -128,38 +128,35 @@ class Pool:
             if good[i] and L % page and N > L and before[self.table[r][L // page]] > 1:
                 wants.setdefault(self.table[r][L // page], []).append(i)
         free = [p for p, n in enumerate(before) if n <= 0]
-        held, at, changes = [], 0, []
+        keeps = {who[0]: p for p, who in wants.items() if len(who) == before[p]}  # all holders are here: the first keeps the page
+        needs, served, at = [], [], 0
         for i, (r, L, N) in enumerate(zip(rows, lens, new)):
-            if not good[i]:
-                held.append(L)
-                continue
             need = []
-            if L % page and N > L:
-                p = self.table[r][L // page]
-                if i in wants.get(p, ()) and not (len(wants[p]) == before[p] and wants[p][0] == i):
-                    need.append(L // page)
-            n_copy = len(need)
-            for j in range(-(-L // page), -(-N // page)):
+            if good[i] and L % page and N > L and i not in keeps and i in wants.get(self.table[r][L // page], ()):
+                need.append(L // page)
+            for j in range(-(-L // page), -(-N // page)) if good[i] else ():
                 p = self.table[r][j]
                 if not (self.ok(p) and before[p] == 1):
                     need.append(j)
             at += len(need)
-            if need and at > len(free):
-                held.append(L)
-                continue
-            for k, j in enumerate(need):
-                p, to = self.table[r][j], free[at - len(need) + k]
+            needs.append(list(zip(need, free[at - len(need):])))
+            served.append(good[i] and (not need or at <= len(free)))
+        for i, p in keeps.items():  # it is not its alone while another goes on holding it
+            served[i] = served[i] and all(served[k] for k in wants[p][1:])
+        changes = []
+        for i, (r, L, N) in enumerate(zip(rows, lens, new)):
+            for j, to in needs[i] if served[i] else ():
+                p = self.table[r][j]
                 changes.append((p if self.ok(p) and before[p] > 1 else -1, to))
                 self.table[r][j] = to
-                if k < n_copy:
+                if j < -(-L // page):  # the page of held positions
                     for c in self.caches:
                         c[to * page:to * page + L % page] = c[p * page:p * page + L % page]
-            held.append(N)
         for p, to in changes:
             self.refs[to] = 1
             if p >= 0:
                 self.refs[p] -= 1
-        return held
+        return [N if s else L for s, L, N in zip(served, lens, new)]
 
     def compact(self):
         """(moved, live)."""

@@ -1046,7 +1046,8 @@ def reserve_pages(table, refs, rows, lens, new_lens, page_size: int, caches=(), 
     new_lens[i] - 1 to (dsa_reserve_pages): new ones, and a copy, in all caches, of a last page that others hold too.
 
     caches: up to 8 contiguous tensors of num_pages * page_size rows.  Returns held [n] int32: new_lens[i], or lens[i] where
-    the free pages did not suffice (ws.status() then has DSA_FLAG_NO_PAGES).  A captured call needs ws."""
+    the free pages did not suffice, for the entry or for another one that shares its last page (ws.status() then has
+    DSA_FLAG_NO_PAGES).  A captured call needs ws."""
     if not table.is_cuda:
         raise ValueError("table must be a CUDA tensor")
     index = table.get_device()

@@ -116,15 +116,15 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ Pages
 // Reserve.
 struct Reserve {
   int* mark;   // [rows] the first entry of a row
-  int* cnt;    // [num_pages] entries of the call that would copy a page
+  int* cnt;    // [num_pages] entries of the call that would copy a page (-1: one of them gets no pages)
   int* first;  // [num_pages] the first of them
   int* item;   // [n + 1] the table entries looked at before entry i's: its copy, if any, and those behind its held pages
   int* off;    // [n + 1] new pages before entry i's
   int* old;    // [num_pages] by new page in order: the page it replaces, -1: none, -2: not given out
   int* list;   // [num_pages] the free pages in order
-  int* csrc;   // [n] what entry i copies: page, to page, rows (0: nothing); csrc is -1 for an entry that is
-  int* cdst;   //     left out, -2 where nothing is copied
-  int* crows;
+  int* csrc;   // [n] what entry i copies: page, to page, rows (0: nothing); csrc is -1 for an entry that is left out,
+  int* cdst;   //     -2 where nothing is copied, -3 for one that keeps a page (in cdst) which others of the call copy,
+  int* crows;  //     -4 for one that was to keep it and gets nothing
   __host__ __device__ Reserve(int32_t* p, int rows, int n, int num_pages)
       : mark(p), cnt(mark + rows), first(cnt + num_pages), item(first + num_pages), off(item + n + 1), old(off + n + 1),
         list(old + num_pages), csrc(list + num_pages), cdst(csrc + n), crows(cdst + n) {}
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
       const int p = R.csrc[i];
       n = pages_of(a.new_lens[i], ps) - pages_of(a.lens[i], ps) + (p >= 0);
       if (p >= 0 && R.cnt[p] == a.refs[p] && R.first[p] == i) {
-        R.csrc[i] = -2;
+        R.csrc[i] = -3;
+        R.cdst[i] = p;
         --n;
       }
     }
@@ -283,11 +284,22 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
   }
   __syncthreads();
   const int nfree = (int)found;
+  // A page that one entry keeps and the others copy is the one's alone only if all the others get their copies: one that
+  // gets nothing still holds it, and what the one wrote there would be in the other's history.
+  if ((int)total > nfree) {
+    for (int i = tid; i < a.n; i += kOne)
+      if (R.csrc[i] >= 0 && R.off[i + 1] > nfree) R.cnt[R.csrc[i]] = -1;
+    __syncthreads();
+    for (int i = tid; i < a.n; i += kOne)
+      if (R.csrc[i] == -3 && R.cnt[R.cdst[i]] < 0) R.csrc[i] = -4;
+    __syncthreads();
+  }
+  auto nothing = [&](int i) { return R.off[i + 1] > nfree || R.csrc[i] == -4; };  // for entry i, if it needs pages
   // given out in the entries' order: all that an entry needs, or nothing
   for (int i = tid; i < a.n; i += kOne) {
     const int p = R.csrc[i], k0 = R.off[i], k1 = R.off[i + 1], L = a.lens[i];
     if (p == -1) continue;
-    if (k0 < k1 && k1 > nfree) {
+    if (p == -4 || (k0 < k1 && nothing(i))) {
       a.held[i] = L;
       atomicOr(a.status, DSA_FLAG_NO_PAGES);
       continue;
@@ -300,7 +312,7 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
   }
   walk([&](int i, int col, int was, bool need, uint32_t at) {
     if (!need || (int)at >= nfree) return;
-    if (R.off[i + 1] > nfree) {
+    if (nothing(i)) {
       R.old[at] = -2;
       return;
     }
