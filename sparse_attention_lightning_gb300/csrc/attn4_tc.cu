@@ -257,7 +257,6 @@ struct Item {
 template <int S>
 __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kThreads, 1)
 attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap) {
-  griddep_launch();  // what comes next may be set up meanwhile; it waits for this grid to end
   const Attn4Args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = S > 1 ? (int)cluster_ctarank() : 0;
@@ -310,7 +309,10 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   else block_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Barriers and tensor memory are set up beside the kernel before; what a caller wrote is read from here on.  Only the merge, which reads
+  // offsets ahead of its own wait, may start early, and not before this wait (a caller's next kernel may read what this one waits for).
   griddep_wait();
+  if (partial) griddep_launch();
   // The barriers' phases go on from item to item: chunks so far, the parity of the items and of those that had any.
   uint32_t done = 0, turn = 0, full_turn = 0;
   // An item's query, its entries' chunks.
