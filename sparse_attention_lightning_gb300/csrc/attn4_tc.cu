@@ -219,7 +219,8 @@ __device__ __forceinline__ void load_row(uint32_t taddr, float (&s)[kN]) {
   for (int i = 0; i < 32; ++i) s[32 + i] = __uint_as_float(r[i]);
 }
 
-// The block's barrier, which each role meets in its own code.
+// The block's barrier, which each role meets in its own code.  (Warp-aligned, as those of the cluster: each reconverges the warp first,
+// whose lanes may come apart from a role's loop.)
 __device__ __forceinline__ void block_sync() {
   __syncwarp();
   asm volatile("barrier.cta.sync.aligned 0;" ::: "memory");
@@ -230,7 +231,10 @@ __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void st_cluster(uint32_t addr, float x, float y) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
@@ -401,6 +405,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
       }
       atomicMax(&tops[(j == kVTiles ? kM : 0) + r], max(t & 0x7fffu, t >> 16 & 0x7fffu));
     }
+    __syncwarp();
     asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kMmaWarp) : "memory");
     if (!ok) return kNoQuery;
     const int e0 = (int)(tops[r] >> 7) - 127, e1 = (int)(tops[kM + r] >> 7) - 127;  // (0 and subnormal: -127)
