@@ -449,7 +449,8 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   // The item's end, of all roles: O, scaled, to shared memory and from there, summed over the query's pieces, to the output: 256
   // columns at a time (pieces of up to 64 heads: all), of which each CTA of the cluster takes its share of all heads.  False: a wait was given up.
   auto finish = [&](const Item& it) -> bool {
-    if (it.nch == 0 && warp == kMmaWarp) mbar_wait_drain(q_staged, turn);  // (nobody else waited for the query)
+    // (Without entries nobody else waited for the query, and where a wait was given up it may still be on its way.)
+    if (warp == kMmaWarp) mbar_wait_drain(q_staged, turn);
     if (S > 1) cluster_wait();  // the pieces' sums are there
     else block_sync();
     bool stopped = false;
