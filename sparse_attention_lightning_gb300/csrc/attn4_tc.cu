@@ -66,9 +66,15 @@ constexpr int kGroups = 2, kDecoders = 8;  // groups of decoding warps, which ta
 constexpr int kMmaWarp = kSoftWarps + kGroups * kDecoders;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole groups of four warps: their registers are set together)
 constexpr int kParts = (kSoftWarps + kGroups * kDecoders) / 4;  // warps that take a quarter of the heads to tensor memory
-// Registers a thread of softmax, of the decoders, of the MMA's four warps; together at most what the block is launched with.
-constexpr int kLaunchRegs = 80, kSoftRegs = 136, kDecodeRegs = 72, kMmaRegs = 56;
-static_assert(128 * kSoftRegs + 32 * kGroups * kDecoders * kDecodeRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "registers");
+// Registers a thread of softmax, of the decoders, of the MMA's four warps; together at most what the block is launched with (a build with
+// fewer would wait forever for those that softmax asks for).  `regs`: what the compiler reports, of which a warp gets whole eights.
+constexpr int kSoftRegs = 136, kDecodeRegs = 72, kMmaRegs = 56;
+constexpr bool registers_suffice(int regs) {
+  const int held = (regs + 7) / 8 * 8;
+  return held >= kDecodeRegs && held <= kSoftRegs &&
+         128 * kSoftRegs + 32 * kGroups * kDecoders * kDecodeRegs + 128 * kMmaRegs <= kThreads * held;
+}
+static_assert(registers_suffice(80) && registers_suffice(73) && !registers_suffice(72) && !registers_suffice(137), "registers");
 constexpr int kRing = kVSlots * kVSlot + kPSlots * kQTile;
 constexpr int kBarBytes = 512, kTopBytes = 2 * kM * 4;
 constexpr int kMostPieces = 8;             // of a query: CTAs of a cluster
@@ -826,22 +832,31 @@ int64_t ctas_of(const Attn4Args& a) {
   return (items < most ? items : most) * a.cluster;
 }
 
+// Whether the kernels were built with the registers that their roles are given: 1 or -1, asked of the runtime once; 0 where it has no
+// device to ask (a workspace's size).
+int built_to_run() {
+  static std::atomic<int> known{0};
+  const int k = known.load(std::memory_order_relaxed);
+  if (k != 0) return k;
+  bool ok = true;
+  for (auto kern : {attn4_tc_kernel<1>, attn4_tc_kernel<2>, attn4_tc_kernel<4>, attn4_tc_kernel<8>}) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    ok = ok && registers_suffice(attr.numRegs);
+  }
+  known.store(ok ? 1 : -1, std::memory_order_relaxed);
+  return ok ? 1 : -1;
+}
+
 template <int S>
 int launch_pieces(const Params& p, const CUtensorMap& qmap, cudaStream_t stream) {
   static std::atomic<bool> allowed[64];
   int rc = allow_smem<kSmem>(attn4_tc_kernel<S>, allowed, "attn4_tc: smem attribute");
   if (rc != DSA_OK) return rc;
-  // (a kernel built with other registers would wait forever for those it sets)
-  static std::atomic<int> regs{0};
   cudaError_t e = cudaSuccess;
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, attn4_tc_kernel<S>);
-    if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
-    regs.store(attr.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) != kLaunchRegs)
-    return set_error(DSA_ERR_UNSUPPORTED, "attn4_tc: built with %d registers, not %d", regs.load(), kLaunchRegs);
   DSA_LAUNCH("attn4_tc", stream,
              e = launch_pdl(attn4_tc_kernel<S>, dim3((unsigned)ctas_of(p.a)), dim3(kThreads), kSmem, stream, p, qmap));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, "attn4_tc: %s", cudaGetErrorString(e));
@@ -851,7 +866,7 @@ int launch_pieces(const Params& p, const CUtensorMap& qmap, cudaStream_t stream)
 }  // namespace
 
 bool attn4_tc_eligible(const Attn4Args& a) {
-  return a.kv_dtype == DSA_BF16 && a.d_c == kDc && a.d_rope == kDr && a.h <= kM;
+  return a.kv_dtype == DSA_BF16 && a.d_c == kDc && a.d_rope == kDr && a.h <= kM && built_to_run() >= 0;
 }
 
 // Few queries are cut into pieces to fill the SMs: a round of items ends with its longest.  Either a cluster of 2, 4 or 8 CTAs takes a
@@ -884,6 +899,7 @@ size_t attn4_tc_scratch(const Attn4Args& a) {
 }
 
 int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
+  if (built_to_run() != 1) return set_error(DSA_ERR_CUDA, "attn4_tc: the kernel's attributes are not to be had");
   Params p{};
   p.a = a;
   p.chunks = chunks_of(a);

@@ -107,7 +107,7 @@ struct Attn4Args {
   float2* part_ml;     // [pieces][total_q · h] (max in log2 units, sum)
   uint8_t* scratch;    // tcgen05 path: attn4_tc_scratch() bytes
 };
-// tcgen05 path (bf16, 512 + 64 columns).
+// tcgen05 path (bf16, 512 + 64 columns; a build whose registers do not suffice for its roles takes the other one).
 bool attn4_tc_eligible(const Attn4Args& a);
 void attn4_tc_plan(Attn4Args& a);  // sets splits, cluster
 size_t attn4_tc_scratch(const Attn4Args& a);
