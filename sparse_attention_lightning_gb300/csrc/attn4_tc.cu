@@ -20,9 +20,10 @@
 // (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.  32 queries of 2,048 entries: 36.4 us
 // of four CTAs each, of which the first MMA comes after 13,000 clocks, eight chunks take 31,000 and O's way out 22,000.
 //
-// The running maximum m of a head only decides the scale of p: it starts as the first chunk's, moves by whole numbers (of log2) when a
-// chunk's maximum is more than 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which is exact,
-// instead of rescaling O.
+// The running maximum m of a head only decides the scale of p: it starts as the first chunk's, rounded up to a whole number (of log2), moves
+// by whole numbers when a chunk's maximum is more than 2^8 above it, and phase 2 brings a chunk's p to the last m by a power of two, which
+// is exact, instead of rescaling O.  (Whole numbers stay whole in fp32 at any size; a sum with a fraction would be rounded, and the step
+// from one m to the next would be no power of two: of logits about 2^17, sums of p were off by up to 1.4 of its roundings.)
 // The sum is in fp32 of the unrounded p.  P is rounded to bf16, which the MMA wants beside bf16 values: 2^-8 of each p at
 // most, in either direction.
 //
@@ -753,7 +754,7 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
           for (int i = 0; i < kN; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
           const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           if (mc > m + kGrowLog2) {  // the first entries always (m = -inf)
-            const float m_new = m == -INFINITY ? mc : m + ceilf(mc - m);
+            const float m_new = m == -INFINITY ? ceilf(mc) : m + ceilf(mc - m);
             l *= ex2(m - m_new);
             m = m_new;
           }
