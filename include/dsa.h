@@ -402,7 +402,7 @@ int dsa_evict(const dsa_problem* p, const float* acc, int64_t ld_acc, int32_t bu
  * x, out: element (t, h, c) at t * x_token + h * x_head + c (strides in elements, >= 0), F32 or BF16,
  * aligned to their element (rows on 16-byte boundaries are faster); out may be x with the same strides,
  * and otherwise must not overlap it (tensors with the same strides that interleave without
- * sharing an element, as two column ranges of one tensor, may) nor the positions.
+ * sharing an element, as two column ranges of one tensor, may, whichever of tokens and heads is outside) nor the positions.
  * positions [axes][ld_pos] device int32, ld_pos >= tokens or 0 (all axes have the same ones); turn [d/2] and axis [d/2] HOST memory, read before
  * the call returns; axis[i] < axes <= 255.  d even, 2 .. 256.  One launch, no workspace; tokens = 0 launches nothing.
  */

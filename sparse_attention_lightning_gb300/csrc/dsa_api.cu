@@ -475,6 +475,29 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// Whether rows of d elements at t · st + h · sh (t < tokens, h < heads; none of them overlap) and the same rows `off` elements further
+// share none.  One of the strides holds all rows of the other one (the rows would overlap otherwise, or interleave in a way that
+// is taken for it), so of its multiples only the two next to off can bring them together, and of the other one's two for each.
+bool rows_apart(int64_t off, int64_t d, int64_t tokens, int64_t st, int64_t heads, int64_t sh) {
+  int64_t n1 = tokens, s1 = st, n2 = heads, s2 = sh;  // outer and inner
+  if (tokens == 1 || (heads > 1 && sh > st)) {
+    n1 = heads; s1 = sh;
+    n2 = tokens; s2 = st;
+  }
+  auto next = [](int64_t r, int64_t s, int64_t n, int i) -> int64_t {  // multiple i of s next to r, of at most n - 1 steps
+    if (n < 2 || s < 1) return 0;
+    int64_t q = r / s - (r % s < 0) + i;
+    q = q < 1 - n ? 1 - n : q > n - 1 ? n - 1 : q;
+    return q * s;
+  };
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j) {
+      const int64_t r1 = off - next(off, s1, n1, i), r = r1 - next(r1, s2, n2, j);
+      if (r < d && -r < d) return false;
+    }
+  return true;
+}
+
 // ----------------------------------------------------------------------------
 // The 4-bit latent cache.
 
@@ -929,15 +952,9 @@ int dsa_rotate_axes(int64_t tokens, int32_t heads, int32_t d, int32_t dtype, int
   const int64_t nx = ((tokens - 1) * x_token + (heads - 1) * x_head + d) * size;
   const int64_t no = ((tokens - 1) * out_token + (heads - 1) * out_head + d) * size;
   const bool same = (tokens == 1 || x_token == out_token) && (heads == 1 || x_head == out_head);
-  if (!(same && x == out) && overlap(x, nx, out, no)) {
-    // same strides: the rows interleave if their starts, modulo the strides, are d columns apart either way
-    const int64_t step = heads > 1 ? out_head : out_token;
-    const int64_t off = (int64_t)((uintptr_t)out - (uintptr_t)x);
-    const int64_t r = step > 0 ? ((off % (step * size)) + step * size) % (step * size) : 0;
-    const bool comb = heads == 1 || tokens == 1 || out_token % out_head == 0;
-    if (!(same && step > 0 && comb && r >= d * size && r <= (step - d) * size))
-      return set_error(DSA_ERR_INVALID_ARG, "out overlaps x");
-  }
+  if (!(same && x == out) && overlap(x, nx, out, no) &&
+      !(same && rows_apart((int64_t)((uintptr_t)out - (uintptr_t)x) / size, d, tokens, out_token, heads, out_head)))
+    return set_error(DSA_ERR_INVALID_ARG, "out overlaps x");
   if (overlap(positions, ((axes - 1) * ld_pos + tokens) * 4, out, no))
     return set_error(DSA_ERR_INVALID_ARG, "out overlaps positions");
   RotaryArgs a{};
