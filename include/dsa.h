@@ -453,7 +453,7 @@ int dsa_read_kv4(const dsa_problem* p, const void* kv4, void* out, void* ws, siz
  * [cache rows][row bytes].  q, idx, out and lse, skipped and repeated entries as there; a row without a valid entry,
  * or whose logits are all -inf, gets out = 0 and lse = -inf.  An entry that is skipped adds nothing, whatever its row holds.
  * Rows of a sequence whose cu_q/cu_k are inconsistent, or that has more than max_q_len queries, set DSA_FLAG_BAD_SEQS
- * and are left as they were.
+ * and are left as they were.  out and lse must not overlap each other, q, kv4 or idx.
  */
 int dsa_sparse_mla_attn4(const dsa_problem* p, const void* q, const void* kv4, const int32_t* idx,
                          void* out, float* lse, void* ws, size_t ws_bytes, void* stream);

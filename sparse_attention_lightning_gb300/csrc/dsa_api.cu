@@ -1036,6 +1036,13 @@ int dsa_sparse_mla_attn4(const dsa_problem* p, const void* q, const void* kv4, c
   DSA_TRY(check_ptr(lse, "lse", true));
   if ((int64_t)p->total_q * p->h >= (int64_t(1) << 31))
     return set_error(DSA_ERR_UNSUPPORTED, "too many (query, head) rows");
+  const int64_t rows = (int64_t)p->total_q * p->h, size = p->kv_dtype == DSA_F32 ? 4 : 2;
+  const Span io[5] = {{q, rows * (p->d_c + p->d_rope) * size, "q"}, {kv4, kv4_bytes(p), "kv4"}, {idx, (int64_t)idx_bytes(p), "idx"},
+                      {out, rows * p->d_c * (p->out_dtype == DSA_F32 ? 4 : 2), "out"}, {lse, rows * 4, "lse"}};
+  for (int i = 3; i < 5 && !none; ++i)  // (the inputs may overlap each other)
+    for (int j = 0; j < i; ++j)
+      if (io[i].p && overlap(io[i].p, io[i].bytes, io[j].p, io[j].bytes))
+        return set_error(DSA_ERR_INVALID_ARG, "%s overlaps %s", io[i].name, io[j].name);
   Attn4Args a = attn4_args(p);
   DSA_TRY(check_ws(ws, ws_bytes, carve_attn4(a, nullptr)));
   if (none) return DSA_OK;
