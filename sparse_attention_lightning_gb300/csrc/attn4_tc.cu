@@ -38,7 +38,7 @@
 // its way from tensor to shared memory, and sums up its share of the columns of all pieces from there, in their order, at 16
 // bytes a clock and CTA (192 KB: 12,000 clocks; half as fast in shares of 128 bytes; loads for several rows at once, shares kept together and a
 // share's sums while the next columns are put there were no faster).  Partial outputs through L2 and a merge in their place took 42 us
-// (the merge 13), but suit pieces shorter than an eighth.
+// (the merge 13), but suit pieces shorter than a quarter.
 #include <float.h>
 
 #include <type_traits>
@@ -78,7 +78,7 @@ constexpr bool registers_suffice(int regs) {
 static_assert(registers_suffice(80) && registers_suffice(73) && !registers_suffice(72) && !registers_suffice(137), "registers");
 constexpr int kRing = kVSlots * kVSlot + kPSlots * kQTile;
 constexpr int kBarBytes = 512, kTopBytes = 2 * kM * 4;
-constexpr int kMostPieces = 8;             // of a query: CTAs of a cluster
+constexpr int kMostPieces = 4;             // of a query: CTAs of a cluster
 constexpr int kSumBytes = kMostPieces * kM * 8;
 constexpr int kSmem = kRing + kGroups * kRaw + kBarBytes + kTopBytes + kSumBytes + 1024;
 constexpr int kQCol = 0, kSCol = kD / 2;   // tensor memory of phase 1: 288 query columns, the logits; of phase 2: O
@@ -819,15 +819,16 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
   }
 }
 
-// In times of a chunk (both phases; two microseconds): an item's start and end, the merge's launch, a partial output's way through L2
-// and what a cluster's CTA reads of the others, of 128 heads.
-constexpr double kStart = 5.5, kMerge = 2, kPartial = 0.04;
-double joining(int cluster) { return cluster > 1 ? 1 + cluster / 2 : 0; }
+// In times of a chunk (both phases; 1.9 us): an item's start and end, the merge's launch, a partial output of 128 heads on its way through
+// L2, and what a cluster's CTAs take to join an output.  Least squares' and then the choices' best fit of 110 sizes (1 to 608 queries, 16, 64
+// and 128 heads, 512 to 2,048 entries) in every form: the rule's form takes 0.3 % longer than the fastest one on average, 9 % at most.
+constexpr double kStart = 4.5, kMerge = 1.25, kPartial = 0.035;
+double joining(int cluster, double heads) { return cluster > 1 ? (0.4 + 0.6 * heads) * (1 + cluster / 2) : 0; }
 constexpr size_t kMostPartial = size_t(1) << 30;
 
 int chunks_of(const Attn4Args& a) { return (a.top_k + kN - 1) / kN; }
 // Clusters that are at work at once (a processing cluster's SMs are cut into them).
-int clusters_of(int pieces) { return pieces == 1 ? num_sms() : pieces == 2 ? num_sms() / 2 : pieces == 4 ? num_sms() * 9 / 38 : num_sms() / 10; }
+int clusters_of(int pieces) { return pieces == 1 ? num_sms() : pieces == 2 ? num_sms() / 2 : num_sms() * 9 / 38; }
 int64_t ctas_of(const Attn4Args& a) {
   const int64_t items = (int64_t)a.seqs.total_q * a.splits, most = clusters_of(a.cluster);
   return (items < most ? items : most) * a.cluster;
@@ -840,7 +841,7 @@ int built_to_run() {
   const int k = known.load(std::memory_order_relaxed);
   if (k != 0) return k;
   bool ok = true;
-  for (auto kern : {attn4_tc_kernel<1>, attn4_tc_kernel<2>, attn4_tc_kernel<4>, attn4_tc_kernel<8>}) {
+  for (auto kern : {attn4_tc_kernel<1>, attn4_tc_kernel<2>, attn4_tc_kernel<4>}) {
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) {
       cudaGetLastError();
@@ -870,11 +871,12 @@ bool attn4_tc_eligible(const Attn4Args& a) {
   return a.kv_dtype == DSA_BF16 && a.d_c == kDc && a.d_rope == kDr && a.h <= kM && built_to_run() >= 0;
 }
 
-// Few queries are cut into pieces to fill the SMs: a round of items ends with its longest.  Either a cluster of 2, 4 or 8 CTAs takes a
+// Few queries are cut into pieces to fill the SMs: a round of items ends with its longest.  Either a cluster of 2 or 4 CTAs takes a
 // query and joins its pieces in shared memory, or any number of CTAs leave partial outputs for a merge: a launch and their way
-// through L2 more, but pieces of any length.  2,048 entries, 128 heads, clusters | partial outputs: 1 query 30.8 us (8 pieces) | 23.9 (32), 12 queries
-// 32.6 | 30.6, 32 queries 36.4 (4) | 41.8 (4), 64 queries 52.0 (2) | 69.6; 16 heads: 4 queries 20.6 | 24.2, 18 queries 26.5 (4) | 24.3 (8), 48
-// queries 40.2 (2) | 35.8 (3).
+// through L2 more, but pieces of any length.  2,048 entries, us, clusters (CTAs) | partial outputs (pieces): 128 heads, 1 query 34.7 (4) | 20.3 (32),
+// 12 queries 35.1 (4) | 29.2 (8), 24 queries 35.5 (4) | 35.9 (6), 32 queries 36.9 (4) | 40.4 (4), 64 queries 52.0 (2) | 67.7 (2); 16 heads, 4 queries
+// 26.2 (4) | 17.7 (16), 18 queries 26.5 (4) | 21.9 (8), 48 queries 40.3 (2) | 33.9 (3), 64 queries 40.8 (2) | 42.5 (2).  (Clusters of 8 were the
+// fastest form of one size in 110, by 1 %.)
 void attn4_tc_plan(Attn4Args& a) {
   const int chunks = chunks_of(a);
   const int64_t queries = a.seqs.total_q;
@@ -883,8 +885,7 @@ void attn4_tc_plan(Attn4Args& a) {
   auto consider = [&](int cluster, int splits) {
     const int64_t rounds = (queries * splits + clusters_of(cluster) - 1) / clusters_of(cluster);
     const int pieces = cluster * splits, longest = (chunks + pieces - 1) / pieces;
-    // (a piece is three chunks long at least: a single one waits for itself)
-    const double cost = rounds * ((longest < 3 ? 3 : longest) + kStart + heads * joining(cluster)) +
+    const double cost = rounds * (longest + kStart + joining(cluster, heads)) +
                         (splits > 1 ? kMerge + kPartial * heads * queries * splits : 0);
     if (cost >= best) return;
     best = cost;
@@ -914,8 +915,7 @@ int launch_attn4_tc(const Attn4Args& a, cudaStream_t stream) {
   switch (a.cluster) {
     case 1: rc = launch_pieces<1>(p, qmap, stream); break;
     case 2: return launch_pieces<2>(p, qmap, stream);
-    case 4: return launch_pieces<4>(p, qmap, stream);
-    default: return launch_pieces<8>(p, qmap, stream);
+    default: return launch_pieces<4>(p, qmap, stream);
   }
   return rc != DSA_OK || a.splits == 1 ? rc : launch_attn4_merge(a, stream);
 }

@@ -32,3 +32,24 @@ def test_kernel_of_a_width(dtype, dims, kernel):
         dsa.sparse_mla_attn4(P, q, kv4, idx)
     names = {name for name, _ in t.records}
     assert kernel in names and len({n for n in names if n.startswith("attn4")}) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("queries,h,top_k,merged", [
+    (1, 128, 2048, True), (12, 128, 2048, True), (18, 128, 2048, True), (32, 128, 2048, False), (64, 128, 2048, False),
+    (152, 128, 2048, False), (4, 16, 2048, True), (18, 16, 2048, True), (48, 16, 2048, True), (64, 16, 2048, False), (2, 128, 512, True),
+    (36, 128, 512, False), (12, 64, 2048, True), (30, 64, 2048, False)])
+def test_form_for_few_queries(queries, h, top_k, merged):
+    """Partial outputs and a merge, or clusters, as measured at these sizes (each at least 2 % apart)."""
+    import sparse_attention_lightning_gb300 as dsa
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    L = 2048 + queries
+    P = dsa.Problem(i32([0, queries]), i32([0, L]), q_lens=[queries], k_lens=[L], h_idx=4, d_idx=32, h=h, d_c=512, d_rope=64,
+                    top_k=top_k, idx_dtype="f32", kv_dtype="bf16")
+    q = torch.randn(queries, h, 576, device="cuda").bfloat16()
+    kv4 = torch.zeros(L, 416, dtype=torch.uint8, device="cuda")
+    idx = torch.arange(top_k, device="cuda", dtype=torch.int32).repeat(queries, 1)
+    with dsa.trace() as t:
+        out, lse = dsa.sparse_mla_attn4(P, q, kv4, idx)
+    assert any("merge" in name for name, _ in t.records) == merged
+    assert (out == 0).all() and torch.allclose(lse, torch.full_like(lse, top_k).log(), rtol=0, atol=1e-4)
