@@ -538,6 +538,8 @@ attn4_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     done += it.nch;
     if (S == 1) {
       if (!it.good) block_sync();
+      // (of offsets that do not rise the merge's search may find another sequence, a consistent one)
+      if (partial && !it.good && threadIdx.x < a.h) a.part_ml[it.piece * rows_all + it.row0 + threadIdx.x] = make_float2(0.f, -1.f);
       stopped = *abort_flag != 0;
     } else if (!it.good) {
       cluster_sync();

@@ -19,7 +19,7 @@ struct PrefixArgs {
   uint32_t* status;
   int splits;                  // pieces a row's keys are cut into
   float* part_o;               // [pieces][total_q · h][d_c] unnormalised partial outputs
-  float2* part_ml;             // [pieces][total_q · h] (max in log2 units, sum); sum 0: no keys
+  float2* part_ml;             // [pieces][total_q · h] (max in log2 units, sum); sum 0: no keys, < 0: the row stays as it was
 };
 
 struct SeqInfo {

@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(128, 64 / U) prefix_merge_kernel(const __grid_
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (l < 0.f) return;  // (the pieces' grid found the row's sequence inconsistent)
   const float inv = l == 0.f ? 0.f : 1.f / l;
   TO* o = static_cast<TO*>(a.out) + row * a.d_c;
   const float* po = a.part_o + row * a.d_c;
