@@ -454,6 +454,10 @@ int dsa_read_kv4(const dsa_problem* p, const void* kv4, void* out, void* ws, siz
  * or whose logits are all -inf, gets out = 0 and lse = -inf.  An entry that is skipped adds nothing, whatever its row holds.
  * Rows of a sequence whose cu_q/cu_k are inconsistent, or that has more than max_q_len queries, set DSA_FLAG_BAD_SEQS
  * and are left as they were.  out and lse must not overlap each other, q, kv4 or idx.
+ * Rounding: fp32 throughout, but for bf16 queries over 512 + 64 columns (tensor cores).  There each probability is rounded to bf16 ahead
+ * of its product with the values (the sum it is divided by is of unrounded ones), also where out_dtype is F32; and a query's
+ * latent columns are held relative to the head's largest finite one, each off by at most 2^-39 of that: columns smaller than
+ * 2^-29 of it lose bits, those smaller than 2^-39 count as 0.
  */
 int dsa_sparse_mla_attn4(const dsa_problem* p, const void* q, const void* kv4, const int32_t* idx,
                          void* out, float* lse, void* ws, size_t ws_bytes, void* stream);

@@ -919,7 +919,10 @@ def read_kv4(P: Problem, kv4, out=None, ws: Optional[Workspace] = None):
 def sparse_mla_attn4(P: Problem, q, kv4, idx, out=None, lse=None, want_lse: bool = True,
                      ws: Optional[Workspace] = None):
     """sparse_mla_attn over the 4-bit latent cache kv4 [cache rows, kv4_row_bytes(d_c, d_rope)] uint8
-    (dsa_sparse_mla_attn4): (out[ΣT, H, d_c], lse or None).  A captured call needs ws."""
+    (dsa_sparse_mla_attn4): (out[ΣT, H, d_c], lse or None).  A captured call needs ws.
+
+    With bf16 queries over 512 + 64 columns probabilities are rounded to bf16 (also for f32 outputs), and a head's latent query
+    columns are exact down to 2^-29 of its largest one and 0 below 2^-39 of it."""
     if not kv4.is_cuda:
         raise ValueError("kv4 must be a CUDA tensor")
     index = kv4.get_device()
