@@ -54,7 +54,9 @@ class Problem:
                  num_pages: int = 0):
         """block_table [B, max_pages] int32 (CUDA) with page_size > 0 and num_pages: the key
         caches (k_idx, kv, k_scale) are paged, num_pages * page_size rows; key position s of
-        sequence b is row block_table[b, s // page_size] * page_size + s % page_size."""
+        sequence b is row block_table[b, s // page_size] * page_size + s % page_size.
+        Calls read block_table as it is when they run, so pages reserved later are seen; a table
+        whose rows are apart is copied (contiguously), and the copy stays as it was."""
         if not (cu_q.is_cuda and cu_k.is_cuda) or cu_q.dtype != torch.int32 \
                 or cu_k.dtype != torch.int32:
             raise ValueError("cu_q/cu_k must be int32 CUDA tensors")

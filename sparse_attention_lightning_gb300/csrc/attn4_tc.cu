@@ -14,10 +14,10 @@
 //
 // What bounds it: not the MMAs (taking all but one of a chunk's out changes nothing), but the way of a chunk through
 // gather, decoding, softmax and their hand-overs, some 4,200 clocks for both phases: instructions (54 % of the issue slots), 1,152
-// clocks of operand stores, and the chains of waits between the roles.  1,024 queries of 2,048 entries, 128 heads: 534 us
-// (0.58 of the MMAs' floor), with one pass 890.  Steps on the way there: rows gathered by TMA, four 416-byte rows a copy (87
+// clocks of operand stores, and the chains of waits between the roles.  1,024 queries of 2,048 entries, 128 heads: 541 us
+// (0.57 of the MMAs' floor), with one pass 890.  Steps on the way there: rows gathered by TMA, four 416-byte rows a copy (87
 // clocks each: 730), by 16-byte asynchronous copies of the decoding warps (662), scales two at a time (618), fp16 logits (591), decoding in two groups
-// (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.  32 queries of 2,048 entries: 36.4 us
+// (538).  Loads straight to registers took 843: a warp's loads and its index loads wait for each other.  32 queries of 2,048 entries: 36.8 us
 // of four CTAs each, of which the first MMA comes after 13,000 clocks, eight chunks take 31,000 and O's way out 22,000.
 //
 // The running maximum m of a head only decides the scale of p: it starts as the first chunk's, rounded up to a whole number (of log2), moves

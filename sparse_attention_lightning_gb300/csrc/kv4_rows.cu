@@ -9,7 +9,8 @@
 //
 // Bound by HBM where there is work enough: a thread takes 16 latent columns (32 or 64 bytes in, 8 and 1 out) or 8 rope
 // columns, and a row's threads are neighbours.  Below some thousand rows it is the launch.  8,192 rows of 512 + 64 bf16
-// columns: written in 10.6 us and read back in 8.4 (1.2 and 1.5 TB/s), both two latencies of scattered 8- and 16-byte pieces long.
+// columns: written in 10.0 us and read back in 8.4 from HBM (1.3 and 1.5 TB/s), 6.1 and 4.6 where they are in L2: latencies in a chain (a row's
+// place by its sequence and page, its data) with scattered 8- and 16-byte pieces behind them.
 #include "kv4.cuh"
 
 namespace dsa {

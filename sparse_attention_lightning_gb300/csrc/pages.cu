@@ -9,7 +9,8 @@
 // kernel of the whole GPU behind it, 32 KB a block at a time, eight 16-byte loads a thread.
 //
 // 32 sequences of up to 32,768 positions and 16 samples of each: free 7.7 us, fork 8.1, reserve 24.4 (a chain of ten
-// steps of one CTA, one to two us each) and its copies 8.1.  A million rows in three caches, half of them gone: counted in 16.4 us and
+// steps of one CTA, one to two us each) and its copies 8.1.  Room for 64 whole prompts of 32,768 positions: 95 us in pages of 64, 352 of 16 (4,096 table
+// entries a round, twice).  A million rows in three caches, half of them gone: counted in 16.4 us and
 // moved in 57 (177 MB in, 177 out: 6.2 TB/s).
 #include <limits.h>
 

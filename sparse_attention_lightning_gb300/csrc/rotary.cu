@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   }
 }
 
-// Any width and alignment: a thread a pair.
+// Any width and alignment: a thread a pair, with 2- or 4-byte accesses and a sine of its own for every head (8,192 tokens of 128 heads, rows of 64
+// columns 2 bytes off: 462 us, ten times the kernel above).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const __grid_constant__ RotaryArgs a) {
   griddep_wait();
