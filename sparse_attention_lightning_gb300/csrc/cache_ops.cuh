@@ -16,7 +16,7 @@ constexpr int kMaxWidth = 1024 + 256;  // of a latent row (d_c + d_rope)
 // be moved ahead of the wait.  Those that begin an operator wait at their very start (the launch itself
 // then passes beside the kernel before: a call of 20 to 140 us is 2 to 3 us shorter in a row of calls), and let only
 // their own operator's next kernel start early, as a caller's next one may read its inputs ahead of its wait, and that only behind
-// their own wait: what such a kernel reads ahead is then complete.
+// their own wait, or behind a kernel of their operator that was launched plainly: what such a kernel reads ahead is then complete.
 
 // 2^x by the special-function unit (relative error about 2^-22; results below the normal numbers are 0).
 __device__ __forceinline__ float ex2(float x) {
